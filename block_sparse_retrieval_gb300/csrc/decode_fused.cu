@@ -31,6 +31,7 @@
 // leader.  Every wait is bounded (SRKV_EFLAG_TIMEOUT); every thread ends at one cluster
 // barrier, so no CTA leaves while another may still reach its shared memory (the leader's
 // consumers arrive on it as soon as every partial has landed, before they merge).
+#include "decode_int4.cuh"
 #include "decode_mma.cuh"
 #include "select.cuh"
 
@@ -58,9 +59,9 @@ constexpr int kBins = 1 << kHistBits;
 constexpr int kBinRank = 32;  // boundary bins up to this size are ranked by one warp
 static_assert(kMaxCand <= 1024, "bin ranks pack a candidate index into 10 bits");
 
-template <int D, bool F8 = false>
+template <int D, int Fmt = kBf16Pages>
 struct FusedCfg {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D, Fmt>;
   // after the ring (every CTA)
   // keys_ready, list_ready, parts_ready, scored
   static constexpr size_t kOffBars = (C::kSmem + 15) & ~size_t(15);
@@ -109,11 +110,11 @@ __device__ __forceinline__ int32_t share_begin(int32_t q, int32_t n, int32_t S) 
 }
 
 // Grid: one cluster of CS CTAs per unit; 8 consumer warps + 1 producer warp per CTA.
-template <int D, bool F8>
+template <int D, int Fmt>
 __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
                                                      const __grid_constant__ TmaMaps maps) {
-  using C = Cfg<D, F8>;
-  using F = FusedCfg<D, F8>;
+  using C = Cfg<D, Fmt>;
+  using F = FusedCfg<D, Fmt>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* keys_ready = reinterpret_cast<uint64_t*>(smem + F::kOffBars);
@@ -148,7 +149,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
   bool arrived = false;  // on the closing cluster barrier (warp-uniform)
 
   if (tid == 0) {
-    init_ring<D, F8>(smem);
+    init_ring<D, Fmt>(smem);
     mbar_init(keys_ready, kMaxCand);            // one per candidate, the rest at once
     mbar_init(list_ready, 1);                   // the leader, once the pool is laid out
     mbar_init(parts_ready, 1);                  // the leader, expecting every partial's bytes
@@ -248,7 +249,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
               break;
             }
           }
-          issue_stage_warp<D, F8>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, tl, armed, abort,
+          issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, tl, armed, abort,
                               eflags, lane);
           ++it;
         }
@@ -286,7 +287,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         } else if (lo < hi) {
           eflags |= SRKV_EFLAG_PAGE_RANGE;
         }
-        issue_stage_warp<D, F8>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, t, armed, abort,
+        issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, t, armed, abort,
                             eflags, lane);
         ++it;
       };
@@ -325,7 +326,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         PageTask none;
         none.page = -1;
         none.lo = none.hi = none.ie = none.ws = 0;
-        issue_stage<D, F8>(a, maps, smem, it, -1, kLast | kSegEnd, none, armed, abort, eflags);
+        issue_stage<D, Fmt>(a, maps, smem, it, -1, kLast | kSegEnd, none, armed, abort, eflags);
         uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
         uint64_t* full_v = full + C::kStages;
         const int64_t first = armed > C::kStages ? armed - C::kStages : 0;
@@ -568,6 +569,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         float l_run = w * l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, o);
+        const bool some = attended_any<Fmt == kInt4Pages>(l_run);
         for (int32_t half = warp / a.G; half < 2; half += hw) {
           // every streaming CTA wrote a partial (zeros if it attended nothing).  The loads and
           // weight shuffles of a batch of 8 slots are unconditional, so they issue together
@@ -603,28 +605,30 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) +
                              ((int64_t)r * a.Hq + (int64_t)h * a.G + head) * D + d0;
           if constexpr (V == 2) {
-            const float x0 = l_run > 0.f ? acc[0] / l_run : 0.f;
-            const float x1 = l_run > 0.f ? acc[1] / l_run : 0.f;
+            const float x0 = some ? acc[0] / l_run : 0.f;
+            const float x1 = some ? acc[1] / l_run : 0.f;
             *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x0, x1);
           } else {
-            *o = __float2bfloat16_rn(l_run > 0.f ? acc[0] / l_run : 0.f);
+            *o = __float2bfloat16_rn(some ? acc[0] / l_run : 0.f);
           }
         }
       }
     } else {
       // 3'. attend list A, then the kept blocks taken from the pool, as one segment; the
       // merged partial goes to the leader's shared memory
-      consumer_loop<D, F8>(a, smem, lane, warp,
-                       [&](const SoftmaxState<D>& st, const StageInfo&, Lane ln) {
-                         // asynchronous stores, each counted on the leader's parts_ready
-                         const uint32_t acc_r = cluster_addr(part_acc + (int64_t)q * a.G * D, 0);
-                         const uint32_t ml_r = cluster_addr(part_ml + (int64_t)q * a.G * 2, 0);
-                         const uint32_t bar_r = cluster_addr(parts_ready, 0);
-                         emit_partial<D, F8>(
-                             st, ln, a.G,
-                             [&](int i, float4 v) { st_async_f4(acc_r + 4u * i, v, bar_r); },
-                             [&](int j, float2 v) { st_async_f2(ml_r + 4u * j, v, bar_r); });
-                       });
+      auto write_partial = [&](const SoftmaxState<D>& st, const StageInfo&, Lane ln) {
+        // asynchronous stores, each counted on the leader's parts_ready
+        const uint32_t acc_r = cluster_addr(part_acc + (int64_t)q * a.G * D, 0);
+        const uint32_t ml_r = cluster_addr(part_ml + (int64_t)q * a.G * 2, 0);
+        const uint32_t bar_r = cluster_addr(parts_ready, 0);
+        emit_partial<D, Fmt>(
+            st, ln, a.G, [&](int i, float4 v) { st_async_f4(acc_r + 4u * i, v, bar_r); },
+            [&](int j, float2 v) { st_async_f2(ml_r + 4u * j, v, bar_r); });
+      };
+      if constexpr (Fmt == kInt4Pages)
+        consumer_loop_int4<D>(a, smem, lane, warp, write_partial);
+      else
+        consumer_loop<D, Fmt>(a, smem, lane, warp, write_partial);
     }
   }
   // nobody leaves while another CTA may still reach its shared memory
@@ -635,10 +639,10 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
 
 }  // namespace
 
-// Clusters of `cs` CTAs of fused_decode_kernel<D, F8> that can be resident at once (0 on error).
-template <int D, bool F8>
+// Clusters of `cs` CTAs of fused_decode_kernel<D, Fmt> that can be resident at once (0 on error).
+template <int D, int Fmt>
 int32_t max_active_clusters(int32_t cs) {
-  using F = FusedCfg<D, F8>;
+  using F = FusedCfg<D, Fmt>;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)cs);
   lc.blockDim = dim3((kConsumerWarps + 1) * 32);
@@ -650,12 +654,12 @@ int32_t max_active_clusters(int32_t cs) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  cudaFuncSetAttribute(fused_decode_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaFuncSetAttribute(fused_decode_kernel<D, Fmt>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)F::kSmemAlloc);
-  cudaFuncSetAttribute(fused_decode_kernel<D, F8>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+  cudaFuncSetAttribute(fused_decode_kernel<D, Fmt>, cudaFuncAttributeNonPortableClusterSizeAllowed,
                        1);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fused_decode_kernel<D, F8>, &lc) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, fused_decode_kernel<D, Fmt>, &lc) != cudaSuccess) {
     (void)cudaGetLastError();
     n = 0;
   }
@@ -671,26 +675,29 @@ int32_t max_active_clusters(int32_t cs) {
 // 0.4 and at 1.0 the three kernels' 152 streaming SMs win (151.3 against 152.6 us, 322
 // against 337).
 int32_t fused_cluster_size(const srkv_config& cfg, int32_t units, int32_t max_blocks,
-                           bool e4m3) {
+                           PageFormat fmt) {
   if (!mma_split_supported(cfg) || units <= 0) return 0;
-  if (e4m3 && cfg.head_dim != 128) return 0;
+  if (fmt == PageFormat::kE4m3 && cfg.head_dim != 128) return 0;
   const int64_t W = (int64_t)max_blocks * kBlock - cfg.local_tokens;
   const int64_t nmax = W > cfg.init_tokens ? (W + kBlock - 1) / kBlock - cfg.init_tokens / kBlock : 0;
   if (nmax > kMaxCand) return 0;
-  // [device][d 64, d 128, d 128 compressed][cluster 16 - c]: max active + 1
+  // [device][d 64, d 128, d 128 E4M3, d 64 and 128 4-bit][cluster 16 - c]: max active + 1
   constexpr int kSizes = kMaxCluster - 3;  // 16 .. 4
-  static int32_t cached[128][3][kSizes];
+  static int32_t cached[128][5][kSizes];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
-  const int di = e4m3 ? 2 : cfg.head_dim == 128 ? 1 : 0;
+  const bool d128 = cfg.head_dim == 128;
+  const int di = fmt == PageFormat::kInt4 ? 3 + d128 : fmt == PageFormat::kE4m3 ? 2 : d128;
   for (int c = 0; c < kSizes; ++c) {
     const int32_t cs = kMaxCluster - c;
     if (nmax > (int64_t)kMaxShare * cs) continue;  // per-CTA scoring share
     if (cs < 8 && (di != 1 || cfg.topk_percent > 0.3)) continue;
     if (cached[dev][di][c] == 0) {
-      const int32_t n = di == 2   ? max_active_clusters<128, true>(cs)
-                        : di == 1 ? max_active_clusters<128, false>(cs)
-                                  : max_active_clusters<64, false>(cs);
+      const int32_t n = di == 4   ? max_active_clusters<128, kInt4Pages>(cs)
+                        : di == 3 ? max_active_clusters<64, kInt4Pages>(cs)
+                        : di == 2 ? max_active_clusters<128, kE4m3Pages>(cs)
+                        : di == 1 ? max_active_clusters<128, kBf16Pages>(cs)
+                                  : max_active_clusters<64, kBf16Pages>(cs);
       cached[dev][di][c] = n + 1;
     }
     if (units <= cached[dev][di][c] - 1) return cs;
@@ -698,17 +705,18 @@ int32_t fused_cluster_size(const srkv_config& cfg, int32_t units, int32_t max_bl
   return 0;
 }
 
-template <int D, bool F8>
+template <int D, int Fmt>
 cudaError_t launch_fused_t(const DecodeArgs& a, int32_t cluster, cudaStream_t stream) {
-  TmaMaps maps;
-  if (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, F8) ||
-      !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, F8))
+  TmaMaps maps = {};  // 4-bit pages need none
+  if (Fmt != kInt4Pages &&
+      (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages) ||
+       !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages)))
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)a.batch * a.Hkv * cluster;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)grid);
   lc.blockDim = dim3((kConsumerWarps + 1) * 32);
-  lc.dynamicSmemBytes = FusedCfg<D, F8>::kSmemAlloc;
+  lc.dynamicSmemBytes = FusedCfg<D, Fmt>::kSmemAlloc;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -719,13 +727,16 @@ cudaError_t launch_fused_t(const DecodeArgs& a, int32_t cluster, cudaStream_t st
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, fused_decode_kernel<D, F8>, a, maps);
+  return cudaLaunchKernelEx(&lc, fused_decode_kernel<D, Fmt>, a, maps);
 }
 
 cudaError_t launch_fused(const DecodeArgs& a, int32_t cluster, cudaStream_t stream) {
-  if (a.k_scale) return launch_fused_t<128, true>(a, cluster, stream);  // compressed pages
-  return a.d == 128 ? launch_fused_t<128, false>(a, cluster, stream)
-                    : launch_fused_t<64, false>(a, cluster, stream);
+  if (a.int4)
+    return a.d == 128 ? launch_fused_t<128, kInt4Pages>(a, cluster, stream)
+                      : launch_fused_t<64, kInt4Pages>(a, cluster, stream);
+  if (a.k_scale) return launch_fused_t<128, kE4m3Pages>(a, cluster, stream);
+  return a.d == 128 ? launch_fused_t<128, kBf16Pages>(a, cluster, stream)
+                    : launch_fused_t<64, kBf16Pages>(a, cluster, stream);
 }
 
 }  // namespace srkv

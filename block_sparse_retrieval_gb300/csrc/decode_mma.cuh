@@ -17,6 +17,7 @@
 #pragma once
 
 #include "decode_plan.cuh"
+#include "int4_page.cuh"
 
 namespace srkv {
 
@@ -34,10 +35,13 @@ struct StageInfo {
   int32_t pad[2];
 };
 
-// F8: the pages hold E4M3 codes (one byte per value) and each stage also carries the 128
-// K and 128 V row scales of its page.
-template <int D, bool F8 = false>
+// What the pages hold: bf16 values, E4M3 codes (each stage then also carries the 128 K and 128 V
+// row scales of its page) or 4-bit codes (int4_page.cuh; a stage is one slab).
+enum : int { kBf16Pages = 0, kE4m3Pages = 1, kInt4Pages = 2 };
+
+template <int D, int Fmt = kBf16Pages>
 struct Cfg {
+  static constexpr bool F8 = Fmt == kE4m3Pages;
   static_assert(!F8 || D == 128, "compressed pages: d 128");
   static constexpr int kElem = F8 ? 1 : 2;              // bytes per cached value
   static constexpr int kSlab = kBlock * D * kElem;      // bytes of one K or V slab
@@ -62,6 +66,27 @@ struct Cfg {
   static constexpr size_t kSmemAlloc = kSmem + 1024;  // the swizzled stages need 1 KiB alignment
   static constexpr int kBoxes = D * kElem / 128;       // 128-byte-wide TMA boxes per slab
   static constexpr int kBoxBytes = kBlock * 128;       // 128 rows of 128 bytes
+};
+
+// 4-bit pages: a stage is one slab (17 408 bytes at d 128), moved by one bulk copy.
+template <int D>
+struct Cfg<D, kInt4Pages> {
+  static constexpr int kSlab = Int4Slab<D>::kBytes;
+  static constexpr int kStages = D == 128 ? 10 : 18;
+  static constexpr int kQBytes = 8 * D * 2;
+  static constexpr int MT = D / 16;
+  static constexpr int kMergeStride = Cfg<D>::kMergeStride;
+  static constexpr int kMergeSlot = Cfg<D>::kMergeSlot;
+
+  static constexpr size_t kOffK = 0;
+  static constexpr size_t kOffQ = (size_t)kStages * kSlab;
+  // the one-kernel decode's leader streams no pages and keeps its partials from here on
+  static constexpr size_t kOffV = (size_t)(kStages / 2) * kSlab;
+  static constexpr size_t kOffMerge = kOffQ + (size_t)kStages * kQBytes;
+  static constexpr size_t kOffInfo = kOffMerge + sizeof(float) * 4 * kMergeSlot;
+  static constexpr size_t kOffBar = kOffInfo + sizeof(StageInfo) * kStages;
+  static constexpr size_t kSmem = kOffBar + sizeof(uint64_t) * (3 * kStages + 3);
+  static constexpr size_t kSmemAlloc = kSmem + 1024;
 };
 
 // Tensor maps of the K and V caches, [page][kv head * 128 + row][d] (bf16).
@@ -143,12 +168,13 @@ __device__ __forceinline__ int d_of(int g, int v) {
 
 // Hands stage `it` to the consumers: waits until it is free, writes its description and
 // arms its mbarrier with the bytes of the copies it starts (called by one producer lane).
-template <int D, bool F8 = false>
+template <int D, int Fmt = kBf16Pages>
 __device__ __forceinline__ void issue_stage(const DecodeArgs& a, const TmaMaps& maps,
                                             unsigned char* smem, int64_t it, int32_t u,
                                             uint32_t fl, const PageTask& t, int64_t& armed,
                                             bool& abort, uint32_t& eflags) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D, Fmt>;
+  constexpr bool F8 = Fmt == kE4m3Pages;
   if (abort) return;
   StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem + C::kOffInfo);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -176,6 +202,24 @@ __device__ __forceinline__ void issue_stage(const DecodeArgs& a, const TmaMaps& 
   // is still arriving.
   const bool rows = load && t.hi > t.lo;
   const uint32_t qbytes = (uint32_t)(a.G * D * 2);
+  if constexpr (Fmt == kInt4Pages) {  // keys, values and rows land together
+    mbar_arrive_expect_tx(&full[s], (rows ? (uint32_t)C::kSlab : 0u) +
+                                        ((fl & kNewUnit) ? qbytes : 0u));
+    mbar_arrive(&full_v[s]);
+    ++armed;
+    if (u < 0) return;
+    const int32_t h = u % a.Hkv, r = u / a.Hkv;
+    if (rows)
+      bulk_load_hint(smem + C::kOffK + (size_t)s * C::kSlab,
+                     static_cast<const unsigned char*>(a.k_cache) +
+                         ((int64_t)t.page * a.Hkv + h) * C::kSlab,
+                     (uint32_t)C::kSlab, &full[s], l2_policy_evict_first());
+    if (fl & kNewUnit)
+      bulk_load(smem + C::kOffQ + (size_t)s * C::kQBytes,
+                static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)r * a.Hq + (int64_t)h * a.G) * D,
+                qbytes, &full[s]);
+    return;
+  } else {
   constexpr uint32_t kRowScales = F8 ? kBlock * 4 : 0;  // one fp32 scale per row
   if (!F8 && rows && t.page >= a.num_pages) {
     // A page of the host pool: the producer warp copies its slabs and then arrives
@@ -222,6 +266,7 @@ __device__ __forceinline__ void issue_stage(const DecodeArgs& a, const TmaMaps& 
                      a.v_scale + ((int64_t)t.page * a.Hkv + h) * kBlock, kRowScales,
                      &full[s], once);
   }
+  }  // bf16 and E4M3 pages
 }
 
 // issue_stage for the whole producer warp (every lane calls it with the same arguments).  A
@@ -229,15 +274,15 @@ __device__ __forceinline__ void issue_stage(const DecodeArgs& a, const TmaMaps& 
 // tensor-map copies produce (128-byte swizzle), so the consumers read both kinds of stage
 // alike: over NVLink-C2C the host pool is read in place, with no staging copy in HBM.  Each
 // lane ties its copies to the stage's barriers, then lane 0 arrives.
-template <int D, bool F8 = false>
+template <int D, int Fmt = kBf16Pages>
 __device__ __forceinline__ void issue_stage_warp(const DecodeArgs& a, const TmaMaps& maps,
                                                  unsigned char* smem, int64_t it, int32_t u,
                                                  uint32_t fl, const PageTask& t, int64_t& armed,
                                                  bool& abort, uint32_t& eflags, int lane) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D, Fmt>;
   // (compressed pages have no host pool)
-  const bool host = !F8 && t.page >= 0 && t.hi > t.lo && t.page >= a.num_pages;  // uniform
-  if (lane == 0) issue_stage<D, F8>(a, maps, smem, it, u, fl, t, armed, abort, eflags);
+  const bool host = Fmt == kBf16Pages && t.page >= 0 && t.hi > t.lo && t.page >= a.num_pages;  // uniform
+  if (lane == 0) issue_stage<D, Fmt>(a, maps, smem, it, u, fl, t, armed, abort, eflags);
   abort = __shfl_sync(0xffffffffu, abort, 0);
   if (!host || abort) return;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -275,12 +320,24 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 
 // A merged state (acc, m, l of the lane's two heads) as a partial of acc[G][D] and ml[G][2]
 // floats: put4(i, v) for the 16-byte piece at acc[i], put2(j, v) for (m, l) at ml[j].
-template <int D, bool F8, typename Put4, typename Put2>
+template <int D, int Fmt, typename Put4, typename Put2>
 __device__ __forceinline__ void emit_partial(const SoftmaxState<D>& st, Lane ln, int G,
                                              Put4 put4, Put2 put2) {
   using C = Cfg<D>;
   const int h0 = 2 * ln.t, h1 = h0 + 1;
-  if constexpr (F8) {
+  if constexpr (Fmt == kInt4Pages) {
+    // m-tiles 2x and 2x + 1 hold d = 32x + 4g + 0, 1 and + 2, 3 (rows g and g + 8)
+#pragma unroll
+    for (int x = 0; x < C::MT / 2; ++x) {
+      const int dd = 32 * x + 4 * ln.g;
+      if (h0 < G)
+        put4(h0 * D + dd, make_float4(st.acc[2 * x][0], st.acc[2 * x][2], st.acc[2 * x + 1][0],
+                                      st.acc[2 * x + 1][2]));
+      if (h1 < G)
+        put4(h1 * D + dd, make_float4(st.acc[2 * x][1], st.acc[2 * x][3], st.acc[2 * x + 1][1],
+                                      st.acc[2 * x + 1][3]));
+    }
+  } else if constexpr (Fmt == kE4m3Pages) {
     // compressed pages: m-tile i row g holds d = 16g + 2i, row g + 8 holds d = 16g + 2i + 1,
     // so the lane's 16 values per head are d = 16g .. 16g + 15 in the order
     // (i 0 row g, i 0 row g+8, i 1 row g, ...)
@@ -321,10 +378,10 @@ __device__ __forceinline__ void emit_partial(const SoftmaxState<D>& st, Lane ln,
 
 // Writes a merged state as a partial through generic pointers (global memory or another
 // CTA's shared memory).
-template <int D, bool F8 = false>
+template <int D, int Fmt = kBf16Pages>
 __device__ __forceinline__ void store_partial(float* accp, float* mlp, const SoftmaxState<D>& st,
                                               Lane ln, int G) {
-  emit_partial<D, F8>(
+  emit_partial<D, Fmt>(
       st, ln, G, [&](int i, float4 v) { *reinterpret_cast<float4*>(accp + i) = v; },
       [&](int j, float2 v) {
         mlp[j] = v.x;
@@ -336,10 +393,11 @@ __device__ __forceinline__ void store_partial(float* accp, float* mlp, const Sof
 // At the end of each segment (a stage flagged kSegEnd; the sentinel may carry the flag too,
 // closing a segment whose length the producer did not know in advance) the warps merge their
 // states and warp 0 calls write_partial(state, stage info, lane) with the merged state.
-template <int D, bool F8 = false, typename WritePartial>
+template <int D, int Fmt = kBf16Pages, typename WritePartial>
 __device__ __forceinline__ void consumer_loop(const DecodeArgs& a, unsigned char* smem, int lane,
                                               int warp, WritePartial&& write_partial) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D, Fmt>;
+  constexpr bool F8 = Fmt == kE4m3Pages;
   unsigned char* sK = smem + C::kOffK;
   unsigned char* sV = smem + C::kOffV;
   unsigned char* sQ = smem + C::kOffQ;
@@ -596,9 +654,9 @@ __device__ __forceinline__ void consumer_loop(const DecodeArgs& a, unsigned char
 }
 
 // Barrier setup of the stage ring (one thread; fenced for the async proxy and the cluster).
-template <int D, bool F8 = false>
+template <int D, int Fmt = kBf16Pages>
 __device__ __forceinline__ void init_ring(unsigned char* smem) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D, Fmt>;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full_v = full + C::kStages;
   uint64_t* empty = full_v + C::kStages;

@@ -18,6 +18,7 @@
 //   consumers: consumer_loop (decode_mma.cuh); at the end of a unit's segment the 8 warps
 //             merge and warp 0 writes the partial to slot unit + CTA of the workspace.
 // Every wait is bounded (SRKV_EFLAG_TIMEOUT).
+#include "decode_int4.cuh"
 #include "decode_mma.cuh"
 
 namespace srkv {
@@ -26,10 +27,10 @@ namespace {
 // 128 registers: a quarter-SM register file (16K) then holds this CTA's three warps on one
 // sub-partition (12K) beside one warp of a combine CTA, so the combine is resident and
 // waiting when the last partial is written.
-template <int D, bool F8>
+template <int D, int Fmt>
 __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
                                                   const __grid_constant__ TmaMaps maps) {
-  using C = Cfg<D, F8>;
+  using C = Cfg<D, Fmt>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem + C::kOffInfo);
@@ -43,7 +44,7 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   // the previous kernel in the stream has finished, and the combine reads them too.
   if (!a.early && !a.wait_late) griddep_wait();
   griddep_launch_dependents();
-  if (tid == 0) init_ring<D, F8>(smem);
+  if (tid == 0) init_ring<D, Fmt>(smem);
   __syncthreads();
 
   if (warp == kProducerWarp) {
@@ -128,7 +129,7 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
           // A selected shared-prefix block loads nothing here (the cascade kernel attends
           // it); it takes a stage only when it opens or closes the unit's segment.
           if (a.prefix_blocks > 0 && t.page < 0 && !(fl & (kNewUnit | kSegEnd))) continue;
-          issue_stage_warp<D, F8>(a, maps, smem, it, u, fl, t, armed, abort, eflags, lane);
+          issue_stage_warp<D, Fmt>(a, maps, smem, it, u, fl, t, armed, abort, eflags, lane);
           ++it;
         }
       }
@@ -137,7 +138,7 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
       PageTask none;
       none.page = -1;
       none.lo = none.hi = none.ie = none.ws = 0;
-      issue_stage<D, F8>(a, maps, smem, it, -1, kLast, none, armed, abort, eflags);  // sentinel
+      issue_stage<D, Fmt>(a, maps, smem, it, -1, kLast, none, armed, abort, eflags);  // sentinel
       // Drain: every copy this CTA issued must land before the CTA exits.
       const int64_t first = armed > C::kStages ? armed - C::kStages : 0;
       for (int64_t i = first; i < armed; ++i)
@@ -154,13 +155,16 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
 
   // -------------------------------------------------------------------- consumers
   // warp 0 writes the partial of (unit, this CTA) into the list's bank
-  consumer_loop<D, F8>(a, smem, lane, warp, [&](const SoftmaxState<D>& st, const StageInfo& inf,
-                                            Lane ln) {
+  auto write_partial = [&](const SoftmaxState<D>& st, const StageInfo& inf, Lane ln) {
     const int64_t slot =
         ((inf.flags & kBankB) ? (int64_t)a.lay.bank : 0) + inf.unit + blockIdx.x;
-    store_partial<D, F8>(reinterpret_cast<float*>(a.ws + a.lay.acc) + slot * a.G * D,
+    store_partial<D, Fmt>(reinterpret_cast<float*>(a.ws + a.lay.acc) + slot * a.G * D,
                      reinterpret_cast<float*>(a.ws + a.lay.ml) + slot * a.G * 2, st, ln, a.G);
-  });
+  };
+  if constexpr (Fmt == kInt4Pages)
+    consumer_loop_int4<D>(a, smem, lane, warp, write_partial);
+  else
+    consumer_loop<D, Fmt>(a, smem, lane, warp, write_partial);
 }
 
 }  // namespace
@@ -234,7 +238,7 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_pages, int
   return true;
 }
 
-template <int D, bool F8>
+template <int D, int Fmt>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
   // The shared-memory opt-in is set once per device (not during graph capture).
   static bool configured[128] = {false};
@@ -243,23 +247,26 @@ cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(split_mma_kernel<D, F8>,
+    e = cudaFuncSetAttribute(split_mma_kernel<D, Fmt>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Cfg<D, F8>::kSmemAlloc);
+                             (int)Cfg<D, Fmt>::kSmemAlloc);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  TmaMaps maps;
-  if (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, F8) ||
-      !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, F8))
+  TmaMaps maps = {};  // 4-bit pages need none: a slab is one bulk copy
+  if (Fmt != kInt4Pages &&
+      (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages) ||
+       !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages)))
     return cudaErrorInvalidValue;
-  return launch_pdl(split_mma_kernel<D, F8>, dim3(a.ctas), dim3(kThreads),
-                    Cfg<D, F8>::kSmemAlloc, stream, a, maps);
+  return launch_pdl(split_mma_kernel<D, Fmt>, dim3(a.ctas), dim3(kThreads),
+                    Cfg<D, Fmt>::kSmemAlloc, stream, a, maps);
 }
 
 cudaError_t launch_split_mma(const DecodeArgs& a, cudaStream_t stream) {
-  if (a.k_scale) return launch_d<128, true>(a, stream);  // compressed pages (d 128)
-  return a.d == 128 ? launch_d<128, false>(a, stream) : launch_d<64, false>(a, stream);
+  if (a.int4)
+    return a.d == 128 ? launch_d<128, kInt4Pages>(a, stream) : launch_d<64, kInt4Pages>(a, stream);
+  if (a.k_scale) return launch_d<128, kE4m3Pages>(a, stream);  // (d 128)
+  return a.d == 128 ? launch_d<128, kBf16Pages>(a, stream) : launch_d<64, kBf16Pages>(a, stream);
 }
 
 }  // namespace srkv

@@ -1,0 +1,363 @@
+// quantize_int4.cu -- 4-bit pages: compressing pages, reading them back, appending tokens.
+//
+// KV-cache survey "大模型推理百倍加速之KV cache篇" lists quantisation of the cache among the
+// ways to shrink it; the format and the rounding are in int4_page.cuh (17 408 bytes a
+// (page, kv head) slab at d 128, against 65 536 in bf16).
+#include "int4_page.cuh"
+
+namespace srkv {
+namespace {
+
+constexpr int kInt4Warps = 8;
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&v);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Smallest and largest of a row's values held 8 per lane by LPR neighbouring lanes (NaN wins).
+template <int LPR>
+__device__ __forceinline__ void row_range(const int4& w, float& lo, float& hi) {
+  const uint32_t u[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
+  __nv_bfloat162 mn = as_bf162(u[0]), mx = mn;
+#pragma unroll
+  for (int e = 1; e < 4; ++e) {
+    mn = __hmin2_nan(mn, as_bf162(u[e]));
+    mx = __hmax2_nan(mx, as_bf162(u[e]));
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mn), o)));
+    mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mx), o)));
+  }
+  lo = __bfloat162float(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn)));
+  hi = __bfloat162float(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx)));
+}
+
+// Codes of a lane's 8 values.
+__device__ __forceinline__ void lane_codes(const int4& w, uint32_t row, uint32_t (&c)[8]) {
+  const uint32_t u[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
+  const float lo = int4_lo(row), scale = int4_scale(row), inv = int4_inv(scale);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c[2 * e] = int4_code(bf16_lo(u[e]), lo, scale, inv);
+    c[2 * e + 1] = int4_code(bf16_hi(u[e]), lo, scale, inv);
+  }
+}
+
+// Warp = 8 consecutive tokens (an octet) of one listed page and kv head, keys and values: d / 8
+// lanes a row with 8 values each (16-byte loads, all issued before the first is used).  A lane's
+// 8 key codes are one word.  Value words hold 8 tokens of one element: each lane first sets its
+// own tokens' nibbles in the words of its 8 elements, then the lanes that share those elements
+// exchange halves and OR them, each keeping its share of finished words.
+// Bytes: 4 d read, d + 8 written a token.
+template <int D>
+__global__ void __launch_bounds__(kInt4Warps * 32)
+    quantize_int4_kernel(const __nv_bfloat16* __restrict__ k_src,
+                         const __nv_bfloat16* __restrict__ v_src, int64_t num_pages,
+                         const int32_t* __restrict__ page_ids, int32_t n_pages, int32_t Hkv,
+                         unsigned char* __restrict__ kv, int64_t num_slab_pages,
+                         const int32_t* __restrict__ slab_ids, int32_t* error_flags) {
+  using F = Int4Slab<D>;
+  constexpr int LPR = D / 8;      // lanes per row
+  constexpr int RPL = 32 / LPR;   // rows per warp-wide load
+  constexpr int LOADS = 8 / RPL;
+  const int lane = threadIdx.x & 31;
+  const int64_t oct = (int64_t)blockIdx.x * kInt4Warps + (threadIdx.x >> 5);
+  if (oct >= (int64_t)n_pages * Hkv * (kBlock / 8)) return;
+  const int32_t o = (int32_t)(oct % (kBlock / 8));
+  const int64_t ih = oct / (kBlock / 8);
+  const int32_t i = (int32_t)(ih / Hkv), h = (int32_t)(ih % Hkv);
+  const int32_t page = page_ids[i], dst = slab_ids ? slab_ids[i] : page;
+  if (page < 0 || (int64_t)page >= num_pages || dst < 0 || (int64_t)dst >= num_slab_pages) {
+    if (lane == 0 && o == 0 && h == 0) raise_flags(error_flags, SRKV_EFLAG_PAGE_RANGE);
+    return;
+  }
+  const int sub = lane / LPR, col = (lane % LPR) * 8;  // row within a load, first element
+  const int64_t src = (((int64_t)page * Hkv + h) * kBlock + o * 8) * D;
+  unsigned char* slab = kv + ((int64_t)dst * Hkv + h) * F::kBytes;
+  int4 kw[LOADS], vw[LOADS];
+#pragma unroll
+  for (int l = 0; l < LOADS; ++l) {
+    const int64_t at = src + (int64_t)(l * RPL + sub) * D + col;
+    kw[l] = *reinterpret_cast<const int4*>(k_src + at);
+    vw[l] = *reinterpret_cast<const int4*>(v_src + at);
+  }
+  uint32_t* k_words = reinterpret_cast<uint32_t*>(slab);
+  uint32_t* v_words = reinterpret_cast<uint32_t*>(slab + F::kVCodes);
+  uint32_t* k_rows = reinterpret_cast<uint32_t*>(slab + F::kKRows);
+  uint32_t* v_rows = reinterpret_cast<uint32_t*>(slab + F::kVRows);
+  uint32_t part[8] = {};
+#pragma unroll
+  for (int l = 0; l < LOADS; ++l) {
+    const int j = l * RPL + sub, tok = o * 8 + j;
+    float lo, hi;
+    uint32_t c[8];
+    row_range<LPR>(kw[l], lo, hi);
+    uint32_t row = int4_row(lo, hi);
+    lane_codes(kw[l], row, c);
+    uint32_t word = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) word |= c[e] << int4_shift(e);
+    k_words[tok * F::kWordsPerRow + col / 8] = word;
+    if (col == 0) k_rows[tok] = row;
+    row_range<LPR>(vw[l], lo, hi);
+    row = int4_row(lo, hi);
+    lane_codes(vw[l], row, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[e] |= c[e] << int4_shift(j);
+    if (col == 0) v_rows[tok] = row;
+  }
+  // Halve the elements and double the tokens, RPL times over: of `have` words each lane sends
+  // the half its partner keeps.
+  int first = 0;  // first of the lane's words, relative to col
+#pragma unroll
+  for (int have = 8, mask = 16; mask >= LPR; mask >>= 1, have >>= 1) {
+    const bool upper = (lane & mask) != 0;
+#pragma unroll
+    for (int e = 0; e < have / 2; ++e) {
+      const uint32_t send = upper ? part[e] : part[e + have / 2];
+      const uint32_t keep = upper ? part[e + have / 2] : part[e];
+      part[e] = keep | __shfl_xor_sync(0xffffffffu, send, mask);
+    }
+    first += upper ? have / 2 : 0;
+  }
+  uint32_t* vd = v_words + int4_v_word<D>(o * 8, col + first);
+  if constexpr (RPL == 2)
+    *reinterpret_cast<uint4*>(vd) = make_uint4(part[0], part[1], part[2], part[3]);
+  else
+    *reinterpret_cast<uint2*>(vd) = make_uint2(part[0], part[1]);
+}
+
+// bf16 pair code * scale + lo of the pair of codes in the low nibbles of x's halves: 128 + code is
+// a bf16 of its own (0x4300 | code), the subtraction is exact and the multiply-add rounds once.
+__device__ __forceinline__ uint32_t pair_values(uint32_t x, __nv_bfloat162 scale,
+                                                __nv_bfloat162 lo) {
+  const __nv_bfloat162 c = __hsub2(as_bf162((x & 0x000f000fu) | 0x43004300u),
+                                   as_bf162(0x43004300u));
+  return as_u32(__hfma2(c, scale, lo));
+}
+
+// Warp = 16 consecutive tokens of one listed page and kv head.  Keys: d / 8 lanes a row, one word
+// in and 16 bytes out a lane.  Values: a lane takes 8 elements of an octet (two 16-byte loads),
+// and its 8 words hold 8 tokens of them: 16 bytes out a token.  Every store of a warp covers
+// whole rows.  Bytes: d + 8 read, 4 d written a token.
+template <int D>
+__global__ void __launch_bounds__(kInt4Warps * 32)
+    dequantize_int4_kernel(const unsigned char* __restrict__ kv, int64_t num_slab_pages,
+                           const int32_t* __restrict__ slab_ids, int32_t n_pages, int32_t Hkv,
+                           __nv_bfloat16* __restrict__ k_dst, __nv_bfloat16* __restrict__ v_dst,
+                           int64_t num_pages, const int32_t* __restrict__ page_ids,
+                           int32_t* error_flags) {
+  using F = Int4Slab<D>;
+  constexpr int LPR = D / 8;     // lanes per row
+  constexpr int RPL = 32 / LPR;  // rows (keys) or octets (values) at once
+  constexpr int kToks = 8 * RPL;  // tokens per warp: 16 (d 128) or 32 (d 64)
+  const int lane = threadIdx.x & 31;
+  const int64_t gw = (int64_t)blockIdx.x * kInt4Warps + (threadIdx.x >> 5);
+  if (gw >= (int64_t)n_pages * Hkv * (kBlock / kToks)) return;
+  const int32_t t0 = (int32_t)(gw % (kBlock / kToks)) * kToks;
+  const int64_t ih = gw / (kBlock / kToks);
+  const int32_t i = (int32_t)(ih / Hkv), h = (int32_t)(ih % Hkv);
+  const int32_t src = slab_ids[i], page = page_ids ? page_ids[i] : src;
+  if (src < 0 || (int64_t)src >= num_slab_pages || page < 0 || (int64_t)page >= num_pages) {
+    if (lane == 0 && t0 == 0 && h == 0) raise_flags(error_flags, SRKV_EFLAG_PAGE_RANGE);
+    return;
+  }
+  const unsigned char* slab = kv + ((int64_t)src * Hkv + h) * F::kBytes;
+  const uint32_t* k_words = reinterpret_cast<const uint32_t*>(slab);
+  const uint32_t* v_words = reinterpret_cast<const uint32_t*>(slab + F::kVCodes);
+  const uint32_t* k_rows = reinterpret_cast<const uint32_t*>(slab + F::kKRows);
+  const uint32_t* v_rows = reinterpret_cast<const uint32_t*>(slab + F::kVRows);
+  const int sub = lane / LPR, col = (lane % LPR) * 8;
+  const int64_t out = (((int64_t)page * Hkv + h) * kBlock + t0) * D + col;
+  const int ot = t0 + 8 * sub;  // the lane's octet of values
+  uint32_t kx[8], kr[8], vr[8];
+#pragma unroll
+  for (int l = 0; l < 8; ++l) {
+    const int tok = t0 + l * RPL + sub;
+    kx[l] = k_words[tok * F::kWordsPerRow + col / 8];
+    kr[l] = k_rows[tok];
+    vr[l] = v_rows[ot + l];
+  }
+  const uint4 va = *reinterpret_cast<const uint4*>(v_words + int4_v_word<D>(ot, col));
+  const uint4 vb = *reinterpret_cast<const uint4*>(v_words + int4_v_word<D>(ot, col + 4));
+  auto scale2 = [](uint32_t row) { return as_bf162(__byte_perm(row, row, 0x1010)); };
+  auto lo2 = [](uint32_t row) { return as_bf162(__byte_perm(row, row, 0x3232)); };
+#pragma unroll
+  for (int l = 0; l < 8; ++l) {
+    const __nv_bfloat162 s = scale2(kr[l]), m = lo2(kr[l]);
+    *reinterpret_cast<uint4*>(k_dst + out + (int64_t)(l * RPL + sub) * D) =
+        make_uint4(pair_values(kx[l], s, m), pair_values(kx[l] >> 4, s, m),
+                   pair_values(kx[l] >> 8, s, m), pair_values(kx[l] >> 12, s, m));
+  }
+  const uint32_t v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {  // tokens j and j + 1: the low and high halves at bit 2 j
+    const __nv_bfloat162 s0 = scale2(vr[j]), m0 = lo2(vr[j]);
+    const __nv_bfloat162 s1 = scale2(vr[j + 1]), m1 = lo2(vr[j + 1]);
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = v[2 * e] >> (2 * j), y = v[2 * e + 1] >> (2 * j);
+      a[e] = pair_values(__byte_perm(x, y, 0x5410), s0, m0);
+      b[e] = pair_values(__byte_perm(x, y, 0x7632), s1, m1);
+    }
+    __nv_bfloat16* p = v_dst + out + (int64_t)(8 * sub + j) * D;
+    *reinterpret_cast<uint4*>(p) = make_uint4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<uint4*>(p + D) = make_uint4(b[0], b[1], b[2], b[3]);
+  }
+}
+
+// CTA (request r, kv head h): the new token's key and value become row L % 128 of page
+// block_table[r][L / 128], and the page's representation vector the fp32 mean of its keys as
+// they now stand (lo + code * scale over rows [0, L % 128]): the rows say all there is, so a
+// token written again, or after the length was set back, gives the same vector.  Thread =
+// (row group, word): fixed order of sums.
+constexpr int kAppendThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads)
+    append_kv_int4_kernel(const __nv_bfloat16* __restrict__ k_new,
+                          const __nv_bfloat16* __restrict__ v_new, unsigned char* kv,
+                          int64_t num_pages, const int32_t* __restrict__ block_table,
+                          int32_t max_blocks, const int32_t* __restrict__ seq_lens, int32_t Hkv,
+                          float* __restrict__ reps, int32_t* error_flags) {
+  using F = Int4Slab<D>;
+  constexpr int LPR = D / 8;                      // words (and lanes) per row
+  constexpr int kGroups = kAppendThreads / LPR;   // row groups
+  __shared__ float part[kGroups][D];
+  __shared__ uint32_t new_k[LPR], new_row;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t r = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
+  griddep_wait();  // programmatic launch: the inputs may be the previous kernel's outputs
+  griddep_launch_dependents();
+  const int32_t L = seq_lens[r];
+  if (L < 0 || (int64_t)L >= (int64_t)max_blocks * kBlock) {
+    if (tid == 0 && h == 0) raise_flags(error_flags, SRKV_EFLAG_SEQ_LEN);
+    return;
+  }
+  const int32_t page = block_table[(int64_t)r * max_blocks + L / kBlock];
+  if (page < 0 || (int64_t)page >= num_pages) {
+    if (tid == 0 && h == 0) raise_flags(error_flags, SRKV_EFLAG_PAGE_RANGE);
+    return;
+  }
+  const int32_t tok = L % kBlock;
+  unsigned char* slab = kv + ((int64_t)page * Hkv + h) * F::kBytes;
+  uint32_t* k_words = reinterpret_cast<uint32_t*>(slab);
+  uint32_t* v_words = reinterpret_cast<uint32_t*>(slab + F::kVCodes);
+  uint32_t* k_rows = reinterpret_cast<uint32_t*>(slab + F::kKRows);
+  uint32_t* v_rows = reinterpret_cast<uint32_t*>(slab + F::kVRows);
+  if (warp < 2) {  // warp 0: the key, warp 1: the value; lanes past the row repeat it
+    const int col = (lane % LPR) * 8;
+    const __nv_bfloat16* x = (warp ? v_new : k_new) + ((int64_t)r * Hkv + h) * D + col;
+    const int4 w = *reinterpret_cast<const int4*>(x);
+    float lo, hi;
+    row_range<LPR>(w, lo, hi);
+    const uint32_t row = int4_row(lo, hi);
+    uint32_t c[8];
+    lane_codes(w, row, c);
+    if (lane < LPR) {
+      if (warp == 0) {
+        uint32_t word = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) word |= c[e] << int4_shift(e);
+        k_words[tok * LPR + lane] = word;
+        new_k[lane] = word;
+        if (lane == 0) {
+          k_rows[tok] = row;
+          new_row = row;
+        }
+      } else {
+        const int sh = int4_shift(tok & 7);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t* p = v_words + int4_v_word<D>(tok, col + e);
+          *p = (*p & ~(15u << sh)) | (c[e] << sh);
+        }
+        if (lane == 0) v_rows[tok] = row;
+      }
+    }
+  }
+  __syncthreads();
+  const int wi = tid % LPR, grp = tid / LPR;
+  float acc[8] = {};
+  for (int t = grp; t <= tok; t += kGroups) {
+    const uint32_t x = t == tok ? new_k[wi] : k_words[t * LPR + wi];
+    const uint32_t row = t == tok ? new_row : k_rows[t];
+    const float s = int4_scale(row), lo = int4_lo(row);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += fmaf((float)((x >> int4_shift(e)) & 15u), s, lo);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part[grp][wi * 8 + e] = acc[e];
+  __syncthreads();
+  if (tid < D) {
+    float s = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) s += part[g][tid];
+    reps[((int64_t)page * Hkv + h) * D + tid] = s / (float)(tok + 1);
+  }
+}
+
+unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kInt4Warps - 1) / kInt4Warps); }
+
+}  // namespace
+
+cudaError_t launch_quantize_int4(const srkv_config& cfg, const void* k_src, const void* v_src,
+                                 int64_t num_pages, const int32_t* page_ids, int32_t n_pages,
+                                 void* kv, int64_t num_slab_pages, const int32_t* slab_ids,
+                                 int32_t* error_flags, cudaStream_t stream) {
+  const int32_t Hkv = cfg.num_kv_heads;
+  const int64_t warps = (int64_t)n_pages * Hkv * (kBlock / 8);
+  if (warps / kInt4Warps >= INT32_MAX) return cudaErrorInvalidValue;
+  const auto* k = static_cast<const __nv_bfloat16*>(k_src);
+  const auto* v = static_cast<const __nv_bfloat16*>(v_src);
+  auto* out = static_cast<unsigned char*>(kv);
+  if (cfg.head_dim == 128)
+    quantize_int4_kernel<128><<<blocks_of(warps), kInt4Warps * 32, 0, stream>>>(
+        k, v, num_pages, page_ids, n_pages, Hkv, out, num_slab_pages, slab_ids, error_flags);
+  else
+    quantize_int4_kernel<64><<<blocks_of(warps), kInt4Warps * 32, 0, stream>>>(
+        k, v, num_pages, page_ids, n_pages, Hkv, out, num_slab_pages, slab_ids, error_flags);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_int4(const srkv_config& cfg, const void* kv, int64_t num_slab_pages,
+                                   const int32_t* slab_ids, int32_t n_pages, void* k_dst,
+                                   void* v_dst, int64_t num_pages, const int32_t* page_ids,
+                                   int32_t* error_flags, cudaStream_t stream) {
+  const int32_t Hkv = cfg.num_kv_heads;
+  const int64_t warps = (int64_t)n_pages * Hkv * (kBlock / (8 * 256 / cfg.head_dim));
+  if (warps / kInt4Warps >= INT32_MAX) return cudaErrorInvalidValue;
+  const auto* in = static_cast<const unsigned char*>(kv);
+  auto* k = static_cast<__nv_bfloat16*>(k_dst);
+  auto* v = static_cast<__nv_bfloat16*>(v_dst);
+  if (cfg.head_dim == 128)
+    dequantize_int4_kernel<128><<<blocks_of(warps), kInt4Warps * 32, 0, stream>>>(
+        in, num_slab_pages, slab_ids, n_pages, Hkv, k, v, num_pages, page_ids, error_flags);
+  else
+    dequantize_int4_kernel<64><<<blocks_of(warps), kInt4Warps * 32, 0, stream>>>(
+        in, num_slab_pages, slab_ids, n_pages, Hkv, k, v, num_pages, page_ids, error_flags);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append_kv_int4(const srkv_config& cfg, const void* k_new, const void* v_new,
+                                  void* kv, int64_t num_pages, const int32_t* block_table,
+                                  int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                  float* reps, int32_t* error_flags, cudaStream_t stream) {
+  const int32_t Hkv = cfg.num_kv_heads;
+  const dim3 grid((unsigned)((int64_t)batch * Hkv)), block(kAppendThreads);
+  const auto* k = static_cast<const __nv_bfloat16*>(k_new);
+  const auto* v = static_cast<const __nv_bfloat16*>(v_new);
+  auto* out = static_cast<unsigned char*>(kv);
+  return cfg.head_dim == 128
+             ? launch_pdl(append_kv_int4_kernel<128>, grid, block, 0, stream, k, v, out, num_pages,
+                          block_table, max_blocks, seq_lens, Hkv, reps, error_flags)
+             : launch_pdl(append_kv_int4_kernel<64>, grid, block, 0, stream, k, v, out, num_pages,
+                          block_table, max_blocks, seq_lens, Hkv, reps, error_flags);
+}
+
+}  // namespace srkv

@@ -7,6 +7,7 @@
 
 #include <mutex>
 
+#include "int4_page.cuh"
 #include "srkv_internal.cuh"
 
 namespace srkv {
@@ -140,6 +141,7 @@ srkv_status prepare_decode(const srkv_config* cfg, const void* q, const void* k_
   a.num_host_pages = 0;
   a.k_scale = nullptr;
   a.v_scale = nullptr;
+  a.int4 = 0;
   a.dense_boundary = cfg->dense_boundary;
   a.topk_percent = cfg->topk_percent;
   return SRKV_OK;
@@ -209,6 +211,7 @@ void prefix_plan(const srkv_config& cfg, DecodeArgs& a, int32_t prefix_blocks) {
 
 // srkv_retrieval_decode over a device pool [0, num_pages) and a host pool
 // [num_pages, num_pages + num_host_pages) of page ids (num_host_pages = 0: no host pool).
+// int4: k_cache (and v_cache) is the slabs of a 4-bit cache.
 srkv_status retrieval_decode(const srkv_config* cfg, const void* q, const void* k_cache,
                              const void* v_cache, int64_t num_pages, const void* k_host,
                              const void* v_host, int64_t num_host_pages, const float* k_scale,
@@ -217,7 +220,7 @@ srkv_status retrieval_decode(const srkv_config* cfg, const void* q, const void* 
                              const int32_t* seq_lens, const int32_t* prompt_lens, int32_t batch,
                              int32_t* sel, int32_t kmax, int32_t* nsel, void* out,
                              void* workspace, size_t workspace_bytes, int32_t* error_flags,
-                             cudaStream_t s, int32_t prefix_blocks = 0) {
+                             cudaStream_t s, int32_t prefix_blocks = 0, bool int4 = false) {
   srkv_status st = check_score(cfg, q, reps, num_pages + num_host_pages, block_table, max_blocks,
                                seq_lens, batch, sel, kmax, nsel);
   if (st != SRKV_OK || batch == 0) return st;
@@ -248,6 +251,7 @@ srkv_status retrieval_decode(const srkv_config* cfg, const void* q, const void* 
   a.num_host_pages = num_host_pages;
   a.k_scale = k_scale;  // compressed pages when set
   a.v_scale = v_scale;
+  a.int4 = int4 ? 1 : 0;
   // The scoring kernel, then the decode, which streams list A while the scoring finishes
   // and knows the selection counts it will write from the lengths.  A scoring CTA keeps its
   // SM to itself, so list A goes to the decode CTAs that find an SM free at once (the grid
@@ -257,9 +261,12 @@ srkv_status retrieval_decode(const srkv_config* cfg, const void* q, const void* 
   a.sel_out = sel;
   a.nsel_out = nsel;
   const bool compressed = k_scale != nullptr;
+  const PageFormat fmt = int4         ? PageFormat::kInt4
+                         : compressed ? PageFormat::kE4m3
+                                      : PageFormat::kBf16;
   // A batch small enough for one cluster per unit to be resident: one kernel does it all.
   const int32_t cluster =
-      fused_cluster_size(*cfg, batch * cfg->num_kv_heads, max_blocks, compressed);
+      fused_cluster_size(*cfg, batch * cfg->num_kv_heads, max_blocks, fmt);
   if (cluster > 0) return cuda_status(launch_fused(a, cluster, s));
   const bool early = mma_split_supported(*cfg);
   const int64_t scoring = score_topk_ctas(*cfg, max_blocks, batch, compressed);
@@ -347,6 +354,71 @@ srkv_status srkv_quantize_kv_fp8(const srkv_config* cfg, const void* k_cache,
   return cuda_status(launch_quantize_fp8(*cfg, k_cache, v_cache, num_pages, page_ids, n_pages,
                                          k_fp8, v_fp8, k_scale, v_scale, error_flags,
                                          (cudaStream_t)stream));
+}
+
+size_t srkv_kv_int4_slab_bytes(const srkv_config* cfg) {
+  return config_ok(cfg) ? (size_t)int4_slab_bytes(cfg->head_dim) : 0;
+}
+
+// Checks shared by the calls that move listed pages between a bf16 and a 4-bit cache.
+static srkv_status check_int4_pages(const srkv_config* cfg, const void* k, const void* v,
+                                    int64_t num_pages, const void* kv, int64_t num_int4_pages,
+                                    const int32_t* ids, int32_t n_pages) {
+  if (!config_ok(cfg) || n_pages < 0 || num_pages < 0 || num_int4_pages < 0)
+    return SRKV_ERR_INVALID_ARG;
+  if (cfg->dtype != SRKV_BF16) return SRKV_ERR_UNSUPPORTED;
+  if (n_pages == 0) return SRKV_OK;
+  if (!k || !v || !kv || !ids || num_pages == 0 || num_int4_pages == 0)
+    return SRKV_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv, 16)) return SRKV_ERR_INVALID_ARG;
+  // a warp an octet of tokens, eight warps a block: the grid's limit
+  if ((int64_t)n_pages * cfg->num_kv_heads > INT32_MAX / 2) return SRKV_ERR_UNSUPPORTED;
+  return SRKV_OK;
+}
+
+srkv_status srkv_quantize_kv_int4(const srkv_config* cfg, const void* k_cache,
+                                  const void* v_cache, int64_t num_pages,
+                                  const int32_t* page_ids, int32_t n_pages, void* kv_int4,
+                                  int64_t num_int4_pages, const int32_t* int4_page_ids,
+                                  int32_t* error_flags, srkv_stream stream) {
+  const srkv_status st = check_int4_pages(cfg, k_cache, v_cache, num_pages, kv_int4,
+                                          num_int4_pages, page_ids, n_pages);
+  if (st != SRKV_OK || n_pages == 0) return st;
+  return cuda_status(launch_quantize_int4(*cfg, k_cache, v_cache, num_pages, page_ids, n_pages,
+                                          kv_int4, num_int4_pages, int4_page_ids, error_flags,
+                                          (cudaStream_t)stream));
+}
+
+srkv_status srkv_dequantize_kv_int4(const srkv_config* cfg, const void* kv_int4,
+                                    int64_t num_int4_pages, const int32_t* int4_page_ids,
+                                    int32_t n_pages, void* k_cache, void* v_cache,
+                                    int64_t num_pages, const int32_t* page_ids,
+                                    int32_t* error_flags, srkv_stream stream) {
+  const srkv_status st = check_int4_pages(cfg, k_cache, v_cache, num_pages, kv_int4,
+                                          num_int4_pages, int4_page_ids, n_pages);
+  if (st != SRKV_OK || n_pages == 0) return st;
+  return cuda_status(launch_dequantize_int4(*cfg, kv_int4, num_int4_pages, int4_page_ids, n_pages,
+                                            k_cache, v_cache, num_pages, page_ids, error_flags,
+                                            (cudaStream_t)stream));
+}
+
+srkv_status srkv_append_kv_int4(const srkv_config* cfg, const void* k_new, const void* v_new,
+                                void* kv_int4, int64_t num_pages, const int32_t* block_table,
+                                int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                float* reps, int32_t* error_flags, srkv_stream stream) {
+  if (!config_ok(cfg) || batch < 0 || max_blocks <= 0 || max_blocks > kMaxBlocks ||
+      num_pages < 0)
+    return SRKV_ERR_INVALID_ARG;
+  if (cfg->dtype != SRKV_BF16) return SRKV_ERR_UNSUPPORTED;
+  if (batch == 0) return SRKV_OK;
+  if (!k_new || !v_new || !kv_int4 || !block_table || !seq_lens || !reps || num_pages == 0)
+    return SRKV_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(kv_int4, 16) || !aligned(reps, 16))
+    return SRKV_ERR_INVALID_ARG;
+  if ((int64_t)batch * cfg->num_kv_heads > INT32_MAX) return SRKV_ERR_UNSUPPORTED;
+  return cuda_status(launch_append_kv_int4(*cfg, k_new, v_new, kv_int4, num_pages, block_table,
+                                           max_blocks, seq_lens, batch, reps, error_flags,
+                                           (cudaStream_t)stream));
 }
 
 srkv_status srkv_append_kv(const srkv_config* cfg, const void* k_new, const void* v_new,
@@ -597,6 +669,21 @@ srkv_status srkv_retrieval_decode_fp8(const srkv_config* cfg, const void* q, con
                           reps, block_table, max_blocks, seq_lens, prompt_lens, batch, sel, kmax,
                           nsel, out, workspace, workspace_bytes, error_flags,
                           (cudaStream_t)stream);
+}
+
+srkv_status srkv_retrieval_decode_int4(const srkv_config* cfg, const void* q, const void* kv_int4,
+                                       const float* reps, int64_t num_pages,
+                                       const int32_t* block_table, int32_t max_blocks,
+                                       const int32_t* seq_lens, const int32_t* prompt_lens,
+                                       int32_t batch, int32_t* sel, int32_t kmax, int32_t* nsel,
+                                       void* out, void* workspace, size_t workspace_bytes,
+                                       int32_t* error_flags, srkv_stream stream) {
+  if (!config_ok(cfg)) return SRKV_ERR_INVALID_ARG;
+  if (!mma_split_supported(*cfg)) return SRKV_ERR_UNSUPPORTED;
+  return retrieval_decode(cfg, q, kv_int4, kv_int4, num_pages, nullptr, nullptr, 0, nullptr,
+                          nullptr, reps, block_table, max_blocks, seq_lens, prompt_lens, batch,
+                          sel, kmax, nsel, out, workspace, workspace_bytes, error_flags,
+                          (cudaStream_t)stream, 0, true);
 }
 
 srkv_status srkv_selftest_wait_timeout(int32_t* error_flags, srkv_stream stream) {

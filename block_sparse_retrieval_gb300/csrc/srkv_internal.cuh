@@ -436,7 +436,20 @@ struct DecodeArgs {
   // Compressed pages (the E4M3 decode): fp32 scale of every (page, kv head, token) row.
   const float* k_scale;
   const float* v_scale;
+  int32_t int4;  // 1: k_cache holds the slabs of the 4-bit format (int4_page.cuh)
 };
+
+// Did a row with this softmax sum attend anything?  Over 4-bit pages a NaN sum (an attended row
+// that was not finite when it was quantised) counts, so that it reaches the output.
+template <bool kInt4>
+__device__ __forceinline__ bool attended_any(float l) {
+  return kInt4 ? !(l == 0.f) : l > 0.f;
+}
+__device__ __forceinline__ bool attended_any(const DecodeArgs& a, float l) {
+  return a.int4 ? attended_any<true>(l) : attended_any<false>(l);
+}
+
+enum class PageFormat { kBf16, kE4m3, kInt4 };
 
 // Page ids a block table may hold: the device pool, then the host pool.
 __host__ __device__ __forceinline__ int64_t total_pages(const DecodeArgs& a) {
@@ -514,6 +527,19 @@ cudaError_t launch_quantize_fp8(const srkv_config& cfg, const void* k_src, const
                                 int64_t num_pages, const int32_t* page_ids, int32_t n_pages,
                                 void* k8, void* v8, float* k_scale, float* v_scale,
                                 int32_t* error_flags, cudaStream_t stream);
+// 4-bit pages: slabs [num_slab_pages][Hkv][128 d + 1024 bytes]; null second ids: the first ones.
+cudaError_t launch_quantize_int4(const srkv_config& cfg, const void* k_src, const void* v_src,
+                                 int64_t num_pages, const int32_t* page_ids, int32_t n_pages,
+                                 void* kv, int64_t num_slab_pages, const int32_t* slab_ids,
+                                 int32_t* error_flags, cudaStream_t stream);
+cudaError_t launch_dequantize_int4(const srkv_config& cfg, const void* kv, int64_t num_slab_pages,
+                                   const int32_t* slab_ids, int32_t n_pages, void* k_dst,
+                                   void* v_dst, int64_t num_pages, const int32_t* page_ids,
+                                   int32_t* error_flags, cudaStream_t stream);
+cudaError_t launch_append_kv_int4(const srkv_config& cfg, const void* k_new, const void* v_new,
+                                  void* kv, int64_t num_pages, const int32_t* block_table,
+                                  int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                  float* reps, int32_t* error_flags, cudaStream_t stream);
 cudaError_t launch_append_kv(const srkv_config& cfg, const void* k_new, const void* v_new,
                              void* k_cache, void* v_cache, int64_t num_pages,
                              const int32_t* block_table, int32_t max_blocks,
@@ -549,7 +575,7 @@ cudaError_t launch_cascade(const DecodeArgs& a, bool pdl, cudaStream_t stream);
 // per (request, kv head) unit: the cluster size to use for `units` units (0 = not
 // applicable: dtype, head size, group, candidates per unit or residency), and its launch.
 int32_t fused_cluster_size(const srkv_config& cfg, int32_t units, int32_t max_blocks,
-                           bool e4m3 = false);
+                           PageFormat fmt = PageFormat::kBf16);
 cudaError_t launch_fused(const DecodeArgs& a, int32_t cluster, cudaStream_t stream);
 
 }  // namespace srkv

@@ -33,7 +33,8 @@ EXPORTS = ("srkv_default_config", "srkv_status_string", "srkv_topk_count",
            "srkv_retrieval_decode_fp8", "srkv_selftest_wait_timeout",
            "srkv_prefix_decode_workspace_size", "srkv_sparse_paged_decode_prefix",
            "srkv_retrieval_decode_prefix", "srkv_host_staging_size",
-           "srkv_retrieval_decode_host")
+           "srkv_retrieval_decode_host", "srkv_kv_int4_slab_bytes", "srkv_quantize_kv_int4",
+           "srkv_dequantize_kv_int4", "srkv_append_kv_int4", "srkv_retrieval_decode_int4")
 NOALLOC_WORKSPACE_BYTES = 16 << 20
 
 
@@ -112,13 +113,25 @@ def load() -> ctypes.CDLL:
     lib.srkv_retrieval_decode_host.argtypes = [ctypes.POINTER(Config), _P, _P, _P, _P, _P, _SZ,
                                                _P, _P, _P, _I64, _P, _I32, _I32, _P, _I32, _P,
                                                _P, _P, _SZ, _P, _P]
+    lib.srkv_kv_int4_slab_bytes.argtypes = [ctypes.POINTER(Config)]
+    lib.srkv_kv_int4_slab_bytes.restype = _SZ
+    lib.srkv_quantize_kv_int4.argtypes = [ctypes.POINTER(Config), _P, _P, _I64, _P, _I32, _P,
+                                          _I64, _P, _P, _P]
+    lib.srkv_dequantize_kv_int4.argtypes = [ctypes.POINTER(Config), _P, _I64, _P, _I32, _P, _P,
+                                            _I64, _P, _P, _P]
+    lib.srkv_append_kv_int4.argtypes = [ctypes.POINTER(Config), _P, _P, _P, _I64, _P, _I32, _P,
+                                        _I32, _P, _P, _P]
+    lib.srkv_retrieval_decode_int4.argtypes = [ctypes.POINTER(Config), _P, _P, _P, _I64, _P, _I32,
+                                               _P, _P, _I32, _P, _I32, _P, _P, _P, _SZ, _P, _P]
     lib.srkv_selftest_wait_timeout.argtypes = [_P, _P]
     lib.srkv_selftest_wait_timeout.restype = ctypes.c_int
     for name in ("srkv_build_block_reps", "srkv_score_topk", "srkv_sparse_paged_decode",
                  "srkv_retrieval_decode", "srkv_sparse_paged_decode_noalloc",
                  "srkv_retrieval_decode_tiered", "srkv_quantize_kv_fp8",
                  "srkv_retrieval_decode_fp8", "srkv_sparse_paged_decode_prefix",
-                 "srkv_retrieval_decode_prefix", "srkv_retrieval_decode_host"):
+                 "srkv_retrieval_decode_prefix", "srkv_retrieval_decode_host",
+                 "srkv_append_kv", "srkv_quantize_kv_int4", "srkv_dequantize_kv_int4",
+                 "srkv_append_kv_int4", "srkv_retrieval_decode_int4"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -598,6 +611,117 @@ def retrieval_decode_fp8(cfg: Mapping, q: torch.Tensor, k_fp8: torch.Tensor,
         workspace.numel() * workspace.element_size(),
         _dev(error_flags, "error_flags", torch.int32), _stream(stream)),
         "srkv_retrieval_decode_fp8")
+
+
+def kv_int4_slab_bytes(cfg: Mapping) -> int:
+    """Bytes of one (page, kv head) slab of a 4-bit cache."""
+    c = config(cfg)
+    return int(load().srkv_kv_int4_slab_bytes(ctypes.byref(c)))
+
+
+def _int4_cache(cfg: Mapping, t: torch.Tensor) -> int:
+    """Checks the shape of a 4-bit cache; returns its pages."""
+    _shape(t, "kv_int4", None, cfg["num_kv_heads"], kv_int4_slab_bytes(cfg))
+    return t.shape[0]
+
+
+def quantize_kv_int4(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     page_ids: torch.Tensor, kv_int4: torch.Tensor,
+                     int4_page_ids: torch.Tensor | None = None,
+                     error_flags: torch.Tensor | None = None, stream=None) -> None:
+    """srkv_quantize_kv_int4: page page_ids[i] of the bf16 caches into page int4_page_ids[i] (None:
+    page_ids[i]) of kv_int4, uint8 [pages][Hkv][kv_int4_slab_bytes(cfg)]."""
+    _, Hkv, S, d = _cache_dims(cfg)
+    _shape(k_cache, "k_cache", None, Hkv, S, d)
+    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
+    pages = _int4_cache(cfg, kv_int4)
+    _shape(page_ids, "page_ids", None)
+    _shape(int4_page_ids, "int4_page_ids", page_ids.numel())
+    c = config(cfg)
+    _check(load().srkv_quantize_kv_int4(
+        ctypes.byref(c), _dev(k_cache, "k_cache", torch.bfloat16),
+        _dev(v_cache, "v_cache", torch.bfloat16), k_cache.shape[0],
+        _dev(page_ids, "page_ids", torch.int32), page_ids.numel(),
+        _dev(kv_int4, "kv_int4", torch.uint8), pages,
+        _dev(int4_page_ids, "int4_page_ids", torch.int32),
+        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), "srkv_quantize_kv_int4")
+
+
+def dequantize_kv_int4(cfg: Mapping, kv_int4: torch.Tensor, int4_page_ids: torch.Tensor,
+                       k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       page_ids: torch.Tensor | None = None,
+                       error_flags: torch.Tensor | None = None, stream=None) -> None:
+    """srkv_dequantize_kv_int4: page int4_page_ids[i] of kv_int4 into page page_ids[i] (None:
+    int4_page_ids[i]) of the bf16 caches."""
+    _, Hkv, S, d = _cache_dims(cfg)
+    _shape(k_cache, "k_cache", None, Hkv, S, d)
+    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
+    pages = _int4_cache(cfg, kv_int4)
+    _shape(int4_page_ids, "int4_page_ids", None)
+    _shape(page_ids, "page_ids", int4_page_ids.numel())
+    c = config(cfg)
+    _check(load().srkv_dequantize_kv_int4(
+        ctypes.byref(c), _dev(kv_int4, "kv_int4", torch.uint8), pages,
+        _dev(int4_page_ids, "int4_page_ids", torch.int32), int4_page_ids.numel(),
+        _dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16),
+        k_cache.shape[0], _dev(page_ids, "page_ids", torch.int32),
+        _dev(error_flags, "error_flags", torch.int32), _stream(stream)),
+        "srkv_dequantize_kv_int4")
+
+
+def append_kv_int4(cfg: Mapping, k_new: torch.Tensor, v_new: torch.Tensor, kv_int4: torch.Tensor,
+                   block_table: torch.Tensor, seq_lens: torch.Tensor, reps: torch.Tensor,
+                   error_flags: torch.Tensor | None = None, stream=None) -> None:
+    """srkv_append_kv_int4: each request's new token (bf16 k_new, v_new: [B][Hkv][d]) quantised
+    into position seq_lens[r] of a 4-bit cache, and that page's vector refreshed; the caller then
+    advances seq_lens."""
+    _, Hkv, _, d = _cache_dims(cfg)
+    _shape(block_table, "block_table", None, None)
+    B = block_table.shape[0]
+    _shape(k_new, "k_new", B, Hkv, d)
+    _shape(v_new, "v_new", B, Hkv, d)
+    pages = _int4_cache(cfg, kv_int4)
+    _shape(seq_lens, "seq_lens", B)
+    _shape(reps, "reps", None, Hkv, d)
+    _rows(reps, "reps", pages)
+    c = config(cfg)
+    _check(load().srkv_append_kv_int4(
+        ctypes.byref(c), _dev(k_new, "k_new", torch.bfloat16),
+        _dev(v_new, "v_new", torch.bfloat16), _dev(kv_int4, "kv_int4", torch.uint8), pages,
+        _dev(block_table, "block_table", torch.int32), block_table.shape[1],
+        _dev(seq_lens, "seq_lens", torch.int32), B, _dev(reps, "reps", torch.float32),
+        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), "srkv_append_kv_int4")
+
+
+def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
+                          reps: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                          prompt_lens: torch.Tensor | None, sel: torch.Tensor,
+                          nsel: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                          error_flags: torch.Tensor | None = None, stream=None) -> None:
+    """srkv_retrieval_decode_int4: the decode step over a 4-bit cache (bf16 query and output)."""
+    Hq, Hkv, _, d = _cache_dims(cfg)
+    _shape(block_table, "block_table", None, None)
+    B, max_blocks = block_table.shape
+    _shape(q, "q", B, Hq, d)
+    pages = _int4_cache(cfg, kv_int4)
+    _shape(seq_lens, "seq_lens", B)
+    _shape(prompt_lens, "prompt_lens", B)
+    _shape(sel, "sel", B, Hkv, None)
+    _shape(nsel, "nsel", B, Hkv)
+    _shape(out, "out", B, Hq, d)
+    _shape(reps, "reps", None, Hkv, d)
+    _rows(reps, "reps", pages)
+    c = config(cfg)
+    _check(load().srkv_retrieval_decode_int4(
+        ctypes.byref(c), _dev(q, "q", torch.bfloat16), _dev(kv_int4, "kv_int4", torch.uint8),
+        _dev(reps, "reps", torch.float32), pages,
+        _dev(block_table, "block_table", torch.int32), max_blocks,
+        _dev(seq_lens, "seq_lens", torch.int32), _dev(prompt_lens, "prompt_lens", torch.int32),
+        B, _dev(sel, "sel", torch.int32), sel.shape[-1], _dev(nsel, "nsel", torch.int32),
+        _dev(out, "out", torch.bfloat16), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(),
+        _dev(error_flags, "error_flags", torch.int32), _stream(stream)),
+        "srkv_retrieval_decode_int4")
 
 
 def selftest_wait_timeout(error_flags: torch.Tensor, stream=None) -> None:

@@ -175,6 +175,67 @@ srkv_status srkv_quantize_kv_fp8(const srkv_config* cfg, const void* k_cache,
                                  int32_t* error_flags, srkv_stream stream);
 
 /*
+ * 4-bit pages (the same survey's quantisation of the cache, at half the bits of E4M3).  A 4-bit cache is
+ * one buffer kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)] bytes, 16-byte aligned; the
+ * slab of a (page, kv head) holds its 128 keys and values.  A row x (one token's d values) is held as
+ *   lo = min x (bf16),  scale = (max x - lo) / 15 rounded up to bf16,
+ *   code = the integer in 0 .. 15 nearest to (x - lo) / scale, ties to even (0 if scale is 0; the
+ *          difference in fp32),
+ * and stands for lo + code * scale.  A row with an infinity or a NaN, or whose range passes fp32, gets
+ * scale = lo = NaN and reads back as NaN.  The 128 d + 1024 bytes of a slab, in order (words are 32 bits;
+ * code j of a word at bit 4 (j / 2) + 16 (j mod 2)):
+ *   keys' codes   [128][d / 8] words: elements 8i .. 8i + 7 of token t in word (t, i);
+ *   values' codes [4][d / 4][4][4] words: element 4c + e of tokens 32w + 8t .. 32w + 8t + 7 in word
+ *                 (w, c, t, e);
+ *   keys' rows, then values' rows, [128] words each: scale (low half) and lo (high half).
+ */
+
+/* Bytes of one (page, kv head) slab: 128 d + 1024; 0 if cfg is invalid. */
+size_t srkv_kv_int4_slab_bytes(const srkv_config* cfg);
+
+/*
+ * Compresses listed pages: page page_ids[i] of the bf16 caches, all 128 rows of it, into page
+ * int4_page_ids[i] of kv_int4 (NULL: page_ids[i]); other pages are untouched.  The two caches may
+ * have different numbers of pages, so that a small bf16 pool can feed a large 4-bit one.
+ *   cfg->dtype must be SRKV_BF16 (else SRKV_ERR_UNSUPPORTED); k_cache, v_cache: [num_pages][Hkv][S][d]
+ *   bf16, 16-byte aligned; num_int4_pages: pages of kv_int4; the ids: device int32 [n_pages].
+ *   An id outside its cache skips that entry and flags SRKV_EFLAG_PAGE_RANGE.  A destination listed
+ *   twice with different sources ends up with a mix of them.  Asynchronous; one kernel.
+ */
+srkv_status srkv_quantize_kv_int4(const srkv_config* cfg, const void* k_cache,
+                                  const void* v_cache, int64_t num_pages,
+                                  const int32_t* page_ids, int32_t n_pages, void* kv_int4,
+                                  int64_t num_int4_pages, const int32_t* int4_page_ids,
+                                  int32_t* error_flags, srkv_stream stream);
+
+/*
+ * Reads listed pages back: page int4_page_ids[i] of kv_int4 into page page_ids[i] of the bf16
+ * caches (NULL: int4_page_ids[i]), as lo + code * scale rounded once to bf16, all 128 rows.  For what
+ * takes full-precision pages (the shared-prefix calls, a later prefill chunk).  Arguments and errors
+ * as for srkv_quantize_kv_int4.
+ */
+srkv_status srkv_dequantize_kv_int4(const srkv_config* cfg, const void* kv_int4,
+                                    int64_t num_int4_pages, const int32_t* int4_page_ids,
+                                    int32_t n_pages, void* k_cache, void* v_cache,
+                                    int64_t num_pages, const int32_t* page_ids,
+                                    int32_t* error_flags, srkv_stream stream);
+
+/*
+ * srkv_append_kv into a 4-bit cache: for every request r and kv head h the new token's key and value
+ * (bf16) are quantised and written as row L % S of page block_table[r][L / S], L = seq_lens[r], and
+ * the page's representation vector becomes the fp32 mean of its keys as held, lo + code * scale over
+ * rows [0, L % S].  (The vectors of pages compressed by srkv_quantize_kv_int4 are the caller's, from
+ * srkv_build_block_reps on the bf16 keys.)  The page's other rows keep their codes.  A token written
+ * again, or written over after the length was set back, gives the same cache and vector as a
+ * first write.  cfg->dtype must be SRKV_BF16 (else SRKV_ERR_UNSUPPORTED).  Other arguments, the page
+ * of its own that each request needs at block L / S, and errors: srkv_append_kv.
+ */
+srkv_status srkv_append_kv_int4(const srkv_config* cfg, const void* k_new, const void* v_new,
+                                void* kv_int4, int64_t num_pages, const int32_t* block_table,
+                                int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                float* reps, int32_t* error_flags, srkv_stream stream);
+
+/*
  * Scoring and top-k ("Overall Solution": inner product of the current query with each
  * representation vector, keep the topK closest).  For every request r and kv head h:
  * sel[r][h][0..nsel[r][h]) = the selected candidate blocks of (r, h), ascending; dense
@@ -330,6 +391,27 @@ srkv_status srkv_retrieval_decode_fp8(const srkv_config* cfg, const void* q, con
                                       int32_t kmax, int32_t* nsel, void* out, void* workspace,
                                       size_t workspace_bytes, int32_t* error_flags,
                                       srkv_stream stream);
+
+/*
+ * srkv_retrieval_decode over a 4-bit cache (srkv_quantize_kv_int4, srkv_append_kv_int4): the attended K and
+ * V values are lo + code * scale.  Both products take the codes as fp16 operands with fp32
+ * accumulation; the query enters as fp16 times one power of two for the heads of a group (exact down
+ * to 2^-25 of the group's largest magnitude, which must be below 2^101), each softmax weight as fp16
+ * times its row's V scale (below 2^36), the scales and minima in fp32.  The selection comes from `reps`,
+ * as in the other calls.
+ *   cfg->dtype = SRKV_BF16 (the query and the output), group <= 8, else SRKV_ERR_UNSUPPORTED;
+ *   head_dim 64 or 128.  kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)].  A NaN row that is
+ *   attended makes the outputs that attend it NaN; rows that are not attended never do.  Other
+ *   arguments, ownership, paths (one kernel for small batches, else three), reproducibility and
+ *   errors: srkv_retrieval_decode.
+ */
+srkv_status srkv_retrieval_decode_int4(const srkv_config* cfg, const void* q, const void* kv_int4,
+                                       const float* reps, int64_t num_pages,
+                                       const int32_t* block_table, int32_t max_blocks,
+                                       const int32_t* seq_lens, const int32_t* prompt_lens,
+                                       int32_t batch, int32_t* sel, int32_t kmax, int32_t* nsel,
+                                       void* out, void* workspace, size_t workspace_bytes,
+                                       int32_t* error_flags, srkv_stream stream);
 
 /*
  * Shared-prefix decode (KV-cache survey "大模型推理百倍加速之KV cache篇", section "Share--KV
