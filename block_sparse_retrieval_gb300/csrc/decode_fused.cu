@@ -48,8 +48,11 @@ constexpr int kMaxCluster = 16;                            // CTAs per unit, at 
 // every CTA's pages and the merge order are then fixed, so the output is bitwise
 // reproducible; longer pools are balanced through the counter (timing decides who takes
 // which of the rest).
-constexpr int kStatic = 16;
-static_assert(kStatic % 2 == 0, "the release carries kStatic / 2 16-byte stores");
+// 4-bit pages: twice as many, one per lane of the producer warp.  Taking an entry from the counter
+// costs two round trips through the cluster, which a bf16 page (1.5 us of an SM's share of the
+// bandwidth) hides and a 4-bit page (0.4 us) does not.
+template <int Fmt>
+constexpr int kStaticOf = Fmt == kInt4Pages ? 32 : 16;
 // The scoring counts the top 12 bits of the keys besides the top 8: on score sets like the
 // method's (a few hundred candidates, scores spread over a few units) the 12-bit bin holding
 // the k-th largest key then holds a few keys, and the selection finishes in one pass over the
@@ -62,6 +65,8 @@ static_assert(kMaxCand <= 1024, "bin ranks pack a candidate index into 10 bits")
 template <int D, int Fmt = kBf16Pages>
 struct FusedCfg {
   using C = Cfg<D, Fmt>;
+  static constexpr int kStatic = kStaticOf<Fmt>;
+  static_assert(kStatic % 2 == 0, "the release carries kStatic / 2 16-byte stores");
   // after the ring (every CTA)
   // keys_ready, list_ready, parts_ready, scored
   static constexpr size_t kOffBars = (C::kSmem + 15) & ~size_t(15);
@@ -115,6 +120,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
                                                      const __grid_constant__ TmaMaps maps) {
   using C = Cfg<D, Fmt>;
   using F = FusedCfg<D, Fmt>;
+  constexpr int kStatic = F::kStatic;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* keys_ready = reinterpret_cast<uint64_t*>(smem + F::kOffBars);
@@ -149,7 +155,10 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
   bool arrived = false;  // on the closing cluster barrier (warp-uniform)
 
   if (tid == 0) {
-    init_ring<D, Fmt>(smem);
+    if constexpr (Fmt == kInt4Pages)
+      Int4Ring<D>{smem}.init(a.G <= 4);
+    else
+      init_ring<D, Fmt>(smem);
     mbar_init(keys_ready, kMaxCand);            // one per candidate, the rest at once
     mbar_init(list_ready, 1);                   // the leader, once the pool is laid out
     mbar_init(parts_ready, 1);                  // the leader, expecting every partial's bytes
@@ -214,6 +223,17 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
   const int32_t q = (int32_t)crank - 1;  // streaming rank
   const int32_t a0 = leader ? 0 : share_begin(q, nA, S), a1 = leader ? 0 : share_begin(q + 1, nA, S);
 
+  // the merged partial of this CTA's segment, into the leader's shared memory
+  auto write_partial = [&](const SoftmaxState<D>& st, Lane ln) {
+    // asynchronous stores, each counted on the leader's parts_ready
+    const uint32_t acc_r = cluster_addr(part_acc + (int64_t)q * a.G * D, 0);
+    const uint32_t ml_r = cluster_addr(part_ml + (int64_t)q * a.G * 2, 0);
+    const uint32_t bar_r = cluster_addr(parts_ready, 0);
+    emit_partial<D, Fmt>(
+        st, ln, a.G, [&](int i, float4 v) { st_async_f4(acc_r + 4u * i, v, bar_r); },
+        [&](int j, float2 v) { st_async_f2(ml_r + 4u * j, v, bar_r); });
+  };
+
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
     cluster_wait();
@@ -221,6 +241,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
       uint32_t eflags = 0;
       bool abort = false;
       int64_t it = 0, armed = 0;
+      Int4Place place;  // (4-bit pages keep theirs here)
       int32_t k = -1;  // the kept count, computed while the producer waits anyway
       // list A: 32 positions resolved at once, handed out in order.  The first kEarlyStages
       // copies go out at once; the rest of the ring waits for this CTA's scoring loads,
@@ -232,6 +253,22 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         task.page = -1;
         task.lo = task.hi = task.ie = task.ws = 0;
         if (lane < cnt) task = resolve_a(g, j0 + lane, bt_r, total_pages(a), eflags);
+        if constexpr (Fmt == kInt4Pages) {  // the lanes issue their own pages
+          const uint32_t fl = place.it == 0 && lane == 0 ? kNewUnit : 0u;
+          const int early = place.it == 0 ? min(cnt, F::kEarlyStages) : 0;
+          issue_batch_int4<D>(a, smem, place, 0, early, u, fl, task, eflags, lane);
+          if (early == F::kEarlyStages && !place.abort) {
+            k = kept_count();
+            bool ok = true;
+            if (lane == 0) ok = mbar_wait(scored, 0);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) {
+              eflags |= SRKV_EFLAG_TIMEOUT;
+              place.abort = true;
+            }
+          }
+          issue_batch_int4<D>(a, smem, place, early, cnt, u, early > 0 ? 0u : fl, task, eflags, lane);
+          abort = place.abort;
+        } else {
         for (int l = 0; l < cnt && !abort; ++l) {
           PageTask tl;
           tl.page = __shfl_sync(0xffffffffu, task.page, l);
@@ -253,6 +290,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
                               eflags, lane);
           ++it;
         }
+        }
       }
       if (k < 0) k = kept_count();
       // list B: the kStatic entries that came with the release, then kept blocks from the
@@ -271,7 +309,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
       }
       uint32_t first = 0xffffffffu;  // lane 0: the first entry taken from the counter
       if (k > 0 && !abort && lane == 0) first = atom_cluster_add(taken, 0, 1u);
-      auto issue_b = [&](const int2 e) {  // kept block (page, block id)
+      auto kept_task = [&](const int2 e) {  // kept block (page, block id)
         PageTask t;
         t.page = -1;
         t.lo = t.hi = t.ie = t.ws = 0;
@@ -287,11 +325,34 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         } else if (lo < hi) {
           eflags |= SRKV_EFLAG_PAGE_RANGE;
         }
-        issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, t, armed, abort,
-                            eflags, lane);
-        ++it;
+        return t;
       };
-      if (k > 0 && !abort) {
+      auto issue_b = [&](const int2 e) {
+        const PageTask t = kept_task(e);
+        if constexpr (Fmt == kInt4Pages) {
+          issue_batch_int4<D>(a, smem, place, 0, 1, u, place.it == 0 ? kNewUnit : 0u, t, eflags,
+                              lane);
+          abort = place.abort;
+        } else {
+          issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, t, armed, abort,
+                                   eflags, lane);
+          ++it;
+        }
+      };
+      if constexpr (Fmt == kInt4Pages) {
+        if (k > 0 && !abort) {  // lane j has entry j
+          static_assert(kStatic == 32, "an entry per lane");
+          const int2 e = mail[lane];
+          const int cnt = __popc(__ballot_sync(0xffffffffu, e.y >= 0));  // beyond the pool: -1
+          PageTask t;
+          t.page = -1;
+          t.lo = t.hi = t.ie = t.ws = 0;
+          if (lane < cnt) t = kept_task(e);
+          issue_batch_int4<D>(a, smem, place, 0, cnt, u,
+                              place.it == 0 && lane == 0 ? kNewUnit : 0u, t, eflags, lane);
+          abort = place.abort;
+        }
+      } else if (k > 0 && !abort) {
 #pragma unroll 1
         for (int j = 0; j < kStatic && !abort; ++j) {
           const int2 e = mail[j];
@@ -321,7 +382,11 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         e0 = next0;
         have = __shfl_sync(0xffffffffu, more, 0);
       }
-      if (lane == 0) {
+      if constexpr (Fmt == kInt4Pages) {
+        place.abort = abort;
+        place.segs = 1;  // the segment is closed even if this CTA took no page
+        finish_ring_int4<D>(a, smem, place, eflags, lane);
+      } else if (lane == 0) {
         // the sentinel closes the segment (empty if this CTA took no page)
         PageTask none;
         none.page = -1;
@@ -339,6 +404,16 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
       }
       eflags = __reduce_or_sync(0xffffffffu, eflags | geflags);
       if (lane == 0) raise_flags(a.error_flags, eflags);
+    }
+  } else if (warp > kProducerWarp) {
+    // ------------------- 4-bit pages: the merger, and consumers that neither score nor select
+    cluster_wait();
+    if constexpr (Fmt == kInt4Pages) {
+      if (!leader && warp == kMergerWarp)
+        merger_loop_int4<D>(a, smem, lane, [&](const SoftmaxState<D>& st, const Int4Segment&,
+                                               Lane ln) { write_partial(st, ln); });
+      else if (!leader)
+        consumer_loop_int4<D>(a, smem, lane, warp - 2);
     }
   } else {
     // ------------------------------------------------------------------ consumers
@@ -394,17 +469,14 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
       // Streaming CTA qq's release: its pool entries qq, qq + S, ... (up to kStatic; (-1, -1)
       // beyond the pool) into its shared memory, then its list_ready (which orders them).
       auto release = [&](int32_t qq) {
-        int2 e[kStatic];
-#pragma unroll
-        for (int j = 0; j < kStatic; ++j) {
-          const int32_t p = qq + j * S;
-          e[j] = p < k ? pool[p] : make_int2(-1, -1);
-        }
         int4* m4 = reinterpret_cast<int4*>(mail);
-#pragma unroll
-        for (int j = 0; j < kStatic; j += 2)
-          st_cluster_int4(m4 + j / 2, (uint32_t)qq + 1,
-                          make_int4(e[j].x, e[j].y, e[j + 1].x, e[j + 1].y));
+#pragma unroll 8
+        for (int j = 0; j < kStatic; j += 2) {
+          const int32_t p0 = qq + j * S, p1 = p0 + S;
+          const int2 e0 = p0 < k ? pool[p0] : make_int2(-1, -1);
+          const int2 e1 = p1 < k ? pool[p1] : make_int2(-1, -1);
+          st_cluster_int4(m4 + j / 2, (uint32_t)qq + 1, make_int4(e0.x, e0.y, e1.x, e1.y));
+        }
         mbar_arrive_cluster(list_ready, (uint32_t)qq + 1);
       };
       if (partial) {
@@ -616,19 +688,13 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
     } else {
       // 3'. attend list A, then the kept blocks taken from the pool, as one segment; the
       // merged partial goes to the leader's shared memory
-      auto write_partial = [&](const SoftmaxState<D>& st, const StageInfo&, Lane ln) {
-        // asynchronous stores, each counted on the leader's parts_ready
-        const uint32_t acc_r = cluster_addr(part_acc + (int64_t)q * a.G * D, 0);
-        const uint32_t ml_r = cluster_addr(part_ml + (int64_t)q * a.G * 2, 0);
-        const uint32_t bar_r = cluster_addr(parts_ready, 0);
-        emit_partial<D, Fmt>(
-            st, ln, a.G, [&](int i, float4 v) { st_async_f4(acc_r + 4u * i, v, bar_r); },
-            [&](int j, float2 v) { st_async_f2(ml_r + 4u * j, v, bar_r); });
-      };
       if constexpr (Fmt == kInt4Pages)
-        consumer_loop_int4<D>(a, smem, lane, warp, write_partial);
+        consumer_loop_int4<D>(a, smem, lane, warp);
       else
-        consumer_loop<D, Fmt>(a, smem, lane, warp, write_partial);
+        consumer_loop<D, Fmt>(a, smem, lane, warp,
+                              [&](const SoftmaxState<D>& st, const StageInfo&, Lane ln) {
+                                write_partial(st, ln);
+                              });
     }
   }
   // nobody leaves while another CTA may still reach its shared memory
@@ -645,7 +711,7 @@ int32_t max_active_clusters(int32_t cs) {
   using F = FusedCfg<D, Fmt>;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)cs);
-  lc.blockDim = dim3((kConsumerWarps + 1) * 32);
+  lc.blockDim = dim3(Cfg<D, Fmt>::kThreads);
   lc.dynamicSmemBytes = F::kSmemAlloc;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -715,7 +781,7 @@ cudaError_t launch_fused_t(const DecodeArgs& a, int32_t cluster, cudaStream_t st
   const int64_t grid = (int64_t)a.batch * a.Hkv * cluster;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)grid);
-  lc.blockDim = dim3((kConsumerWarps + 1) * 32);
+  lc.blockDim = dim3(Cfg<D, Fmt>::kThreads);
   lc.dynamicSmemBytes = FusedCfg<D, Fmt>::kSmemAlloc;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -12,8 +12,13 @@
 // exact there), and one shift per word reaches the other four.  The powers of two are taken out of
 // the query (16 times smaller at the second kind's elements) and of the weights likewise.
 //
-// A page is 4 groups of 32 tokens, a warp takes kTok of them and a page kGroupWarps warps; the
-// CTA's 8 warps work on kGroups consecutive stages at once.  Lane (g, t) of a warp (g = lane / 4):
+// A page is 4 groups of 32 tokens, one for each warp of a group of 4; the CTA's groups work on
+// consecutive stages (3 of them, 2 for more than 4 heads), so that 3 warps share a scheduler and
+// hide one another's latencies.  A group visits its own stages only.  Stages name their segment (a
+// unit's positions in a list) by its number; a warp that meets a new number leaves its state
+// of the old segment in shared memory and goes on at once, and a merger warp joins the states and
+// writes the partial.  (Draining the groups and merging in them cost 5 us a segment.)
+// Lane (g, t) of a warp (g = lane / 4):
 //   S^T = K . Q^T, two 16-token tiles j per 32 tokens: tile row m holds token 8 (m / 2) + 4 j + (m & 1)
 //     for m < 8 and that + 2 for row m + 8, so that rows 2t, 2t + 1, 2t + 8, 2t + 9 are the four
 //     tokens whose nibbles sit in bits 8j .. 8j + 7 of both halves of octet t's value words: the
@@ -22,57 +27,254 @@
 //     to a 16-row tile.
 // Both layouts make every 8-lane phase of the 16-byte shared loads contiguous (128 bytes).
 //
+// Groups of at most 4 heads leave half of the 8 columns of S^T free.  Columns 4..7 then repeat
+// the heads 0..3, so that lanes t and t + 2 hold the same heads and each takes one of the two rows
+// (g, g + 8) through the softmax: half the work per lane.  One movmatrix turns both rows' weights at
+// once (columns 4..7 come out as the rows g + 8 of heads 0..3), a shuffle brings the second half over.
+//
 // Online softmax with a lazy reference: the weights are 2^(s - m) for a reference m that is raised
-// only when some s + log2 vs exceeds it by 2^8, which a vote finds; then the accumulators are
-// rescaled.  log2 vs is in it so that the weight times scale that enters the second product as fp16
-// stays within its range whatever the values' magnitude (up to 2^8 * 64).
+// only when some s exceeds it by 2^8, which a vote finds.  Likewise the fp16 operand of the second
+// product, weight * vs / vlim * 128, has a power of two vlim that is raised when some vs exceeds it.
+// Then the accumulators are rescaled.  The operand stays below 2^15 whatever the values' magnitude.
 #pragma once
 
 #include "decode_mma.cuh"
+#include "int4_page.cuh"
 
 namespace srkv {
 
-constexpr float kInt4Headroom = 8.f;       // log2 of the most a weight may exceed its reference
-constexpr float kInt4PScale = 64.f;        // on the fp16 weights: 2^(8 + 6) < 65504
-constexpr float kInt4VScaleLog2Max = 30.f;  // log2 vs is taken within +-30 in the reference
+constexpr float kInt4Headroom = 8.f;   // log2 of the most a weight may exceed its reference
+constexpr float kInt4PScale = 128.f;   // on the fp16 operand: 2^(8 + 7) < 65504
+constexpr int kMergerWarp = kProducerWarp + 1;  // warps past it are consumers 8, 9, ...
 
-template <int D, typename WritePartial>
-__device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned char* smem,
-                                                   int lane, int warp,
-                                                   WritePartial&& write_partial) {
+struct Int4Stage {
+  int32_t seg;  // number of the segment; kInt4End in `last`: no page, every segment below is over
+  int32_t last;
+  int32_t lo, hi, ie, ws;
+  int32_t pad[2];
+};
+struct Int4Segment {
+  int32_t unit, flags;  // kBankB
+};
+
+// A stage is one slab (17 408 bytes at d 128), moved by one bulk copy.
+template <int D>
+struct Cfg<D, kInt4Pages> {
+  static constexpr int kSlab = Int4Slab<D>::kBytes;
+  static constexpr int kGroupWarps = 4;                 // warps that share a stage
+  static constexpr int kNarrowWarps = 12, kWideWarps = 8;  // consumer warps (G <= 4, G > 4)
+  static constexpr int kThreads = (kNarrowWarps + 2) * 32;  // + the producer and the merger
+  static constexpr int kStages = D == 128 ? 9 : 16;
+  // A warp may be one stage of its group plus the ring behind the producer.
+  static constexpr int kSegs = kStages + kNarrowWarps / kGroupWarps;
+  static constexpr int kQBytes = 8 * D * 2;
+  static constexpr int MT = D / 16;
+  // A warp's state in shared memory: (acc, m, l) of the lanes that hold heads.
+  static constexpr int kStateStride = MT * 4 + 4;
+  static constexpr int kNarrowState = 16 * kStateStride, kWideState = 32 * kStateStride;
+  static constexpr int kStates = kNarrowWarps * kNarrowState > kWideWarps * kWideState
+                                     ? kNarrowWarps * kNarrowState
+                                     : kWideWarps * kWideState;
+
+  static constexpr size_t kOffK = 0;
+  static constexpr size_t kOffQ = (size_t)kStages * kSlab;
+  // the one-kernel decode's leader streams no pages and keeps its partials from here on
+  static constexpr size_t kOffV = (size_t)(kStages / 2) * kSlab;
+  static constexpr size_t kOffState = kOffQ + (size_t)kSegs * kQBytes;
+  static constexpr size_t kOffInfo = kOffState + sizeof(float) * kStates;
+  static constexpr size_t kOffSeg = kOffInfo + sizeof(Int4Stage) * kStages;
+  static constexpr size_t kOffBar = kOffSeg + ((sizeof(Int4Segment) * kSegs + 15) & ~size_t(15));
+  // full[kStages], empty[kStages], query[kSegs], left (a segment's states), merged; then `done`
+  static constexpr int kBars = 2 * kStages + kSegs + 2;
+  static constexpr size_t kOffDone = kOffBar + sizeof(uint64_t) * kBars;
+  static constexpr size_t kSmem = kOffDone + 16;
+  static constexpr size_t kSmemAlloc = kSmem + 1024;
+  static_assert(kSmemAlloc <= 232448, "shared memory opt-in limit");
+};
+
+template <int D>
+struct Int4Ring {
+  using C = Cfg<D, kInt4Pages>;
+  unsigned char* smem;
+  __device__ __forceinline__ uint64_t* full(int s) const { return bars() + s; }
+  __device__ __forceinline__ uint64_t* empty(int s) const { return bars() + C::kStages + s; }
+  __device__ __forceinline__ uint64_t* query(int s) const { return bars() + 2 * C::kStages + s; }
+  __device__ __forceinline__ uint64_t* left() const { return query(C::kSegs); }
+  __device__ __forceinline__ uint64_t* merged() const { return query(C::kSegs) + 1; }
+  __device__ __forceinline__ Int4Stage* stage(int s) const {
+    return reinterpret_cast<Int4Stage*>(smem + C::kOffInfo) + s;
+  }
+  __device__ __forceinline__ Int4Segment* segment(int s) const {
+    return reinterpret_cast<Int4Segment*>(smem + C::kOffSeg) + s;
+  }
+  __device__ __forceinline__ volatile int32_t* done() const {
+    return reinterpret_cast<volatile int32_t*>(smem + C::kOffDone);
+  }
+  __device__ __forceinline__ unsigned char* slab(int s) const {
+    return smem + C::kOffK + (size_t)s * C::kSlab;
+  }
+  __device__ __forceinline__ unsigned char* q(int s) const {
+    return smem + C::kOffQ + (size_t)s * C::kQBytes;
+  }
+  __device__ __forceinline__ float* state(int floats) const {
+    return reinterpret_cast<float*>(smem + C::kOffState) + floats;
+  }
+  // Barrier set-up (one thread).
+  __device__ __forceinline__ void init(bool narrow) const {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), C::kGroupWarps);
+    }
+    for (int s = 0; s < C::kSegs; ++s) mbar_init(query(s), 1);
+    mbar_init(left(), narrow ? C::kNarrowWarps : C::kWideWarps);
+    mbar_init(merged(), 1);
+    *done() = 0;
+    fence_mbar_init();
+  }
+
+ private:
+  __device__ __forceinline__ uint64_t* bars() const {
+    return reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  }
+};
+
+// The producer's place: stages and segments handed out so far (uniform over its warp).
+struct Int4Place {
+  int64_t it = 0;
+  int32_t segs = 0;
+  int32_t queries = 0;  // of them with a query copied
+  bool abort = false;
+};
+
+// Hands the pages of lanes [first, last) to the consumers, in lane order (the whole producer warp
+// calls it): the lane's page is task t of unit u; kNewUnit in fl opens a segment, kBankB says of which
+// list.  Each lane issues its own page.  A 4-bit page lasts an SM 0.4 us, so what a page costs the
+// producer counts: everything but the wait for the stage, its description and the copy is computed by
+// the lanes side by side.
+template <int D>
+__device__ __forceinline__ void issue_batch_int4(const DecodeArgs& a, unsigned char* smem,
+                                                 Int4Place& pl, int first, int last, int32_t u,
+                                                 uint32_t fl, const PageTask& t, uint32_t& eflags,
+                                                 int lane) {
+  using C = Cfg<D, kInt4Pages>;
+  const Int4Ring<D> ring{smem};
+  const int64_t mine = pl.it + (lane - first);
+  const int s = (int)(mine % C::kStages);
+  const uint32_t parity = (uint32_t)((mine / C::kStages - 1) & 1);
+  const bool rows = t.page >= 0 && t.hi > t.lo;
+  const bool fresh = lane >= first && lane < last && (fl & kNewUnit) != 0;
+  const uint32_t opens = __ballot_sync(0xffffffffu, fresh);
+  const int32_t seg = pl.segs + __popc(opens & (0xffffffffu >> (31 - lane))) - 1;
+  const int32_t h = u % a.Hkv, r = u / a.Hkv;
+  const uint32_t qbytes = (uint32_t)(a.G * D * 2);
+  const unsigned char* src = static_cast<const unsigned char*>(a.k_cache) +
+                             ((int64_t)(rows ? t.page : 0) * a.Hkv + h) * C::kSlab;
+  const __nv_bfloat16* q =
+      static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)r * a.Hq + (int64_t)h * a.G) * D;
+  const uint64_t once = l2_policy_evict_first();  // pages are read once per step
+  for (int l = first; l < last && !pl.abort; ++l) {
+    bool ok = true;
+    if (lane == l) {
+      ok = mine < C::kStages || mbar_wait(ring.empty(s), parity);
+      if (ok) {
+        if (fresh) {  // (the slot of segment seg - kSegs: every warp is past it, see kSegs)
+          const int qslot = seg % C::kSegs;
+          *ring.segment(qslot) = Int4Segment{u, (int32_t)(fl & kBankB)};
+          mbar_arrive_expect_tx(ring.query(qslot), qbytes);
+          bulk_load(ring.q(qslot), q, qbytes, ring.query(qslot));
+        }
+        int4* info = reinterpret_cast<int4*>(ring.stage(s));
+        info[0] = make_int4(seg, 0, rows ? t.lo : 0, rows ? t.hi : 0);
+        info[1] = make_int4(t.ie, t.ws, 0, 0);
+        mbar_arrive_expect_tx(ring.full(s), rows ? (uint32_t)C::kSlab : 0u);
+        if (rows) bulk_load_hint(ring.slab(s), src, (uint32_t)C::kSlab, ring.full(s), once);
+      }
+    }
+    __syncwarp();  // a segment's entry is written before any later stage of it is handed out
+    if (__all_sync(0xffffffffu, ok)) {
+      ++pl.it;
+    } else {  // the caller still waits (bounded) for the copies already started
+      pl.abort = true;
+      eflags |= SRKV_EFLAG_TIMEOUT;
+    }
+  }
+  pl.segs += __popc(opens);
+  pl.queries += __popc(opens);
+}
+
+// The end: a stage for each group that closes every segment, then every copy lands.
+template <int D>
+__device__ __forceinline__ void finish_ring_int4(const DecodeArgs& a, unsigned char* smem,
+                                                 Int4Place& pl, uint32_t& eflags, int lane) {
+  using C = Cfg<D, kInt4Pages>;
+  const Int4Ring<D> ring{smem};
+  if (lane != 0) return;
+  const int groups = (a.G <= 4 ? C::kNarrowWarps : C::kWideWarps) / C::kGroupWarps;
+  for (int g = 0; g < groups && !pl.abort; ++g) {
+    const int s = (int)(pl.it % C::kStages);
+    if (pl.it >= C::kStages && !mbar_wait(ring.empty(s), (uint32_t)((pl.it / C::kStages - 1) & 1))) {
+      pl.abort = true;
+      eflags |= SRKV_EFLAG_TIMEOUT;
+      break;
+    }
+    *ring.stage(s) = Int4Stage{pl.segs, 1, 0, 0, 0, 0, {0, 0}};
+    mbar_arrive(ring.full(s));
+    ++pl.it;
+  }
+  for (int64_t i = pl.it > C::kStages ? pl.it - C::kStages : 0; i < pl.it; ++i)
+    if (!mbar_wait(ring.full((int)(i % C::kStages)), (uint32_t)((i / C::kStages) & 1))) {
+      eflags |= SRKV_EFLAG_TIMEOUT;
+      return;
+    }
+  for (int32_t i = pl.queries > C::kSegs ? pl.queries - C::kSegs : 0; i < pl.queries; ++i)
+    if (!mbar_wait(ring.query(i % C::kSegs), (uint32_t)((i / C::kSegs) & 1))) {
+      eflags |= SRKV_EFLAG_TIMEOUT;
+      return;
+    }
+}
+
+// kNarrow: the group has at most 4 heads.
+template <int D, bool kNarrow>
+__device__ __forceinline__ void consume_int4(const DecodeArgs& a, unsigned char* smem, int lane,
+                                             int warp) {
   using C = Cfg<D, kInt4Pages>;
   using F = Int4Slab<D>;
-  constexpr int kGroupWarps = 2;                       // warps per page
-  constexpr int kGroups = kConsumerWarps / kGroupWarps;  // pages at once
-  constexpr int kTok = kBlock / kGroupWarps;           // tokens per warp and page
-  constexpr int NW = kTok / 32;                        // 32-token groups per warp
-  constexpr int KW = D / 32;                           // key words per lane and row
-  constexpr int VX = D / 32;                           // 16-byte value loads per lane and octet
-  float* sMerge = reinterpret_cast<float*>(smem + C::kOffMerge);
-  StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem + C::kOffInfo);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* empty = full + 2 * C::kStages;
-  uint64_t* mb_w1 = empty + C::kStages;
-  uint64_t* mb_w2 = mb_w1 + 1;
-  uint64_t* mb_r2 = mb_w1 + 2;
+  constexpr int kGroupWarps = C::kGroupWarps;       // warps per page
+  constexpr int kWarps = kNarrow ? C::kNarrowWarps : C::kWideWarps;
+  constexpr int kGroups = kWarps / kGroupWarps;     // pages at once
+  const Int4Ring<D> ring{smem};
+  constexpr int kTok = kBlock / kGroupWarps;        // tokens per warp and page
+  constexpr int NW = kTok / 32;                     // 32-token groups per warp
+  constexpr int KW = D / 32;                        // key words per lane and row
+  constexpr int VX = D / 32;                        // 16-byte value loads per lane and octet
+  constexpr int R = kNarrow ? 1 : 2;                // rows of a tile in a lane's softmax
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   const Lane ln{lane >> 2, lane & 3};
   const int group = warp / kGroupWarps, row0 = (warp % kGroupWarps) * kTok;
   const int tile_row = 8 * (ln.g >> 1) + (ln.g & 1);  // token of tile row g within 32 tokens
+  const bool second = kNarrow && ln.t >= 2;           // this lane takes rows g + 8
+  const int my_row = row0 + tile_row + (second ? 2 : 0);
+  const int hd = kNarrow ? 2 * (ln.t & 1) : 2 * ln.t;  // this lane's heads: hd, hd + 1
+  // lanes of the same heads: the g's, and with kNarrow also t + 2
+  constexpr int kFirstXor = kNarrow ? 2 : 4;
   SoftmaxState<D> st;
   st.reset();
-  float pm[2] = {0.f, 0.f};  // sum of weight * vlo, heads 2t and 2t + 1 (this lane's tokens)
+  float pm[2] = {0.f, 0.f};  // sum of weight * vlo of the lane's heads and tokens
+  float vlim = 0.f;          // a power of two no vs so far exceeds (0: none seen but zeros)
+  float vf[R];               // vs to the fp16 operand: scale over vlim, 16 times less for rows g + 8
+#pragma unroll
+  for (int x = 0; x < R; ++x) vf[x] = 0.f;
   uint32_t qb[KW][2][2];     // [word][bits 0..7, 8..15 of its halves][codes * 2^-24, * 2^-20]
 #pragma unroll
   for (int i = 0; i < KW; ++i) qb[i][0][0] = qb[i][0][1] = qb[i][1][0] = qb[i][1][1] = 0u;
-  float qs = 0.f;            // what the integer-like logits are to be multiplied by (log2 domain)
-  float qm0 = 0.f, qm1 = 0.f;  // sum_d q_d of heads 2t, 2t + 1 (log2 domain)
-  bool abort = false;
-  int32_t merges = 0;
+  float qs = 0.f;              // factor of the logits (log2 domain)
+  float qm0 = 0.f, qm1 = 0.f;  // sum_d q_d of the lane's heads (log2 domain)
 
-  // End of a segment: reduce the per-lane sums, merge the 8 warps, write the partial.
-  auto close_segment = [&](const StageInfo& inf) {
+  // Leaves this warp's state of segment `seg` for the merger (once it is done with the segment
+  // before).  False: a wait ran out.
+  auto leave = [&](int32_t seg) {
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
+    for (int o = kFirstXor; o < 32; o <<= 1) {
       st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
       st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
       pm[0] += __shfl_xor_sync(0xffffffffu, pm[0], o);
@@ -81,42 +283,33 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
     // only NaN rows seen: a finite reference, so that the merges do not take the part for empty
     if (st.m[0] == -INFINITY && !(st.l[0] == 0.f)) st.m[0] = 0.f;
     if (st.m[1] == -INFINITY && !(st.l[1] == 0.f)) st.m[1] = 0.f;
-    constexpr float kUnit = 16777216.f / kInt4PScale;  // 2^24 of the subnormals
+    if (seg > 0 && !mbar_wait(ring.merged(), (uint32_t)((seg - 1) & 1))) return false;
+    if (!kNarrow || ln.t < 2) {
+      const float unit = vlim * (16777216.f / kInt4PScale);  // 2^24 of the subnormals
+      const int slot = kNarrow ? ln.g * 2 + ln.t : lane;
+      float4* p = reinterpret_cast<float4*>(
+          ring.state(warp * (kNarrow ? C::kNarrowState : C::kWideState) + slot * C::kStateStride));
+      p[0] = make_float4(st.m[0], st.m[1], st.l[0], st.l[1]);
 #pragma unroll
-    for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) st.acc[i][c] = fmaf(st.acc[i][c], kUnit, pm[c & 1]);
-    const uint32_t ph = (uint32_t)(merges & 1);
-    if (warp >= 4) {
-      if (merges > 0 && !mbar_wait(mb_r2, ph ^ 1u)) abort = true;
-      st.store(sMerge + (warp - 4) * C::kMergeSlot, lane);
-      warp_arrive(mb_w1);
-    } else {
-      if (!mbar_wait(mb_w1, ph)) abort = true;
-      st.merge_from(sMerge + warp * C::kMergeSlot, lane);
-      if (warp >= 1) {
-        st.store(sMerge + warp * C::kMergeSlot, lane);
-        warp_arrive(mb_w2);
-      } else {
-        if (!mbar_wait(mb_w2, ph)) abort = true;
-        for (int w = 1; w < 4; ++w) st.merge_from(sMerge + w * C::kMergeSlot, lane);
-        warp_arrive(mb_r2);
-        write_partial(st, inf, ln);
-      }
+      for (int i = 0; i < C::MT; ++i)
+        p[1 + i] = make_float4(fmaf(st.acc[i][0], unit, pm[0]), fmaf(st.acc[i][1], unit, pm[1]),
+                               fmaf(st.acc[i][2], unit, pm[0]), fmaf(st.acc[i][3], unit, pm[1]));
     }
-    ++merges;
+    warp_arrive(ring.left());
+    return true;
   };
 
   // The unit's query: fp16 with one power of two for all of its heads, the largest magnitude
   // put into [2^14, 2^15), so that bf16's 8 significant bits stay exact down to 2^-25 of it.
   auto load_query = [&](const unsigned char* q) {
-    constexpr int QV = D / 32;  // 16-byte loads: elements (D / 4) t .. of head g
+    constexpr int QV = D / 32;  // 16-byte loads: elements (D / 4) t .. of the column's head
+    const int head = kNarrow ? ln.g & 3 : ln.g;
     int4 w[QV];
     uint32_t top = 0u;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < QV; ++i) {
-      w[i] = ln.g < a.G ? lds128(q + ((size_t)ln.g * D + (D / 4) * ln.t + 8 * i) * 2)
+      w[i] = head < a.G ? lds128(q + ((size_t)head * D + (D / 4) * ln.t + 8 * i) * 2)
                         : make_int4(0, 0, 0, 0);
       const uint32_t u[4] = {(uint32_t)w[i].x, (uint32_t)w[i].y, (uint32_t)w[i].z,
                              (uint32_t)w[i].w};
@@ -131,8 +324,8 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
     top = __reduce_max_sync(0xffffffffu, top);
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    qm0 = __shfl_sync(0xffffffffu, sum, 8 * ln.t) * a.scale_log2;      // head 2t
-    qm1 = __shfl_sync(0xffffffffu, sum, 8 * ln.t + 4) * a.scale_log2;  // head 2t + 1
+    qm0 = __shfl_sync(0xffffffffu, sum, 4 * hd) * a.scale_log2;
+    qm1 = __shfl_sync(0xffffffffu, sum, 4 * hd + 4) * a.scale_log2;
     int e = (int)(top >> 23) - 127;        // floor(log2 top), -127 for zeros and subnormals
     e = min(max(e, -112), 100);
     const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
@@ -149,170 +342,263 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
     }
   };
 
-  for (int64_t it = 0;; ++it) {
-    const int s = (int)(it % C::kStages);
-    if (!mbar_wait(&full[s], (uint32_t)((it / C::kStages) & 1))) {
-      if (lane == 0) raise_flags(a.error_flags, SRKV_EFLAG_TIMEOUT);
-      break;
-    }
-    const StageInfo inf = sInfo[s];
-    if (inf.flags & kLast) {  // the sentinel; it may close the last segment
-      if (inf.flags & kSegEnd) {
-        close_segment(inf);
-        if (abort && lane == 0) raise_flags(a.error_flags, SRKV_EFLAG_TIMEOUT);
-      }
-      break;
-    }
-    if (inf.flags & kNewUnit) {
-      st.reset();
-      pm[0] = pm[1] = 0.f;
-      load_query(smem + C::kOffQ + (size_t)s * C::kQBytes);
-    }
-    if ((int)(it % kGroups) == group && row0 < inf.hi && row0 + kTok > inf.lo) {
-      const unsigned char* slab = smem + C::kOffK + (size_t)s * C::kSlab;
-      const uint32_t* k_rows = reinterpret_cast<const uint32_t*>(slab + F::kKRows);
-      const uint32_t* v_rows = reinterpret_cast<const uint32_t*>(slab + F::kVRows);
-      constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-      // ---- logits (log2 domain) of the warp's tokens: [32 tokens][tile][row g: heads 2t, 2t+1,
-      //      row g + 8: the same]; vs and vlo of those rows
-      float z[NW][2][4], vs[NW][2][2], vl[NW][2][2];
+  // The warp's tokens of the page in stage s.
+  auto attend = [&](const Int4Stage& inf, const unsigned char* slab) {
+    const uint32_t* k_rows = reinterpret_cast<const uint32_t*>(slab + F::kKRows) + my_row;
+    const uint32_t* v_rows = reinterpret_cast<const uint32_t*>(slab + F::kVRows) + my_row;
+    // ---- logits (log2 domain) of the lane's rows and heads, and vs and vlo of the rows
+    float z[NW][2][R][2], vs[NW][2][R], vl[NW][2][R];
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int ra = row0 + 32 * w + tile_row + 4 * j, rb = ra + 2;
-          uint32_t ka[KW], kb[KW];
-          if constexpr (KW == 4) {
-            const int4 x = lds128(slab + ra * (D / 2) + ln.t * 16);
-            const int4 y = lds128(slab + rb * (D / 2) + ln.t * 16);
-            ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
-            kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
-          } else {
-            const int2 x = *reinterpret_cast<const int2*>(slab + ra * (D / 2) + ln.t * 8);
-            const int2 y = *reinterpret_cast<const int2*>(slab + rb * (D / 2) + ln.t * 8);
-            ka[0] = x.x, ka[1] = x.y;
-            kb[0] = y.x, kb[1] = y.y;
-          }
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < KW; ++i)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint32_t x = ka[i] >> (8 * p), y = kb[i] >> (8 * p);
-              mma_16816_f16(acc, x & kLow, y & kLow, x & kHigh, y & kHigh, qb[i][p][0],
-                            qb[i][p][1]);
-            }
-          const uint32_t pa = k_rows[ra], pb = k_rows[rb], va = v_rows[ra], vb = v_rows[rb];
-          const float fa = int4_scale(pa) * qs, fb = int4_scale(pb) * qs;
-          z[w][j][0] = fmaf(acc[0], fa, int4_lo(pa) * qm0);
-          z[w][j][1] = fmaf(acc[1], fa, int4_lo(pa) * qm1);
-          z[w][j][2] = fmaf(acc[2], fb, int4_lo(pb) * qm0);
-          z[w][j][3] = fmaf(acc[3], fb, int4_lo(pb) * qm1);
-          vs[w][j][0] = int4_scale(va);
-          vs[w][j][1] = int4_scale(vb);
-          vl[w][j][0] = int4_lo(va);
-          vl[w][j][1] = int4_lo(vb);
+      for (int j = 0; j < 2; ++j) {
+        const int ra = row0 + 32 * w + tile_row + 4 * j, rb = ra + 2;
+        uint32_t ka[KW], kb[KW];
+        if constexpr (KW == 4) {
+          const int4 x = lds128(slab + ra * (D / 2) + ln.t * 16);
+          const int4 y = lds128(slab + rb * (D / 2) + ln.t * 16);
+          ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
+          kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
+        } else {
+          const int2 x = *reinterpret_cast<const int2*>(slab + ra * (D / 2) + ln.t * 8);
+          const int2 y = *reinterpret_cast<const int2*>(slab + rb * (D / 2) + ln.t * 8);
+          ka[0] = x.x, ka[1] = x.y;
+          kb[0] = y.x, kb[1] = y.y;
         }
-      // ---- rows that are not attended: weight 0, and their parameters are not data
-      const bool whole = inf.lo <= row0 && inf.hi >= row0 + kTok &&
-                         (inf.ie >= row0 + kTok || inf.ws <= row0 || inf.ws <= inf.ie);
-      if (!whole) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
+        for (int i = 0; i < KW; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t x = ka[i] >> (8 * p), y = kb[i] >> (8 * p);
+            mma_16816_f16(acc, x & kLow, y & kLow, x & kHigh, y & kHigh, qb[i][p][0], qb[i][p][1]);
+          }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int r = row0 + 32 * w + tile_row + 4 * j + 2 * x;
-              if (!(r >= inf.lo && r < inf.hi && (r < inf.ie || r >= inf.ws))) {
-                z[w][j][2 * x] = z[w][j][2 * x + 1] = -INFINITY;
-                vs[w][j][x] = vl[w][j][x] = 0.f;
-              }
-            }
+        for (int x = 0; x < R; ++x) {
+          const uint32_t kr = k_rows[32 * w + 4 * j + 2 * x], vr = v_rows[32 * w + 4 * j + 2 * x];
+          const float c0 = kNarrow ? (second ? acc[2] : acc[0]) : acc[2 * x];
+          const float c1 = kNarrow ? (second ? acc[3] : acc[1]) : acc[2 * x + 1];
+          const float f = int4_scale(kr) * qs, lo = int4_lo(kr);
+          z[w][j][x][0] = fmaf(c0, f, lo * qm0);
+          z[w][j][x][1] = fmaf(c1, f, lo * qm1);
+          vs[w][j][x] = int4_scale(vr);
+          vl[w][j][x] = int4_lo(vr);
+        }
       }
-      // ---- raise the reference if some weight would pass its headroom
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+    // ---- rows that are not attended: weight 0, and their parameters are not data
+    const bool whole = inf.lo <= row0 && inf.hi >= row0 + kTok &&
+                       (inf.ie >= row0 + kTok || inf.ws <= row0 || inf.ws <= inf.ie);
+    if (!whole) {
 #pragma unroll
       for (int w = 0; w < NW; ++w)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float lv = fminf(fmaxf(__log2f(vs[w][j][x]), -kInt4VScaleLog2Max),
-                                   kInt4VScaleLog2Max);
-            mx0 = fmaxf(mx0, z[w][j][2 * x] + lv);
-            mx1 = fmaxf(mx1, z[w][j][2 * x + 1] + lv);
+          for (int x = 0; x < R; ++x) {
+            const int r = my_row + 32 * w + 4 * j + 2 * x;
+            if (!(r >= inf.lo && r < inf.hi && (r < inf.ie || r >= inf.ws))) {
+              z[w][j][x][0] = z[w][j][x][1] = -INFINITY;
+              vs[w][j][x] = vl[w][j][x] = 0.f;
+            }
           }
-      if (__any_sync(0xffffffffu,
-                     mx0 > st.m[0] + kInt4Headroom || mx1 > st.m[1] + kInt4Headroom)) {
+    }
+    // ---- raise the references if some weight or scale would pass them
+    float mx0 = -INFINITY, mx1 = -INFINITY, mv = 0.f;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+          mx0 = fmaxf(mx0, z[w][j][x][0]);
+          mx1 = fmaxf(mx1, z[w][j][x][1]);
+          mv = fmaxf(mv, vs[w][j][x]);
         }
-        const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
-        const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(st.m[0] - n0);
-        const float a1 = n1 == -INFINITY ? 1.f : fast_exp2(st.m[1] - n1);
-        st.m[0] = n0;
-        st.m[1] = n1;
-        st.l[0] *= a0;
-        st.l[1] *= a1;
-        pm[0] *= a0;
-        pm[1] *= a1;
+    if (__any_sync(0xffffffffu, mx0 > st.m[0] + kInt4Headroom ||
+                                    mx1 > st.m[1] + kInt4Headroom || mv > vlim)) {
 #pragma unroll
-        for (int i = 0; i < C::MT; ++i) {
-          st.acc[i][0] *= a0;
-          st.acc[i][1] *= a1;
-          st.acc[i][2] *= a0;
-          st.acc[i][3] *= a1;
+      for (int o = kFirstXor; o < 32; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+      }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(mv));  // mv >= 0
+      const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
+      const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(st.m[0] - n0);
+      const float a1 = n1 == -INFINITY ? 1.f : fast_exp2(st.m[1] - n1);
+      st.m[0] = n0;
+      st.m[1] = n1;
+      st.l[0] *= a0;
+      st.l[1] *= a1;
+      pm[0] *= a0;
+      pm[1] *= a1;
+      float grow = 1.f;  // old vlim over new
+      if (__uint_as_float(top) > vlim) {
+        // the power of two above the largest scale, within 2^-100 .. 2^120
+        const uint32_t e = min(max((top >> 23) + 1u, 27u), 247u);
+        const float lim = __uint_as_float(e << 23), inv = __uint_as_float((254u - e) << 23);
+        grow = vlim * inv;
+        vlim = lim;
+        if constexpr (kNarrow) {
+          vf[0] = inv * (second ? kInt4PScale / 16.f : kInt4PScale);
+        } else {
+          vf[0] = inv * kInt4PScale;
+          vf[1] = inv * (kInt4PScale / 16.f);
         }
       }
-      const float base0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
-      const float base1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-      // ---- weights and O^T += V^T . P
+      const float g0 = a0 * grow, g1 = a1 * grow;
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i) {
+        st.acc[i][0] *= g0;
+        st.acc[i][1] *= g1;
+        st.acc[i][2] *= g0;
+        st.acc[i][3] *= g1;
+      }
+    }
+    const float base0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
+    const float base1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
+    // ---- weights, as operands of the second product: fp16 (half a step is 2^-11 of each,
+    //      independent over the tokens)
+    uint32_t b[NW][2][2];
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t p[R];
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+          const float e0 = fast_exp2(z[w][j][x][0] - base0);
+          const float e1 = fast_exp2(z[w][j][x][1] - base1);
+          st.l[0] += e0;
+          st.l[1] += e1;
+          pm[0] = fmaf(e0, vl[w][j][x], pm[0]);
+          pm[1] = fmaf(e1, vl[w][j][x], pm[1]);
+          const float f = vs[w][j][x] * vf[x];
+          p[x] = movmatrix_trans(pack_f16(e0 * f, e1 * f));
+        }
+        b[w][j][0] = p[0];
+        b[w][j][1] = kNarrow ? __shfl_xor_sync(0xffffffffu, p[0], 16) : p[R - 1];
+      }
+    // ---- O^T += V^T . P.  The products of this page's tokens are summed from zero and added in
+    // fp32: a tensor core's sums truncate, and over a long segment of nearly equal weights that
+    // drift would show against the small difference of sum u c and sum w lo that is the output.
+    const unsigned char* v = slab + F::kVCodes + (row0 / 32) * (D / 4) * 64 + ln.t * 16;
+#pragma unroll
+    for (int x = 0; x < VX; ++x) {
+      float o[2][4] = {};
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        uint32_t b[2][2];
+        const int4 q4 = lds128(v + (w * (D / 4) + ln.g + 8 * x) * 64);
+        const uint32_t u[4] = {(uint32_t)q4.x, (uint32_t)q4.y, (uint32_t)q4.z, (uint32_t)q4.w};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float e0 = fast_exp2(z[w][j][0] - base0), e1 = fast_exp2(z[w][j][1] - base1);
-          const float e2 = fast_exp2(z[w][j][2] - base0), e3 = fast_exp2(z[w][j][3] - base1);
-          st.l[0] += e0 + e2;
-          st.l[1] += e1 + e3;
-          pm[0] = fmaf(e0, vl[w][j][0], fmaf(e2, vl[w][j][1], pm[0]));
-          pm[1] = fmaf(e1, vl[w][j][0], fmaf(e3, vl[w][j][1], pm[1]));
-          // fp16 weights (half a step is 2^-12 of each, independent over the tokens); the rows
-          // g + 8 meet the codes * 2^-20
-          const float fa = vs[w][j][0] * kInt4PScale, fb = vs[w][j][1] * (kInt4PScale / 16.f);
-          b[j][0] = movmatrix_trans(pack_f16(e0 * fa, e1 * fa));
-          b[j][1] = movmatrix_trans(pack_f16(e2 * fb, e3 * fb));
-        }
-        const unsigned char* v = slab + F::kVCodes + (row0 / 32 + w) * (D / 4) * 64 + ln.t * 16;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int x = 0; x < VX; ++x) {
-          const int4 q4 = lds128(v + (ln.g + 8 * x) * 64);
-          const uint32_t u[4] = {(uint32_t)q4.x, (uint32_t)q4.y, (uint32_t)q4.z, (uint32_t)q4.w};
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t p = u[2 * h] >> (8 * j), q = u[2 * h + 1] >> (8 * j);
-              mma_16816_f16(st.acc[2 * x + h], p & kLow, q & kLow, p & kHigh, q & kHigh, b[j][0],
-                            b[j][1]);
-            }
-        }
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t p = u[2 * h] >> (8 * j), q = u[2 * h + 1] >> (8 * j);
+            mma_16816_f16(o[h], p & kLow, q & kLow, p & kHigh, q & kHigh, b[w][j][0], b[w][j][1]);
+          }
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st.acc[2 * x + h][c] += o[h][c];
     }
-    // release the stage
-    warp_arrive(&empty[s]);
+  };
 
-    if (inf.flags & kSegEnd) {
-      close_segment(inf);
-      if (abort) {
-        if (lane == 0) raise_flags(a.error_flags, SRKV_EFLAG_TIMEOUT);
-        break;
+  int s = group;  // this group's stages: group, group + kGroups, ...
+  uint32_t parity = 0u;
+  int32_t cur = -1;  // the segment the state belongs to
+  bool ok = true;
+  for (;;) {
+    ok = mbar_wait(ring.full(s), parity);
+    if (!ok) break;
+    const Int4Stage inf = *ring.stage(s);
+    while (cur < inf.seg && ok) {  // the segments up to this one are over for this warp
+      if (cur >= 0) ok = leave(cur);
+      ++cur;
+      st.reset();
+      pm[0] = pm[1] = 0.f;
+      vlim = 0.f;
+#pragma unroll
+      for (int x = 0; x < R; ++x) vf[x] = 0.f;
+      if (cur == inf.seg && !inf.last && ok) {
+        ok = mbar_wait(ring.query(cur % C::kSegs), (uint32_t)((cur / C::kSegs) & 1));
+        load_query(ring.q(cur % C::kSegs));
       }
     }
+    if (!ok || inf.last) break;
+    if (row0 < inf.hi && row0 + kTok > inf.lo) attend(inf, ring.slab(s));
+    warp_arrive(ring.empty(s));  // release the stage
+    s += kGroups;
+    if (s >= C::kStages) {
+      s -= C::kStages;
+      parity ^= 1u;
+    }
+  }
+  // after the last segment is merged, tell the merger that there is no other
+  if (ok && cur > 0) ok = mbar_wait(ring.merged(), (uint32_t)((cur - 1) & 1));
+  if (!ok) {
+    if (lane == 0) raise_flags(a.error_flags, SRKV_EFLAG_TIMEOUT);
+    return;
+  }
+  if (lane == 0) *ring.done() = 1;
+  warp_arrive(ring.left());
+}
+
+// The consumer warps' part (warp: 0 .. kNarrowWarps - 1).
+template <int D>
+__device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned char* smem,
+                                                   int lane, int warp) {
+  using C = Cfg<D, kInt4Pages>;
+  if (a.G <= 4)
+    consume_int4<D, true>(a, smem, lane, warp);
+  else if (warp < C::kWideWarps)
+    consume_int4<D, false>(a, smem, lane, warp);
+}
+
+// The merger warp: segment after segment, joins the consumer warps' states and calls
+// write_partial(state, segment, lane) with the result.
+template <int D, typename WritePartial>
+__device__ __forceinline__ void merger_loop_int4(const DecodeArgs& a, unsigned char* smem, int lane,
+                                                 WritePartial&& write_partial) {
+  using C = Cfg<D, kInt4Pages>;
+  const Int4Ring<D> ring{smem};
+  const Lane ln{lane >> 2, lane & 3};
+  const bool narrow = a.G <= 4, holds = !narrow || ln.t < 2;
+  const int warps = narrow ? C::kNarrowWarps : C::kWideWarps;
+  const int stride = narrow ? C::kNarrowState : C::kWideState;
+  const int slot = holds ? (narrow ? ln.g * 2 + ln.t : lane) : 0;
+  const float* mine = ring.state(slot * C::kStateStride);
+  for (int32_t seg = 0;; ++seg) {
+    if (!mbar_wait(ring.left(), (uint32_t)(seg & 1))) {
+      if (lane == 0) raise_flags(a.error_flags, SRKV_EFLAG_TIMEOUT);
+      return;
+    }
+    if (*ring.done()) return;
+    SoftmaxState<D> st;
+    st.reset();
+    for (int w = 0; w < warps; ++w) st.m[0] = fmaxf(st.m[0], mine[w * stride]);
+    for (int w = 0; w < warps; ++w) st.m[1] = fmaxf(st.m[1], mine[w * stride + 1]);
+    const float b0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
+    const float b1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
+#pragma unroll 2
+    for (int w = 0; w < warps; ++w) {
+      const float4* p = reinterpret_cast<const float4*>(mine + w * stride);
+      const float4 ml = p[0];
+      const float f0 = fast_exp2(ml.x - b0), f1 = fast_exp2(ml.y - b1);
+      st.l[0] = fmaf(ml.z, f0, st.l[0]);
+      st.l[1] = fmaf(ml.w, f1, st.l[1]);
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i) {
+        const float4 v = p[1 + i];
+        st.acc[i][0] = fmaf(v.x, f0, st.acc[i][0]);
+        st.acc[i][1] = fmaf(v.y, f1, st.acc[i][1]);
+        st.acc[i][2] = fmaf(v.z, f0, st.acc[i][2]);
+        st.acc[i][3] = fmaf(v.w, f1, st.acc[i][3]);
+      }
+    }
+    const Int4Segment sg = *ring.segment(seg % C::kSegs);
+    warp_arrive(ring.merged());
+    write_partial(st, sg, ln);
   }
 }
 

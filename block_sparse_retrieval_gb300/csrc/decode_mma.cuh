@@ -17,12 +17,10 @@
 #pragma once
 
 #include "decode_plan.cuh"
-#include "int4_page.cuh"
 
 namespace srkv {
 
 constexpr int kConsumerWarps = 8;
-constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kProducerWarp = kConsumerWarps;
 constexpr uint32_t kNewUnit = 1, kSegEnd = 2, kBankB = 4, kLast = 8;
 // Compressed pages: factor on the V-scaled weights and on their sum (a power of two).
@@ -36,12 +34,13 @@ struct StageInfo {
 };
 
 // What the pages hold: bf16 values, E4M3 codes (each stage then also carries the 128 K and 128 V
-// row scales of its page) or 4-bit codes (int4_page.cuh; a stage is one slab).
+// row scales of its page) or 4-bit codes (decode_int4.cuh has their stages).
 enum : int { kBf16Pages = 0, kE4m3Pages = 1, kInt4Pages = 2 };
 
 template <int D, int Fmt = kBf16Pages>
 struct Cfg {
   static constexpr bool F8 = Fmt == kE4m3Pages;
+  static constexpr int kThreads = (kConsumerWarps + 1) * 32;
   static_assert(!F8 || D == 128, "compressed pages: d 128");
   static constexpr int kElem = F8 ? 1 : 2;              // bytes per cached value
   static constexpr int kSlab = kBlock * D * kElem;      // bytes of one K or V slab
@@ -66,27 +65,6 @@ struct Cfg {
   static constexpr size_t kSmemAlloc = kSmem + 1024;  // the swizzled stages need 1 KiB alignment
   static constexpr int kBoxes = D * kElem / 128;       // 128-byte-wide TMA boxes per slab
   static constexpr int kBoxBytes = kBlock * 128;       // 128 rows of 128 bytes
-};
-
-// 4-bit pages: a stage is one slab (17 408 bytes at d 128), moved by one bulk copy.
-template <int D>
-struct Cfg<D, kInt4Pages> {
-  static constexpr int kSlab = Int4Slab<D>::kBytes;
-  static constexpr int kStages = D == 128 ? 10 : 18;
-  static constexpr int kQBytes = 8 * D * 2;
-  static constexpr int MT = D / 16;
-  static constexpr int kMergeStride = Cfg<D>::kMergeStride;
-  static constexpr int kMergeSlot = Cfg<D>::kMergeSlot;
-
-  static constexpr size_t kOffK = 0;
-  static constexpr size_t kOffQ = (size_t)kStages * kSlab;
-  // the one-kernel decode's leader streams no pages and keeps its partials from here on
-  static constexpr size_t kOffV = (size_t)(kStages / 2) * kSlab;
-  static constexpr size_t kOffMerge = kOffQ + (size_t)kStages * kQBytes;
-  static constexpr size_t kOffInfo = kOffMerge + sizeof(float) * 4 * kMergeSlot;
-  static constexpr size_t kOffBar = kOffInfo + sizeof(StageInfo) * kStages;
-  static constexpr size_t kSmem = kOffBar + sizeof(uint64_t) * (3 * kStages + 3);
-  static constexpr size_t kSmemAlloc = kSmem + 1024;
 };
 
 // Tensor maps of the K and V caches, [page][kv head * 128 + row][d] (bf16).
@@ -202,24 +180,6 @@ __device__ __forceinline__ void issue_stage(const DecodeArgs& a, const TmaMaps& 
   // is still arriving.
   const bool rows = load && t.hi > t.lo;
   const uint32_t qbytes = (uint32_t)(a.G * D * 2);
-  if constexpr (Fmt == kInt4Pages) {  // keys, values and rows land together
-    mbar_arrive_expect_tx(&full[s], (rows ? (uint32_t)C::kSlab : 0u) +
-                                        ((fl & kNewUnit) ? qbytes : 0u));
-    mbar_arrive(&full_v[s]);
-    ++armed;
-    if (u < 0) return;
-    const int32_t h = u % a.Hkv, r = u / a.Hkv;
-    if (rows)
-      bulk_load_hint(smem + C::kOffK + (size_t)s * C::kSlab,
-                     static_cast<const unsigned char*>(a.k_cache) +
-                         ((int64_t)t.page * a.Hkv + h) * C::kSlab,
-                     (uint32_t)C::kSlab, &full[s], l2_policy_evict_first());
-    if (fl & kNewUnit)
-      bulk_load(smem + C::kOffQ + (size_t)s * C::kQBytes,
-                static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)r * a.Hq + (int64_t)h * a.G) * D,
-                qbytes, &full[s]);
-    return;
-  } else {
   constexpr uint32_t kRowScales = F8 ? kBlock * 4 : 0;  // one fp32 scale per row
   if (!F8 && rows && t.page >= a.num_pages) {
     // A page of the host pool: the producer warp copies its slabs and then arrives
@@ -266,7 +226,6 @@ __device__ __forceinline__ void issue_stage(const DecodeArgs& a, const TmaMaps& 
                      a.v_scale + ((int64_t)t.page * a.Hkv + h) * kBlock, kRowScales,
                      &full[s], once);
   }
-  }  // bf16 and E4M3 pages
 }
 
 // issue_stage for the whole producer warp (every lane calls it with the same arguments).  A

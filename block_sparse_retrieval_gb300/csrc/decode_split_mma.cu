@@ -24,6 +24,70 @@
 namespace srkv {
 namespace {
 
+// One list of a 4-bit cache through the ring (the whole producer warp calls it): batches of 32
+// positions, one per lane, each lane finding its own unit, page and rows; the next batch is
+// resolved between the halves of this one, while the copies of the first half are in flight.
+template <int D>
+__device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned char* smem, int list,
+                                                 const ListRange& rg, Int4Place& pl,
+                                                 uint32_t& eflags, int lane) {
+  const uint32_t bank = list == kListB ? kBankB : 0u;
+  const int64_t npos = rg.end - rg.begin;
+  uint32_t dummy = 0;
+  auto geom = [&](int32_t u) {
+    return list == kListA ? unit_geom_a(a, u, dummy) : unit_geom(a, u, dummy);
+  };
+  auto count = [&](const Geom& g) { return list == kListA ? list_a_count(g) : g.ns; };
+  // the lane's position: unit u, its geometry, position j of its n
+  int32_t u = rg.u0;
+  int64_t j = rg.begin - rg.base0 + lane;
+  Geom g = geom(u);
+  int32_t n = count(g);
+  struct Item {
+    int32_t u;
+    uint32_t flags;
+    PageTask t;
+  };
+  auto resolve = [&](int64_t done) {
+    Item x;
+    x.u = 0;
+    x.flags = 0;
+    x.t.page = -1;
+    x.t.lo = x.t.hi = x.t.ie = x.t.ws = 0;
+    if (done + lane < npos) {
+      while (j >= n) {
+        j -= n;
+        g = geom(++u);
+        n = count(g);
+      }
+      x.u = u;
+      x.flags = bank | ((j == 0 || done + lane == 0) ? kNewUnit : 0u);
+      const int32_t* bt_r = a.block_table + (int64_t)(u / a.Hkv) * a.max_blocks;
+      // Early mode: the count the plan assumed must be the one the scoring wrote.
+      const int32_t written = list == kListB && a.early ? a.nsel[u] : g.ns;
+      x.t = list == kListA
+                ? resolve_a(g, (int32_t)j, bt_r, total_pages(a), eflags)
+                : resolve_b(g, (int32_t)j, a.sel + (int64_t)u * a.kmax, bt_r, total_pages(a),
+                            a.init_tokens, eflags);
+      if (list == kListB && (j >= written || (j == 0 && written != g.ns))) {
+        eflags |= SRKV_EFLAG_SELECTION;
+        if (j >= written) x.t.page = -1;
+      }
+      j += 32;
+    }
+    return x;
+  };
+  Item x = resolve(0);
+  for (int64_t done = 0; done < npos && !pl.abort; done += 32) {
+    const int cnt = npos - done < 32 ? (int)(npos - done) : 32;
+    const int half = cnt < 16 ? cnt : 16;
+    issue_batch_int4<D>(a, smem, pl, 0, half, x.u, x.flags, x.t, eflags, lane);
+    const Item next = resolve(done + 32);
+    issue_batch_int4<D>(a, smem, pl, half, cnt, x.u, x.flags, x.t, eflags, lane);
+    x = next;
+  }
+}
+
 // 128 registers: a quarter-SM register file (16K) then holds this CTA's three warps on one
 // sub-partition (12K) beside one warp of a combine CTA, so the combine is resident and
 // waiting when the last partial is written.
@@ -33,10 +97,6 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   using C = Cfg<D, Fmt>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  StageInfo* sInfo = reinterpret_cast<StageInfo*>(smem + C::kOffInfo);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* full_v = full + C::kStages;
-  uint64_t* empty = full_v + C::kStages;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // The combine may be scheduled once every CTA has passed this point (it waits for this
@@ -44,7 +104,12 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   // the previous kernel in the stream has finished, and the combine reads them too.
   if (!a.early && !a.wait_late) griddep_wait();
   griddep_launch_dependents();
-  if (tid == 0) init_ring<D, Fmt>(smem);
+  if (tid == 0) {
+    if constexpr (Fmt == kInt4Pages)
+      Int4Ring<D>{smem}.init(a.G <= 4);
+    else
+      init_ring<D, Fmt>(smem);
+  }
   __syncthreads();
 
   if (warp == kProducerWarp) {
@@ -53,6 +118,7 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
     bool abort = false;
     int64_t it = 0;     // stages handed out so far (uniform over the warp)
     int64_t armed = 0;  // stages lane 0 armed
+    Int4Place place;    // (4-bit pages keep theirs here)
     // Both lists are planned first: list B's counts are the selection counts, known from
     // the lengths alone in the early mode.  CTA 0 leaves each list's unit offsets for the
     // combine kernel.
@@ -72,6 +138,10 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
       const ListRange rg = rgs[list];
       const int64_t npos = rg.end - rg.begin;
       if (npos <= 0) continue;
+      if constexpr (Fmt == kInt4Pages) {
+        stream_list_int4<D>(a, smem, list, rg, place, eflags, lane);
+        abort = place.abort;
+      } else {
       const uint32_t bank = list == kListB ? kBankB : 0u;
       int32_t cu = rg.u0;  // walk state: unit and position within its list
       int64_t cj = rg.begin - rg.base0;
@@ -133,8 +203,13 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
           ++it;
         }
       }
+      }
     }
-    if (lane == 0) {
+    if constexpr (Fmt == kInt4Pages) {
+      finish_ring_int4<D>(a, smem, place, eflags, lane);
+    } else if (lane == 0) {
+      uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+      uint64_t* full_v = full + C::kStages;
       PageTask none;
       none.page = -1;
       none.lo = none.hi = none.ie = none.ws = 0;
@@ -154,17 +229,24 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   }
 
   // -------------------------------------------------------------------- consumers
-  // warp 0 writes the partial of (unit, this CTA) into the list's bank
-  auto write_partial = [&](const SoftmaxState<D>& st, const StageInfo& inf, Lane ln) {
-    const int64_t slot =
-        ((inf.flags & kBankB) ? (int64_t)a.lay.bank : 0) + inf.unit + blockIdx.x;
+  // the partial of (unit, this CTA) goes into the list's bank
+  auto write_partial = [&](const SoftmaxState<D>& st, int32_t unit, int32_t flags, Lane ln) {
+    const int64_t slot = ((flags & kBankB) ? (int64_t)a.lay.bank : 0) + unit + blockIdx.x;
     store_partial<D, Fmt>(reinterpret_cast<float*>(a.ws + a.lay.acc) + slot * a.G * D,
-                     reinterpret_cast<float*>(a.ws + a.lay.ml) + slot * a.G * 2, st, ln, a.G);
+                          reinterpret_cast<float*>(a.ws + a.lay.ml) + slot * a.G * 2, st, ln, a.G);
   };
-  if constexpr (Fmt == kInt4Pages)
-    consumer_loop_int4<D>(a, smem, lane, warp, write_partial);
-  else
-    consumer_loop<D, Fmt>(a, smem, lane, warp, write_partial);
+  if constexpr (Fmt == kInt4Pages) {
+    if (warp == kMergerWarp)
+      merger_loop_int4<D>(a, smem, lane, [&](const SoftmaxState<D>& st, const Int4Segment& sg,
+                                             Lane ln) { write_partial(st, sg.unit, sg.flags, ln); });
+    else
+      consumer_loop_int4<D>(a, smem, lane, warp < kProducerWarp ? warp : warp - 2);
+  } else {
+    consumer_loop<D, Fmt>(a, smem, lane, warp, [&](const SoftmaxState<D>& st, const StageInfo& inf,
+                                                   Lane ln) {
+      write_partial(st, inf.unit, inf.flags, ln);
+    });
+  }
 }
 
 }  // namespace
@@ -258,7 +340,7 @@ cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
       (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages) ||
        !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages)))
     return cudaErrorInvalidValue;
-  return launch_pdl(split_mma_kernel<D, Fmt>, dim3(a.ctas), dim3(kThreads),
+  return launch_pdl(split_mma_kernel<D, Fmt>, dim3(a.ctas), dim3(Cfg<D, Fmt>::kThreads),
                     Cfg<D, Fmt>::kSmemAlloc, stream, a, maps);
 }
 
