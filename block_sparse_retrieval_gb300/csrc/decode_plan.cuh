@@ -142,19 +142,35 @@ struct ListRange {
   int64_t base0;  // first position of unit u0
 };
 
+// Are the counts of a list the same for every kv head of a request?  List A's are, and list B's
+// while they come from the lengths (early).
+__device__ __forceinline__ bool count_per_request(const DecodeArgs& a, int list) {
+  return list == kListA || a.early;
+}
+
 // Warp-level plan of one list for CTA `c` of `C`; every lane returns the same range.  When
 // `offsets` is not null the list's unit offsets [U + 1] are written (used by the combine).
-// When `prefix` is not null, prefix[k] receives the first position of the units of lane k's
-// chunk (chunk = ceil(U / 32) units) and prefix[32] the total.
+// The lanes share the units in chunks of `per` units with one count (a request's kv heads where
+// they have the same count: the count's double-precision steps are then taken once a request).
 __device__ __forceinline__ ListRange warp_plan(const DecodeArgs& a, int list, int64_t c,
-                                               int64_t C, int64_t* offsets, int64_t* prefix,
-                                               uint32_t& eflags) {
+                                               int64_t C, int64_t* offsets, uint32_t& eflags) {
   const int lane = threadIdx.x & 31;
   const int32_t U = a.batch * a.Hkv;
-  const int32_t chunk = (U + 31) / 32;
-  const int32_t u_lo = min(U, lane * chunk), u_hi = min(U, u_lo + chunk);
+  const int32_t per = count_per_request(a, list) ? a.Hkv : 1;
+  const int32_t items = U / per;
+  const int32_t chunk = (items + 31) / 32;
+  const int32_t i_lo = min(items, lane * chunk), i_hi = min(items, i_lo + chunk);
+  constexpr int kCached = 4;  // counts a lane keeps for the second pass
+  int32_t cached[kCached] = {};
   int64_t local = 0;
-  for (int32_t u = u_lo; u < u_hi; ++u) local += list_count(a, list, u, eflags);
+#pragma unroll
+  for (int x = 0; x < kCached; ++x)
+    if (i_lo + x < i_hi) {
+      cached[x] = list_count(a, list, (i_lo + x) * per, eflags);
+      local += (int64_t)cached[x] * per;
+    }
+  for (int32_t i = i_lo + kCached; i < i_hi; ++i)
+    local += (int64_t)list_count(a, list, i * per, eflags) * per;
   int64_t incl = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -164,10 +180,6 @@ __device__ __forceinline__ ListRange warp_plan(const DecodeArgs& a, int list, in
   const int64_t excl = incl - local;
   ListRange rg;
   rg.T = __shfl_sync(0xffffffffu, incl, 31);
-  if (prefix) {
-    prefix[lane] = excl;
-    if (lane == 31) prefix[32] = rg.T;
-  }
   rg.begin = cta_begin(c < C ? c : C, rg.T, C);  // a CTA c >= C has no position
   rg.end = cta_begin(c < C ? c + 1 : C, rg.T, C);
   int32_t u0 = 0;
@@ -177,16 +189,21 @@ __device__ __forceinline__ ListRange warp_plan(const DecodeArgs& a, int list, in
     int64_t pos = excl;
     uint32_t dummy = 0;
     bool found = false;
-    for (int32_t u = u_lo; u < u_hi; ++u) {
-      const int32_t n = list_count(a, list, u, dummy);
-      if (offsets) offsets[u] = pos;
-      if (mine && !found && rg.begin < pos + n) {
-        u0 = u;
-        base0 = pos;
+    auto item = [&](int32_t i, int32_t n) {
+      if (offsets)
+        for (int32_t k = 0; k < per; ++k) offsets[i * per + k] = pos + (int64_t)k * n;
+      if (mine && !found && rg.begin < pos + (int64_t)n * per) {
+        const int32_t k = (int32_t)((rg.begin - pos) / n);  // n > 0: begin lies inside the item
+        u0 = i * per + k;
+        base0 = pos + (int64_t)k * n;
         found = true;
       }
-      pos += n;
-    }
+      pos += (int64_t)n * per;
+    };
+#pragma unroll
+    for (int x = 0; x < kCached; ++x)
+      if (i_lo + x < i_hi) item(i_lo + x, cached[x]);
+    for (int32_t i = i_lo + kCached; i < i_hi; ++i) item(i, list_count(a, list, i * per, dummy));
     if (offsets && lane == 31) offsets[U] = rg.T;
   }
   const uint32_t who = __ballot_sync(0xffffffffu, mine);

@@ -38,11 +38,21 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
     return list == kListA ? unit_geom_a(a, u, dummy) : unit_geom(a, u, dummy);
   };
   auto count = [&](const Geom& g) { return list == kListA ? list_a_count(g) : g.ns; };
-  // the lane's position: unit u, its geometry, position j of its n
+  // the lane's position: unit u, its geometry (one for all heads of a request where the count is),
+  // position j of its n
+  const bool per_request = count_per_request(a, list);
   int32_t u = rg.u0;
   int64_t j = rg.begin - rg.base0 + lane;
-  Geom g = geom(u);
-  int32_t n = count(g);
+  Geom g;
+  int32_t n = 0;
+  if (npos > 0) {
+    g = geom(u);
+    n = count(g);
+  }
+  // The selection must exist from here on.  (Every CTA waits, with positions or without: a kernel
+  // behind this one may then count on the scoring kernel's end.)
+  if (list == kListB && (a.early || a.wait_late)) griddep_wait();
+  if (npos <= 0) return;
   struct Item {
     int32_t u;
     uint32_t flags;
@@ -57,8 +67,11 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
     if (done + lane < npos) {
       while (j >= n) {
         j -= n;
-        g = geom(++u);
-        n = count(g);
+        ++u;
+        if (!per_request || u % a.Hkv == 0) {
+          g = geom(u);
+          n = count(g);
+        }
       }
       x.u = u;
       x.flags = bank | ((j == 0 || done + lane == 0) ? kNewUnit : 0u);
@@ -129,19 +142,20 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
                              ? reinterpret_cast<int64_t*>(a.ws + (list == kListA ? a.lay.off_a
                                                                                  : a.lay.off_b))
                              : nullptr;
-      rgs[list] = warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets, nullptr, eflags);
+      rgs[list] = warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets, eflags);
     }
     for (int list = kListA; list <= kListB && !abort; ++list) {
+      if constexpr (Fmt == kInt4Pages) {
+        stream_list_int4<D>(a, smem, list, rgs[list], place, eflags, lane);
+        abort = place.abort;
+        continue;
+      } else {
       // the selection (or, behind the shared-prefix kernel, that kernel's partials) must
       // exist from here on
       if (list == kListB && (a.early || a.wait_late)) griddep_wait();
       const ListRange rg = rgs[list];
       const int64_t npos = rg.end - rg.begin;
       if (npos <= 0) continue;
-      if constexpr (Fmt == kInt4Pages) {
-        stream_list_int4<D>(a, smem, list, rg, place, eflags, lane);
-        abort = place.abort;
-      } else {
       const uint32_t bank = list == kListB ? kBankB : 0u;
       int32_t cu = rg.u0;  // walk state: unit and position within its list
       int64_t cj = rg.begin - rg.base0;

@@ -54,8 +54,7 @@ __global__ void __launch_bounds__(kThreads) split_simt_kernel(const DecodeArgs a
                              ? reinterpret_cast<int64_t*>(a.ws + (list == kListA ? a.lay.off_a
                                                                                  : a.lay.off_b))
                              : nullptr;
-      const ListRange rg = warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets, nullptr,
-                                     eflags);
+      const ListRange rg = warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets, eflags);
       if (lane == 0) s_rg = rg;
     }
     __syncthreads();

@@ -3,7 +3,7 @@
 // A slab is one (page, kv head): 128 tokens of keys and values.  A row x of d values (one
 // token's key or value) is held as 4-bit codes with its own scale and minimum,
 //   lo = min x (bf16, exact),  scale = (max x - lo) / 15 rounded up to bf16,
-//   code = the integer nearest to (x - lo) / scale (the difference in fp32, ties to even),
+//   code = the integer nearest to (x - lo) / scale (difference and quotient in fp32, ties to even),
 // and stands for lo + code * scale.  Rounding the scale up keeps 15 * scale >= max x - lo, so no
 // code is clipped; it costs at most 2^-7 of the step.  One scale per row (as the E4M3 pages have)
 // because a row is what a decode step appends.  A constant row has scale 0.  A row that holds
@@ -55,37 +55,76 @@ __device__ __forceinline__ float int4_lo(uint32_t row) { return bf16_hi(row); }
 constexpr uint32_t kInt4BadRow = 0x7fc07fc0u;  // scale = lo = NaN
 
 // The row's word from its smallest and largest value (exact bf16 values; NaN or an infinity
-// among the row's values shows in one of them).
+// among the row's values shows in one of them).  The scale is the smallest bf16 whose 15-fold (exact
+// in fp32) reaches the range: range / 15 cut to bf16, or the next one.
 __device__ __forceinline__ uint32_t int4_row(float lo, float hi) {
-  const float s = __fdiv_rn(hi - lo, 15.f);
-  const uint32_t up = (__float_as_uint(s) + 0xffffu) & 0xffff0000u;  // s >= 0: towards +inf
-  const bool ok = fmaf(15.f, __uint_as_float(up), fabsf(lo)) < INFINITY;  // false for NaN too
-  return ok ? (up >> 16) | (__float_as_uint(lo) & 0xffff0000u) : kInt4BadRow;
+  const float range = hi - lo;
+  uint32_t s = __float_as_uint(range * (1.f / 15.f)) & 0xffff0000u;
+  if (15.f * __uint_as_float(s) < range) s += 0x10000u;
+  const bool ok = fmaf(15.f, __uint_as_float(s), fabsf(lo)) < INFINITY;  // false for NaN too
+  return ok ? (s >> 16) | (__float_as_uint(lo) & 0xffff0000u) : kInt4BadRow;
 }
 
-// Code of x in a row of that scale and minimum.  t = (x - lo) * inv (inv = 1 / scale in fp32) is
-// within 15 * 2^-22 of the quotient, so its nearest integer c is the quotient's unless the
-// quotient lies about half-way between two: then the remainder x - lo - c * scale decides.  It is
-// exact in fp32 (a multiple of the difference's last place, no larger than the scale).
-__device__ __forceinline__ uint32_t int4_code(float x, float lo, float scale, float inv) {
-  const float diff = __fsub_rn(x, lo);
-  const float t = __fmul_rn(diff, inv);
-  float c = rintf(t);
-  if (fabsf(t - c) > 0.4999f) {
-    const float r = fmaf(-c, scale, diff), half = 0.5f * scale;
-    const bool odd = (int)c & 1;
-    if (r > half || (r == half && odd)) c += 1.f;
-    if (r < -half || (r == -half && odd)) c -= 1.f;
-  }
-  c = fminf(fmaxf(c, 0.f), 15.f);  // NaN (a bad row) becomes 0
-  return (uint32_t)c;
-}
-
-// 1 / scale for int4_code; 0 for a constant or a bad row (every code is then 0).  A scale
-// below 2^-126 (only where a row's whole range is below 2^-122) has no finite reciprocal
-// of full precision: such a row is taken as constant, off by less than 2^-122.
+// About 1 / scale (2^-22 off at most); 0 for a constant or a bad row, and for a scale below 2^-126
+// (a row whose whole range is below 2^-122: taken as constant).
 __device__ __forceinline__ float int4_inv(float scale) {
-  return scale >= 1.17549435e-38f ? __fdiv_rn(1.f, scale) : 0.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+  return scale >= 1.17549435e-38f ? r : 0.f;
 }
+
+// Pairs of fp32 in one 64-bit register: one instruction for both.
+struct F32x2 {
+  uint64_t v;
+  __device__ __forceinline__ F32x2() {}
+  __device__ __forceinline__ F32x2(float x, float y) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  }
+  __device__ __forceinline__ void get(uint32_t& x, uint32_t& y) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+  }
+};
+__device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
+  F32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F32x2 mul2(F32x2 a, F32x2 b) {
+  F32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F32x2 fma2(F32x2 a, F32x2 b, F32x2 c) {
+  F32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// Codes of rows' values, a pair of bf16 at a time.
+struct Int4Coder {
+  F32x2 neg_lo, inv, neg_scale;
+  uint32_t keep;  // 0 for a bad row
+  __device__ __forceinline__ explicit Int4Coder(uint32_t row) {
+    const float s = int4_scale(row), lo = int4_lo(row), r = int4_inv(s);
+    neg_lo = F32x2(-lo, -lo);
+    inv = F32x2(r, r);
+    neg_scale = F32x2(-s, -s);
+    keep = row == kInt4BadRow ? 0u : 0x000f000fu;
+  }
+  // The pair's codes in the low nibbles of the result's halves.  t = (x - lo) * inv is a few ulps
+  // off the quotient; its remainder (exact) times inv corrects it to the nearest fp32, which is the
+  // quotient itself where fp32 holds it, a half-way case among them.  Adding 1.5 * 2^23 rounds to an
+  // integer, ties to even, and leaves it in the low bits.
+  __device__ __forceinline__ uint32_t pair(uint32_t bf16x2) const {
+    const F32x2 x(bf16_lo(bf16x2), bf16_hi(bf16x2));
+    const F32x2 diff = add2(x, neg_lo);
+    F32x2 t = mul2(diff, inv);
+    t = fma2(fma2(t, neg_scale, diff), inv, t);
+    t = add2(t, F32x2(12582912.f, 12582912.f));
+    uint32_t a, b;
+    t.get(a, b);
+    return __byte_perm(a, b, 0x5410) & keep;
+  }
+};
 
 }  // namespace srkv

@@ -17,9 +17,10 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Smallest and largest of a row's values held 8 per lane by LPR neighbouring lanes (NaN wins).
+// The word (scale, lo) of a row whose values are held 8 per lane by LPR neighbouring lanes.  The
+// smallest value and the largest one's negative go round as one pair (NaN wins).
 template <int LPR>
-__device__ __forceinline__ void row_range(const int4& w, float& lo, float& hi) {
+__device__ __forceinline__ uint32_t row_word(const int4& w) {
   const uint32_t u[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
   __nv_bfloat162 mn = as_bf162(u[0]), mx = mn;
 #pragma unroll
@@ -27,31 +28,34 @@ __device__ __forceinline__ void row_range(const int4& w, float& lo, float& hi) {
     mn = __hmin2_nan(mn, as_bf162(u[e]));
     mx = __hmax2_nan(mx, as_bf162(u[e]));
   }
+  const uint32_t neg = as_u32(mx) ^ 0x80008000u;
+  __nv_bfloat162 both = __hmin2_nan(as_bf162(__byte_perm(as_u32(mn), neg, 0x5410)),
+                                    as_bf162(__byte_perm(as_u32(mn), neg, 0x7632)));
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) {
-    mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mn), o)));
-    mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mx), o)));
-  }
-  lo = __bfloat162float(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn)));
-  hi = __bfloat162float(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx)));
+  for (int o = LPR / 2; o > 0; o >>= 1)
+    both = __hmin2_nan(both, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(both), o)));
+  return int4_row(bf16_lo(as_u32(both)), -bf16_hi(as_u32(both)));
 }
 
-// Codes of a lane's 8 values.
-__device__ __forceinline__ void lane_codes(const int4& w, uint32_t row, uint32_t (&c)[8]) {
-  const uint32_t u[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
-  const float lo = int4_lo(row), scale = int4_scale(row), inv = int4_inv(scale);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    c[2 * e] = int4_code(bf16_lo(u[e]), lo, scale, inv);
-    c[2 * e + 1] = int4_code(bf16_hi(u[e]), lo, scale, inv);
-  }
+// Codes of a lane's 8 values: pair p in the low nibbles of out[p]'s halves.
+__device__ __forceinline__ void lane_codes(const int4& w, uint32_t row, uint32_t (&out)[4]) {
+  const Int4Coder code(row);
+  out[0] = code.pair((uint32_t)w.x);
+  out[1] = code.pair((uint32_t)w.y);
+  out[2] = code.pair((uint32_t)w.z);
+  out[3] = code.pair((uint32_t)w.w);
+}
+
+// The key word of a lane's 8 codes.
+__device__ __forceinline__ uint32_t key_word(const uint32_t (&c)[4]) {
+  return c[0] | (c[1] << 4) | (c[2] << 8) | (c[3] << 12);
 }
 
 // Warp = 8 consecutive tokens (an octet) of one listed page and kv head, keys and values: d / 8
 // lanes a row with 8 values each (16-byte loads, all issued before the first is used).  A lane's
-// 8 key codes are one word.  Value words hold 8 tokens of one element: each lane first sets its
-// own tokens' nibbles in the words of its 8 elements, then the lanes that share those elements
-// exchange halves and OR them, each keeping its share of finished words.
+// 8 key codes are one word.  Value words hold 8 tokens of one element: each lane first joins its
+// own tokens' nibbles, pairs of elements in the halves of a register, then the lanes that share
+// those elements exchange them, each keeping its share of the words.
 // Bytes: 4 d read, d + 8 written a token.
 template <int D>
 __global__ void __launch_bounds__(kInt4Warps * 32)
@@ -89,46 +93,52 @@ __global__ void __launch_bounds__(kInt4Warps * 32)
   uint32_t* v_words = reinterpret_cast<uint32_t*>(slab + F::kVCodes);
   uint32_t* k_rows = reinterpret_cast<uint32_t*>(slab + F::kKRows);
   uint32_t* v_rows = reinterpret_cast<uint32_t*>(slab + F::kVRows);
-  uint32_t part[8] = {};
+  // part[p]: elements 2p (low half) and 2p + 1, this lane's tokens j at bit 4 (j / 2)
+  uint32_t part[4] = {};
 #pragma unroll
   for (int l = 0; l < LOADS; ++l) {
     const int j = l * RPL + sub, tok = o * 8 + j;
-    float lo, hi;
-    uint32_t c[8];
-    row_range<LPR>(kw[l], lo, hi);
-    uint32_t row = int4_row(lo, hi);
+    uint32_t c[4];
+    uint32_t row = row_word<LPR>(kw[l]);
     lane_codes(kw[l], row, c);
-    uint32_t word = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) word |= c[e] << int4_shift(e);
-    k_words[tok * F::kWordsPerRow + col / 8] = word;
+    k_words[tok * F::kWordsPerRow + col / 8] = key_word(c);
     if (col == 0) k_rows[tok] = row;
-    row_range<LPR>(vw[l], lo, hi);
-    row = int4_row(lo, hi);
+    row = row_word<LPR>(vw[l]);
     lane_codes(vw[l], row, c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[e] |= c[e] << int4_shift(j);
+    for (int p = 0; p < 4; ++p) part[p] |= c[p] << (4 * (l * RPL / 2));
     if (col == 0) v_rows[tok] = row;
   }
-  // Halve the elements and double the tokens, RPL times over: of `have` words each lane sends
-  // the half its partner keeps.
-  int first = 0;  // first of the lane's words, relative to col
+  int first = 0;  // first of the lane's elements, relative to col
+  if constexpr (RPL == 4) {  // tokens 2, 3, 6, 7 sit with the lanes 16 further on
+    const bool upper = (lane & 16) != 0;
 #pragma unroll
-  for (int have = 8, mask = 16; mask >= LPR; mask >>= 1, have >>= 1) {
-    const bool upper = (lane & mask) != 0;
+    for (int p = 0; p < 4; ++p) part[p] <<= upper ? 4 : 0;
 #pragma unroll
-    for (int e = 0; e < have / 2; ++e) {
-      const uint32_t send = upper ? part[e] : part[e + have / 2];
-      const uint32_t keep = upper ? part[e + have / 2] : part[e];
-      part[e] = keep | __shfl_xor_sync(0xffffffffu, send, mask);
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t send = upper ? part[p] : part[p + 2], keep = upper ? part[p + 2] : part[p];
+      part[p] = keep | __shfl_xor_sync(0xffffffffu, send, 16);
     }
-    first += upper ? have / 2 : 0;
+    first = upper ? 4 : 0;
   }
+  // even tokens (low halves of the words) sit with the lanes of even rows, odd ones LPR further on
+  constexpr int kOwn = RPL == 4 ? 1 : 2;  // pairs of elements a lane keeps
+  const bool odd = (sub & 1) != 0;
+  uint32_t word[2 * kOwn];
+#pragma unroll
+  for (int p = 0; p < kOwn; ++p) {
+    const uint32_t send = odd ? part[p] : part[p + kOwn], keep = odd ? part[p + kOwn] : part[p];
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, send, LPR);
+    const uint32_t even_tokens = odd ? got : keep, odd_tokens = odd ? keep : got;
+    word[2 * p] = __byte_perm(even_tokens, odd_tokens, 0x5410);
+    word[2 * p + 1] = __byte_perm(even_tokens, odd_tokens, 0x7632);
+  }
+  first += odd ? 2 * kOwn : 0;
   uint32_t* vd = v_words + int4_v_word<D>(o * 8, col + first);
   if constexpr (RPL == 2)
-    *reinterpret_cast<uint4*>(vd) = make_uint4(part[0], part[1], part[2], part[3]);
+    *reinterpret_cast<uint4*>(vd) = make_uint4(word[0], word[1], word[2], word[3]);
   else
-    *reinterpret_cast<uint2*>(vd) = make_uint2(part[0], part[1]);
+    *reinterpret_cast<uint2*>(vd) = make_uint2(word[0], word[1]);
 }
 
 // bf16 pair code * scale + lo of the pair of codes in the low nibbles of x's halves: 128 + code is
@@ -254,16 +264,12 @@ __global__ void __launch_bounds__(kAppendThreads)
     const int col = (lane % LPR) * 8;
     const __nv_bfloat16* x = (warp ? v_new : k_new) + ((int64_t)r * Hkv + h) * D + col;
     const int4 w = *reinterpret_cast<const int4*>(x);
-    float lo, hi;
-    row_range<LPR>(w, lo, hi);
-    const uint32_t row = int4_row(lo, hi);
-    uint32_t c[8];
+    const uint32_t row = row_word<LPR>(w);
+    uint32_t c[4];
     lane_codes(w, row, c);
     if (lane < LPR) {
       if (warp == 0) {
-        uint32_t word = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) word |= c[e] << int4_shift(e);
+        const uint32_t word = key_word(c);
         k_words[tok * LPR + lane] = word;
         new_k[lane] = word;
         if (lane == 0) {
@@ -275,7 +281,8 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           uint32_t* p = v_words + int4_v_word<D>(tok, col + e);
-          *p = (*p & ~(15u << sh)) | (c[e] << sh);
+          const uint32_t code = (e & 1) ? c[e / 2] >> 16 : c[e / 2] & 15u;
+          *p = (*p & ~(15u << sh)) | (code << sh);
         }
         if (lane == 0) v_rows[tok] = row;
       }

@@ -11,6 +11,7 @@ A configuration is a mapping with the keys of :data:`CFG_KEYS` (``dtype`` 0 = bf
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Mapping
 
@@ -613,16 +614,80 @@ def retrieval_decode_fp8(cfg: Mapping, q: torch.Tensor, k_fp8: torch.Tensor,
         "srkv_retrieval_decode_fp8")
 
 
+# The 4-bit cache's calls.  A decode step over it is a few microseconds of GPU time, so its marshalling is kept
+# lean: shapes are compared as tuples, pointers go as integers, equal configurations share a structure.
+
 def kv_int4_slab_bytes(cfg: Mapping) -> int:
     """Bytes of one (page, kv head) slab of a 4-bit cache."""
-    c = config(cfg)
-    return int(load().srkv_kv_int4_slab_bytes(ctypes.byref(c)))
+    return int(load().srkv_kv_int4_slab_bytes(ctypes.byref(config(cfg))))
 
 
-def _int4_cache(cfg: Mapping, t: torch.Tensor) -> int:
+_configs: dict[tuple, tuple] = {}
+_cfg_values = operator.itemgetter(*CFG_KEYS)
+
+
+def _cfg_ref(cfg: Mapping):
+    """config(cfg) by reference, one structure for equal values."""
+    key = _cfg_values(cfg)
+    got = _configs.get(key)
+    if got is None:
+        if len(_configs) >= 64:
+            _configs.clear()
+        c = Config(*key)
+        got = _configs[key] = (c, ctypes.byref(c))
+    return got[1]
+
+
+def _need(t: torch.Tensor, name: str, shape: tuple) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device all tensors of a call are on: the current one, on whose streams the library launches."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is a CUDA tensor of device {dev}, not of the current device")
+    return dev
+
+
+def _ptr(t: torch.Tensor | None, name: str, dtype: torch.dtype, dev: int) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_of(stream, dev: int) -> int:
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(dev)
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _int4_pages(cfg: Mapping, kv_int4: torch.Tensor) -> int:
     """Checks the shape of a 4-bit cache; returns its pages."""
-    _shape(t, "kv_int4", None, cfg["num_kv_heads"], kv_int4_slab_bytes(cfg))
-    return t.shape[0]
+    shape = kv_int4.shape
+    want = (cfg["num_kv_heads"], cfg["block_size"] * (cfg["head_dim"] + 8))
+    if len(shape) != 3 or shape[1:] != want:
+        raise ValueError(f"kv_int4 must have shape [*, {want[0]}, {want[1]}], got {list(shape)}")
+    return shape[0]
+
+
+def _bf16_pages(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor) -> int:
+    shape, want = k_cache.shape, (cfg["num_kv_heads"], cfg["block_size"], cfg["head_dim"])
+    if len(shape) != 4 or shape[1:] != want:
+        raise ValueError(f"k_cache must have shape [*, {', '.join(map(str, want))}], got {list(shape)}")
+    _need(v_cache, "v_cache", tuple(shape))
+    return shape[0]
 
 
 def quantize_kv_int4(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -631,20 +696,19 @@ def quantize_kv_int4(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_quantize_kv_int4: page page_ids[i] of the bf16 caches into page int4_page_ids[i] (None:
     page_ids[i]) of kv_int4, uint8 [pages][Hkv][kv_int4_slab_bytes(cfg)]."""
-    _, Hkv, S, d = _cache_dims(cfg)
-    _shape(k_cache, "k_cache", None, Hkv, S, d)
-    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
-    pages = _int4_cache(cfg, kv_int4)
+    pages, slabs = _bf16_pages(cfg, k_cache, v_cache), _int4_pages(cfg, kv_int4)
     _shape(page_ids, "page_ids", None)
-    _shape(int4_page_ids, "int4_page_ids", page_ids.numel())
-    c = config(cfg)
+    n = page_ids.shape[0]
+    if int4_page_ids is not None:
+        _need(int4_page_ids, "int4_page_ids", (n,))
+    dev = _device(k_cache, "k_cache")
     _check(load().srkv_quantize_kv_int4(
-        ctypes.byref(c), _dev(k_cache, "k_cache", torch.bfloat16),
-        _dev(v_cache, "v_cache", torch.bfloat16), k_cache.shape[0],
-        _dev(page_ids, "page_ids", torch.int32), page_ids.numel(),
-        _dev(kv_int4, "kv_int4", torch.uint8), pages,
-        _dev(int4_page_ids, "int4_page_ids", torch.int32),
-        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), "srkv_quantize_kv_int4")
+        _cfg_ref(cfg), _ptr(k_cache, "k_cache", torch.bfloat16, dev),
+        _ptr(v_cache, "v_cache", torch.bfloat16, dev), pages,
+        _ptr(page_ids, "page_ids", torch.int32, dev), n, _ptr(kv_int4, "kv_int4", torch.uint8, dev),
+        slabs, _ptr(int4_page_ids, "int4_page_ids", torch.int32, dev),
+        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
+        "srkv_quantize_kv_int4")
 
 
 def dequantize_kv_int4(cfg: Mapping, kv_int4: torch.Tensor, int4_page_ids: torch.Tensor,
@@ -653,19 +717,19 @@ def dequantize_kv_int4(cfg: Mapping, kv_int4: torch.Tensor, int4_page_ids: torch
                        error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_dequantize_kv_int4: page int4_page_ids[i] of kv_int4 into page page_ids[i] (None:
     int4_page_ids[i]) of the bf16 caches."""
-    _, Hkv, S, d = _cache_dims(cfg)
-    _shape(k_cache, "k_cache", None, Hkv, S, d)
-    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
-    pages = _int4_cache(cfg, kv_int4)
+    pages, slabs = _bf16_pages(cfg, k_cache, v_cache), _int4_pages(cfg, kv_int4)
     _shape(int4_page_ids, "int4_page_ids", None)
-    _shape(page_ids, "page_ids", int4_page_ids.numel())
-    c = config(cfg)
+    n = int4_page_ids.shape[0]
+    if page_ids is not None:
+        _need(page_ids, "page_ids", (n,))
+    dev = _device(kv_int4, "kv_int4")
     _check(load().srkv_dequantize_kv_int4(
-        ctypes.byref(c), _dev(kv_int4, "kv_int4", torch.uint8), pages,
-        _dev(int4_page_ids, "int4_page_ids", torch.int32), int4_page_ids.numel(),
-        _dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16),
-        k_cache.shape[0], _dev(page_ids, "page_ids", torch.int32),
-        _dev(error_flags, "error_flags", torch.int32), _stream(stream)),
+        _cfg_ref(cfg), _ptr(kv_int4, "kv_int4", torch.uint8, dev), slabs,
+        _ptr(int4_page_ids, "int4_page_ids", torch.int32, dev), n,
+        _ptr(k_cache, "k_cache", torch.bfloat16, dev),
+        _ptr(v_cache, "v_cache", torch.bfloat16, dev), pages,
+        _ptr(page_ids, "page_ids", torch.int32, dev),
+        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
         "srkv_dequantize_kv_int4")
 
 
@@ -675,22 +739,23 @@ def append_kv_int4(cfg: Mapping, k_new: torch.Tensor, v_new: torch.Tensor, kv_in
     """srkv_append_kv_int4: each request's new token (bf16 k_new, v_new: [B][Hkv][d]) quantised
     into position seq_lens[r] of a 4-bit cache, and that page's vector refreshed; the caller then
     advances seq_lens."""
-    _, Hkv, _, d = _cache_dims(cfg)
+    Hkv, d = cfg["num_kv_heads"], cfg["head_dim"]
     _shape(block_table, "block_table", None, None)
-    B = block_table.shape[0]
-    _shape(k_new, "k_new", B, Hkv, d)
-    _shape(v_new, "v_new", B, Hkv, d)
-    pages = _int4_cache(cfg, kv_int4)
-    _shape(seq_lens, "seq_lens", B)
+    B, max_blocks = block_table.shape
+    _need(k_new, "k_new", (B, Hkv, d))
+    _need(v_new, "v_new", (B, Hkv, d))
+    pages = _int4_pages(cfg, kv_int4)
+    _need(seq_lens, "seq_lens", (B,))
     _shape(reps, "reps", None, Hkv, d)
     _rows(reps, "reps", pages)
-    c = config(cfg)
+    dev = _device(k_new, "k_new")
     _check(load().srkv_append_kv_int4(
-        ctypes.byref(c), _dev(k_new, "k_new", torch.bfloat16),
-        _dev(v_new, "v_new", torch.bfloat16), _dev(kv_int4, "kv_int4", torch.uint8), pages,
-        _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-        _dev(seq_lens, "seq_lens", torch.int32), B, _dev(reps, "reps", torch.float32),
-        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), "srkv_append_kv_int4")
+        _cfg_ref(cfg), _ptr(k_new, "k_new", torch.bfloat16, dev),
+        _ptr(v_new, "v_new", torch.bfloat16, dev), _ptr(kv_int4, "kv_int4", torch.uint8, dev), pages,
+        _ptr(block_table, "block_table", torch.int32, dev), max_blocks,
+        _ptr(seq_lens, "seq_lens", torch.int32, dev), B, _ptr(reps, "reps", torch.float32, dev),
+        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
+        "srkv_append_kv_int4")
 
 
 def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
@@ -699,28 +764,30 @@ def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
                           nsel: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
                           error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_retrieval_decode_int4: the decode step over a 4-bit cache (bf16 query and output)."""
-    Hq, Hkv, _, d = _cache_dims(cfg)
+    Hq, Hkv, d = cfg["num_q_heads"], cfg["num_kv_heads"], cfg["head_dim"]
     _shape(block_table, "block_table", None, None)
     B, max_blocks = block_table.shape
-    _shape(q, "q", B, Hq, d)
-    pages = _int4_cache(cfg, kv_int4)
-    _shape(seq_lens, "seq_lens", B)
-    _shape(prompt_lens, "prompt_lens", B)
-    _shape(sel, "sel", B, Hkv, None)
-    _shape(nsel, "nsel", B, Hkv)
-    _shape(out, "out", B, Hq, d)
+    _need(q, "q", (B, Hq, d))
+    _need(out, "out", (B, Hq, d))
+    pages = _int4_pages(cfg, kv_int4)
+    _need(seq_lens, "seq_lens", (B,))
+    if prompt_lens is not None:
+        _need(prompt_lens, "prompt_lens", (B,))
+    kmax = sel.shape[-1] if sel.dim() else 0
+    _need(sel, "sel", (B, Hkv, kmax))
+    _need(nsel, "nsel", (B, Hkv))
     _shape(reps, "reps", None, Hkv, d)
     _rows(reps, "reps", pages)
-    c = config(cfg)
+    dev = _device(q, "q")
     _check(load().srkv_retrieval_decode_int4(
-        ctypes.byref(c), _dev(q, "q", torch.bfloat16), _dev(kv_int4, "kv_int4", torch.uint8),
-        _dev(reps, "reps", torch.float32), pages,
-        _dev(block_table, "block_table", torch.int32), max_blocks,
-        _dev(seq_lens, "seq_lens", torch.int32), _dev(prompt_lens, "prompt_lens", torch.int32),
-        B, _dev(sel, "sel", torch.int32), sel.shape[-1], _dev(nsel, "nsel", torch.int32),
-        _dev(out, "out", torch.bfloat16), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(),
-        _dev(error_flags, "error_flags", torch.int32), _stream(stream)),
+        _cfg_ref(cfg), _ptr(q, "q", torch.bfloat16, dev), _ptr(kv_int4, "kv_int4", torch.uint8, dev),
+        _ptr(reps, "reps", torch.float32, dev), pages,
+        _ptr(block_table, "block_table", torch.int32, dev), max_blocks,
+        _ptr(seq_lens, "seq_lens", torch.int32, dev),
+        _ptr(prompt_lens, "prompt_lens", torch.int32, dev), B, _ptr(sel, "sel", torch.int32, dev),
+        kmax, _ptr(nsel, "nsel", torch.int32, dev), _ptr(out, "out", torch.bfloat16, dev),
+        _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
+        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
         "srkv_retrieval_decode_int4")
 
 

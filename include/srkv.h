@@ -179,8 +179,8 @@ srkv_status srkv_quantize_kv_fp8(const srkv_config* cfg, const void* k_cache,
  * one buffer kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)] bytes, 16-byte aligned; the
  * slab of a (page, kv head) holds its 128 keys and values.  A row x (one token's d values) is held as
  *   lo = min x (bf16),  scale = (max x - lo) / 15 rounded up to bf16,
- *   code = the integer in 0 .. 15 nearest to (x - lo) / scale, ties to even (0 if scale is 0; the
- *          difference in fp32),
+ *   code = the integer in 0 .. 15 nearest to (x - lo) / scale, ties to even (0 if scale is 0;
+ *          difference and quotient in fp32),
  * and stands for lo + code * scale.  A row with an infinity or a NaN, or whose range passes fp32, gets
  * scale = lo = NaN and reads back as NaN.  The 128 d + 1024 bytes of a slab, in order (words are 32 bits;
  * code j of a word at bit 4 (j / 2) + 16 (j mod 2)):
@@ -397,7 +397,7 @@ srkv_status srkv_retrieval_decode_fp8(const srkv_config* cfg, const void* q, con
  * V values are lo + code * scale.  Both products take the codes as fp16 operands with fp32
  * accumulation; the query enters as fp16 times one power of two for the heads of a group (exact down
  * to 2^-25 of the group's largest magnitude, which must be below 2^101), each softmax weight as fp16
- * times its row's V scale (below 2^36), the scales and minima in fp32.  The selection comes from `reps`,
+ * times its row's V scale (below 2^120), the scales and minima in fp32.  The selection comes from `reps`,
  * as in the other calls.
  *   cfg->dtype = SRKV_BF16 (the query and the output), group <= 8, else SRKV_ERR_UNSUPPORTED;
  *   head_dim 64 or 128.  kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)].  A NaN row that is
