@@ -140,37 +140,21 @@ struct ListRange {
   int64_t end;    // one past its last
   int32_t u0;     // unit holding `begin`
   int64_t base0;  // first position of unit u0
+  // warp_plan_early only: what unit u0's geometry is made of
+  int32_t len0;   // its request's length, as given
+  int32_t ns0;    // its selection count (list B)
 };
-
-// Are the counts of a list the same for every kv head of a request?  List A's are, and list B's
-// while they come from the lengths (early).
-__device__ __forceinline__ bool count_per_request(const DecodeArgs& a, int list) {
-  return list == kListA || a.early;
-}
 
 // Warp-level plan of one list for CTA `c` of `C`; every lane returns the same range.  When
 // `offsets` is not null the list's unit offsets [U + 1] are written (used by the combine).
-// The lanes share the units in chunks of `per` units with one count (a request's kv heads where
-// they have the same count: the count's double-precision steps are then taken once a request).
 __device__ __forceinline__ ListRange warp_plan(const DecodeArgs& a, int list, int64_t c,
                                                int64_t C, int64_t* offsets, uint32_t& eflags) {
   const int lane = threadIdx.x & 31;
   const int32_t U = a.batch * a.Hkv;
-  const int32_t per = count_per_request(a, list) ? a.Hkv : 1;
-  const int32_t items = U / per;
-  const int32_t chunk = (items + 31) / 32;
-  const int32_t i_lo = min(items, lane * chunk), i_hi = min(items, i_lo + chunk);
-  constexpr int kCached = 4;  // counts a lane keeps for the second pass
-  int32_t cached[kCached] = {};
+  const int32_t chunk = (U + 31) / 32;
+  const int32_t u_lo = min(U, lane * chunk), u_hi = min(U, u_lo + chunk);
   int64_t local = 0;
-#pragma unroll
-  for (int x = 0; x < kCached; ++x)
-    if (i_lo + x < i_hi) {
-      cached[x] = list_count(a, list, (i_lo + x) * per, eflags);
-      local += (int64_t)cached[x] * per;
-    }
-  for (int32_t i = i_lo + kCached; i < i_hi; ++i)
-    local += (int64_t)list_count(a, list, i * per, eflags) * per;
+  for (int32_t u = u_lo; u < u_hi; ++u) local += list_count(a, list, u, eflags);
   int64_t incl = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -189,28 +173,114 @@ __device__ __forceinline__ ListRange warp_plan(const DecodeArgs& a, int list, in
     int64_t pos = excl;
     uint32_t dummy = 0;
     bool found = false;
-    auto item = [&](int32_t i, int32_t n) {
-      if (offsets)
-        for (int32_t k = 0; k < per; ++k) offsets[i * per + k] = pos + (int64_t)k * n;
-      if (mine && !found && rg.begin < pos + (int64_t)n * per) {
-        const int32_t k = (int32_t)((rg.begin - pos) / n);  // n > 0: begin lies inside the item
-        u0 = i * per + k;
-        base0 = pos + (int64_t)k * n;
+    for (int32_t u = u_lo; u < u_hi; ++u) {
+      const int32_t n = list_count(a, list, u, dummy);
+      if (offsets) offsets[u] = pos;
+      if (mine && !found && rg.begin < pos + n) {
+        u0 = u;
+        base0 = pos;
         found = true;
       }
-      pos += (int64_t)n * per;
-    };
-#pragma unroll
-    for (int x = 0; x < kCached; ++x)
-      if (i_lo + x < i_hi) item(i_lo + x, cached[x]);
-    for (int32_t i = i_lo + kCached; i < i_hi; ++i) item(i, list_count(a, list, i * per, dummy));
+      pos += n;
+    }
     if (offsets && lane == 31) offsets[U] = rg.T;
   }
   const uint32_t who = __ballot_sync(0xffffffffu, mine);
   const int src = who ? __ffs(who) - 1 : 0;
   rg.u0 = __shfl_sync(0xffffffffu, u0, src);
   rg.base0 = __shfl_sync(0xffffffffu, base0, src);
+  rg.len0 = rg.ns0 = 0;
   return rg;
+}
+
+// Length and prompt of the first request of the lane's chunk, loaded ahead of the plans so that
+// the latency is spent on the kernel's set-up.
+struct PlanLens {
+  int32_t len, prompt;
+};
+
+__device__ __forceinline__ PlanLens plan_lens(const DecodeArgs& a) {
+  const int32_t i = (int32_t)(threadIdx.x & 31) * ((a.batch + 31) / 32);
+  PlanLens p;
+  p.len = i < a.batch ? a.seq_lens[i] : 0;
+  p.prompt = i < a.batch && a.prompt_lens ? a.prompt_lens[i] : p.len;
+  return p;
+}
+
+// warp_plan when the selection counts come from the lengths (early): every kv head of a request
+// has the same count, so a lane's chunk is of requests.  One list at a time, so that list B's
+// counts (double-precision steps) are made while list A's first pages are on their way.
+__device__ __forceinline__ ListRange warp_plan_early(const DecodeArgs& a, int list, int64_t c,
+                                                     const PlanLens& pre, int64_t* offsets,
+                                                     uint32_t& eflags) {
+  const int lane = threadIdx.x & 31;
+  const int32_t B = a.batch, H = a.Hkv;
+  const int32_t chunk = (B + 31) / 32;
+  const int32_t i_lo = min(B, lane * chunk), i_hi = min(B, i_lo + chunk);
+  int32_t len = pre.len;
+  auto count = [&](int32_t i, uint32_t& fl) {
+    int32_t prompt = pre.prompt;
+    if (i != i_lo) {
+      len = a.seq_lens[i];
+      prompt = a.prompt_lens ? a.prompt_lens[i] : len;
+    } else {
+      len = pre.len;
+    }
+    if (list == kListB)
+      return selection_count(len, prompt, a.max_blocks, a.kmax, a.init_tokens, a.local_tokens,
+                             a.dense_boundary, a.topk_percent)
+          .k;
+    Geom g = make_geom(len, 0, a.max_blocks, a.kmax, a.init_tokens, a.local_tokens, fl);
+    g.pb = prefix_of(g, a.prefix_blocks);
+    return list_a_count(g);
+  };
+  int32_t n = i_lo < i_hi ? count(i_lo, eflags) : 0;  // (kept where the chunk is one request)
+  int64_t local = n;
+#pragma unroll 1
+  for (int32_t i = i_lo + 1; i < i_hi; ++i) local += count(i, eflags);
+  local *= H;
+  int64_t incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int64_t C = list_ctas(a, list), excl = incl - local;
+  ListRange r;
+  r.T = __shfl_sync(0xffffffffu, incl, 31);
+  r.begin = cta_begin(c < C ? c : C, r.T, C);  // a CTA c >= C has no position
+  r.end = cta_begin(c < C ? c + 1 : C, r.T, C);
+  int32_t u0 = 0, len0 = 0, ns0 = 0;
+  int64_t base0 = 0;
+  const bool mine = r.begin < r.end && excl <= r.begin && r.begin < excl + local;
+  if (mine || offsets) {
+    int64_t pos = excl;
+    uint32_t dummy = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int32_t i = i_lo; i < i_hi; ++i) {
+      if (chunk > 1) n = count(i, dummy);
+      if (offsets)
+        for (int32_t k = 0; k < H; ++k) offsets[(int64_t)i * H + k] = pos + (int64_t)k * n;
+      if (mine && !found && r.begin < pos + (int64_t)n * H) {
+        const int32_t k = (int32_t)quotient(r.begin - pos, n);  // n > 0: begin lies inside
+        u0 = i * H + k;
+        base0 = pos + (int64_t)k * n;
+        len0 = len;
+        ns0 = n;
+        found = true;
+      }
+      pos += (int64_t)n * H;
+    }
+    if (offsets && lane == 31) offsets[(int64_t)B * H] = r.T;
+  }
+  const uint32_t who = __ballot_sync(0xffffffffu, mine);
+  const int src = who ? __ffs(who) - 1 : 0;
+  r.u0 = __shfl_sync(0xffffffffu, u0, src);
+  r.base0 = __shfl_sync(0xffffffffu, base0, src);
+  r.len0 = __shfl_sync(0xffffffffu, len0, src);
+  r.ns0 = __shfl_sync(0xffffffffu, ns0, src);
+  return r;
 }
 
 }  // namespace srkv

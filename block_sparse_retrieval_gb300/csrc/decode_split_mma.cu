@@ -26,7 +26,8 @@ namespace {
 
 // One list of a 4-bit cache through the ring (the whole producer warp calls it): batches of 32
 // positions, one per lane, each lane finding its own unit, page and rows; the next batch is
-// resolved between the halves of this one, while the copies of the first half are in flight.
+// resolved between the halves of this one, while the copies of the first half are in flight.  (Always
+// behind the scoring kernel, in the early mode.)
 template <int D>
 __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned char* smem, int list,
                                                  const ListRange& rg, Int4Place& pl,
@@ -38,20 +39,15 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
     return list == kListA ? unit_geom_a(a, u, dummy) : unit_geom(a, u, dummy);
   };
   auto count = [&](const Geom& g) { return list == kListA ? list_a_count(g) : g.ns; };
-  // the lane's position: unit u, its geometry (one for all heads of a request where the count is),
-  // position j of its n
-  const bool per_request = count_per_request(a, list);
+  // the lane's position: unit u, its geometry (one for all heads of a request), position j of its n
   int32_t u = rg.u0;
   int64_t j = rg.begin - rg.base0 + lane;
-  Geom g;
-  int32_t n = 0;
-  if (npos > 0) {
-    g = geom(u);
-    n = count(g);
-  }
+  Geom g = make_geom(rg.len0, list == kListA ? 0 : rg.ns0, a.max_blocks, a.kmax, a.init_tokens,
+                     a.local_tokens, dummy);
+  int32_t n = count(g);
   // The selection must exist from here on.  (Every CTA waits, with positions or without: a kernel
   // behind this one may then count on the scoring kernel's end.)
-  if (list == kListB && (a.early || a.wait_late)) griddep_wait();
+  if (list == kListB) griddep_wait();
   if (npos <= 0) return;
   struct Item {
     int32_t u;
@@ -68,7 +64,7 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
       while (j >= n) {
         j -= n;
         ++u;
-        if (!per_request || u % a.Hkv == 0) {
+        if (u % a.Hkv == 0) {
           g = geom(u);
           n = count(g);
         }
@@ -76,8 +72,8 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
       x.u = u;
       x.flags = bank | ((j == 0 || done + lane == 0) ? kNewUnit : 0u);
       const int32_t* bt_r = a.block_table + (int64_t)(u / a.Hkv) * a.max_blocks;
-      // Early mode: the count the plan assumed must be the one the scoring wrote.
-      const int32_t written = list == kListB && a.early ? a.nsel[u] : g.ns;
+      // The count the plan assumed must be the one the scoring wrote.
+      const int32_t written = list == kListB ? a.nsel[u] : g.ns;
       x.t = list == kListA
                 ? resolve_a(g, (int32_t)j, bt_r, total_pages(a), eflags)
                 : resolve_b(g, (int32_t)j, a.sel + (int64_t)u * a.kmax, bt_r, total_pages(a),
@@ -117,6 +113,8 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   // the previous kernel in the stream has finished, and the combine reads them too.
   if (!a.early && !a.wait_late) griddep_wait();
   griddep_launch_dependents();
+  PlanLens pre;
+  if (warp == kProducerWarp && a.early) pre = plan_lens(a);
   if (tid == 0) {
     if constexpr (Fmt == kInt4Pages)
       Int4Ring<D>{smem}.init(a.G <= 4);
@@ -132,21 +130,25 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
     int64_t it = 0;     // stages handed out so far (uniform over the warp)
     int64_t armed = 0;  // stages lane 0 armed
     Int4Place place;    // (4-bit pages keep theirs here)
+    // CTA 0 leaves each list's unit offsets for the combine kernel.
+    const bool leave = blockIdx.x == 0;
+    int64_t* const offsets[2] = {
+        leave ? reinterpret_cast<int64_t*>(a.ws + a.lay.off_a) : nullptr,
+        leave ? reinterpret_cast<int64_t*>(a.ws + a.lay.off_b) : nullptr};
     // Both lists are planned first: list B's counts are the selection counts, known from
-    // the lengths alone in the early mode.  CTA 0 leaves each list's unit offsets for the
-    // combine kernel.
+    // the lengths alone in the early mode.
     ListRange rgs[2];
+    if constexpr (Fmt != kInt4Pages) {
 #pragma unroll
-    for (int list = kListA; list <= kListB; ++list) {
-      int64_t* offsets = blockIdx.x == 0
-                             ? reinterpret_cast<int64_t*>(a.ws + (list == kListA ? a.lay.off_a
-                                                                                 : a.lay.off_b))
-                             : nullptr;
-      rgs[list] = warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets, eflags);
+      for (int list = kListA; list <= kListB; ++list)
+        rgs[list] = a.early ? warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags)
+                            : warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets[list],
+                                        eflags);
     }
     for (int list = kListA; list <= kListB && !abort; ++list) {
-      if constexpr (Fmt == kInt4Pages) {
-        stream_list_int4<D>(a, smem, list, rgs[list], place, eflags, lane);
+      if constexpr (Fmt == kInt4Pages) {  // always early; list B is planned once list A is out
+        const ListRange rg = warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags);
+        stream_list_int4<D>(a, smem, list, rg, place, eflags, lane);
         abort = place.abort;
         continue;
       } else {
