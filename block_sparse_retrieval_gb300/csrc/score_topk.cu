@@ -52,8 +52,12 @@ struct ScoreArgs {
 };
 
 // Grid: one cluster of `cluster_size()` CTAs per (request, kv head) unit.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 4) score_topk_kernel(ScoreArgs a) {
+// kLarge: shares of more than 128 candidates a CTA, 16 a round of loads and warp (two CTAs an SM
+// at most); smaller shares take 8 a round and keep room for four CTAs.  16 ragged requests of
+// 32k-128k (960 candidates a CTA): a 4-bit step 100.0 -> 96.4 us; 64 requests of 8192 (55 a CTA):
+// 56.6 -> 62.5 us with the large rounds.
+template <typename T, int D, bool kLarge>
+__global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(ScoreArgs a) {
   extern __shared__ uint32_t smem[];
   uint32_t* keys = smem;                                             // [max_blocks], leader
   int32_t* pages = reinterpret_cast<int32_t*>(smem + a.max_blocks);  // [max_blocks]
@@ -119,9 +123,9 @@ __global__ void __launch_bounds__(kThreads, 4) score_topk_kernel(ScoreArgs a) {
 
   // 2. scores of the share, one warp per candidate, into the leader's keys and histogram
   cluster_wait();
-  eflags |= score_share<D, kWarps>(qbar, pages, s_lo, min(s_hi, n), a.reps, a.num_pages, a.Hkv,
-                                   h, keys, &hist[0][0], nullptr, nullptr, warp, lane, [] {},
-                                   [](uint32_t) {});
+  eflags |= score_share<D, kWarps, 8, kLarge ? 16 : 8>(
+      qbar, pages, s_lo, min(s_hi, n), a.reps, a.num_pages, a.Hkv, h, keys, &hist[0][0], nullptr,
+      nullptr, warp, lane, [] {}, [](uint32_t) {});
   if (lane == 0 && eflags) raise_flags(a.error_flags, eflags);
   cluster_sync();  // every key and the pass-0 histogram are in the leader
   if (crank != 0) return;
@@ -195,11 +199,11 @@ __global__ void __launch_bounds__(kThreads, 4) score_topk_kernel(ScoreArgs a) {
   if (lane == 0) a.nsel[u] = total;
 }
 
-template <typename T, int D>
-cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, cudaStream_t s) {
+template <typename T, int D, bool kLarge>
+cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cudaStream_t s) {
   size_t smem = sizeof(uint32_t) * 2 * (size_t)a.max_blocks;
   if (smem < (size_t)kScoreExclusiveSmem) smem = kScoreExclusiveSmem;
-  auto kernel = score_topk_kernel<T, D>;
+  auto kernel = score_topk_kernel<T, D, kLarge>;
   // Once per device: the largest dynamic shared memory the host checks allow, and the full
   // shared-memory carveout, so that an SM running this kernel keeps room for a decode CTA
   // launched early behind it (programmatic launch).
@@ -233,6 +237,12 @@ cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, cudaStrea
   lc.attrs = attr;
   lc.numAttrs = 2;
   return cudaLaunchKernelEx(&lc, kernel, a);
+}
+
+template <typename T, int D>
+cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, cudaStream_t s) {
+  return (a.nmax + cluster - 1) / cluster > 128 ? launch_share<T, D, true>(a, units, cluster, s)
+                                                : launch_share<T, D, false>(a, units, cluster, s);
 }
 
 // Candidates of the longest request the block table allows.
