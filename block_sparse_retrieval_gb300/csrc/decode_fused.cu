@@ -490,9 +490,45 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
           if (lane == 0) {
             fast_flag[0] = bd.cnt <= kBinRank;
             fast_flag[1] = bd.digit;
+            fast_flag[2] = bd.above;
           }
         }
         bar();
+        int shift = 32 - kHistBits;  // of the bin's digit
+        if constexpr (Fmt == kInt4Pages) {
+          // Scores with a large common part share their top 12 bits: then the next 12 bits of the
+          // bin's keys are counted, and the bin of 24 bits is ranked instead.  (A 4-bit step of
+          // 65 536 tokens waits for the selection: the radix passes cost it 3 us more.  Not for the
+          // other formats, whose pools would come in another order.)
+          if (!fast_flag[0]) {
+            const uint32_t top = (uint32_t)fast_flag[1];
+            const int32_t above = fast_flag[2];
+            int4* h4 = reinterpret_cast<int4*>(hist12);
+            for (int i = tid; i < kBins / 4; i += kSelThreads) h4[i] = make_int4(0, 0, 0, 0);
+            bar();
+            for (int32_t i = tid; i < n; i += kSelThreads) {
+              const uint32_t key = keys[i];
+              if (key >> shift == top) {
+                atomicAdd(&hist12[(key >> (shift - kHistBits)) & (kBins - 1)], 1);
+                atomicAdd(&hist[1][(key >> (shift - 8)) & 255u], 1);
+              }
+            }
+            bar();
+            if (warp == 0) {
+              const Boundary bd = warp_boundary(&hist[1][0], hist12, k - above, lane);
+              if (lane == 0) {
+                fast_flag[0] = bd.cnt <= kBinRank;
+                fast_flag[1] = (int32_t)(top << kHistBits) | bd.digit;
+              }
+            }
+            bar();
+            shift -= kHistBits;
+            if (!fast_flag[0]) {  // many equal scores: the radix passes, which expect zeros there
+              hist[1][tid] = 0;
+              bar();
+            }
+          }
+        }
         if (fast_flag[0]) {
           constexpr int kRounds = kMaxCand / 32 / kConsumerWarps;  // a warp's rounds at most
           const uint32_t lt = (1u << lane) - 1u;
@@ -508,7 +544,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
 #pragma unroll
           for (int x = 0; x < kRounds; ++x) {
             const int32_t rr = warp + kConsumerWarps * x, i = 32 * rr + lane;
-            const uint32_t dg = kk[x] >> (32 - kHistBits);
+            const uint32_t dg = kk[x] >> shift;
             ma[x] = __ballot_sync(0xffffffffu, i < n && dg > dsel);
             mb[x] = __ballot_sync(0xffffffffu, i < n && dg == dsel);
             if (lane == 0 && 32 * rr < n) {
@@ -535,7 +571,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
               // rank key: the key's low bits (its top bits are the bin's), then the lower
               // block; unique, larger = kept first
               bnd[sb] = i;
-              bin_key[sb] = ((kk[x] & ((1u << (32 - kHistBits)) - 1u)) << 10) |
+              bin_key[sb] = ((kk[x] & ((1u << shift) - 1u)) << 10) |
                             (uint32_t)(kMaxCand - 1 - i);
             }
           }
