@@ -18,8 +18,10 @@ namespace {
 
 
 constexpr int kWarps = 4;
-constexpr int kPartsPerWarp = 16;
-constexpr int kRound = kWarps * kPartsPerWarp;  // partials fetched per round of loads
+// Partials a warp fetches per round of loads.  Behind the 4-bit decode 8: its CTAs hold more registers
+// than the other formats' (14 warps), so a combine CTA of 16 could not wait beside one, and units have
+// fewer partials (13 ragged requests at d 64: a step 27.8 -> 25.8 us).
+constexpr int kParts = 16, kInt4Parts = 8;
 constexpr int32_t kDirectUnits = 64;            // up to here the offsets are derived
 
 // Where the partials of unit u in one list are: the list has T positions, the unit's are
@@ -129,8 +131,10 @@ __device__ __forceinline__ void store_vec<__nv_bfloat16>(__nv_bfloat16* p, const
 // every round i: lane l owns d elements [l V, l V + V) (V = d / 32) of each part, lanes
 // 0..15 hold the parts' (m, l) pairs and the weights go round by shuffles.  The four warp
 // results are merged through shared memory by warp 0.
-template <typename TOut, int D>
-__global__ void __launch_bounds__(kWarps * 32) combine_kernel(const DecodeArgs a) {
+template <typename TOut, int D, int kPartsPerWarp>
+__global__ void __launch_bounds__(kWarps * 32)
+    __maxnreg__(kPartsPerWarp == kParts ? 128 : 96) combine_kernel(const DecodeArgs a) {
+  constexpr int kRound = kWarps * kPartsPerWarp;  // partials fetched per round of loads
   constexpr int V = D / 32;  // 4 (d 128) or 2 (d 64)
   __shared__ float s_acc[kWarps][D];
   __shared__ float s_ml[kWarps][2];
@@ -245,8 +249,10 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(const DecodeArgs a
 // partials per head), so one CTA per unit with one warp per query head (G warps) merges them,
 // 16 partials per round of loads, with no cross-warp merge; the unit's offsets are found once
 // per CTA.  (The kernel above spends 4 warps per head, for heads with many partials.)
-template <typename TOut, int D>
-__global__ void __launch_bounds__(256) combine_unit_kernel(const DecodeArgs a) {
+template <typename TOut, int D, int kPartsPerWarp>
+__global__ void __launch_bounds__(256)
+    __maxnreg__(kPartsPerWarp == kParts ? 128 : D == 128 ? 80 : 64)
+    combine_unit_kernel(const DecodeArgs a) {
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;  // warp j: query head j
   const int32_t G = a.G;
@@ -320,25 +326,28 @@ __global__ void __launch_bounds__(256) combine_unit_kernel(const DecodeArgs a) {
   store_vec<TOut>(out, v, V);
 }
 
-cudaError_t launch_combine(const DecodeArgs& a, int32_t dtype, cudaStream_t stream) {
+template <typename TOut, int D, int kPartsPerWarp>
+cudaError_t launch_parts(const DecodeArgs& a, cudaStream_t stream) {
   const int64_t units = (int64_t)a.batch * a.Hkv;
-  if (units > kDirectUnits && units >= a.ctas && a.G <= 8) {
-    const dim3 grid((unsigned)units), block((unsigned)(a.G * 32));
-    if (dtype == SRKV_BF16)
-      return a.d == 128 ? launch_pdl(combine_unit_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, a)
-                        : launch_pdl(combine_unit_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, a);
-    return a.d == 128 ? launch_pdl(combine_unit_kernel<float, 128>, grid, block, 0, stream, a)
-                      : launch_pdl(combine_unit_kernel<float, 64>, grid, block, 0, stream, a);
-  }
-  const int64_t heads = (int64_t)a.batch * a.Hkv * a.G;
+  if (units > kDirectUnits && units >= a.ctas && a.G <= 8)
+    return launch_pdl(combine_unit_kernel<TOut, D, kPartsPerWarp>, dim3((unsigned)units),
+                      dim3((unsigned)(a.G * 32)), 0, stream, a);
+  const int64_t heads = units * a.G;
   if (heads == 0) return cudaSuccess;
   if (heads > INT32_MAX) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)heads);
+  return launch_pdl(combine_kernel<TOut, D, kPartsPerWarp>, dim3((unsigned)heads),
+                    dim3(kWarps * 32), 0, stream, a);
+}
+
+cudaError_t launch_combine(const DecodeArgs& a, int32_t dtype, cudaStream_t stream) {
+  if (a.int4)
+    return a.d == 128 ? launch_parts<__nv_bfloat16, 128, kInt4Parts>(a, stream)
+                      : launch_parts<__nv_bfloat16, 64, kInt4Parts>(a, stream);
   if (dtype == SRKV_BF16)
-    return a.d == 128 ? launch_pdl(combine_kernel<__nv_bfloat16, 128>, grid, dim3(kWarps * 32), 0, stream, a)
-                      : launch_pdl(combine_kernel<__nv_bfloat16, 64>, grid, dim3(kWarps * 32), 0, stream, a);
-  return a.d == 128 ? launch_pdl(combine_kernel<float, 128>, grid, dim3(kWarps * 32), 0, stream, a)
-                    : launch_pdl(combine_kernel<float, 64>, grid, dim3(kWarps * 32), 0, stream, a);
+    return a.d == 128 ? launch_parts<__nv_bfloat16, 128, kParts>(a, stream)
+                      : launch_parts<__nv_bfloat16, 64, kParts>(a, stream);
+  return a.d == 128 ? launch_parts<float, 128, kParts>(a, stream)
+                    : launch_parts<float, 64, kParts>(a, stream);
 }
 
 }  // namespace srkv

@@ -225,7 +225,9 @@ __global__ void __launch_bounds__(kInt4Warps * 32)
 // block_table[r][L / 128], and the page's representation vector the fp32 mean of its keys as
 // they now stand (lo + code * scale over rows [0, L % 128]): the rows say all there is, so a
 // token written again, or after the length was set back, gives the same vector.  Thread =
-// (row group, word): fixed order of sums.
+// (row group, word): fixed order of sums.  Bound by its chain of dependent loads (length, page id,
+// page): the new rows are loaded beside the length and the page's earlier rows beside their
+// quantisation, so the chain has three links.
 constexpr int kAppendThreads = 256;
 
 template <int D>
@@ -236,8 +238,9 @@ __global__ void __launch_bounds__(kAppendThreads)
                           int32_t max_blocks, const int32_t* __restrict__ seq_lens, int32_t Hkv,
                           float* __restrict__ reps, int32_t* error_flags) {
   using F = Int4Slab<D>;
-  constexpr int LPR = D / 8;                      // words (and lanes) per row
-  constexpr int kGroups = kAppendThreads / LPR;   // row groups
+  constexpr int LPR = D / 8;                     // words (and lanes) per row
+  constexpr int kGroups = kAppendThreads / LPR;  // row groups
+  constexpr int kRows = kBlock / kGroups;        // rows per thread at most
   __shared__ float part[kGroups][D];
   __shared__ uint32_t new_k[LPR], new_row;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -245,6 +248,10 @@ __global__ void __launch_bounds__(kAppendThreads)
   griddep_wait();  // programmatic launch: the inputs may be the previous kernel's outputs
   griddep_launch_dependents();
   const int32_t L = seq_lens[r];
+  int4 x = make_int4(0, 0, 0, 0);
+  const int col = (lane % LPR) * 8;
+  if (warp < 2)  // warp 0: the key, warp 1: the value; lanes past the row repeat it
+    x = *reinterpret_cast<const int4*>((warp ? v_new : k_new) + ((int64_t)r * Hkv + h) * D + col);
   if (L < 0 || (int64_t)L >= (int64_t)max_blocks * kBlock) {
     if (tid == 0 && h == 0) raise_flags(error_flags, SRKV_EFLAG_SEQ_LEN);
     return;
@@ -260,13 +267,25 @@ __global__ void __launch_bounds__(kAppendThreads)
   uint32_t* v_words = reinterpret_cast<uint32_t*>(slab + F::kVCodes);
   uint32_t* k_rows = reinterpret_cast<uint32_t*>(slab + F::kKRows);
   uint32_t* v_rows = reinterpret_cast<uint32_t*>(slab + F::kVRows);
-  if (warp < 2) {  // warp 0: the key, warp 1: the value; lanes past the row repeat it
-    const int col = (lane % LPR) * 8;
-    const __nv_bfloat16* x = (warp ? v_new : k_new) + ((int64_t)r * Hkv + h) * D + col;
-    const int4 w = *reinterpret_cast<const int4*>(x);
-    const uint32_t row = row_word<LPR>(w);
+  // the earlier rows of the page (row tok comes from shared memory)
+  const int wi = tid % LPR, grp = tid / LPR;
+  uint32_t words[kRows], rows[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int t = grp + i * kGroups;
+    words[i] = t < tok ? k_words[t * LPR + wi] : 0u;
+    rows[i] = t < tok ? k_rows[t] : 0u;
+  }
+  if (warp < 2) {
+    uint32_t* p = v_words + int4_v_word<D>(tok, col);  // elements col .. + 3; the next 4 16 words on
+    uint4 va, vb;
+    if (warp == 1) {
+      va = *reinterpret_cast<const uint4*>(p);
+      vb = *reinterpret_cast<const uint4*>(p + 16);
+    }
+    const uint32_t row = row_word<LPR>(x);
     uint32_t c[4];
-    lane_codes(w, row, c);
+    lane_codes(x, row, c);
     if (lane < LPR) {
       if (warp == 0) {
         const uint32_t word = key_word(c);
@@ -278,25 +297,26 @@ __global__ void __launch_bounds__(kAppendThreads)
         }
       } else {
         const int sh = int4_shift(tok & 7);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint32_t* p = v_words + int4_v_word<D>(tok, col + e);
-          const uint32_t code = (e & 1) ? c[e / 2] >> 16 : c[e / 2] & 15u;
-          *p = (*p & ~(15u << sh)) | (code << sh);
-        }
+        auto put = [&](uint32_t w, uint32_t code) { return (w & ~(15u << sh)) | (code << sh); };
+        *reinterpret_cast<uint4*>(p) = make_uint4(put(va.x, c[0] & 15u), put(va.y, c[0] >> 16),
+                                                  put(va.z, c[1] & 15u), put(va.w, c[1] >> 16));
+        *reinterpret_cast<uint4*>(p + 16) = make_uint4(put(vb.x, c[2] & 15u), put(vb.y, c[2] >> 16),
+                                                       put(vb.z, c[3] & 15u), put(vb.w, c[3] >> 16));
         if (lane == 0) v_rows[tok] = row;
       }
     }
   }
   __syncthreads();
-  const int wi = tid % LPR, grp = tid / LPR;
   float acc[8] = {};
-  for (int t = grp; t <= tok; t += kGroups) {
-    const uint32_t x = t == tok ? new_k[wi] : k_words[t * LPR + wi];
-    const uint32_t row = t == tok ? new_row : k_rows[t];
-    const float s = int4_scale(row), lo = int4_lo(row);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += fmaf((float)((x >> int4_shift(e)) & 15u), s, lo);
+  for (int i = 0; i < kRows; ++i) {
+    const int t = grp + i * kGroups;
+    if (t <= tok) {
+      const uint32_t w = t == tok ? new_k[wi] : words[i], row = t == tok ? new_row : rows[i];
+      const float s = int4_scale(row), lo = int4_lo(row);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += fmaf((float)((w >> int4_shift(e)) & 15u), s, lo);
+    }
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) part[grp][wi * 8 + e] = acc[e];
