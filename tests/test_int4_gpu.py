@@ -302,6 +302,15 @@ CASES = {
     "d64-group-7": lambda: make(seq_lens=[3000, 0, 257, 4444] * 5, num_q_heads=14, num_kv_heads=2,
                                 head_dim=64, init_tokens=100, local_tokens=300, seed=94),
     "shared-prefix": lambda: make(seq_lens=[2000, 3000], shared_prefix_tokens=1024, seed=95),
+    "group-5": lambda: make(seq_lens=[5000, 77], num_q_heads=10, num_kv_heads=2, seed=106),
+    "group-2-seventy-requests": lambda: make(seq_lens=[(97 * i) % 1500 for i in range(70)], num_q_heads=4,
+                                             num_kv_heads=2, init_tokens=128, local_tokens=200, seed=107),
+    # more kept blocks than go out with the selection: the rest from the shared pool
+    "long-mostly-kept": lambda: make(seq_lens=[131000], num_q_heads=2, num_kv_heads=1,
+                                     topk_percent=0.9, seed=108),
+    # more candidates than the one-kernel path takes
+    "longer-than-one-kernel": lambda: make(seq_lens=[150000], num_q_heads=2, num_kv_heads=1,
+                                           head_dim=64, topk_percent=0.1, seed=109),
 }
 
 
@@ -315,6 +324,83 @@ def test_decode_matches_64_bits(name):
     assert int(buf.error_flags.item()) == 0
     same_selection(case, buf)
     check(case, kv, buf)
+
+
+@pytest.mark.parametrize("batch", [1, 20])
+@pytest.mark.parametrize("distinct", [1, 3, 40])
+def test_scores_that_are_equal_or_close_keep_the_lower_blocks(batch, distinct):
+    """Blocks that share a few pages have equal scores (hundreds in one bin of any digit), and keys with a
+    large common part scores that agree in their top bits."""
+    case = make(seq_lens=[40000] * batch, topk_percent=0.37, seed=110)
+    case.k_cache += 3.0
+    pages = case.block_table[:, :distinct].clone()
+    case.block_table[:, 2:-4] = pages[:, torch.arange(case.max_blocks - 6, device=DEV) % distinct]
+    kv, buf = int4_case(case)
+    step(case, kv, buf)
+    torch.cuda.synchronize()
+    assert int(buf.error_flags.item()) == 0
+    same_selection(case, buf)
+    check(case, kv, buf, units=[(0, 0), (batch - 1, 1)])
+
+
+def test_a_cache_past_32_bit_offsets():
+    """The last pages of a cache of more than 2^32 bytes: written, appended to, read back, attended."""
+    cfg = config(Hq=32, Hkv=8, init_tokens=128, local_tokens=128)
+    P = (1 << 32) // (8 * 17408) + 200
+    kv = torch.empty(P, 8, 17408, dtype=torch.uint8, device=DEV)
+    assert kv.numel() > 1 << 32
+    n = 12
+    k, v = random_pages(cfg, n, 111)
+    ids = torch.arange(n, dtype=i32, device=DEV)
+    top = (P - 1 - ids).contiguous()
+    srkv.quantize_kv_int4(cfg, k, v, ids, kv, top)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    L = torch.tensor([n * 128 - 30], dtype=i32, device=DEV)
+    table = top.view(1, n).contiguous()
+    reps = torch.zeros(P, 8, 128, device=DEV)
+    reps[top.long()] = k.float().mean(2)
+    srkv.append_kv_int4(cfg, k[:1, :, 3].contiguous(), v[:1, :, 3].contiguous(), kv, table, L, reps)
+    srkv.dequantize_kv_int4(cfg, kv, top, ko, vo, ids)
+    buf = srkv.DecodeBuffers(cfg, 1, n, 1, device=DEV)
+    q = random_pages(cfg, 1, 112)[0][:, :, :4].reshape(1, 32, 128).contiguous()
+    L += 1
+    srkv.retrieval_decode_int4(cfg, q, kv, reps, table, L, None, buf.sel, buf.nsel, buf.out, buf.workspace,
+                               buf.error_flags)
+    torch.cuda.synchronize()
+    assert int(buf.error_flags.item()) == 0
+    got = kv[top.long()].cpu().numpy()
+    kh, vh = ref.host(k), ref.host(v)
+    row = n * 128 - 30
+    kh[n - 1, :, row % 128], vh[n - 1, :, row % 128] = kh[0, :, 3], vh[0, :, 3]
+    for p in (0, n - 1):
+        for h in range(8):
+            check_slab(got[p, h], kh[p, h], vh[p, h], 128)
+            np.testing.assert_array_equal(ref.host(ko[p, h]), ref.to_bf16(ref.values(got[p, h], 128)[0]))
+    sel, nsel = buf.sel.cpu().numpy(), buf.nsel.cpu().numpy()
+    for h in (0, 7):
+        want, bound = ref.decode_unit(ref.host(q)[0, 4 * h:4 * h + 4], got, np.arange(n), row + 1,
+                                      sel[0, h, :nsel[0, h]], cfg, h)
+        assert (np.abs(ref.host(buf.out)[0, 4 * h:4 * h + 4] - want) <= bound).all()
+
+
+def test_two_streams_at_once():
+    """Two requests' steps on two streams over one cache, each with buffers of its own, against the same
+    steps one after the other."""
+    cases = [make(seq_lens=[9000, 4000], seed=113), make(seq_lens=[6000, 2000] * 12, seed=114)]
+    sets = [(c, *int4_case(c)) for c in cases]
+    want = []
+    for c, kv, buf in sets:
+        step(c, kv, buf)
+        torch.cuda.synchronize()
+        want.append(buf.out.clone())
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for (c, kv, buf), s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                step(c, kv, buf)
+    torch.cuda.synchronize()
+    for (c, kv, buf), w in zip(sets, want):
+        assert int(buf.error_flags.item()) == 0 and torch.equal(buf.out, w)
 
 
 def test_a_cache_without_pages_is_refused():
