@@ -154,11 +154,11 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
   const bool leader = crank == 0;
   bool arrived = false;  // on the closing cluster barrier (warp-uniform)
 
+  if constexpr (Fmt == kInt4Pages) {
+    if (warp == 1) Int4Ring<D>{smem}.init(a.G <= 4, lane);
+  }
   if (tid == 0) {
-    if constexpr (Fmt == kInt4Pages)
-      Int4Ring<D>{smem}.init(a.G <= 4);
-    else
-      init_ring<D, Fmt>(smem);
+    if constexpr (Fmt != kInt4Pages) init_ring<D, Fmt>(smem);
     mbar_init(keys_ready, kMaxCand);            // one per candidate, the rest at once
     mbar_init(list_ready, 1);                   // the leader, once the pool is laid out
     mbar_init(parts_ready, 1);                  // the leader, expecting every partial's bytes

@@ -119,16 +119,16 @@ struct Int4Ring {
   __device__ __forceinline__ float* state(int floats) const {
     return reinterpret_cast<float*>(smem + C::kOffState) + floats;
   }
-  // Barrier set-up (one thread).
-  __device__ __forceinline__ void init(bool narrow) const {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), C::kGroupWarps);
+  // Barrier set-up (a whole warp: one thread's 32 would stand before every decode's first copy).
+  __device__ __forceinline__ void init(bool narrow, int lane) const {
+    for (int i = lane; i < C::kBars; i += 32) {
+      const bool is_empty = i >= C::kStages && i < 2 * C::kStages;
+      const bool is_left = bars() + i == left();
+      mbar_init(bars() + i, is_empty  ? C::kGroupWarps
+                            : is_left ? (narrow ? C::kNarrowWarps : C::kWideWarps)
+                                      : 1);
     }
-    for (int s = 0; s < C::kSegs; ++s) mbar_init(query(s), 1);
-    mbar_init(left(), narrow ? C::kNarrowWarps : C::kWideWarps);
-    mbar_init(merged(), 1);
-    *done() = 0;
+    if (lane == 0) *done() = 0;
     fence_mbar_init();
   }
 

@@ -115,11 +115,10 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   griddep_launch_dependents();
   PlanLens pre;
   if (warp == kProducerWarp && a.early) pre = plan_lens(a);
-  if (tid == 0) {
-    if constexpr (Fmt == kInt4Pages)
-      Int4Ring<D>{smem}.init(a.G <= 4);
-    else
-      init_ring<D, Fmt>(smem);
+  if constexpr (Fmt == kInt4Pages) {
+    if (warp == 0) Int4Ring<D>{smem}.init(a.G <= 4, lane);
+  } else if (tid == 0) {
+    init_ring<D, Fmt>(smem);
   }
   __syncthreads();
 
