@@ -52,7 +52,7 @@ constexpr int kMaxCluster = 16;                            // CTAs per unit, at 
 // costs two round trips through the cluster, which a bf16 page (1.5 us of an SM's share of the
 // bandwidth) hides and a 4-bit page (0.4 us) does not.
 template <int Fmt>
-constexpr int kStaticOf = Fmt == kInt4Pages ? 32 : 16;
+constexpr int kStaticOf = is_int4(Fmt) ? 32 : 16;
 // The scoring counts the top 12 bits of the keys besides the top 8: on score sets like the
 // method's (a few hundred candidates, scores spread over a few units) the 12-bit bin holding
 // the k-th largest key then holds a few keys, and the selection finishes in one pass over the
@@ -154,11 +154,11 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
   const bool leader = crank == 0;
   bool arrived = false;  // on the closing cluster barrier (warp-uniform)
 
-  if constexpr (Fmt == kInt4Pages) {
-    if (warp == 1) Int4Ring<D>{smem}.init(a.G <= 4, lane);
+  if constexpr (is_int4(Fmt)) {
+    if (warp == 1) Int4Ring<D, Fmt>{smem}.init(lane);
   }
   if (tid == 0) {
-    if constexpr (Fmt != kInt4Pages) init_ring<D, Fmt>(smem);
+    if constexpr (!is_int4(Fmt)) init_ring<D, Fmt>(smem);
     mbar_init(keys_ready, kMaxCand);            // one per candidate, the rest at once
     mbar_init(list_ready, 1);                   // the leader, once the pool is laid out
     mbar_init(parts_ready, 1);                  // the leader, expecting every partial's bytes
@@ -253,10 +253,10 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         task.page = -1;
         task.lo = task.hi = task.ie = task.ws = 0;
         if (lane < cnt) task = resolve_a(g, j0 + lane, bt_r, total_pages(a), eflags);
-        if constexpr (Fmt == kInt4Pages) {  // the lanes issue their own pages
+        if constexpr (is_int4(Fmt)) {  // the lanes issue their own pages
           const uint32_t fl = place.it == 0 && lane == 0 ? kNewUnit : 0u;
           const int early = place.it == 0 ? min(cnt, F::kEarlyStages) : 0;
-          issue_batch_int4<D>(a, smem, place, 0, early, u, fl, task, eflags, lane);
+          issue_batch_int4<D, Fmt>(a, smem, place, 0, early, u, fl, task, eflags, lane);
           if (early == F::kEarlyStages && !place.abort) {
             k = kept_count();
             bool ok = true;
@@ -266,7 +266,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
               place.abort = true;
             }
           }
-          issue_batch_int4<D>(a, smem, place, early, cnt, u, early > 0 ? 0u : fl, task, eflags, lane);
+          issue_batch_int4<D, Fmt>(a, smem, place, early, cnt, u, early > 0 ? 0u : fl, task, eflags, lane);
           abort = place.abort;
         } else {
         for (int l = 0; l < cnt && !abort; ++l) {
@@ -329,8 +329,8 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
       };
       auto issue_b = [&](const int2 e) {
         const PageTask t = kept_task(e);
-        if constexpr (Fmt == kInt4Pages) {
-          issue_batch_int4<D>(a, smem, place, 0, 1, u, place.it == 0 ? kNewUnit : 0u, t, eflags,
+        if constexpr (is_int4(Fmt)) {
+          issue_batch_int4<D, Fmt>(a, smem, place, 0, 1, u, place.it == 0 ? kNewUnit : 0u, t, eflags,
                               lane);
           abort = place.abort;
         } else {
@@ -339,7 +339,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
           ++it;
         }
       };
-      if constexpr (Fmt == kInt4Pages) {
+      if constexpr (is_int4(Fmt)) {
         if (k > 0 && !abort) {  // lane j has entry j
           static_assert(kStatic == 32, "an entry per lane");
           const int2 e = mail[lane];
@@ -348,7 +348,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
           t.page = -1;
           t.lo = t.hi = t.ie = t.ws = 0;
           if (lane < cnt) t = kept_task(e);
-          issue_batch_int4<D>(a, smem, place, 0, cnt, u,
+          issue_batch_int4<D, Fmt>(a, smem, place, 0, cnt, u,
                               place.it == 0 && lane == 0 ? kNewUnit : 0u, t, eflags, lane);
           abort = place.abort;
         }
@@ -382,10 +382,10 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         e0 = next0;
         have = __shfl_sync(0xffffffffu, more, 0);
       }
-      if constexpr (Fmt == kInt4Pages) {
+      if constexpr (is_int4(Fmt)) {
         place.abort = abort;
         place.segs = 1;  // the segment is closed even if this CTA took no page
-        finish_ring_int4<D>(a, smem, place, eflags, lane);
+        finish_ring_int4<D, Fmt>(smem, place, eflags, lane);
       } else if (lane == 0) {
         // the sentinel closes the segment (empty if this CTA took no page)
         PageTask none;
@@ -408,12 +408,12 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
   } else if (warp > kProducerWarp) {
     // ------------------- 4-bit pages: the merger, and consumers that neither score nor select
     cluster_wait();
-    if constexpr (Fmt == kInt4Pages) {
+    if constexpr (is_int4(Fmt)) {
       if (!leader && warp == kMergerWarp)
-        merger_loop_int4<D>(a, smem, lane, [&](const SoftmaxState<D>& st, const Int4Segment&,
+        merger_loop_int4<D, Fmt>(a, smem, lane, [&](const SoftmaxState<D>& st, const Int4Segment&,
                                                Lane ln) { write_partial(st, ln); });
       else if (!leader)
-        consumer_loop_int4<D>(a, smem, lane, warp - 2);
+        consumer_loop_int4<D, Fmt>(a, smem, lane, warp - 2);
     }
   } else {
     // ------------------------------------------------------------------ consumers
@@ -495,7 +495,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         }
         bar();
         int shift = 32 - kHistBits;  // of the bin's digit
-        if constexpr (Fmt == kInt4Pages) {
+        if constexpr (is_int4(Fmt)) {
           // Scores with a large common part share their top 12 bits: then the next 12 bits of the
           // bin's keys are counted, and the bin of 24 bits is ranked instead.  (A 4-bit step of
           // 65 536 tokens waits for the selection: the radix passes cost it 3 us more.  Not for the
@@ -677,7 +677,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         float l_run = w * l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, o);
-        const bool some = attended_any<Fmt == kInt4Pages>(l_run);
+        const bool some = attended_any<is_int4(Fmt)>(l_run);
         for (int32_t half = warp / a.G; half < 2; half += hw) {
           // every streaming CTA wrote a partial (zeros if it attended nothing).  The loads and
           // weight shuffles of a batch of 8 slots are unconditional, so they issue together
@@ -724,8 +724,8 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
     } else {
       // 3'. attend list A, then the kept blocks taken from the pool, as one segment; the
       // merged partial goes to the leader's shared memory
-      if constexpr (Fmt == kInt4Pages)
-        consumer_loop_int4<D>(a, smem, lane, warp);
+      if constexpr (is_int4(Fmt))
+        consumer_loop_int4<D, Fmt>(a, smem, lane, warp);
       else
         consumer_loop<D, Fmt>(a, smem, lane, warp,
                               [&](const SoftmaxState<D>& st, const StageInfo&, Lane ln) {
@@ -783,20 +783,26 @@ int32_t fused_cluster_size(const srkv_config& cfg, int32_t units, int32_t max_bl
   const int64_t W = (int64_t)max_blocks * kBlock - cfg.local_tokens;
   const int64_t nmax = W > cfg.init_tokens ? (W + kBlock - 1) / kBlock - cfg.init_tokens / kBlock : 0;
   if (nmax > kMaxCand) return 0;
-  // [device][d 64, d 128, d 128 E4M3, d 64 and 128 4-bit][cluster 16 - c]: max active + 1
+  // [device][d 64, d 128, d 128 E4M3, 4-bit d 64 and 128, more than 4 heads d 64 and 128]
+  // [cluster 16 - c]: max active + 1
   constexpr int kSizes = kMaxCluster - 3;  // 16 .. 4
-  static int32_t cached[128][5][kSizes];
+  static int32_t cached[128][7][kSizes];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
   const bool d128 = cfg.head_dim == 128;
-  const int di = fmt == PageFormat::kInt4 ? 3 + d128 : fmt == PageFormat::kE4m3 ? 2 : d128;
+  const bool wide = cfg.num_q_heads / cfg.num_kv_heads > 4;
+  const int di = fmt == PageFormat::kInt4   ? 3 + d128 + 2 * wide
+                 : fmt == PageFormat::kE4m3 ? 2
+                                            : d128;
   for (int c = 0; c < kSizes; ++c) {
     const int32_t cs = kMaxCluster - c;
     if (nmax > (int64_t)kMaxShare * cs) continue;  // per-CTA scoring share
     if (cs < 8 && (di != 1 || cfg.topk_percent > 0.3)) continue;
     if (cached[dev][di][c] == 0) {
-      const int32_t n = di == 4   ? max_active_clusters<128, kInt4Pages>(cs)
-                        : di == 3 ? max_active_clusters<64, kInt4Pages>(cs)
+      const int32_t n = di == 6   ? max_active_clusters<128, kInt4Wide>(cs)
+                        : di == 5 ? max_active_clusters<64, kInt4Wide>(cs)
+                        : di == 4 ? max_active_clusters<128, kInt4Narrow>(cs)
+                        : di == 3 ? max_active_clusters<64, kInt4Narrow>(cs)
                         : di == 2 ? max_active_clusters<128, kE4m3Pages>(cs)
                         : di == 1 ? max_active_clusters<128, kBf16Pages>(cs)
                                   : max_active_clusters<64, kBf16Pages>(cs);
@@ -810,7 +816,7 @@ int32_t fused_cluster_size(const srkv_config& cfg, int32_t units, int32_t max_bl
 template <int D, int Fmt>
 cudaError_t launch_fused_t(const DecodeArgs& a, int32_t cluster, cudaStream_t stream) {
   TmaMaps maps = {};  // 4-bit pages need none
-  if (Fmt != kInt4Pages &&
+  if (!is_int4(Fmt) &&
       (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages) ||
        !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages)))
     return cudaErrorInvalidValue;
@@ -834,8 +840,10 @@ cudaError_t launch_fused_t(const DecodeArgs& a, int32_t cluster, cudaStream_t st
 
 cudaError_t launch_fused(const DecodeArgs& a, int32_t cluster, cudaStream_t stream) {
   if (a.int4)
-    return a.d == 128 ? launch_fused_t<128, kInt4Pages>(a, cluster, stream)
-                      : launch_fused_t<64, kInt4Pages>(a, cluster, stream);
+    return a.G <= 4 ? (a.d == 128 ? launch_fused_t<128, kInt4Narrow>(a, cluster, stream)
+                                  : launch_fused_t<64, kInt4Narrow>(a, cluster, stream))
+                    : (a.d == 128 ? launch_fused_t<128, kInt4Wide>(a, cluster, stream)
+                                  : launch_fused_t<64, kInt4Wide>(a, cluster, stream));
   if (a.k_scale) return launch_fused_t<128, kE4m3Pages>(a, cluster, stream);
   return a.d == 128 ? launch_fused_t<128, kBf16Pages>(a, cluster, stream)
                     : launch_fused_t<64, kBf16Pages>(a, cluster, stream);

@@ -13,7 +13,7 @@
 // the query (16 times smaller at the second kind's elements) and of the weights likewise.
 //
 // A page is 4 groups of 32 tokens, one for each warp of a group of 4; the CTA's groups work on
-// consecutive stages (3 of them, 2 for more than 4 heads), so that 3 warps share a scheduler and
+// consecutive stages (3 of them, 2 for groups of more than 4 heads), so that 3 warps share a scheduler and
 // hide one another's latencies.  A group visits its own stages only.  Stages name their segment (a
 // unit's positions in a list) by its number; a warp that meets a new number leaves its state
 // of the old segment in shared memory and goes on at once, and a merger warp joins the states and
@@ -58,30 +58,33 @@ struct Int4Segment {
 };
 
 // A stage is one slab (17 408 bytes at d 128), moved by one bulk copy.
-template <int D>
-struct Cfg<D, kInt4Pages> {
+template <int D, bool kNarrow>
+struct Int4Cfg {
+  static constexpr int kHeads = kNarrow ? 4 : 8;  // of a group, at most
   static constexpr int kSlab = Int4Slab<D>::kBytes;
-  static constexpr int kGroupWarps = 4;                 // warps that share a stage
-  static constexpr int kNarrowWarps = 12, kWideWarps = 8;  // consumer warps (G <= 4, G > 4)
-  static constexpr int kThreads = (kNarrowWarps + 2) * 32;  // + the producer and the merger
-  static constexpr int kStages = D == 128 ? 9 : 16;
+  static constexpr int kGroupWarps = 4;           // warps that share a stage
+  static constexpr int kWarps = kNarrow ? 12 : 8;  // consumer warps
+  static constexpr int kGroups = kWarps / kGroupWarps;
+  static constexpr int kThreads = (kWarps + 2) * 32;  // + the producer and the merger
+  static constexpr int kStages = D == 128 ? (kNarrow ? 9 : 8) : (kNarrow ? 18 : 16);
+  // A group waits for its own stages only, so each slot of the ring has to be one group's: a wait by
+  // parity takes the phase before the current one for complete, and would pass at once on a slot
+  // whose last use, another group's, has not landed.
+  static_assert(kStages % kGroups == 0, "a ring slot belongs to one group");
   // A warp may be one stage of its group plus the ring behind the producer.
-  static constexpr int kSegs = kStages + kNarrowWarps / kGroupWarps;
-  static constexpr int kQBytes = 8 * D * 2;
+  static constexpr int kSegs = kStages + kGroups;
+  static constexpr int kQBytes = kHeads * D * 2;
   static constexpr int MT = D / 16;
-  // A warp's state in shared memory: (acc, m, l) of the lanes that hold heads.
+  // A warp's state in shared memory: (m, l) and acc of the lanes that hold heads.
   static constexpr int kStateStride = MT * 4 + 4;
-  static constexpr int kNarrowState = 16 * kStateStride, kWideState = 32 * kStateStride;
-  static constexpr int kStates = kNarrowWarps * kNarrowState > kWideWarps * kWideState
-                                     ? kNarrowWarps * kNarrowState
-                                     : kWideWarps * kWideState;
+  static constexpr int kState = (kNarrow ? 16 : 32) * kStateStride;
 
   static constexpr size_t kOffK = 0;
   static constexpr size_t kOffQ = (size_t)kStages * kSlab;
   // the one-kernel decode's leader streams no pages and keeps its partials from here on
   static constexpr size_t kOffV = (size_t)(kStages / 2) * kSlab;
   static constexpr size_t kOffState = kOffQ + (size_t)kSegs * kQBytes;
-  static constexpr size_t kOffInfo = kOffState + sizeof(float) * kStates;
+  static constexpr size_t kOffInfo = kOffState + sizeof(float) * kWarps * kState;
   static constexpr size_t kOffSeg = kOffInfo + sizeof(Int4Stage) * kStages;
   static constexpr size_t kOffBar = kOffSeg + ((sizeof(Int4Segment) * kSegs + 15) & ~size_t(15));
   // full[kStages], empty[kStages], query[kSegs], left (a segment's states), merged; then `done`
@@ -91,10 +94,14 @@ struct Cfg<D, kInt4Pages> {
   static constexpr size_t kSmemAlloc = kSmem + 1024;
   static_assert(kSmemAlloc <= 232448, "shared memory opt-in limit");
 };
-
 template <int D>
+struct Cfg<D, kInt4Narrow> : Int4Cfg<D, true> {};
+template <int D>
+struct Cfg<D, kInt4Wide> : Int4Cfg<D, false> {};
+
+template <int D, int Fmt>
 struct Int4Ring {
-  using C = Cfg<D, kInt4Pages>;
+  using C = Cfg<D, Fmt>;
   unsigned char* smem;
   __device__ __forceinline__ uint64_t* full(int s) const { return bars() + s; }
   __device__ __forceinline__ uint64_t* empty(int s) const { return bars() + C::kStages + s; }
@@ -120,12 +127,12 @@ struct Int4Ring {
     return reinterpret_cast<float*>(smem + C::kOffState) + floats;
   }
   // Barrier set-up (a whole warp: one thread's 32 would stand before every decode's first copy).
-  __device__ __forceinline__ void init(bool narrow, int lane) const {
+  __device__ __forceinline__ void init(int lane) const {
     for (int i = lane; i < C::kBars; i += 32) {
       const bool is_empty = i >= C::kStages && i < 2 * C::kStages;
       const bool is_left = bars() + i == left();
       mbar_init(bars() + i, is_empty  ? C::kGroupWarps
-                            : is_left ? (narrow ? C::kNarrowWarps : C::kWideWarps)
+                            : is_left ? C::kWarps
                                       : 1);
     }
     if (lane == 0) *done() = 0;
@@ -151,13 +158,13 @@ struct Int4Place {
 // list.  Each lane issues its own page.  A 4-bit page lasts an SM 0.4 us, so what a page costs the
 // producer counts: everything but the wait for the stage, its description and the copy is computed by
 // the lanes side by side.
-template <int D>
+template <int D, int Fmt>
 __device__ __forceinline__ void issue_batch_int4(const DecodeArgs& a, unsigned char* smem,
                                                  Int4Place& pl, int first, int last, int32_t u,
                                                  uint32_t fl, const PageTask& t, uint32_t& eflags,
                                                  int lane) {
-  using C = Cfg<D, kInt4Pages>;
-  const Int4Ring<D> ring{smem};
+  using C = Cfg<D, Fmt>;
+  const Int4Ring<D, Fmt> ring{smem};
   const int64_t mine = pl.it + (lane - first);
   const int s = (int)(mine % C::kStages);
   const uint32_t parity = (uint32_t)((mine / C::kStages - 1) & 1);
@@ -203,14 +210,13 @@ __device__ __forceinline__ void issue_batch_int4(const DecodeArgs& a, unsigned c
 }
 
 // The end: a stage for each group that closes every segment, then every copy lands.
-template <int D>
-__device__ __forceinline__ void finish_ring_int4(const DecodeArgs& a, unsigned char* smem,
-                                                 Int4Place& pl, uint32_t& eflags, int lane) {
-  using C = Cfg<D, kInt4Pages>;
-  const Int4Ring<D> ring{smem};
+template <int D, int Fmt>
+__device__ __forceinline__ void finish_ring_int4(unsigned char* smem, Int4Place& pl,
+                                                 uint32_t& eflags, int lane) {
+  using C = Cfg<D, Fmt>;
+  const Int4Ring<D, Fmt> ring{smem};
   if (lane != 0) return;
-  const int groups = (a.G <= 4 ? C::kNarrowWarps : C::kWideWarps) / C::kGroupWarps;
-  for (int g = 0; g < groups && !pl.abort; ++g) {
+  for (int g = 0; g < C::kGroups && !pl.abort; ++g) {
     const int s = (int)(pl.it % C::kStages);
     if (pl.it >= C::kStages && !mbar_wait(ring.empty(s), (uint32_t)((pl.it / C::kStages - 1) & 1))) {
       pl.abort = true;
@@ -233,16 +239,16 @@ __device__ __forceinline__ void finish_ring_int4(const DecodeArgs& a, unsigned c
     }
 }
 
-// kNarrow: the group has at most 4 heads.
-template <int D, bool kNarrow>
-__device__ __forceinline__ void consume_int4(const DecodeArgs& a, unsigned char* smem, int lane,
-                                             int warp) {
-  using C = Cfg<D, kInt4Pages>;
+// The consumer warps' part (warp: 0 .. kWarps - 1).
+template <int D, int Fmt>
+__device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned char* smem,
+                                                   int lane, int warp) {
+  constexpr bool kNarrow = Fmt == kInt4Narrow;
+  using C = Cfg<D, Fmt>;
   using F = Int4Slab<D>;
   constexpr int kGroupWarps = C::kGroupWarps;       // warps per page
-  constexpr int kWarps = kNarrow ? C::kNarrowWarps : C::kWideWarps;
-  constexpr int kGroups = kWarps / kGroupWarps;     // pages at once
-  const Int4Ring<D> ring{smem};
+  constexpr int kGroups = C::kGroups;               // pages at once
+  const Int4Ring<D, Fmt> ring{smem};
   constexpr int kTok = kBlock / kGroupWarps;        // tokens per warp and page
   constexpr int NW = kTok / 32;                     // 32-token groups per warp
   constexpr int KW = D / 32;                        // key words per lane and row
@@ -288,7 +294,7 @@ __device__ __forceinline__ void consume_int4(const DecodeArgs& a, unsigned char*
       const float unit = vlim * (16777216.f / kInt4PScale);  // 2^24 of the subnormals
       const int slot = kNarrow ? ln.g * 2 + ln.t : lane;
       float4* p = reinterpret_cast<float4*>(
-          ring.state(warp * (kNarrow ? C::kNarrowState : C::kWideState) + slot * C::kStateStride));
+          ring.state(warp * C::kState + slot * C::kStateStride));
       p[0] = make_float4(st.m[0], st.m[1], st.l[0], st.l[1]);
 #pragma unroll
       for (int i = 0; i < C::MT; ++i)
@@ -544,29 +550,17 @@ __device__ __forceinline__ void consume_int4(const DecodeArgs& a, unsigned char*
   warp_arrive(ring.left());
 }
 
-// The consumer warps' part (warp: 0 .. kNarrowWarps - 1).
-template <int D>
-__device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned char* smem,
-                                                   int lane, int warp) {
-  using C = Cfg<D, kInt4Pages>;
-  if (a.G <= 4)
-    consume_int4<D, true>(a, smem, lane, warp);
-  else if (warp < C::kWideWarps)
-    consume_int4<D, false>(a, smem, lane, warp);
-}
-
 // The merger warp: segment after segment, joins the consumer warps' states and calls
 // write_partial(state, segment, lane) with the result.
-template <int D, typename WritePartial>
+template <int D, int Fmt, typename WritePartial>
 __device__ __forceinline__ void merger_loop_int4(const DecodeArgs& a, unsigned char* smem, int lane,
                                                  WritePartial&& write_partial) {
-  using C = Cfg<D, kInt4Pages>;
-  const Int4Ring<D> ring{smem};
+  using C = Cfg<D, Fmt>;
+  const Int4Ring<D, Fmt> ring{smem};
   const Lane ln{lane >> 2, lane & 3};
-  const bool narrow = a.G <= 4, holds = !narrow || ln.t < 2;
-  const int warps = narrow ? C::kNarrowWarps : C::kWideWarps;
-  const int stride = narrow ? C::kNarrowState : C::kWideState;
-  const int slot = holds ? (narrow ? ln.g * 2 + ln.t : lane) : 0;
+  constexpr bool kNarrow = Fmt == kInt4Narrow;
+  constexpr int warps = C::kWarps, stride = C::kState;
+  const int slot = !kNarrow ? lane : ln.t < 2 ? ln.g * 2 + ln.t : 0;  // (lanes past the heads: any)
   const float* mine = ring.state(slot * C::kStateStride);
   for (int32_t seg = 0;; ++seg) {
     if (!mbar_wait(ring.left(), (uint32_t)(seg & 1))) {

@@ -34,8 +34,10 @@ struct StageInfo {
 };
 
 // What the pages hold: bf16 values, E4M3 codes (each stage then also carries the 128 K and 128 V
-// row scales of its page) or 4-bit codes (decode_int4.cuh has their stages).
-enum : int { kBf16Pages = 0, kE4m3Pages = 1, kInt4Pages = 2 };
+// row scales of its page) or 4-bit codes (decode_int4.cuh has their stages; apart for groups of at
+// most 4 heads and of more).
+enum : int { kBf16Pages = 0, kE4m3Pages = 1, kInt4Narrow = 2, kInt4Wide = 3 };
+__host__ __device__ constexpr bool is_int4(int fmt) { return fmt >= kInt4Narrow; }
 
 template <int D, int Fmt = kBf16Pages>
 struct Cfg {
@@ -284,7 +286,7 @@ __device__ __forceinline__ void emit_partial(const SoftmaxState<D>& st, Lane ln,
                                              Put4 put4, Put2 put2) {
   using C = Cfg<D>;
   const int h0 = 2 * ln.t, h1 = h0 + 1;
-  if constexpr (Fmt == kInt4Pages) {
+  if constexpr (is_int4(Fmt)) {
     // m-tiles 2x and 2x + 1 hold d = 32x + 4g + 0, 1 and + 2, 3 (rows g and g + 8)
 #pragma unroll
     for (int x = 0; x < C::MT / 2; ++x) {

@@ -28,7 +28,7 @@ namespace {
 // positions, one per lane, each lane finding its own unit, page and rows; the next batch is
 // resolved between the halves of this one, while the copies of the first half are in flight.  (Always
 // behind the scoring kernel, in the early mode.)
-template <int D>
+template <int D, int Fmt>
 __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned char* smem, int list,
                                                  const ListRange& rg, Int4Place& pl,
                                                  uint32_t& eflags, int lane) {
@@ -90,9 +90,9 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
   for (int64_t done = 0; done < npos && !pl.abort; done += 32) {
     const int cnt = npos - done < 32 ? (int)(npos - done) : 32;
     const int half = cnt < 16 ? cnt : 16;
-    issue_batch_int4<D>(a, smem, pl, 0, half, x.u, x.flags, x.t, eflags, lane);
+    issue_batch_int4<D, Fmt>(a, smem, pl, 0, half, x.u, x.flags, x.t, eflags, lane);
     const Item next = resolve(done + 32);
-    issue_batch_int4<D>(a, smem, pl, half, cnt, x.u, x.flags, x.t, eflags, lane);
+    issue_batch_int4<D, Fmt>(a, smem, pl, half, cnt, x.u, x.flags, x.t, eflags, lane);
     x = next;
   }
 }
@@ -115,8 +115,8 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
   griddep_launch_dependents();
   PlanLens pre;
   if (warp == kProducerWarp && a.early) pre = plan_lens(a);
-  if constexpr (Fmt == kInt4Pages) {
-    if (warp == 0) Int4Ring<D>{smem}.init(a.G <= 4, lane);
+  if constexpr (is_int4(Fmt)) {
+    if (warp == 0) Int4Ring<D, Fmt>{smem}.init(lane);
   } else if (tid == 0) {
     init_ring<D, Fmt>(smem);
   }
@@ -137,7 +137,7 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
     // Both lists are planned first: list B's counts are the selection counts, known from
     // the lengths alone in the early mode.
     ListRange rgs[2];
-    if constexpr (Fmt != kInt4Pages) {
+    if constexpr (!is_int4(Fmt)) {
 #pragma unroll
       for (int list = kListA; list <= kListB; ++list)
         rgs[list] = a.early ? warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags)
@@ -145,9 +145,9 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
                                         eflags);
     }
     for (int list = kListA; list <= kListB && !abort; ++list) {
-      if constexpr (Fmt == kInt4Pages) {  // always early; list B is planned once list A is out
+      if constexpr (is_int4(Fmt)) {  // always early; list B is planned once list A is out
         const ListRange rg = warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags);
-        stream_list_int4<D>(a, smem, list, rg, place, eflags, lane);
+        stream_list_int4<D, Fmt>(a, smem, list, rg, place, eflags, lane);
         abort = place.abort;
         continue;
       } else {
@@ -220,8 +220,8 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
       }
       }
     }
-    if constexpr (Fmt == kInt4Pages) {
-      finish_ring_int4<D>(a, smem, place, eflags, lane);
+    if constexpr (is_int4(Fmt)) {
+      finish_ring_int4<D, Fmt>(smem, place, eflags, lane);
     } else if (lane == 0) {
       uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
       uint64_t* full_v = full + C::kStages;
@@ -250,12 +250,12 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
     store_partial<D, Fmt>(reinterpret_cast<float*>(a.ws + a.lay.acc) + slot * a.G * D,
                           reinterpret_cast<float*>(a.ws + a.lay.ml) + slot * a.G * 2, st, ln, a.G);
   };
-  if constexpr (Fmt == kInt4Pages) {
+  if constexpr (is_int4(Fmt)) {
     if (warp == kMergerWarp)
-      merger_loop_int4<D>(a, smem, lane, [&](const SoftmaxState<D>& st, const Int4Segment& sg,
+      merger_loop_int4<D, Fmt>(a, smem, lane, [&](const SoftmaxState<D>& st, const Int4Segment& sg,
                                              Lane ln) { write_partial(st, sg.unit, sg.flags, ln); });
     else
-      consumer_loop_int4<D>(a, smem, lane, warp < kProducerWarp ? warp : warp - 2);
+      consumer_loop_int4<D, Fmt>(a, smem, lane, warp < kProducerWarp ? warp : warp - 2);
   } else {
     consumer_loop<D, Fmt>(a, smem, lane, warp, [&](const SoftmaxState<D>& st, const StageInfo& inf,
                                                    Lane ln) {
@@ -351,7 +351,7 @@ cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
     configured[dev] = true;
   }
   TmaMaps maps = {};  // 4-bit pages need none: a slab is one bulk copy
-  if (Fmt != kInt4Pages &&
+  if (!is_int4(Fmt) &&
       (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages) ||
        !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, Fmt == kE4m3Pages)))
     return cudaErrorInvalidValue;
@@ -361,7 +361,10 @@ cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_split_mma(const DecodeArgs& a, cudaStream_t stream) {
   if (a.int4)
-    return a.d == 128 ? launch_d<128, kInt4Pages>(a, stream) : launch_d<64, kInt4Pages>(a, stream);
+    return a.G <= 4 ? (a.d == 128 ? launch_d<128, kInt4Narrow>(a, stream)
+                                  : launch_d<64, kInt4Narrow>(a, stream))
+                    : (a.d == 128 ? launch_d<128, kInt4Wide>(a, stream)
+                                  : launch_d<64, kInt4Wide>(a, stream));
   if (a.k_scale) return launch_d<128, kE4m3Pages>(a, stream);  // (d 128)
   return a.d == 128 ? launch_d<128, kBf16Pages>(a, stream) : launch_d<64, kBf16Pages>(a, stream);
 }

@@ -383,6 +383,23 @@ def test_a_cache_past_32_bit_offsets():
         assert (np.abs(ref.host(buf.out)[0, 4 * h:4 * h + 4] - want) <= bound).all()
 
 
+@pytest.mark.parametrize("head_dim,group", [(64, 3), (64, 8), (128, 4), (128, 5)])
+def test_long_dense_steps_repeat_bit_for_bit(head_dim, group):
+    """Rings that turn over hundreds of times, every group size's: the three-kernel path gives the same
+    bits on every call, and those of the definition."""
+    case = make(seq_lens=[30000 + 128 * i for i in range(24)], num_q_heads=2 * group, num_kv_heads=2,
+                head_dim=head_dim, topk_percent=1.0, shared_prefix_tokens=8192, seed=115)
+    kv, buf = int4_case(case)
+    step(case, kv, buf)
+    torch.cuda.synchronize()
+    first = buf.out.clone()
+    check(case, kv, buf, units=[(0, 1), (23, 0)])
+    for _ in range(50):
+        step(case, kv, buf)
+        assert torch.equal(buf.out, first)
+    assert int(buf.error_flags.item()) == 0
+
+
 def test_two_streams_at_once():
     """Two requests' steps on two streams over one cache, each with buffers of its own, against the same
     steps one after the other."""
