@@ -559,9 +559,11 @@ __device__ __forceinline__ void merger_loop_int4(const DecodeArgs& a, unsigned c
   const Int4Ring<D, Fmt> ring{smem};
   const Lane ln{lane >> 2, lane & 3};
   constexpr bool kNarrow = Fmt == kInt4Narrow;
-  constexpr int warps = C::kWarps, stride = C::kState;
-  const int slot = !kNarrow ? lane : ln.t < 2 ? ln.g * 2 + ln.t : 0;  // (lanes past the heads: any)
-  const float* mine = ring.state(slot * C::kStateStride);
+  // Groups of at most 4 heads: lanes t and t + 2 hold the same heads and take half of the warps each.
+  constexpr int kShare = kNarrow ? C::kWarps / 2 : C::kWarps;
+  const int slot = kNarrow ? ln.g * 2 + (ln.t & 1) : lane;
+  const float4* mine = reinterpret_cast<const float4*>(
+      ring.state((kNarrow && ln.t >= 2 ? kShare : 0) * C::kState + slot * C::kStateStride));
   for (int32_t seg = 0;; ++seg) {
     if (!mbar_wait(ring.left(), (uint32_t)(seg & 1))) {
       if (lane == 0) raise_flags(a.error_flags, SRKV_EFLAG_TIMEOUT);
@@ -570,25 +572,46 @@ __device__ __forceinline__ void merger_loop_int4(const DecodeArgs& a, unsigned c
     if (*ring.done()) return;
     SoftmaxState<D> st;
     st.reset();
-    for (int w = 0; w < warps; ++w) st.m[0] = fmaxf(st.m[0], mine[w * stride]);
-    for (int w = 0; w < warps; ++w) st.m[1] = fmaxf(st.m[1], mine[w * stride + 1]);
+    float f0[kShare], f1[kShare];  // the shares' references, then their weights
+    float l0[kShare], l1[kShare];
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) {
+      const float4 ml = mine[w * (C::kState / 4)];
+      f0[w] = ml.x, f1[w] = ml.y, l0[w] = ml.z, l1[w] = ml.w;
+      st.m[0] = fmaxf(st.m[0], ml.x);
+      st.m[1] = fmaxf(st.m[1], ml.y);
+    }
+    if constexpr (kNarrow) {
+      st.m[0] = fmaxf(st.m[0], __shfl_xor_sync(0xffffffffu, st.m[0], 2));
+      st.m[1] = fmaxf(st.m[1], __shfl_xor_sync(0xffffffffu, st.m[1], 2));
+    }
     const float b0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
     const float b1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-#pragma unroll 2
-    for (int w = 0; w < warps; ++w) {
-      const float4* p = reinterpret_cast<const float4*>(mine + w * stride);
-      const float4 ml = p[0];
-      const float f0 = fast_exp2(ml.x - b0), f1 = fast_exp2(ml.y - b1);
-      st.l[0] = fmaf(ml.z, f0, st.l[0]);
-      st.l[1] = fmaf(ml.w, f1, st.l[1]);
 #pragma unroll
-      for (int i = 0; i < C::MT; ++i) {
-        const float4 v = p[1 + i];
-        st.acc[i][0] = fmaf(v.x, f0, st.acc[i][0]);
-        st.acc[i][1] = fmaf(v.y, f1, st.acc[i][1]);
-        st.acc[i][2] = fmaf(v.z, f0, st.acc[i][2]);
-        st.acc[i][3] = fmaf(v.w, f1, st.acc[i][3]);
+    for (int w = 0; w < kShare; ++w) {
+      f0[w] = fast_exp2(f0[w] - b0);
+      f1[w] = fast_exp2(f1[w] - b1);
+      st.l[0] = fmaf(l0[w], f0[w], st.l[0]);
+      st.l[1] = fmaf(l1[w], f1[w], st.l[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+      for (int w = 0; w < kShare; ++w) {
+        const float4 v = mine[w * (C::kState / 4) + 1 + i];
+        st.acc[i][0] = fmaf(v.x, f0[w], st.acc[i][0]);
+        st.acc[i][1] = fmaf(v.y, f1[w], st.acc[i][1]);
+        st.acc[i][2] = fmaf(v.z, f0[w], st.acc[i][2]);
+        st.acc[i][3] = fmaf(v.w, f1[w], st.acc[i][3]);
       }
+    if constexpr (kNarrow) {
+      st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 2);
+      st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], 2);
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st.acc[i][c] += __shfl_xor_sync(0xffffffffu, st.acc[i][c], 2);
     }
     const Int4Segment sg = *ring.segment(seg % C::kSegs);
     warp_arrive(ring.merged());
