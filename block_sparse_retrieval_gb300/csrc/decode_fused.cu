@@ -104,7 +104,8 @@ struct FusedCfg {
   // Those loads queue behind the copies already issued (a full ring is ~17 MB over the
   // cluster's SMs), so the rest of the ring waits for them; two stages still keep the
   // consumers fed once they turn to the pages.
-  static constexpr int kEarlyStages = 2;
+  // (4-bit pages are a quarter as large: four of them)
+  static constexpr int kEarlyStages = is_int4(Fmt) ? 4 : 2;
   static_assert(kEarlyStages < C::kStages, "the ring is never filled before the scoring");
 };
 
