@@ -1,20 +1,29 @@
-// decode_int4.cuh -- the consumer warps' loop of the decode over 4-bit pages (int4_page.cuh).
+// decode_int4.cuh -- the decode's stages over 4-bit pages (int4_page.cuh): the ring between the
+// producer warp and the consumers, the consumers' attention, and the merger of their states.
 //
 // softmax(q K^T / sqrt(d)) V with K = klo_t + ks_t ck_td and V = vlo_t + vs_t cv_td (token t, element
 // d, codes c in 0..15):
 //   logit_t = ks_t (sum_d q_d ck_td) + klo_t (sum_d q_d),
 //   out_d   = sum_t (w_t vs_t) cv_td + sum_t w_t vlo_t,     w_t = softmax weight,
 // so both products take the bare codes and a row's scale and minimum enter once per (token, head).
-// What bounds it: per token and kv head 136 bytes arrive (d 128) and 256 codes have to become
-// matrix operands, so a code may cost a few instructions of an SM's 4 a cycle and no more.  A
-// code costs 5/8 of one here: a word masked with 0x000f000f or 0x00f000f0 is two fp16 subnormals,
-// code * 2^-24 or code * 2^-20, operands of m16n8k16 products as they are (subnormals are
-// exact there), and one shift per word reaches the other four.  The powers of two are taken out of
-// the query (16 times smaller at the second kind's elements) and of the weights likewise.
+//
+// What bounds it: per token and kv head 136 bytes arrive (d 128; an SM's share of the bandwidth
+// brings them in 5.8 cycles) and 256 codes have to become matrix operands, so a code may cost a few
+// instructions of an SM's 4 a cycle and no more.  The products are m16n8k16 ones with the group's
+// heads as the N = 8 side, fed from registers: tensor memory would need the codes widened in shared
+// memory first.  A code costs 5/8 of an instruction here: a word masked with 0x000f000f or 0x00f000f0
+// is two fp16 subnormals, code * 2^-24 or code * 2^-20, operands as they are (subnormals are exact
+// there), and one shift per word reaches the other four.  The powers of two are taken out of the query
+// (16 times smaller at the second kind's elements) and of the weights likewise.
+// Measured: dense batch 4 x 131072 (570 MB of slabs) 99.4 us, 85 % of the copy peak, 12.6 instructions
+// a token and kv head; an SM issues on 46 % of its cycles and its warps wait for pages a third of the
+// time (profiles/split_mma_int4_4x65536_dense.md).  At top-k 0.2 43.6 us (54 %): the scoring and the
+// launches around the 23 us of bytes.  The 65536-token layer 13.5 us in one kernel, of which 3.4 are bytes.
 //
 // A page is 4 groups of 32 tokens, one for each warp of a group of 4; the CTA's groups work on
-// consecutive stages (3 of them, 2 for groups of more than 4 heads), so that 3 warps share a scheduler and
-// hide one another's latencies.  A group visits its own stages only.  Stages name their segment (a
+// consecutive stages (3 of them, 2 for groups of more than 4 heads), so that 3 warps share a scheduler
+// and hide one another's latencies (8 warps of 64 tokens: 135 us against 105 in the dense case; 16 of
+// 32 with 96 registers: 146).  A group visits its own stages only.  Stages name their segment (a
 // unit's positions in a list) by its number; a warp that meets a new number leaves its state
 // of the old segment in shared memory and goes on at once, and a merger warp joins the states and
 // writes the partial.  (Draining the groups and merging in them cost 5 us a segment.)
@@ -48,8 +57,8 @@ constexpr float kInt4PScale = 128.f;   // on the fp16 operand: 2^(8 + 7) < 65504
 constexpr int kMergerWarp = kProducerWarp + 1;  // warps past it are consumers 8, 9, ...
 
 struct Int4Stage {
-  int32_t seg;  // number of the segment; kInt4End in `last`: no page, every segment below is over
-  int32_t last;
+  int32_t seg;   // number of the segment
+  int32_t last;  // 1: no page and no stage behind it; every segment below `seg` is over
   int32_t lo, hi, ie, ws;
   int32_t pad[2];
 };
@@ -157,7 +166,7 @@ struct Int4Place {
 // calls it): the lane's page is task t of unit u; kNewUnit in fl opens a segment, kBankB says of which
 // list.  Each lane issues its own page.  A 4-bit page lasts an SM 0.4 us, so what a page costs the
 // producer counts: everything but the wait for the stage, its description and the copy is computed by
-// the lanes side by side.
+// the lanes side by side (one lane for all: 0.75 us a page, 161 us in the dense case).
 template <int D, int Fmt>
 __device__ __forceinline__ void issue_batch_int4(const DecodeArgs& a, unsigned char* smem,
                                                  Int4Place& pl, int first, int last, int32_t u,
@@ -439,8 +448,8 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
       pm[1] *= a1;
       float grow = 1.f;  // old vlim over new
       if (__uint_as_float(top) > vlim) {
-        // the power of two above the largest scale, within 2^-100 .. 2^120
-        const uint32_t e = min(max((top >> 23) + 1u, 27u), 247u);
+        // the power of two above the largest scale, within 2^-100 .. 2^110 (times 2^17 it is finite)
+        const uint32_t e = min(max((top >> 23) + 1u, 27u), 237u);
         const float lim = __uint_as_float(e << 23), inv = __uint_as_float((254u - e) << 23);
         grow = vlim * inv;
         vlim = lim;

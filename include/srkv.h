@@ -397,13 +397,13 @@ srkv_status srkv_retrieval_decode_fp8(const srkv_config* cfg, const void* q, con
  * V values are lo + code * scale.  Both products take the codes as fp16 operands with fp32
  * accumulation; the query enters as fp16 times one power of two for the heads of a group (exact down
  * to 2^-25 of the group's largest magnitude, which must be below 2^101), each softmax weight as fp16
- * times its row's V scale (below 2^120), the scales and minima in fp32.  The selection comes from `reps`,
+ * times its row's V scale (2^-100 to 2^110), the scales and minima in fp32.  The selection comes from `reps`,
  * as in the other calls.
  *   cfg->dtype = SRKV_BF16 (the query and the output), group <= 8, else SRKV_ERR_UNSUPPORTED;
  *   head_dim 64 or 128.  kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)].  A NaN row that is
  *   attended makes the outputs that attend it NaN; rows that are not attended never do.  Other
- *   arguments, ownership, paths (one kernel for small batches, else three), reproducibility and
- *   errors: srkv_retrieval_decode.
+ *   arguments, ownership, errors and reproducibility: srkv_retrieval_decode; the one-kernel path
+ *   takes up to 15 units, and assigns 32 kept blocks to each streaming CTA with the selection.
  */
 srkv_status srkv_retrieval_decode_int4(const srkv_config* cfg, const void* q, const void* kv_int4,
                                        const float* reps, int64_t num_pages,

@@ -486,7 +486,8 @@ def test_a_request_of_nan_rows_alone_is_nan():
 
 
 @pytest.mark.parametrize("scale_q,scale_k,scale_v", [(1e4, 1e-4, 1.0), (1e-6, 1e6, 1e5), (1.0, 1.0, 1e-6),
-                                                     (1.0, 1.0, 1e9), (30.0, 1.0, 1.0)])
+                                                     (1.0, 1.0, 1e9), (30.0, 1.0, 1.0), (1.0, 1.0, 1e30),
+                                                     (1.0, 1.0, 1e-29), (1e-30, 1e30, 1.0), (1e29, 1e-29, 1.0)])
 def test_magnitudes(scale_q, scale_k, scale_v):
     """Queries, keys and values far from 1, and logits that leave a few tokens all the weight."""
     case = make(seq_lens=[3000, 2000], seed=99)
