@@ -673,6 +673,21 @@ def _stream_of(stream, dev: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _table(block_table: torch.Tensor) -> tuple[int, int]:
+    shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"block_table must have shape [*, *], got {list(shape)}")
+    return shape
+
+
+def _vectors(reps: torch.Tensor, Hkv: int, d: int, pages: int) -> None:
+    shape = reps.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != d:
+        raise ValueError(f"reps must have shape [*, {Hkv}, {d}], got {list(shape)}")
+    if shape[0] < pages:
+        raise ValueError(f"reps needs at least {pages} rows, got {shape[0]}")
+
+
 def _int4_pages(cfg: Mapping, kv_int4: torch.Tensor) -> int:
     """Checks the shape of a 4-bit cache; returns its pages."""
     shape = kv_int4.shape
@@ -740,14 +755,12 @@ def append_kv_int4(cfg: Mapping, k_new: torch.Tensor, v_new: torch.Tensor, kv_in
     into position seq_lens[r] of a 4-bit cache, and that page's vector refreshed; the caller then
     advances seq_lens."""
     Hkv, d = cfg["num_kv_heads"], cfg["head_dim"]
-    _shape(block_table, "block_table", None, None)
-    B, max_blocks = block_table.shape
+    B, max_blocks = _table(block_table)
     _need(k_new, "k_new", (B, Hkv, d))
     _need(v_new, "v_new", (B, Hkv, d))
     pages = _int4_pages(cfg, kv_int4)
     _need(seq_lens, "seq_lens", (B,))
-    _shape(reps, "reps", None, Hkv, d)
-    _rows(reps, "reps", pages)
+    _vectors(reps, Hkv, d, pages)
     dev = _device(k_new, "k_new")
     _check(load().srkv_append_kv_int4(
         _cfg_ref(cfg), _ptr(k_new, "k_new", torch.bfloat16, dev),
@@ -765,8 +778,7 @@ def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
                           error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_retrieval_decode_int4: the decode step over a 4-bit cache (bf16 query and output)."""
     Hq, Hkv, d = cfg["num_q_heads"], cfg["num_kv_heads"], cfg["head_dim"]
-    _shape(block_table, "block_table", None, None)
-    B, max_blocks = block_table.shape
+    B, max_blocks = _table(block_table)
     _need(q, "q", (B, Hq, d))
     _need(out, "out", (B, Hq, d))
     pages = _int4_pages(cfg, kv_int4)
@@ -776,8 +788,7 @@ def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
     kmax = sel.shape[-1] if sel.dim() else 0
     _need(sel, "sel", (B, Hkv, kmax))
     _need(nsel, "nsel", (B, Hkv))
-    _shape(reps, "reps", None, Hkv, d)
-    _rows(reps, "reps", pages)
+    _vectors(reps, Hkv, d, pages)
     dev = _device(q, "q")
     _check(load().srkv_retrieval_decode_int4(
         _cfg_ref(cfg), _ptr(q, "q", torch.bfloat16, dev), _ptr(kv_int4, "kv_int4", torch.uint8, dev),
