@@ -302,6 +302,8 @@ CASES = {
     "d64-group-7": lambda: make(seq_lens=[3000, 0, 257, 4444] * 5, num_q_heads=14, num_kv_heads=2,
                                 head_dim=64, init_tokens=100, local_tokens=300, seed=94),
     "shared-prefix": lambda: make(seq_lens=[2000, 3000], shared_prefix_tokens=1024, seed=95),
+    "d64-group-6-one-kernel": lambda: make(seq_lens=[5000, 3333], num_q_heads=6, num_kv_heads=1,
+                                           head_dim=64, seed=105),
     "group-5": lambda: make(seq_lens=[5000, 77], num_q_heads=10, num_kv_heads=2, seed=106),
     "group-2-seventy-requests": lambda: make(seq_lens=[(97 * i) % 1500 for i in range(70)], num_q_heads=4,
                                              num_kv_heads=2, init_tokens=128, local_tokens=200, seed=107),
@@ -485,6 +487,24 @@ def test_a_request_of_nan_rows_alone_is_nan():
         assert torch.isnan(buf.out[0]).all() and torch.isfinite(buf.out[1:]).all()
 
 
+@pytest.mark.parametrize("group", [4, 8])
+def test_a_query_that_is_not_finite_is_its_heads_own(group):
+    case = make(seq_lens=[1500] * 2, num_q_heads=2 * group, topk_percent=1.0, seed=116)
+    case.q[0, group + 1, 5], case.q[1, 2, 0] = float("inf"), float("nan")
+    kv, buf = int4_case(case)
+    step(case, kv, buf)
+    torch.cuda.synchronize()
+    bad = torch.zeros(2, 2 * group, dtype=torch.bool, device=DEV)
+    bad[0, group + 1] = bad[1, 2] = True
+    assert torch.isnan(buf.out[bad]).all() and torch.isfinite(buf.out[~bad]).all()
+    case.q[0, group + 1, 5] = case.q[1, 2, 0] = 0
+    kv, other = int4_case(case)
+    step(case, kv, other)
+    torch.cuda.synchronize()
+    assert torch.equal(other.out[~bad], buf.out[~bad])
+    check(case, kv, other)
+
+
 @pytest.mark.parametrize("scale_q,scale_k,scale_v", [(1e4, 1e-4, 1.0), (1e-6, 1e6, 1e5), (1.0, 1.0, 1e-6),
                                                      (1.0, 1.0, 1e9), (30.0, 1.0, 1.0), (1.0, 1.0, 1e30),
                                                      (1.0, 1.0, 1e-29), (1e-30, 1e30, 1.0), (1e29, 1e-29, 1.0)])
@@ -597,3 +617,15 @@ def test_refusals_reach_python():
     with pytest.raises(ValueError, match="kv_int4 must have shape"):
         srkv.append_kv_int4(cfg, *(x[:1, :, 0].contiguous() for x in (case.k_cache, case.v_cache)),
                             kv[..., :-1], case.block_table, case.seq_lens, buf.reps)
+    with pytest.raises(ValueError, match="contiguous"):
+        srkv.retrieval_decode_int4(case.cfg, case.q, kv.transpose(0, 1).contiguous().transpose(0, 1),
+                                   buf.reps, case.block_table, case.seq_lens, None, buf.sel, buf.nsel,
+                                   buf.out, buf.workspace)
+    with pytest.raises(ValueError, match="must be torch.float32"):
+        srkv.retrieval_decode_int4(case.cfg, case.q, kv, buf.reps.double(), case.block_table,
+                                   case.seq_lens, None, buf.sel, buf.nsel, buf.out, buf.workspace)
+    off = torch.zeros(kv.numel() + 8, dtype=torch.uint8, device=DEV)[8:].view(kv.shape)  # 8-byte aligned
+    with pytest.raises(srkv.SrkvError, match="invalid argument"):
+        srkv.quantize_kv_int4(case.cfg, case.k_cache, case.v_cache, case.page_ids, off)
+    with pytest.raises(ValueError, match="CUDA tensor on device"):
+        srkv.dequantize_kv_int4(case.cfg, kv, case.page_ids.cpu(), case.k_cache, case.v_cache)
