@@ -15,9 +15,9 @@
 // is two fp16 subnormals, code * 2^-24 or code * 2^-20, operands as they are (subnormals are exact
 // there), and one shift per word reaches the other four.  The powers of two are taken out of the query
 // (16 times smaller at the second kind's elements) and of the weights likewise.
-// Measured: dense batch 4 x 131072 (570 MB of slabs) 99.4 us, 85 % of the copy peak, 12.6 instructions
+// Measured: dense batch 4 x 131072 (570 MB of slabs) 98.7 us, 85 % of the copy peak, 12.6 instructions
 // a token and kv head; an SM issues on 46 % of its cycles and its warps wait for pages a third of the
-// time (profiles/split_mma_int4_4x65536_dense.md).  At top-k 0.2 43.6 us (54 %): the scoring and the
+// time.  At top-k 0.2 43.6 us (54 %): the scoring and the
 // launches around the 23 us of bytes.  The 65536-token layer 13.5 us in one kernel, of which 3.4 are bytes.
 //
 // A page is 4 groups of 32 tokens, one for each warp of a group of 4; the CTA's groups work on
@@ -56,7 +56,7 @@ constexpr float kInt4Headroom = 8.f;   // log2 of the most a weight may exceed i
 constexpr float kInt4PScale = 128.f;   // on the fp16 operand: 2^(8 + 7) < 65504
 constexpr int kMergerWarp = kProducerWarp + 1;  // warps past it are consumers 8, 9, ...
 
-struct Int4Stage {
+struct alignas(16) Int4Stage {  // two 16-byte loads
   int32_t seg;   // number of the segment
   int32_t last;  // 1: no page and no stage behind it; every segment below `seg` is over
   int32_t lo, hi, ie, ws;
