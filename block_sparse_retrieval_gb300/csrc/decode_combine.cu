@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int e = 0; e < V; ++e) o[e] += f * s_acc[w][lane * V + e];
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = attended_any(a, lsum) ? o[e] / lsum : 0.f;
+    for (int e = 0; e < V; ++e) v[e] = attended_any<kPartsPerWarp == kInt4Parts>(lsum) ? o[e] / lsum : 0.f;
   }
   TOut* out = static_cast<TOut*>(a.out) + ((int64_t)r * a.Hq + (int64_t)h * G + j) * D + lane * V;
   store_vec<TOut>(out, v, V);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(256)
   }
   float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < V; ++e) v[e] = attended_any(a, l_run) ? acc[e] / l_run : 0.f;
+  for (int e = 0; e < V; ++e) v[e] = attended_any<kPartsPerWarp == kInt4Parts>(l_run) ? acc[e] / l_run : 0.f;
   TOut* out = static_cast<TOut*>(a.out) + ((int64_t)r * a.Hq + (int64_t)h * G + j) * D + lane * V;
   store_vec<TOut>(out, v, V);
 }

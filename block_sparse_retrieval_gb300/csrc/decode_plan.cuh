@@ -140,9 +140,11 @@ struct ListRange {
   int64_t end;    // one past its last
   int32_t u0;     // unit holding `begin`
   int64_t base0;  // first position of unit u0
-  // warp_plan_early only: what unit u0's geometry is made of
-  int32_t len0;   // its request's length, as given
-  int32_t ns0;    // its selection count (list B)
+};
+// ... and what unit u0's geometry is made of (warp_plan_early).
+struct EarlyRange : ListRange {
+  int32_t len0;  // its request's length, as given
+  int32_t ns0;   // its selection count (list B)
 };
 
 // Warp-level plan of one list for CTA `c` of `C`; every lane returns the same range.  When
@@ -189,7 +191,6 @@ __device__ __forceinline__ ListRange warp_plan(const DecodeArgs& a, int list, in
   const int src = who ? __ffs(who) - 1 : 0;
   rg.u0 = __shfl_sync(0xffffffffu, u0, src);
   rg.base0 = __shfl_sync(0xffffffffu, base0, src);
-  rg.len0 = rg.ns0 = 0;
   return rg;
 }
 
@@ -210,9 +211,9 @@ __device__ __forceinline__ PlanLens plan_lens(const DecodeArgs& a) {
 // warp_plan when the selection counts come from the lengths (early): every kv head of a request
 // has the same count, so a lane's chunk is of requests.  One list at a time, so that list B's
 // counts (double-precision steps) are made while list A's first pages are on their way.
-__device__ __forceinline__ ListRange warp_plan_early(const DecodeArgs& a, int list, int64_t c,
-                                                     const PlanLens& pre, int64_t* offsets,
-                                                     uint32_t& eflags) {
+__device__ __forceinline__ EarlyRange warp_plan_early(const DecodeArgs& a, int list, int64_t c,
+                                                      const PlanLens& pre, int64_t* offsets,
+                                                      uint32_t& eflags) {
   const int lane = threadIdx.x & 31;
   const int32_t B = a.batch, H = a.Hkv;
   const int32_t chunk = (B + 31) / 32;
@@ -246,7 +247,7 @@ __device__ __forceinline__ ListRange warp_plan_early(const DecodeArgs& a, int li
     if (lane >= o) incl += y;
   }
   const int64_t C = list_ctas(a, list), excl = incl - local;
-  ListRange r;
+  EarlyRange r;
   r.T = __shfl_sync(0xffffffffu, incl, 31);
   r.begin = cta_begin(c < C ? c : C, r.T, C);  // a CTA c >= C has no position
   r.end = cta_begin(c < C ? c + 1 : C, r.T, C);

@@ -30,7 +30,7 @@ namespace {
 // behind the scoring kernel, in the early mode.)
 template <int D, int Fmt>
 __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned char* smem, int list,
-                                                 const ListRange& rg, Int4Place& pl,
+                                                 const EarlyRange& rg, Int4Place& pl,
                                                  uint32_t& eflags, int lane) {
   const uint32_t bank = list == kListB ? kBankB : 0u;
   const int64_t npos = rg.end - rg.begin;
@@ -140,13 +140,14 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
     if constexpr (!is_int4(Fmt)) {
 #pragma unroll
       for (int list = kListA; list <= kListB; ++list)
-        rgs[list] = a.early ? warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags)
+        rgs[list] = a.early ? (ListRange)warp_plan_early(a, list, blockIdx.x, pre, offsets[list],
+                                                         eflags)
                             : warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets[list],
                                         eflags);
     }
     for (int list = kListA; list <= kListB && !abort; ++list) {
       if constexpr (is_int4(Fmt)) {  // always early; list B is planned once list A is out
-        const ListRange rg = warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags);
+        const EarlyRange rg = warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags);
         stream_list_int4<D, Fmt>(a, smem, list, rg, place, eflags, lane);
         abort = place.abort;
         continue;

@@ -54,8 +54,9 @@ struct ScoreArgs {
 // Grid: one cluster of `cluster_size()` CTAs per (request, kv head) unit.
 // kLarge: shares of more than 128 candidates a CTA, 16 a round of loads and warp (two CTAs an SM
 // at most); smaller shares take 8 a round and keep room for four CTAs.  16 ragged requests of
-// 32k-128k (960 candidates a CTA): a 4-bit step 100.0 -> 96.4 us; 64 requests of 8192 (55 a CTA):
-// 56.6 -> 62.5 us with the large rounds.
+// 32k-128k (960 candidates a CTA): a 4-bit step 100.0 -> 96.4 us, a bf16 one 222.6 -> 220.9; 64
+// requests of 8192 (55 a CTA): 56.6 -> 62.5 us with the large rounds.  Not ahead of an E4M3 decode, whose
+// CTAs no longer fit beside its registers (the ragged batch: 177.0 -> 189.8 us).
 template <typename T, int D, bool kLarge>
 __global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(ScoreArgs a) {
   extern __shared__ uint32_t smem[];
@@ -240,9 +241,11 @@ cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cud
 }
 
 template <typename T, int D>
-cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, cudaStream_t s) {
-  return (a.nmax + cluster - 1) / cluster > 128 ? launch_share<T, D, true>(a, units, cluster, s)
-                                                : launch_share<T, D, false>(a, units, cluster, s);
+cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, bool compressed,
+                   cudaStream_t s) {
+  return !compressed && (a.nmax + cluster - 1) / cluster > 128
+             ? launch_share<T, D, true>(a, units, cluster, s)
+             : launch_share<T, D, false>(a, units, cluster, s);
 }
 
 // Candidates of the longest request the block table allows.
@@ -314,10 +317,11 @@ cudaError_t launch_score_topk(const srkv_config& cfg, const void* q, const float
   const int32_t cluster = cluster_for_batch(nmax, units, compressed);
   if ((int64_t)units * cluster > INT32_MAX) return cudaErrorInvalidValue;
   if (cfg.dtype == SRKV_BF16)
-    return cfg.head_dim == 128 ? launch<__nv_bfloat16, 128>(a, units, cluster, stream)
-                               : launch<__nv_bfloat16, 64>(a, units, cluster, stream);
-  return cfg.head_dim == 128 ? launch<float, 128>(a, units, cluster, stream)
-                             : launch<float, 64>(a, units, cluster, stream);
+    return cfg.head_dim == 128
+               ? launch<__nv_bfloat16, 128>(a, units, cluster, compressed, stream)
+               : launch<__nv_bfloat16, 64>(a, units, cluster, compressed, stream);
+  return cfg.head_dim == 128 ? launch<float, 128>(a, units, cluster, compressed, stream)
+                             : launch<float, 64>(a, units, cluster, compressed, stream);
 }
 
 }  // namespace srkv

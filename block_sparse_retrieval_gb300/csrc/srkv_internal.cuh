@@ -452,9 +452,6 @@ template <bool kInt4>
 __device__ __forceinline__ bool attended_any(float l) {
   return kInt4 ? !(l == 0.f) : l > 0.f;
 }
-__device__ __forceinline__ bool attended_any(const DecodeArgs& a, float l) {
-  return a.int4 ? attended_any<true>(l) : attended_any<false>(l);
-}
 
 enum class PageFormat { kBf16, kE4m3, kInt4 };
 
