@@ -179,8 +179,8 @@ srkv_status srkv_quantize_kv_fp8(const srkv_config* cfg, const void* k_cache,
  * one buffer kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)] bytes, 16-byte aligned; the
  * slab of a (page, kv head) holds its 128 keys and values.  A row x (one token's d values) is held as
  *   lo = min x (bf16),  scale = (max x - lo) / 15 rounded up to bf16,
- *   code = the integer in 0 .. 15 nearest to (x - lo) / scale, ties to even (0 if scale is 0;
- *          difference and quotient in fp32),
+ *   code = the integer in 0 .. 15 nearest to (x - lo) / scale, ties to even (difference and quotient in
+ *          fp32); 0 if the scale is below 2^-126 (a row whose values are all equal, or nearly zero),
  * and stands for lo + code * scale.  A row with an infinity or a NaN, or whose range passes fp32, gets
  * scale = lo = NaN and reads back as NaN.  The 128 d + 1024 bytes of a slab, in order (words are 32 bits;
  * code j of a word at bit 4 (j / 2) + 16 (j mod 2)):

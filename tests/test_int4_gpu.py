@@ -135,6 +135,26 @@ def test_rows_that_are_not_finite_read_back_as_nan():
     assert (np.abs(x - y) <= step[:, None] / 2 + 2.0 ** -8 * np.abs(y) + 2.0 ** -23 * np.abs(x)).all()
 
 
+def test_rows_of_nearly_one_value_are_held_as_their_minimum():
+    """Ranges around 2^-122, where the scale passes 2^-126: codes 0 below it, codes of the definition above.
+    All values are multiples of 2^-133, bf16's smallest, so nothing here rounds."""
+    cfg = config()
+    k, _ = random_pages(cfg, 1, 7)
+    steps = torch.randint(0, 16, k.shape, generator=torch.Generator().manual_seed(8)).to(DEV)
+    steps[..., 0], steps[..., 1] = 0, 15
+    unit = 2.0 ** torch.randint(-133, -120, k.shape[:3], generator=torch.Generator().manual_seed(9)).double()
+    k = (steps.double() * unit.to(DEV)[..., None]).bfloat16()
+    kv = cache(cfg, 1)
+    srkv.quantize_kv_int4(cfg, k, k, torch.zeros(1, dtype=i32, device=DEV), kv)
+    ko, vo = torch.empty_like(k), torch.empty_like(k)
+    srkv.dequantize_kv_int4(cfg, kv, torch.zeros(1, dtype=i32, device=DEV), ko, vo)
+    torch.cuda.synchronize()
+    small = (unit < 2.0 ** -126)[..., None].to(DEV)  # 15 steps of `unit`: the scale is `unit`
+    want = torch.where(small, torch.zeros_like(k), k)
+    assert small.any() and not small.all()
+    assert torch.equal(ko, want) and torch.equal(vo, want)
+
+
 def test_empty_lists_and_batches_do_nothing():
     cfg = config()
     k, v = random_pages(cfg, 2, 4)
