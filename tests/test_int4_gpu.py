@@ -327,6 +327,10 @@ CASES = {
     "group-5": lambda: make(seq_lens=[5000, 77], num_q_heads=10, num_kv_heads=2, seed=106),
     "group-2-seventy-requests": lambda: make(seq_lens=[(97 * i) % 1500 for i in range(70)], num_q_heads=4,
                                              num_kv_heads=2, init_tokens=128, local_tokens=200, seed=107),
+    # prompts on both sides of the dense boundary, several requests to a lane of the plan
+    "prompts-around-the-boundary": lambda: make(seq_lens=[900 + 71 * (i % 23) for i in range(45)],
+                                                prompt_lens=[700 + 40 * (i % 17) for i in range(45)],
+                                                dense_boundary=1000, seed=117),
     # more kept blocks than go out with the selection: the rest from the shared pool
     "long-mostly-kept": lambda: make(seq_lens=[131000], num_q_heads=2, num_kv_heads=1,
                                      topk_percent=0.9, seed=108),
@@ -440,6 +444,67 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (c, kv, buf), w in zip(sets, want):
         assert int(buf.error_flags.item()) == 0 and torch.equal(buf.out, w)
+
+
+def test_streams_given_by_hand_and_no_flags():
+    """Every call with a stream object, then with its handle, neither of them current, and no error flags."""
+    case = make(seq_lens=[2000, 1500], seed=118)
+    kv, buf = int4_case(case)
+    step(case, kv, buf)
+    torch.cuda.synchronize()
+    want, pages = buf.out.clone(), kv.clone()
+    ids = torch.arange(case.num_pages, dtype=i32, device=DEV)
+    new = case.k_cache[:2, :, 5].contiguous()
+    at = case.seq_lens.clone()  # the last blocks have room
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        kv.zero_(), buf.out.zero_()
+        k, v = torch.zeros_like(case.k_cache), torch.zeros_like(case.v_cache)
+        torch.cuda.synchronize()
+        srkv.quantize_kv_int4(case.cfg, case.k_cache, case.v_cache, ids, kv, stream=stream)
+        srkv.retrieval_decode_int4(case.cfg, case.q, kv, buf.reps, case.block_table, case.seq_lens,
+                                   case.prompt_lens, buf.sel, buf.nsel, buf.out, buf.workspace,
+                                   stream=stream)
+        s.synchronize()
+        # (the one-kernel path's fp32 sums may differ in order: a step of bf16, 2^-7, where they round apart)
+        assert torch.equal(kv, pages) and torch.allclose(buf.out.float(), want.float(), rtol=2.0 ** -7, atol=1e-3)
+        reps = buf.reps.clone()
+        torch.cuda.synchronize()
+        srkv.append_kv_int4(case.cfg, new, new, kv, case.block_table, at, reps, stream=stream)
+        srkv.dequantize_kv_int4(case.cfg, kv, ids, k, v, stream=stream)
+        s.synchronize()
+        for r in range(2):
+            L = int(at[r])
+            row = k[int(case.block_table[r, L // 128]), :, L % 128].float()
+            step_of = (new[r].float().amax(-1) - new[r].float().amin(-1)) / 15
+            # half a step of codes, the scale's rounding over 15 codes, and a rounding to bf16
+            assert ((row - new[r].float()).abs() <= (step_of * (0.5 + 2.0 ** -7 * 8))[:, None]
+                    + 2.0 ** -8 * new[r].float().abs().amax(-1, keepdim=True)).all()
+
+
+def test_two_graphs_over_one_workspace():
+    """Steps of two batches captured with the same workspace, replayed in turn on one stream."""
+    cases = [make(seq_lens=[3000, 1234] * 12, seed=119), make(seq_lens=[2500, 0, 129] * 9, seed=120)]
+    sets = [(c, *int4_case(c)) for c in cases]
+    shared = max((b.workspace for _, _, b in sets), key=lambda t: t.numel())
+    want, graphs = [], []
+    s = torch.cuda.Stream()
+    for c, kv, buf in sets:
+        buf.workspace = shared
+        step(c, kv, buf)
+        torch.cuda.synchronize()
+        want.append(buf.out.clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            step(c, kv, buf)
+    for _ in range(10):
+        for _, _, buf in sets:
+            buf.out.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        for (_, _, buf), w in zip(sets, want):
+            assert torch.equal(buf.out, w)
 
 
 def test_a_cache_without_pages_is_refused():
