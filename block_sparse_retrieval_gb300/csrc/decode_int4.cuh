@@ -17,7 +17,7 @@
 // (16 times smaller at the second kind's elements) and of the weights likewise.
 // Measured: dense batch 4 x 131072 (570 MB of slabs) 99 us, 85 % of the copy peak, 12.6 instructions
 // a token and kv head; an SM issues on 46 % of its cycles and its warps wait for pages a third of the
-// time.  At top-k 0.2 43.6 us (54 %): the scoring and the
+// time.  At top-k 0.2 41.0 us (57 %): the scoring and the
 // launches around the 23 us of bytes.  The 65536-token layer 13.5 us in one kernel, of which 3.4 are bytes.
 //
 // A page is 4 groups of 32 tokens, one for each warp of a group of 4; the CTA's groups work on

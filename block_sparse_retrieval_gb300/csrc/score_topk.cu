@@ -29,8 +29,8 @@
 namespace srkv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 256;  // threads that select, and that score a small share
+constexpr int kRound = 8;      // candidates of a warp in one round of loads
 constexpr int kMaxDynamicSmem = 200 * 1024;  // keys + pages of up to 25600 blocks
 
 struct ScoreArgs {
@@ -52,13 +52,16 @@ struct ScoreArgs {
 };
 
 // Grid: one cluster of `cluster_size()` CTAs per (request, kv head) unit.
-// kLarge: shares of more than 128 candidates a CTA, 16 a round of loads and warp (two CTAs an SM
-// at most); smaller shares take 8 a round and keep room for four CTAs.  16 ragged requests of
-// 32k-128k (960 candidates a CTA): a 4-bit step 100.0 -> 96.4 us, a bf16 one 222.6 -> 220.9; 64
-// requests of 8192 (55 a CTA): 56.6 -> 62.5 us with the large rounds.  Not ahead of an E4M3 decode, whose
-// CTAs no longer fit beside its registers (the ragged batch: 177.0 -> 189.8 us).
+// kLarge: shares of more candidates than 256 threads take in one round of loads (64) are scored by
+// 512, of which half go on to select: batch 4 x 131072 (480 a CTA) a 4-bit step 43.7 -> 41.0 us, 16
+// ragged requests of 32k-128k (960 a CTA) 95.9 -> 91.8, in bf16 220.7 -> 218.3; smaller shares keep room
+// for four CTAs an SM.  (1024 threads: 41.4 and 90.6; rounds of 16: 41.0 and 91.8, with twice the
+// registers.)  Not ahead of an E4M3 decode, whose CTAs would not fit beside the registers (16 ragged
+// requests: 177.1 -> 185.2 us).
 template <typename T, int D, bool kLarge>
-__global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(ScoreArgs a) {
+__global__ void __launch_bounds__(kLarge ? 2 * kThreads : kThreads, kLarge ? 2 : 4)
+    score_topk_kernel(ScoreArgs a) {
+  constexpr int kAll = kLarge ? 2 * kThreads : kThreads;
   extern __shared__ uint32_t smem[];
   uint32_t* keys = smem;                                             // [max_blocks], leader
   int32_t* pages = reinterpret_cast<int32_t*>(smem + a.max_blocks);  // [max_blocks]
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(Sc
   const uint32_t crank = cluster_rank(), csize = cluster_size();
   const int32_t u = blockIdx.x / csize;
   const int32_t r = u / a.Hkv, h = u % a.Hkv;
-  for (int i = tid; i < 3 * 256; i += kThreads) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < 3 * 256; i += kAll) (&hist[0][0])[i] = 0;
   cluster_arrive();  // the leader's histograms are zero before any CTA adds to them
 
   // 1. independent loads.  The share of block-table entries is fixed by the longest
@@ -82,9 +85,9 @@ __global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(Sc
   const int32_t s_lo = (int32_t)((int64_t)a.nmax * crank / csize);
   const int32_t s_hi = (int32_t)((int64_t)a.nmax * (crank + 1) / csize);
   const int32_t* bt_r = a.block_table + (int64_t)r * a.max_blocks + b_lo;
-  for (int32_t i = s_lo + tid; i < s_hi; i += kThreads) pages[i - s_lo] = bt_r[i];
+  for (int32_t i = s_lo + tid; i < s_hi; i += kAll) pages[i - s_lo] = bt_r[i];
   const T* q = static_cast<const T*>(a.q) + ((int64_t)r * a.Hq + (int64_t)h * a.G) * D;
-  for (int e = tid; e < D; e += kThreads) {
+  for (int e = tid; e < D; e += kAll) {
     float s = 0.f;
     int j = 0;
     for (; j + 4 <= a.G; j += 4) {  // four independent loads in flight
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(Sc
   // cluster barrier it arrived at).
   if ((k == n && n <= a.kmax) || k == 0) {  // all candidates, or none: no scoring
     if (crank == 0) {
-      for (int32_t i = tid; i < k; i += kThreads) sel_u[i] = b_lo + i;
+      for (int32_t i = tid; i < k; i += kAll) sel_u[i] = b_lo + i;
       if (tid == 0) {
         a.nsel[u] = k;
         raise_flags(a.error_flags, eflags);
@@ -124,15 +127,15 @@ __global__ void __launch_bounds__(kThreads, kLarge ? 2 : 4) score_topk_kernel(Sc
 
   // 2. scores of the share, one warp per candidate, into the leader's keys and histogram
   cluster_wait();
-  eflags |= score_share<D, kWarps, 8, kLarge ? 16 : 8>(
+  eflags |= score_share<D, kAll / 32, 8, kRound>(
       qbar, pages, s_lo, min(s_hi, n), a.reps, a.num_pages, a.Hkv, h, keys, &hist[0][0], nullptr,
       nullptr, warp, lane, [] {}, [](uint32_t) {});
   if (lane == 0 && eflags) raise_flags(a.error_flags, eflags);
   cluster_sync();  // every key and the pass-0 histogram are in the leader
-  if (crank != 0) return;
+  if (crank != 0 || tid >= kThreads) return;
 
   // 3. radix select until the boundary bin is small enough for one warp to rank
-  auto bar = [] { __syncthreads(); };
+  auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   const RadixState rs = radix_narrow<kThreads>(keys, n, k, hist, tid, bar);
 
   // 4. kept blocks written ascending
@@ -224,7 +227,7 @@ cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cud
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(units * cluster));
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(kLarge ? 2 * kThreads : kThreads);
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute attr[2];
@@ -243,7 +246,7 @@ cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cud
 template <typename T, int D>
 cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, bool compressed,
                    cudaStream_t s) {
-  return !compressed && (a.nmax + cluster - 1) / cluster > 128
+  return !compressed && (a.nmax + cluster - 1) / cluster > kThreads / 32 * kRound
              ? launch_share<T, D, true>(a, units, cluster, s)
              : launch_share<T, D, false>(a, units, cluster, s);
 }
