@@ -267,30 +267,31 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
               place.abort = true;
             }
           }
-          issue_batch_int4<D, Fmt>(a, smem, place, early, cnt, u, early > 0 ? 0u : fl, task, eflags, lane);
+          issue_batch_int4<D, Fmt>(a, smem, place, early, cnt, u, early > 0 ? 0u : fl, task, eflags,
+                                   lane);
           abort = place.abort;
         } else {
-        for (int l = 0; l < cnt && !abort; ++l) {
-          PageTask tl;
-          tl.page = __shfl_sync(0xffffffffu, task.page, l);
-          tl.lo = __shfl_sync(0xffffffffu, task.lo, l);
-          tl.hi = __shfl_sync(0xffffffffu, task.hi, l);
-          tl.ie = __shfl_sync(0xffffffffu, task.ie, l);
-          tl.ws = __shfl_sync(0xffffffffu, task.ws, l);
-          if (it == F::kEarlyStages) {  // the rest once this CTA's scores are in
-            k = kept_count();             // (its steps overlap the wait)
-            bool ok = true;
-            if (lane == 0) ok = mbar_wait(scored, 0);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) {
-              eflags |= SRKV_EFLAG_TIMEOUT;
-              abort = true;
-              break;
+          for (int l = 0; l < cnt && !abort; ++l) {
+            PageTask tl;
+            tl.page = __shfl_sync(0xffffffffu, task.page, l);
+            tl.lo = __shfl_sync(0xffffffffu, task.lo, l);
+            tl.hi = __shfl_sync(0xffffffffu, task.hi, l);
+            tl.ie = __shfl_sync(0xffffffffu, task.ie, l);
+            tl.ws = __shfl_sync(0xffffffffu, task.ws, l);
+            if (it == F::kEarlyStages) {  // the rest once this CTA's scores are in
+              k = kept_count();             // (its steps overlap the wait)
+              bool ok = true;
+              if (lane == 0) ok = mbar_wait(scored, 0);
+              if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                eflags |= SRKV_EFLAG_TIMEOUT;
+                abort = true;
+                break;
+              }
             }
+            issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, tl, armed, abort,
+                                eflags, lane);
+            ++it;
           }
-          issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, tl, armed, abort,
-                              eflags, lane);
-          ++it;
-        }
         }
       }
       if (k < 0) k = kept_count();
@@ -332,7 +333,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
         const PageTask t = kept_task(e);
         if constexpr (is_int4(Fmt)) {
           issue_batch_int4<D, Fmt>(a, smem, place, 0, 1, u, place.it == 0 ? kNewUnit : 0u, t, eflags,
-                              lane);
+                                   lane);
           abort = place.abort;
         } else {
           issue_stage_warp<D, Fmt>(a, maps, smem, it, u, it == 0 ? kNewUnit : 0u, t, armed, abort,
@@ -350,7 +351,7 @@ __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
           t.lo = t.hi = t.ie = t.ws = 0;
           if (lane < cnt) t = kept_task(e);
           issue_batch_int4<D, Fmt>(a, smem, place, 0, cnt, u,
-                              place.it == 0 && lane == 0 ? kNewUnit : 0u, t, eflags, lane);
+                                   place.it == 0 && lane == 0 ? kNewUnit : 0u, t, eflags, lane);
           abort = place.abort;
         }
       } else if (k > 0 && !abort) {
@@ -772,8 +773,7 @@ int32_t max_active_clusters(int32_t cs) {
 // Cluster size for `units` units (0 = the fused path does not apply): the largest of 16 down
 // to 4 CTAs per unit such that every cluster is resident at once (on a GB300: 16 CTAs for up
 // to 7 units, 12 for 8, 10 for up to 13, 9 for up to 15, 6 for up to 23, 5 for up to 28, 4
-// for up to 36).  e4m3: compressed pages.  Clusters of fewer than 8 only for bf16 pages, d 128, top-k
-// ratio <= 0.3: there the dynamic pool's balance beats the three kernels on every SM (batch 4
+// for up to 36).  Clusters of fewer than 8 only for bf16 pages, d 128, top-k ratio <= 0.3: there the dynamic pool's balance beats the three kernels on every SM (batch 4
 // x 131072 on clusters of 4: 60.4 against 67.4 us at 0.1, 91.1 against 96.1 at 0.2), while at
 // 0.4 and at 1.0 the three kernels' 152 streaming SMs win (151.3 against 152.6 us, 322
 // against 337).

@@ -152,73 +152,73 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
         abort = place.abort;
         continue;
       } else {
-      // the selection (or, behind the shared-prefix kernel, that kernel's partials) must
-      // exist from here on
-      if (list == kListB && (a.early || a.wait_late)) griddep_wait();
-      const ListRange rg = rgs[list];
-      const int64_t npos = rg.end - rg.begin;
-      if (npos <= 0) continue;
-      const uint32_t bank = list == kListB ? kBankB : 0u;
-      int32_t cu = rg.u0;  // walk state: unit and position within its list
-      int64_t cj = rg.begin - rg.base0;
-      uint32_t dummy = 0;
-      Geom cg = list == kListA ? unit_geom_a(a, cu, dummy) : unit_geom(a, cu, dummy);
-      int32_t cn = list == kListA ? list_a_count(cg) : cg.ns;
-      for (int64_t done = 0; done < npos && !abort; done += 32) {
-        const int cnt = npos - done < 32 ? (int)(npos - done) : 32;
-        // Assign positions done .. done+cnt-1 to lanes (uniform walk over the units).
-        int32_t my_u = 0, my_j = 0;
-        Geom my_g = cg;
-        uint32_t my_flags = 0;
-        for (int l = 0; l < cnt; ++l) {
-          while (cj >= cn) {
-            ++cu;
-            cj = 0;
-            cg = list == kListA ? unit_geom_a(a, cu, dummy) : unit_geom(a, cu, dummy);
-            cn = list == kListA ? list_a_count(cg) : cg.ns;
+        // the selection (or, behind the shared-prefix kernel, that kernel's partials) must
+        // exist from here on
+        if (list == kListB && (a.early || a.wait_late)) griddep_wait();
+        const ListRange rg = rgs[list];
+        const int64_t npos = rg.end - rg.begin;
+        if (npos <= 0) continue;
+        const uint32_t bank = list == kListB ? kBankB : 0u;
+        int32_t cu = rg.u0;  // walk state: unit and position within its list
+        int64_t cj = rg.begin - rg.base0;
+        uint32_t dummy = 0;
+        Geom cg = list == kListA ? unit_geom_a(a, cu, dummy) : unit_geom(a, cu, dummy);
+        int32_t cn = list == kListA ? list_a_count(cg) : cg.ns;
+        for (int64_t done = 0; done < npos && !abort; done += 32) {
+          const int cnt = npos - done < 32 ? (int)(npos - done) : 32;
+          // Assign positions done .. done+cnt-1 to lanes (uniform walk over the units).
+          int32_t my_u = 0, my_j = 0;
+          Geom my_g = cg;
+          uint32_t my_flags = 0;
+          for (int l = 0; l < cnt; ++l) {
+            while (cj >= cn) {
+              ++cu;
+              cj = 0;
+              cg = list == kListA ? unit_geom_a(a, cu, dummy) : unit_geom(a, cu, dummy);
+              cn = list == kListA ? list_a_count(cg) : cg.ns;
+            }
+            const int64_t p = rg.begin + done + l;
+            if (lane == l) {
+              my_u = cu;
+              my_j = (int32_t)cj;
+              my_g = cg;
+              my_flags = bank | ((cj == 0 || p == rg.begin) ? kNewUnit : 0u) |
+                         ((cj == cn - 1 || p == rg.end - 1) ? kSegEnd : 0u);
+            }
+            ++cj;
           }
-          const int64_t p = rg.begin + done + l;
-          if (lane == l) {
-            my_u = cu;
-            my_j = (int32_t)cj;
-            my_g = cg;
-            my_flags = bank | ((cj == 0 || p == rg.begin) ? kNewUnit : 0u) |
-                       ((cj == cn - 1 || p == rg.end - 1) ? kSegEnd : 0u);
+          PageTask task;
+          task.page = -1;
+          task.lo = task.hi = task.ie = task.ws = 0;
+          if (lane < cnt) {
+            const int32_t* bt_r = a.block_table + (int64_t)(my_u / a.Hkv) * a.max_blocks;
+            // Early mode: the count the plan assumed must be the one the scoring wrote.
+            const int32_t written = list == kListB && a.early ? a.nsel[my_u] : my_g.ns;
+            task = list == kListA
+                       ? resolve_a(my_g, my_j, bt_r, total_pages(a), eflags)
+                       : resolve_b(my_g, my_j, a.sel + (int64_t)my_u * a.kmax, bt_r, total_pages(a),
+                                   a.init_tokens, eflags);
+            if (list == kListB && (my_j >= written || (my_j == 0 && written != my_g.ns))) {
+              eflags |= SRKV_EFLAG_SELECTION;
+              if (my_j >= written) task.page = -1;
+            }
           }
-          ++cj;
-        }
-        PageTask task;
-        task.page = -1;
-        task.lo = task.hi = task.ie = task.ws = 0;
-        if (lane < cnt) {
-          const int32_t* bt_r = a.block_table + (int64_t)(my_u / a.Hkv) * a.max_blocks;
-          // Early mode: the count the plan assumed must be the one the scoring wrote.
-          const int32_t written = list == kListB && a.early ? a.nsel[my_u] : my_g.ns;
-          task = list == kListA
-                     ? resolve_a(my_g, my_j, bt_r, total_pages(a), eflags)
-                     : resolve_b(my_g, my_j, a.sel + (int64_t)my_u * a.kmax, bt_r, total_pages(a),
-                                 a.init_tokens, eflags);
-          if (list == kListB && (my_j >= written || (my_j == 0 && written != my_g.ns))) {
-            eflags |= SRKV_EFLAG_SELECTION;
-            if (my_j >= written) task.page = -1;
+          for (int l = 0; l < cnt; ++l) {
+            PageTask t;
+            const int32_t u = __shfl_sync(0xffffffffu, my_u, l);
+            const uint32_t fl = __shfl_sync(0xffffffffu, my_flags, l);
+            t.page = __shfl_sync(0xffffffffu, task.page, l);
+            t.lo = __shfl_sync(0xffffffffu, task.lo, l);
+            t.hi = __shfl_sync(0xffffffffu, task.hi, l);
+            t.ie = __shfl_sync(0xffffffffu, task.ie, l);
+            t.ws = __shfl_sync(0xffffffffu, task.ws, l);
+            // A selected shared-prefix block loads nothing here (the cascade kernel attends
+            // it); it takes a stage only when it opens or closes the unit's segment.
+            if (a.prefix_blocks > 0 && t.page < 0 && !(fl & (kNewUnit | kSegEnd))) continue;
+            issue_stage_warp<D, Fmt>(a, maps, smem, it, u, fl, t, armed, abort, eflags, lane);
+            ++it;
           }
         }
-        for (int l = 0; l < cnt; ++l) {
-          PageTask t;
-          const int32_t u = __shfl_sync(0xffffffffu, my_u, l);
-          const uint32_t fl = __shfl_sync(0xffffffffu, my_flags, l);
-          t.page = __shfl_sync(0xffffffffu, task.page, l);
-          t.lo = __shfl_sync(0xffffffffu, task.lo, l);
-          t.hi = __shfl_sync(0xffffffffu, task.hi, l);
-          t.ie = __shfl_sync(0xffffffffu, task.ie, l);
-          t.ws = __shfl_sync(0xffffffffu, task.ws, l);
-          // A selected shared-prefix block loads nothing here (the cascade kernel attends
-          // it); it takes a stage only when it opens or closes the unit's segment.
-          if (a.prefix_blocks > 0 && t.page < 0 && !(fl & (kNewUnit | kSegEnd))) continue;
-          issue_stage_warp<D, Fmt>(a, maps, smem, it, u, fl, t, armed, abort, eflags, lane);
-          ++it;
-        }
-      }
       }
     }
     if constexpr (is_int4(Fmt)) {
