@@ -614,8 +614,9 @@ def retrieval_decode_fp8(cfg: Mapping, q: torch.Tensor, k_fp8: torch.Tensor,
         "srkv_retrieval_decode_fp8")
 
 
-# The 4-bit cache's calls.  A decode step over it is a few microseconds of GPU time, so its marshalling is kept
-# lean: shapes are compared as tuples, pointers go as integers, equal configurations share a structure.
+# The 4-bit cache's calls.  A step over it is a few microseconds of GPU time, so they are kept lean: shapes are
+# compared as tuples, the tensors of one type are looked at in one loop (what is wrong is found once something
+# is), pointers go as integers, equal configurations share a structure.
 
 def kv_int4_slab_bytes(cfg: Mapping) -> int:
     """Bytes of one (page, kv head) slab of a 4-bit cache."""
@@ -624,11 +625,11 @@ def kv_int4_slab_bytes(cfg: Mapping) -> int:
 
 _configs: dict[tuple, tuple] = {}
 _cfg_values = operator.itemgetter(*CFG_KEYS)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _cfg_ref(cfg: Mapping):
-    """config(cfg) by reference, one structure for equal values."""
-    key = _cfg_values(cfg)
+def _cfg_ref(key: tuple):
+    """The configuration of these values (in the order of CFG_KEYS) by reference, one structure for equal ones."""
     got = _configs.get(key)
     if got is None:
         if len(_configs) >= 64:
@@ -643,26 +644,30 @@ def _need(t: torch.Tensor, name: str, shape: tuple) -> None:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
-def _device(t: torch.Tensor, name: str) -> int:
-    """The device all tensors of a call are on: the current one, on whose streams the library launches."""
-    dev = t.get_device()
+def _held(dev: int, dtype: torch.dtype, *tensors: torch.Tensor) -> bool:
+    """Are all of them contiguous, of that type and on that device, the current one?"""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
+def _refuse(dev: int, first: str, **tensors) -> None:
+    """Raises for the first of name=(tensor, dtype) that the library cannot take; `first` names the tensor
+    whose device `dev` is."""
     if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is a CUDA tensor of device {dev}, not of the current device")
-    return dev
-
-
-def _ptr(t: torch.Tensor | None, name: str, dtype: torch.dtype, dev: int) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{first} must be a CUDA tensor")
+    if dev != _current_device():  # on whose streams the library launches
+        raise ValueError(f"{first} is a CUDA tensor of device {dev}, not of the current device")
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 def _stream_of(stream, dev: int) -> int:
@@ -688,20 +693,20 @@ def _vectors(reps: torch.Tensor, Hkv: int, d: int, pages: int) -> None:
         raise ValueError(f"reps needs at least {pages} rows, got {shape[0]}")
 
 
-def _int4_pages(cfg: Mapping, kv_int4: torch.Tensor) -> int:
+def _int4_pages(kv_int4: torch.Tensor, Hkv: int, slab: int) -> int:
     """Checks the shape of a 4-bit cache; returns its pages."""
     shape = kv_int4.shape
-    want = (cfg["num_kv_heads"], cfg["block_size"] * (cfg["head_dim"] + 8))
-    if len(shape) != 3 or shape[1:] != want:
-        raise ValueError(f"kv_int4 must have shape [*, {want[0]}, {want[1]}], got {list(shape)}")
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != slab:
+        raise ValueError(f"kv_int4 must have shape [*, {Hkv}, {slab}], got {list(shape)}")
     return shape[0]
 
 
-def _bf16_pages(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor) -> int:
-    shape, want = k_cache.shape, (cfg["num_kv_heads"], cfg["block_size"], cfg["head_dim"])
+def _bf16_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, want: tuple) -> int:
+    shape = k_cache.shape
     if len(shape) != 4 or shape[1:] != want:
         raise ValueError(f"k_cache must have shape [*, {', '.join(map(str, want))}], got {list(shape)}")
-    _need(v_cache, "v_cache", tuple(shape))
+    if v_cache.shape != shape:
+        _need(v_cache, "v_cache", tuple(shape))
     return shape[0]
 
 
@@ -711,18 +716,26 @@ def quantize_kv_int4(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_quantize_kv_int4: page page_ids[i] of the bf16 caches into page int4_page_ids[i] (None:
     page_ids[i]) of kv_int4, uint8 [pages][Hkv][kv_int4_slab_bytes(cfg)]."""
-    pages, slabs = _bf16_pages(cfg, k_cache, v_cache), _int4_pages(cfg, kv_int4)
+    key = _cfg_values(cfg)
+    _, Hkv, d, S = key[:4]
+    pages = _bf16_pages(k_cache, v_cache, (Hkv, S, d))
+    slabs = _int4_pages(kv_int4, Hkv, S * (d + 8))
     _shape(page_ids, "page_ids", None)
     n = page_ids.shape[0]
     if int4_page_ids is not None:
         _need(int4_page_ids, "int4_page_ids", (n,))
-    dev = _device(k_cache, "k_cache")
-    _check(load().srkv_quantize_kv_int4(
-        _cfg_ref(cfg), _ptr(k_cache, "k_cache", torch.bfloat16, dev),
-        _ptr(v_cache, "v_cache", torch.bfloat16, dev), pages,
-        _ptr(page_ids, "page_ids", torch.int32, dev), n, _ptr(kv_int4, "kv_int4", torch.uint8, dev),
-        slabs, _ptr(int4_page_ids, "int4_page_ids", torch.int32, dev),
-        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
+    dev = k_cache.get_device()
+    if not (0 <= dev == _current_device() and _held(dev, torch.bfloat16, k_cache, v_cache)
+            and _held(dev, torch.uint8, kv_int4) and _held(dev, torch.int32, page_ids)
+            and (int4_page_ids is None or _held(dev, torch.int32, int4_page_ids))
+            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+        _refuse(dev, "k_cache", k_cache=(k_cache, torch.bfloat16), v_cache=(v_cache, torch.bfloat16),
+                page_ids=(page_ids, torch.int32), kv_int4=(kv_int4, torch.uint8),
+                int4_page_ids=(int4_page_ids, torch.int32), error_flags=(error_flags, torch.int32))
+    _check((_lib or load()).srkv_quantize_kv_int4(
+        _cfg_ref(key), k_cache.data_ptr(), v_cache.data_ptr(), pages, page_ids.data_ptr(), n,
+        kv_int4.data_ptr(), slabs, None if int4_page_ids is None else int4_page_ids.data_ptr(),
+        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)),
         "srkv_quantize_kv_int4")
 
 
@@ -732,19 +745,26 @@ def dequantize_kv_int4(cfg: Mapping, kv_int4: torch.Tensor, int4_page_ids: torch
                        error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_dequantize_kv_int4: page int4_page_ids[i] of kv_int4 into page page_ids[i] (None:
     int4_page_ids[i]) of the bf16 caches."""
-    pages, slabs = _bf16_pages(cfg, k_cache, v_cache), _int4_pages(cfg, kv_int4)
+    key = _cfg_values(cfg)
+    _, Hkv, d, S = key[:4]
+    pages = _bf16_pages(k_cache, v_cache, (Hkv, S, d))
+    slabs = _int4_pages(kv_int4, Hkv, S * (d + 8))
     _shape(int4_page_ids, "int4_page_ids", None)
     n = int4_page_ids.shape[0]
     if page_ids is not None:
         _need(page_ids, "page_ids", (n,))
-    dev = _device(kv_int4, "kv_int4")
-    _check(load().srkv_dequantize_kv_int4(
-        _cfg_ref(cfg), _ptr(kv_int4, "kv_int4", torch.uint8, dev), slabs,
-        _ptr(int4_page_ids, "int4_page_ids", torch.int32, dev), n,
-        _ptr(k_cache, "k_cache", torch.bfloat16, dev),
-        _ptr(v_cache, "v_cache", torch.bfloat16, dev), pages,
-        _ptr(page_ids, "page_ids", torch.int32, dev),
-        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
+    dev = kv_int4.get_device()
+    if not (0 <= dev == _current_device() and _held(dev, torch.bfloat16, k_cache, v_cache)
+            and _held(dev, torch.uint8, kv_int4) and _held(dev, torch.int32, int4_page_ids)
+            and (page_ids is None or _held(dev, torch.int32, page_ids))
+            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+        _refuse(dev, "kv_int4", kv_int4=(kv_int4, torch.uint8), int4_page_ids=(int4_page_ids, torch.int32),
+                k_cache=(k_cache, torch.bfloat16), v_cache=(v_cache, torch.bfloat16),
+                page_ids=(page_ids, torch.int32), error_flags=(error_flags, torch.int32))
+    _check((_lib or load()).srkv_dequantize_kv_int4(
+        _cfg_ref(key), kv_int4.data_ptr(), slabs, int4_page_ids.data_ptr(), n, k_cache.data_ptr(),
+        v_cache.data_ptr(), pages, None if page_ids is None else page_ids.data_ptr(),
+        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)),
         "srkv_dequantize_kv_int4")
 
 
@@ -754,20 +774,29 @@ def append_kv_int4(cfg: Mapping, k_new: torch.Tensor, v_new: torch.Tensor, kv_in
     """srkv_append_kv_int4: each request's new token (bf16 k_new, v_new: [B][Hkv][d]) quantised
     into position seq_lens[r] of a 4-bit cache, and that page's vector refreshed; the caller then
     advances seq_lens."""
-    Hkv, d = cfg["num_kv_heads"], cfg["head_dim"]
+    key = _cfg_values(cfg)
+    _, Hkv, d, S = key[:4]
     B, max_blocks = _table(block_table)
-    _need(k_new, "k_new", (B, Hkv, d))
-    _need(v_new, "v_new", (B, Hkv, d))
-    pages = _int4_pages(cfg, kv_int4)
-    _need(seq_lens, "seq_lens", (B,))
+    rows = (B, Hkv, d)
+    if k_new.shape != rows or v_new.shape != rows or seq_lens.shape != (B,):
+        _need(k_new, "k_new", rows)
+        _need(v_new, "v_new", rows)
+        _need(seq_lens, "seq_lens", (B,))
+    pages = _int4_pages(kv_int4, Hkv, S * (d + 8))
     _vectors(reps, Hkv, d, pages)
-    dev = _device(k_new, "k_new")
-    _check(load().srkv_append_kv_int4(
-        _cfg_ref(cfg), _ptr(k_new, "k_new", torch.bfloat16, dev),
-        _ptr(v_new, "v_new", torch.bfloat16, dev), _ptr(kv_int4, "kv_int4", torch.uint8, dev), pages,
-        _ptr(block_table, "block_table", torch.int32, dev), max_blocks,
-        _ptr(seq_lens, "seq_lens", torch.int32, dev), B, _ptr(reps, "reps", torch.float32, dev),
-        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
+    dev = k_new.get_device()
+    if not (0 <= dev == _current_device() and _held(dev, torch.bfloat16, k_new, v_new)
+            and _held(dev, torch.uint8, kv_int4) and _held(dev, torch.int32, block_table, seq_lens)
+            and _held(dev, torch.float32, reps)
+            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+        _refuse(dev, "k_new", k_new=(k_new, torch.bfloat16), v_new=(v_new, torch.bfloat16),
+                kv_int4=(kv_int4, torch.uint8), block_table=(block_table, torch.int32),
+                seq_lens=(seq_lens, torch.int32), reps=(reps, torch.float32),
+                error_flags=(error_flags, torch.int32))
+    _check((_lib or load()).srkv_append_kv_int4(
+        _cfg_ref(key), k_new.data_ptr(), v_new.data_ptr(), kv_int4.data_ptr(), pages,
+        block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B, reps.data_ptr(),
+        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)),
         "srkv_append_kv_int4")
 
 
@@ -777,28 +806,40 @@ def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
                           nsel: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
                           error_flags: torch.Tensor | None = None, stream=None) -> None:
     """srkv_retrieval_decode_int4: the decode step over a 4-bit cache (bf16 query and output)."""
-    Hq, Hkv, d = cfg["num_q_heads"], cfg["num_kv_heads"], cfg["head_dim"]
+    key = _cfg_values(cfg)
+    Hq, Hkv, d, S = key[:4]
     B, max_blocks = _table(block_table)
-    _need(q, "q", (B, Hq, d))
-    _need(out, "out", (B, Hq, d))
-    pages = _int4_pages(cfg, kv_int4)
-    _need(seq_lens, "seq_lens", (B,))
-    if prompt_lens is not None:
-        _need(prompt_lens, "prompt_lens", (B,))
-    kmax = sel.shape[-1] if sel.dim() else 0
-    _need(sel, "sel", (B, Hkv, kmax))
-    _need(nsel, "nsel", (B, Hkv))
+    heads, units, sel_shape = (B, Hq, d), (B, Hkv), sel.shape
+    if (q.shape != heads or out.shape != heads or seq_lens.shape != (B,) or nsel.shape != units
+            or len(sel_shape) != 3 or sel_shape[:2] != units
+            or (prompt_lens is not None and prompt_lens.shape != (B,))):
+        _need(q, "q", heads)
+        _need(out, "out", heads)
+        _need(seq_lens, "seq_lens", (B,))
+        if prompt_lens is not None:
+            _need(prompt_lens, "prompt_lens", (B,))
+        _need(sel, "sel", (*units, sel_shape[-1] if sel_shape else 0))
+        _need(nsel, "nsel", units)
+    pages = _int4_pages(kv_int4, Hkv, S * (d + 8))
     _vectors(reps, Hkv, d, pages)
-    dev = _device(q, "q")
-    _check(load().srkv_retrieval_decode_int4(
-        _cfg_ref(cfg), _ptr(q, "q", torch.bfloat16, dev), _ptr(kv_int4, "kv_int4", torch.uint8, dev),
-        _ptr(reps, "reps", torch.float32, dev), pages,
-        _ptr(block_table, "block_table", torch.int32, dev), max_blocks,
-        _ptr(seq_lens, "seq_lens", torch.int32, dev),
-        _ptr(prompt_lens, "prompt_lens", torch.int32, dev), B, _ptr(sel, "sel", torch.int32, dev),
-        kmax, _ptr(nsel, "nsel", torch.int32, dev), _ptr(out, "out", torch.bfloat16, dev),
-        _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
-        _ptr(error_flags, "error_flags", torch.int32, dev), _stream_of(stream, dev)),
+    dev = q.get_device()
+    if not (0 <= dev == _current_device() and _held(dev, torch.bfloat16, q, out)
+            and _held(dev, torch.uint8, kv_int4) and _held(dev, torch.float32, reps)
+            and _held(dev, torch.int32, block_table, seq_lens, sel, nsel)
+            and _held(dev, workspace.dtype, workspace)
+            and (prompt_lens is None or _held(dev, torch.int32, prompt_lens))
+            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+        _refuse(dev, "q", q=(q, torch.bfloat16), kv_int4=(kv_int4, torch.uint8), reps=(reps, torch.float32),
+                block_table=(block_table, torch.int32), seq_lens=(seq_lens, torch.int32),
+                prompt_lens=(prompt_lens, torch.int32), sel=(sel, torch.int32), nsel=(nsel, torch.int32),
+                out=(out, torch.bfloat16), workspace=(workspace, workspace.dtype),
+                error_flags=(error_flags, torch.int32))
+    _check((_lib or load()).srkv_retrieval_decode_int4(
+        _cfg_ref(key), q.data_ptr(), kv_int4.data_ptr(), reps.data_ptr(), pages,
+        block_table.data_ptr(), max_blocks, seq_lens.data_ptr(),
+        None if prompt_lens is None else prompt_lens.data_ptr(), B, sel.data_ptr(), sel_shape[2],
+        nsel.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)),
         "srkv_retrieval_decode_int4")
 
 
