@@ -507,6 +507,40 @@ def test_two_graphs_over_one_workspace():
             assert torch.equal(buf.out, w)
 
 
+@pytest.mark.parametrize("prefix", [False, True])
+def test_pages_read_back_feed_the_full_precision_calls(prefix):
+    """Read back into bf16 pages and attended there at once, with nothing between the launches: the bits of
+    the same calls with the stream waited for in between."""
+    case = make(seq_lens=[5000 + 64 * i for i in range(12)], num_q_heads=16, num_kv_heads=4,
+                shared_prefix_tokens=2048, seed=121)
+    kv, _ = int4_case(case)
+    buf = srkv.DecodeBuffers(case.cfg, case.batch, case.max_blocks, case.num_pages, device=DEV, prefix=True)
+    srkv.build_block_reps(case.cfg, case.k_cache, case.page_ids, case.page_valid, buf.reps)
+    ids = torch.arange(case.num_pages, dtype=i32, device=DEV)
+    k, v = torch.empty_like(case.k_cache), torch.empty_like(case.v_cache)
+
+    def run(wait):
+        k.zero_(), v.zero_()
+        srkv.dequantize_kv_int4(case.cfg, kv, ids, k, v, error_flags=buf.error_flags)
+        if wait:
+            torch.cuda.synchronize()
+        if prefix:
+            srkv.retrieval_decode_prefix(case.cfg, case.q, k, v, buf.reps, case.block_table, case.seq_lens,
+                                         None, 16, buf.sel, buf.nsel, buf.out, buf.workspace,
+                                         buf.error_flags)
+        else:
+            srkv.sparse_paged_decode(case.cfg, case.q, k, v, case.block_table, case.seq_lens, buf.sel,
+                                     buf.nsel, buf.out, buf.workspace, buf.error_flags)
+        return buf.out.clone()
+
+    srkv.score_topk(case.cfg, case.q, buf.reps, case.block_table, case.seq_lens, None, buf.sel, buf.nsel)
+    want = run(True)
+    assert torch.isfinite(want).all() and (want != 0).any()
+    for _ in range(10):
+        assert torch.equal(run(False), want)
+    assert int(buf.error_flags.item()) == 0
+
+
 def test_a_cache_without_pages_is_refused():
     case = make(seq_lens=[0, 0, 0], extra_blocks=2, seed=85)
     assert case.num_pages == 0
