@@ -135,15 +135,21 @@ __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
         leave ? reinterpret_cast<int64_t*>(a.ws + a.lay.off_a) : nullptr,
         leave ? reinterpret_cast<int64_t*>(a.ws + a.lay.off_b) : nullptr};
     // Both lists are planned first: list B's counts are the selection counts, known from
-    // the lengths alone in the early mode.
+    // the lengths alone in the early mode.  There one copy of the plan's code serves both lists: two come
+    // from DRAM one after the other when other kernels have used the caches since the last step
+    // (every block of 2 x 65536, caches flushed: 115 -> 110 us, E4M3 91 -> 83; warm alike).  The plan of
+    // a given selection reads more per list and is faster with a copy for each (512 units: 102.5 -> 101.0).
     ListRange rgs[2];
     if constexpr (!is_int4(Fmt)) {
+      if (a.early) {
+#pragma unroll 1
+        for (int list = kListA; list <= kListB; ++list)
+          rgs[list] = warp_plan_early(a, list, blockIdx.x, pre, offsets[list], eflags);
+      } else {
 #pragma unroll
-      for (int list = kListA; list <= kListB; ++list)
-        rgs[list] = a.early ? (ListRange)warp_plan_early(a, list, blockIdx.x, pre, offsets[list],
-                                                         eflags)
-                            : warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets[list],
-                                        eflags);
+        for (int list = kListA; list <= kListB; ++list)
+          rgs[list] = warp_plan(a, list, blockIdx.x, list_ctas(a, list), offsets[list], eflags);
+      }
     }
     for (int list = kListA; list <= kListB && !abort; ++list) {
       if constexpr (is_int4(Fmt)) {  // always early; list B is planned once list A is out
