@@ -246,7 +246,10 @@ cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cud
 template <typename T, int D>
 cudaError_t launch(const ScoreArgs& a, int32_t units, int32_t cluster, bool compressed,
                    cudaStream_t s) {
-  return !compressed && (a.nmax + cluster - 1) / cluster > kThreads / 32 * kRound
+  // (At ratio 1 every candidate is kept and none is scored: the smaller CTAs start sooner, a call for
+  // every block of 4 x 131072 3.67 -> 3.22 us.)
+  return !compressed && a.topk_percent < 1.0 &&
+                 (a.nmax + cluster - 1) / cluster > kThreads / 32 * kRound
              ? launch_share<T, D, true>(a, units, cluster, s)
              : launch_share<T, D, false>(a, units, cluster, s);
 }
