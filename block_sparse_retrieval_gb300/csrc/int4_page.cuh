@@ -5,7 +5,8 @@
 //   lo = min x (bf16, exact),  scale = (max x - lo) / 15 rounded up to bf16,
 //   code = the integer nearest to (x - lo) / scale (difference and quotient in fp32, ties to even),
 // and stands for lo + code * scale.  Rounding the scale up keeps 15 * scale >= max x - lo, so no
-// code is clipped; it costs at most 2^-7 of the step.  One scale per row (as the E4M3 pages have)
+// code is clipped; it costs at most 2^-7 of the step.  (Down where lo + 15 * scale would round past
+// bf16's largest value, so that every finite row reads back finite.)  One scale per row (as the E4M3 pages have)
 // because a row is what a decode step appends.  A constant row has scale 0.  A row that holds
 // an infinity or a NaN, or whose range passes fp32, has scale = lo = NaN: it reads back as
 // NaN and is not hidden behind finite codes.
@@ -53,16 +54,20 @@ __device__ __forceinline__ float int4_scale(uint32_t row) { return bf16_lo(row);
 __device__ __forceinline__ float int4_lo(uint32_t row) { return bf16_hi(row); }
 
 constexpr uint32_t kInt4BadRow = 0x7fc07fc0u;  // scale = lo = NaN
+constexpr float kPastBf16 = 3.39617752923046e38f;  // 2^128 - 2^119: rounds past bf16's last value
 
 // The row's word from its smallest and largest value (exact bf16 values; NaN or an infinity
 // among the row's values shows in one of them).  The scale is the smallest bf16 whose 15-fold (exact
-// in fp32) reaches the range: range / 15 cut to bf16, or the next one.
+// in fp32) reaches the range: range / 15 cut to bf16, or the next one.  Where that would make the
+// row's top read back as infinity, the one below it: the top then lies 15 (1 + 2^-7) < 15.5 steps
+// up at most, so that no code passes 15 either.
 __device__ __forceinline__ uint32_t int4_row(float lo, float hi) {
   const float range = hi - lo;
   uint32_t s = __float_as_uint(range * (1.f / 15.f)) & 0xffff0000u;
   if (15.f * __uint_as_float(s) < range) s += 0x10000u;
-  const bool ok = fmaf(15.f, __uint_as_float(s), fabsf(lo)) < INFINITY;  // false for NaN too
-  return ok ? (s >> 16) | (__float_as_uint(lo) & 0xffff0000u) : kInt4BadRow;
+  if (fmaf(15.f, __uint_as_float(s), lo) >= kPastBf16) s -= 0x10000u;
+  return range < INFINITY ? (s >> 16) | (__float_as_uint(lo) & 0xffff0000u)  // (NaN: false)
+                          : kInt4BadRow;
 }
 
 // About 1 / scale (2^-22 off at most); 0 for a constant or a bad row, and for a scale below 2^-126

@@ -178,7 +178,8 @@ srkv_status srkv_quantize_kv_fp8(const srkv_config* cfg, const void* k_cache,
  * 4-bit pages (the same survey's quantisation of the cache, at half the bits of E4M3).  A 4-bit cache is
  * one buffer kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)] bytes, 16-byte aligned; the
  * slab of a (page, kv head) holds its 128 keys and values.  A row x (one token's d values) is held as
- *   lo = min x (bf16),  scale = (max x - lo) / 15 rounded up to bf16,
+ *   lo = min x (bf16),  scale = (max x - lo) / 15 rounded up to bf16 (the bf16 below that where
+ *          lo + 15 scale would round past bf16's largest value),
  *   code = the integer in 0 .. 15 nearest to (x - lo) / scale, ties to even (difference and quotient in
  *          fp32); 0 if the scale is below 2^-126 (a row whose values are all equal, or nearly zero),
  * and stands for lo + code * scale.  A row with an infinity or a NaN, or whose range passes fp32, gets
