@@ -43,8 +43,10 @@
 //
 // Online softmax with a lazy reference: the weights are 2^(s - m) for a reference m that is raised
 // only when some s exceeds it by 2^8, which a vote finds.  Likewise the fp16 operand of the second
-// product, weight * vs / vlim * 128, has a power of two vlim that is raised when some vs exceeds it.
-// Then the accumulators are rescaled.  The operand stays below 2^15 whatever the values' magnitude.
+// product, weight * vs * 2^11 / lim, has a power of two lim for each head that is raised when some operand
+// passes 2^15 (the same vote).  Then the accumulators are rescaled.  lim follows the products and not
+// the scales: a row with a large scale and next to no weight would otherwise press the other rows'
+// operands below fp16's range.  When the weights' reference rises, lim falls with them.
 #pragma once
 
 #include "decode_mma.cuh"
@@ -53,7 +55,10 @@
 namespace srkv {
 
 constexpr float kInt4Headroom = 8.f;   // log2 of the most a weight may exceed its reference
-constexpr float kInt4PScale = 128.f;   // on the fp16 operand: 2^(8 + 7) < 65504
+// log2 of the fp16 operand at weight * vs = lim: room for products 16 times larger before lim is raised
+// (14, room for 2: 65536-token layer 13.55 -> 13.8 us, dense 99.8 -> 100.7), and the largest product met is
+// 2^10 at least, so that 11 bits stay down to 2^-24 of it (rows g + 8: 2^-20).
+constexpr int kInt4PLog2 = 11;
 constexpr int kMergerWarp = kProducerWarp + 1;  // warps past it are consumers 8, 9, ...
 
 struct alignas(16) Int4Stage {  // two 16-byte loads
@@ -107,6 +112,22 @@ template <int D>
 struct Cfg<D, kInt4Narrow> : Int4Cfg<D, true> {};
 template <int D>
 struct Cfg<D, kInt4Wide> : Int4Cfg<D, false> {};
+
+// 2^n, and 1 / f of a power of two f (normal numbers both).
+__device__ __forceinline__ constexpr float exp2_of(int n) {
+  return n < 0 ? 1.f / (float)(1ull << -n / 2) / (float)(1ull << (-n + 1) / 2)
+               : (float)(1ull << n / 2) * (float)(1ull << (n + 1) / 2);
+}
+__device__ __forceinline__ float inverse_exp2(float f) {
+  return __uint_as_float(0x7f000000u - __float_as_uint(f));
+}
+
+// The larger of each half (NaN if one is).
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t x, uint32_t y) {
+  const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&x),
+                                *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 
 template <int D, int Fmt>
 struct Int4Ring {
@@ -275,10 +296,10 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
   SoftmaxState<D> st;
   st.reset();
   float pm[2] = {0.f, 0.f};  // sum of weight * vlo of the lane's heads and tokens
-  float vlim = 0.f;          // a power of two no vs so far exceeds (0: none seen but zeros)
-  float vf[R];               // vs to the fp16 operand: scale over vlim, 16 times less for rows g + 8
-#pragma unroll
-  for (int x = 0; x < R; ++x) vf[x] = 0.f;
+  // weight * vs to the fp16 operand, for each head: 2^11 over its lim (rows g + 8: 16 times less, here
+  // for kNarrow, in their vs otherwise).  lim is 2^-100 at least, and that at first.
+  const float vf_start = exp2_of(kInt4PLog2 + 100) * (second ? 0.0625f : 1.f);
+  float vf[2] = {vf_start, vf_start};
   uint32_t qb[KW][2][2];     // [word][bits 0..7, 8..15 of its halves][codes * 2^-24, * 2^-20]
 #pragma unroll
   for (int i = 0; i < KW; ++i) qb[i][0][0] = qb[i][0][1] = qb[i][1][0] = qb[i][1][1] = 0u;
@@ -300,15 +321,16 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
     if (st.m[1] == -INFINITY && !(st.l[1] == 0.f)) st.m[1] = 0.f;
     if (seg > 0 && !mbar_wait(ring.merged(), (uint32_t)((seg - 1) & 1))) return false;
     if (!kNarrow || ln.t < 2) {
-      const float unit = vlim * (16777216.f / kInt4PScale);  // 2^24 of the subnormals
+      const float unit0 = exp2_of(24) * inverse_exp2(vf[0]);  // 2^24 of the subnormals
+      const float unit1 = exp2_of(24) * inverse_exp2(vf[1]);
       const int slot = kNarrow ? ln.g * 2 + ln.t : lane;
       float4* p = reinterpret_cast<float4*>(
           ring.state(warp * C::kState + slot * C::kStateStride));
       p[0] = make_float4(st.m[0], st.m[1], st.l[0], st.l[1]);
 #pragma unroll
       for (int i = 0; i < C::MT; ++i)
-        p[1 + i] = make_float4(fmaf(st.acc[i][0], unit, pm[0]), fmaf(st.acc[i][1], unit, pm[1]),
-                               fmaf(st.acc[i][2], unit, pm[0]), fmaf(st.acc[i][3], unit, pm[1]));
+        p[1 + i] = make_float4(fmaf(st.acc[i][0], unit0, pm[0]), fmaf(st.acc[i][1], unit1, pm[1]),
+                               fmaf(st.acc[i][2], unit0, pm[0]), fmaf(st.acc[i][3], unit1, pm[1]));
     }
     warp_arrive(ring.left());
     return true;
@@ -396,7 +418,7 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
           const float f = int4_scale(kr) * qs, lo = int4_lo(kr);
           z[w][j][x][0] = fmaf(c0, f, lo * qm0);
           z[w][j][x][1] = fmaf(c1, f, lo * qm1);
-          vs[w][j][x] = int4_scale(vr);
+          vs[w][j][x] = int4_scale(vr) * (x == 0 ? 1.f : 0.0625f);
           vl[w][j][x] = int4_lo(vr);
         }
       }
@@ -417,8 +439,40 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
             }
           }
     }
-    // ---- raise the references if some weight or scale would pass them
-    float mx0 = -INFINITY, mx1 = -INFINITY, mv = 0.f;
+    // ---- weights, and as operands of the second product times vs: fp16 (half a step is 2^-11 of
+    //      each, independent over the tokens)
+    float ex[NW][2][R][2];
+    auto weigh = [&] {
+      const float base0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
+      const float base1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < R; ++x) {
+            ex[w][j][x][0] = fast_exp2(z[w][j][x][0] - base0);
+            ex[w][j][x][1] = fast_exp2(z[w][j][x][1] - base1);
+          }
+    };
+    uint32_t p[NW][2][R], top;
+    auto operands = [&] {
+      top = 0u;
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < R; ++x) {
+            const float v = vs[w][j][x];
+            p[w][j][x] = pack_f16(ex[w][j][x][0] * v * vf[0], ex[w][j][x][1] * v * vf[1]);
+            top = max_f16x2(top, p[w][j][x]);  // (a NaN stays)
+          }
+    };
+    weigh();
+    operands();
+    // ---- raise the references if some weight or operand passes them
+    float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w)
 #pragma unroll
@@ -427,16 +481,15 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
         for (int x = 0; x < R; ++x) {
           mx0 = fmaxf(mx0, z[w][j][x][0]);
           mx1 = fmaxf(mx1, z[w][j][x][1]);
-          mv = fmaxf(mv, vs[w][j][x]);
         }
-    if (__any_sync(0xffffffffu, mx0 > st.m[0] + kInt4Headroom ||
-                                    mx1 > st.m[1] + kInt4Headroom || mv > vlim)) {
+    const bool past = ((top + 0x08000800u) & 0x80008000u) != 0u;  // a half of 2^15 or more, or NaN
+    if (__any_sync(0xffffffffu,
+                   mx0 > st.m[0] + kInt4Headroom || mx1 > st.m[1] + kInt4Headroom || past)) {
 #pragma unroll
       for (int o = kFirstXor; o < 32; o <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
       }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(mv));  // mv >= 0
       const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
       const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(st.m[0] - n0);
       const float a1 = n1 == -INFINITY ? 1.f : fast_exp2(st.m[1] - n1);
@@ -446,21 +499,36 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
       st.l[1] *= a1;
       pm[0] *= a0;
       pm[1] *= a1;
-      float grow = 1.f;  // old vlim over new
-      if (__uint_as_float(top) > vlim) {
-        // the power of two above the largest scale, within 2^-100 .. 2^110 (times 2^17 it is finite)
-        const uint32_t e = min(max((top >> 23) + 1u, 27u), 237u);
-        const float lim = __uint_as_float(e << 23), inv = __uint_as_float((254u - e) << 23);
-        grow = vlim * inv;
-        vlim = lim;
-        if constexpr (kNarrow) {
-          vf[0] = inv * (second ? kInt4PScale / 16.f : kInt4PScale);
-        } else {
-          vf[0] = inv * kInt4PScale;
-          vf[1] = inv * (kInt4PScale / 16.f);
-        }
+      weigh();
+      float u0 = 0.f, u1 = 0.f;  // the largest weight * vs of these rows
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < R; ++x) {
+            const float v = vs[w][j][x] * (x == 0 ? 1.f : 16.f);
+            u0 = fmaxf(u0, ex[w][j][x][0] * v);
+            u1 = fmaxf(u1, ex[w][j][x][1] * v);
+          }
+#pragma unroll
+      for (int o = kFirstXor; o < 32; o <<= 1) {
+        u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
+        u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
       }
-      const float g0 = a0 * grow, g1 = a1 * grow;
+      // Sets f for products up to u beside accumulators of the old lim times a; returns what they are
+      // multiplied by.  lim becomes the power of two above u or the one below the old lim times a, the
+      // larger one, within 2^-100 .. 2^110: never more than twice the largest product met.
+      auto raise = [&](float& f, float u, float a) {
+        const float one = exp2_of(kInt4PLog2) * (second ? 0.0625f : 1.f);
+        const float old = inverse_exp2(f) * one * a;
+        const uint32_t e = min(max(max((__float_as_uint(u) >> 23) + 1u, __float_as_uint(old) >> 23),
+                                   27u), 237u);
+        const float inv = __uint_as_float((254u - e) << 23);
+        f = inv * one;
+        return old * inv;
+      };
+      const float g0 = raise(vf[0], u0, a0), g1 = raise(vf[1], u1, a1);
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) {
         st.acc[i][0] *= g0;
@@ -468,30 +536,24 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
         st.acc[i][2] *= g0;
         st.acc[i][3] *= g1;
       }
+      operands();
     }
-    const float base0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
-    const float base1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-    // ---- weights, as operands of the second product: fp16 (half a step is 2^-11 of each,
-    //      independent over the tokens)
     uint32_t b[NW][2][2];
 #pragma unroll
     for (int w = 0; w < NW; ++w)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t p[R];
 #pragma unroll
         for (int x = 0; x < R; ++x) {
-          const float e0 = fast_exp2(z[w][j][x][0] - base0);
-          const float e1 = fast_exp2(z[w][j][x][1] - base1);
+          const float e0 = ex[w][j][x][0], e1 = ex[w][j][x][1];
           st.l[0] += e0;
           st.l[1] += e1;
           pm[0] = fmaf(e0, vl[w][j][x], pm[0]);
           pm[1] = fmaf(e1, vl[w][j][x], pm[1]);
-          const float f = vs[w][j][x] * vf[x];
-          p[x] = movmatrix_trans(pack_f16(e0 * f, e1 * f));
+          p[w][j][x] = movmatrix_trans(p[w][j][x]);
         }
-        b[w][j][0] = p[0];
-        b[w][j][1] = kNarrow ? __shfl_xor_sync(0xffffffffu, p[0], 16) : p[R - 1];
+        b[w][j][0] = p[w][j][0];
+        b[w][j][1] = kNarrow ? __shfl_xor_sync(0xffffffffu, p[w][j][0], 16) : p[w][j][R - 1];
       }
     // ---- O^T += V^T . P.  The products of this page's tokens are summed from zero and added in
     // fp32: a tensor core's sums truncate, and over a long segment of nearly equal weights that
@@ -532,9 +594,7 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
       ++cur;
       st.reset();
       pm[0] = pm[1] = 0.f;
-      vlim = 0.f;
-#pragma unroll
-      for (int x = 0; x < R; ++x) vf[x] = 0.f;
+      vf[0] = vf[1] = vf_start;
       if (cur == inf.seg && !inf.last && ok) {
         ok = mbar_wait(ring.query(cur % C::kSegs), (uint32_t)((cur / C::kSegs) & 1));
         load_query(ring.q(cur % C::kSegs));

@@ -397,9 +397,13 @@ srkv_status srkv_retrieval_decode_fp8(const srkv_config* cfg, const void* q, con
  * srkv_retrieval_decode over a 4-bit cache (srkv_quantize_kv_int4, srkv_append_kv_int4): the attended K and
  * V values are lo + code * scale.  Both products take the codes as fp16 operands with fp32
  * accumulation; the query enters as fp16 times one power of two for the heads of a group (exact down
- * to 2^-25 of the group's largest magnitude, which must be below 2^101), each softmax weight as fp16
- * times its row's V scale (2^-100 to 2^110), the scales and minima in fp32.  The selection comes from `reps`,
- * as in the other calls.
+ * to 2^-25 of the group's largest magnitude), each softmax weight times its row's V scale as fp16 (11 bits
+ * down to 2^-20 of the largest such product of the head's tokens that a warp has met, to half a step of
+ * 2^-31 of it below), the scales and minima in fp32.
+ *   Magnitudes: fp32 holds the logits and their parts (|lo| times the query's sum, scale times the query) and the
+ *   sums of up to 2^8 times the values over the attended tokens.  So |q| below 2^101, the largest |q| times a
+ *   row's K scale or minimum below 2^117, |V| below 2^98 (and V scales below 2^-100 lose bits).
+ *   The selection comes from `reps`, as in the other calls.
  *   cfg->dtype = SRKV_BF16 (the query and the output), group <= 8, else SRKV_ERR_UNSUPPORTED;
  *   head_dim 64 or 128.  kv_int4: [num_pages][Hkv][srkv_kv_int4_slab_bytes(cfg)].  A NaN row that is
  *   attended makes the outputs that attend it NaN; rows that are not attended never do.  Other

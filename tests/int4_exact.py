@@ -1,5 +1,7 @@
-"""The 4-bit rows from the sentences of include/srkv.h, in numpy: apart from int4_ref.py, whose test for rows
-that get NaN parameters takes |lo| where the header takes lo (rows from about -1.7e38 down)."""
+"""The 4-bit rows and the step over them from the sentences of include/srkv.h, in 64 bits (numpy): apart from
+int4_ref.py, whose rule for NaN rows takes |lo| where the header takes lo (rows from about -1.7e38 down), and
+whose bound on the step's output charges every rounding at the largest row and logit, so that on long requests
+it passes the outputs themselves."""
 from __future__ import annotations
 
 import numpy as np
@@ -41,3 +43,71 @@ def check_slab(slab, k, v, d):
         np.testing.assert_array_equal(scale, s)
         np.testing.assert_array_equal(lo, m)
         np.testing.assert_array_equal(codes, c)
+
+
+def attended(cfg, L, sel):
+    """The attended tokens of a request as a mask [blocks][128]."""
+    t = np.arange(-(-L // 128) * 128).reshape(-1, 128)
+    W = L - cfg["local_tokens"]
+    kept = np.isin(t // 128, np.asarray(sel, np.int64)) & (t >= cfg["init_tokens"]) & (t < W)
+    return ((t < cfg["init_tokens"]) | (t >= W) | kept) & (t < L)
+
+
+def gather(kv, pages, L, sel, cfg, h, d):
+    """The attended rows of one (request, kv head): codes [N][d] and scales, minima [N] of keys and values."""
+    on = attended(cfg, L, sel)
+    parts = []
+    for b in np.flatnonzero(on.any(1)):
+        k, v, ks, kl, vs, vl = ref.unpack(kv[pages[b], h], d)
+        parts.append([a[on[b]] for a in (k, ks, kl, v, vs, vl)])
+    return [np.concatenate(a) for a in zip(*parts)] if parts else None
+
+
+def query_error(q):
+    """What the group's query [G][d] (bf16 values) loses as fp16 times one power of two: the largest magnitude goes to
+    [2^14, 2^15), elements whose codes sit in the upper nibble of a byte 16 times lower."""
+    top = np.abs(q).max()
+    e = np.clip(np.frexp(top)[1] - 1, -112, 100) if top > 0 else -112
+    f = np.ldexp(np.where(np.arange(q.shape[1]) % 8 // 2 % 2 == 1, 2.0 ** -4, 1.0), 14 - e)
+    return np.abs((q * f).astype(np.float16).astype(np.float64) / f - q)
+
+
+def attend(q, rows):
+    """Output [G][d] over gathered rows, and what the step's arithmetic may differ from it.
+
+    Roundings at half a step each (finfo.eps / 2 of the type), p the softmax weights, every sum one of this
+    unit and head, each element of its own:
+      * logits: what the query loses in fp16; d products and the rows' two parameters in fp32 (2^-23, the
+        tensor cores' sums may truncate) of sum |q| ks ck + |kl| sum |q|; the difference from the reference,
+        2^-24 of it; 2^-20 for the exponentials (the weight's, the merges').  A logit off by e moves the output by
+        p e |V - out|;
+      * weight times scale in fp16: 2^-11 of sum p vs cv; below fp16's normal range half a subnormal step, 2^-25:
+        the largest product p vs that a warp has met is an operand of 2^10 at least, in half of the rows 16 times
+        less, so 2^-31 of the unit's largest product, a token;
+      * sums over the tokens in fp32: a lane adds four times a page (128 tokens), then come some hundred
+        merges: (N / 32 + 128) 2^-24 of sum p (vs cv + |vl|), and of the output for the weights' own sum;
+      * the output in bf16: 2^-8 of it.
+    """
+    G, d = q.shape
+    if rows is None:
+        return np.zeros((G, d)), np.zeros((G, d))
+    kc, ks, kl, vc, vs, vl = rows
+    K, V = kl[:, None] + kc * ks[:, None], vl[:, None] + vc * vs[:, None]
+    z = q @ K.T / np.sqrt(d)
+    p = np.exp(z - z.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    out = p @ V
+    N, kcs, vcs = len(K), kc * ks[:, None], vc * vs[:, None]
+    size = (np.abs(q) @ kcs.T + np.abs(q).sum(1, keepdims=True) * np.abs(kl)) / np.sqrt(d)
+    dz = (query_error(q) @ kcs.T / np.sqrt(d) + (d + 16) * 2.0 ** -23 * size
+          + 2.0 ** -24 * (z.max(1, keepdims=True) - z) + 2.0 ** -20)
+    bound = (2.0 ** -11 * (p @ vcs) + 15 * N * 2.0 ** -31 * (p * vs).max(1, keepdims=True)
+             + (N / 32 + 128) * 2.0 ** -24 * (p @ (vcs + np.abs(vl)[:, None]) + np.abs(out)))
+    for g in range(G):
+        bound[g] += (p[g] * dz[g]) @ np.abs(V - out[g])
+    return out, 1.01 * bound + 2.0 ** -8 * (np.abs(out) + bound)
+
+
+def decode_unit(q, kv, pages, L, sel, cfg, h):
+    """attend() of one (request, kv head): q [G][d] float64, kv [P][Hkv][bytes], its block table row, its kept blocks."""
+    return attend(q, gather(kv, pages, L, sel, cfg, h, q.shape[1]))
