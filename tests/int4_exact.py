@@ -72,7 +72,7 @@ def query_error(q):
     return np.abs((q * f).astype(np.float16).astype(np.float64) / f - q)
 
 
-def attend(q, rows):
+def attend(q, rows, random=False):
     """Output [G][d] over gathered rows, and what the step's arithmetic may differ from it.
 
     Roundings at half a step each (finfo.eps / 2 of the type), p the softmax weights, every sum one of this
@@ -85,8 +85,12 @@ def attend(q, rows):
         the largest product p vs that a warp has met is an operand of 2^10 at least, in half of the rows 16 times
         less, so 2^-31 of the unit's largest product, a token;
       * sums over the tokens in fp32: a lane adds four times a page (128 tokens), then come some hundred
-        merges: (N / 32 + 128) 2^-24 of sum p (vs cv + |vl|), and of the output for the weights' own sum;
+        merges: n = N / 32 + 128 times 2^-24 of sum p (vs cv + |vl|), and of the output for the weights' own sum;
+        the products of a page on the tensor cores, 2^-19 of the same;
       * the output in bf16: 2^-8 of it.
+    random: the rows are random, so that the roundings of different tokens are independent and of mean 0.  N of them,
+    r_t each at most, then pass 8 sqrt(sum r_t^2) with a probability below 2 exp(-32) = 3e-14 (Hoeffding's
+    inequality): 2^-11 8 sqrt(sum (p vs cv)^2) for the operands, 8 sqrt(n) instead of n for the sums.
     """
     G, d = q.shape
     if rows is None:
@@ -101,13 +105,18 @@ def attend(q, rows):
     size = (np.abs(q) @ kcs.T + np.abs(q).sum(1, keepdims=True) * np.abs(kl)) / np.sqrt(d)
     dz = (query_error(q) @ kcs.T / np.sqrt(d) + (d + 16) * 2.0 ** -23 * size
           + 2.0 ** -24 * (z.max(1, keepdims=True) - z) + 2.0 ** -20)
-    bound = (2.0 ** -11 * (p @ vcs) + 15 * N * 2.0 ** -31 * (p * vs).max(1, keepdims=True)
-             + (N / 32 + 128) * 2.0 ** -24 * (p @ (vcs + np.abs(vl)[:, None]) + np.abs(out)))
+    n, operands = N / 32 + 128, p @ vcs
+    if random:
+        n = min(n, 8 * np.sqrt(n))
+        operands = np.minimum(operands, 8 * np.sqrt(p ** 2 @ vcs ** 2))
+    sums = p @ (vcs + np.abs(vl)[:, None])
+    bound = (2.0 ** -11 * operands + 15 * N * 2.0 ** -31 * (p * vs).max(1, keepdims=True)
+             + n * 2.0 ** -24 * (sums + np.abs(out)) + 2.0 ** -19 * sums)
     for g in range(G):
         bound[g] += (p[g] * dz[g]) @ np.abs(V - out[g])
     return out, 1.01 * bound + 2.0 ** -8 * (np.abs(out) + bound)
 
 
-def decode_unit(q, kv, pages, L, sel, cfg, h):
+def decode_unit(q, kv, pages, L, sel, cfg, h, random=False):
     """attend() of one (request, kv head): q [G][d] float64, kv [P][Hkv][bytes], its block table row, its kept blocks."""
-    return attend(q, gather(kv, pages, L, sel, cfg, h, q.shape[1]))
+    return attend(q, gather(kv, pages, L, sel, cfg, h, q.shape[1]), random)
