@@ -57,6 +57,19 @@ def test_long_dense_steps(head_dim, group):
     check(case, kv, buf, [(0, 1), (11, 0), (23, 1)])
 
 
+@pytest.mark.parametrize("group", [4, 8])
+@pytest.mark.parametrize("log_q,log_k,log_v", [(98, -98, 0), (-100, 100, 0), (14, -13, 60), (5, 0, -60), (0, 0, 95), (-20, 20, -96),
+                                               (4, 0, 0), (-8, 0, 0)])
+def test_magnitudes_to_the_documented_ends(group, log_q, log_k, log_v):
+    """Queries to 2^101, keys to match, values to 2^98 and down to V scales of 2^-100, as accurate as at 1."""
+    case = make(seq_lens=[3000, 2000] * (1 if group == 4 else 10), num_q_heads=2 * group, topk_percent=1.0, seed=137)
+    for t, n in ((case.q, log_q), (case.k_cache, log_k), (case.v_cache, log_v)):
+        t.mul_(2.0 ** n)
+    kv, buf = int4_case(case)
+    run(case, kv, buf)
+    check(case, kv, buf, [(0, 0), (1, 1)], share=0.5)
+
+
 # ---- every 32 tokens, once -----------------------------------------------------------------------------
 
 COUNTS = {
