@@ -79,6 +79,9 @@ COUNTS = {
     "odd-bounds": dict(seq_lens=[3001, 2777, 4095, 130, 1, 0] * 5, init_tokens=77, local_tokens=333),
     "odd-bounds-wide": dict(seq_lens=[3001, 2777, 4095, 130, 1, 0] * 5, num_q_heads=14, init_tokens=77,
                             local_tokens=333, head_dim=64),
+    "longest": dict(seq_lens=[25600 * 128 - 5], num_q_heads=4, num_kv_heads=1, topk_percent=1.0),
+    "longest-wide": dict(seq_lens=[25600 * 128 - 5], num_q_heads=8, num_kv_heads=1, head_dim=64, topk_percent=0.7),
+    "a-thousand": dict(seq_lens=[(37 * i) % 700 for i in range(1000)], init_tokens=100, local_tokens=130),
     "seventy": dict(seq_lens=[(97 * i) % 1500 for i in range(70)], num_q_heads=4, init_tokens=128, local_tokens=200),
     **{f"long-{d}-{g}": dict(seq_lens=[30000 + 128 * i for i in range(24)], num_q_heads=2 * g, head_dim=d, topk_percent=1.0)
        for d, g in ((64, 3), (64, 8), (128, 4), (128, 5))},
