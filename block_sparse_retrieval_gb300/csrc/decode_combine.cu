@@ -18,9 +18,10 @@ namespace {
 
 
 constexpr int kWarps = 4;
-// Partials a warp fetches per round of loads.  Behind the 4-bit decode 8: its CTAs hold more registers
-// than the other formats' (14 warps), so a combine CTA of 16 could not wait beside one, and units have
-// fewer partials (13 ragged requests at d 64: a step 27.8 -> 25.8 us).
+// Partials a warp fetches per round of loads.  Behind the 4-bit decode 8 in fewer registers: more combine
+// CTAs at once, and where the decode's CTAs leave room (not the 14 warps at d 128) they wait beside
+// them.  A step, 16 against 8: 64 x 8192 at d 64 56.6 -> 54.3 us, dense 4 x 131072 100.5 -> 99.3, groups of 8
+// heads 4 x 131072 43.1 -> 42.0; none slower.
 constexpr int kParts = 16, kInt4Parts = 8;
 constexpr int32_t kDirectUnits = 64;            // up to here the offsets are derived
 

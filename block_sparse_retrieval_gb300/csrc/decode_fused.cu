@@ -115,7 +115,8 @@ __device__ __forceinline__ int32_t share_begin(int32_t q, int32_t n, int32_t S) 
   return n * q / S;
 }
 
-// Grid: one cluster of CS CTAs per unit; 8 consumer warps + 1 producer warp per CTA.
+// Grid: one cluster of CS CTAs per unit; 8 consumer warps + 1 producer warp per CTA.  (4-bit pages:
+// and the merger warp, and for groups of at most 4 heads 4 more consumers, which neither score nor select.)
 template <int D, int Fmt>
 __global__ void __maxnreg__(128) fused_decode_kernel(const DecodeArgs a,
                                                      const __grid_constant__ TmaMaps maps) {

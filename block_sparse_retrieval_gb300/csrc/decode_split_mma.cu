@@ -1,4 +1,4 @@
-// decode_split_mma.cu -- split phase of sparse paged decode on tensor cores (bf16).
+// decode_split_mma.cu -- split phase of sparse paged decode on tensor cores (bf16, E4M3 and 4-bit pages).
 //
 // openGauss DataVec "KV Cache Query-Based Computation Inference Acceleration", section
 // "Overall Solution": the selected blocks are concatenated with the initial tokens and the
@@ -8,7 +8,7 @@
 // moved by tiled TMA copies into shared memory (decode_mma.cuh).
 //
 // CTA = 1 producer warp + 8 consumer warps, one CTA per SM (persistent), each CTA owning
-// an equal share of all units' page lists (see decode_plan.cuh).
+// an equal share of all units' page lists (see decode_plan.cuh).  Over bf16 and E4M3 pages:
 //   producer: plans list A (initial + window pages) and list B (selected pages) with
 //             warp-level scans, resolves 32 list positions at once (one per lane), and lane 0
 //             streams the pages through the ring.  When the previous kernel is the scoring
@@ -17,6 +17,9 @@
 //             ends the consumers' loop;
 //   consumers: consumer_loop (decode_mma.cuh); at the end of a unit's segment the 8 warps
 //             merge and warp 0 writes the partial to slot unit + CTA of the workspace.
+// Over 4-bit pages (decode_int4.cuh) there are 12 consumer warps, 8 for groups of more than 4 heads, and
+// a merger warp; the producer's lanes issue a page each, and plan list B once list A is out; the
+// consumers leave their states of a segment and the merger writes the partial.
 // Every wait is bounded (SRKV_EFLAG_TIMEOUT).
 #include "decode_int4.cuh"
 #include "decode_mma.cuh"
@@ -97,9 +100,10 @@ __device__ __forceinline__ void stream_list_int4(const DecodeArgs& a, unsigned c
   }
 }
 
-// 128 registers: a quarter-SM register file (16K) then holds this CTA's three warps on one
-// sub-partition (12K) beside one warp of a combine CTA, so the combine is resident and
-// waiting when the last partial is written.
+// 128 registers: a quarter-SM register file (16K) then holds the three warps of a CTA of 9 or 10
+// on one sub-partition (12K) beside one warp of a combine CTA, so the combine is resident and
+// waiting when the last partial is written.  (4-bit pages, groups of at most 4 heads: 14 warps fill two
+// sub-partitions at d 128, and the combine starts as CTAs end; at d 64 they hold 96 registers and leave room.)
 template <int D, int Fmt>
 __global__ void __maxnreg__(128) split_mma_kernel(const DecodeArgs a,
                                                   const __grid_constant__ TmaMaps maps) {

@@ -117,7 +117,8 @@ struct Int4Coder {
     keep = row == kInt4BadRow ? 0u : 0x000f000fu;
   }
   // The pair's codes in the low nibbles of the result's halves.  t = (x - lo) * inv is a few ulps
-  // off the quotient; its remainder (exact) times inv corrects it to the nearest fp32, which is the
+  // off the quotient; its remainder (exact) times inv corrects it to the nearest fp32 (Markstein's step,
+  // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), which is the
   // quotient itself where fp32 holds it, a half-way case among them.  Adding 1.5 * 2^23 rounds to an
   // integer, ties to even, and leaves it in the low bits.
   __device__ __forceinline__ uint32_t pair(uint32_t bf16x2) const {

@@ -209,8 +209,9 @@ cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cud
   if (smem < (size_t)kScoreExclusiveSmem) smem = kScoreExclusiveSmem;
   auto kernel = score_topk_kernel<T, D, kLarge>;
   // Once per device: the largest dynamic shared memory the host checks allow, and the full
-  // shared-memory carveout, so that an SM running this kernel keeps room for a decode CTA
-  // launched early behind it (programmatic launch).
+  // shared-memory carveout, so that an SM is ready for the decode CTA launched early behind this
+  // kernel (programmatic launch): beside a scoring CTA of 256 threads where it fits (E4M3, 4-bit), else
+  // as soon as the scoring leaves the SM.
   static bool configured[128] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -235,7 +236,7 @@ cudaError_t launch_share(const ScoreArgs& a, int32_t units, int32_t cluster, cud
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  // One CTA of a cluster per SM, so that every SM keeps room for a decode CTA.
+  // One CTA of a cluster per SM, so that no two keep a decode CTA from one.
   attr[1].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
   attr[1].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicySpread;
   lc.attrs = attr;

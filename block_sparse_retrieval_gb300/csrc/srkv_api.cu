@@ -254,7 +254,7 @@ srkv_status retrieval_decode(const srkv_config* cfg, const void* q, const void* 
   a.int4 = int4 ? 1 : 0;
   // The scoring kernel, then the decode, which streams list A while the scoring finishes
   // and knows the selection counts it will write from the lengths.  A scoring CTA keeps its
-  // SM to itself, so list A goes to the decode CTAs that find an SM free at once (the grid
+  // SM to itself (kScoreExclusiveSmem), so list A goes to the decode CTAs that find an SM free at once (the grid
   // is scheduled in block order); list B, read once the selection exists, to every CTA.
   a.prompt_lens = prompt_lens;
   a.reps = reps;

@@ -465,8 +465,10 @@ __host__ __device__ __forceinline__ int32_t list_ctas(const DecodeArgs& a, int l
   return list == 0 ? a.ctas_a : a.ctas_b;
 }
 
-// Shared memory a scoring CTA takes at least: with it no decode CTA (about 217 KB) fits on
-// the same SM (228 KB), so the scoring never shares an SM with pages streaming in.
+// Shared memory a scoring CTA takes at least: with it no decode CTA over bf16 pages (209 to 217 KB)
+// fits on the same SM (228 KB), so the scoring never shares an SM with pages streaming in.  (The 4-bit decode
+// of groups of up to 4 heads at d 128 is kept off by its registers.  E4M3 and the other 4-bit CTAs, 184 to
+// 194 KB, fit beside a scoring CTA of 256 threads; list A is divided as if they did not.)
 constexpr int kScoreExclusiveSmem = 16 * 1024;
 
 // k = min(n, ceil(p*n - 1e-9)) with separately rounded operations (no contraction), so
