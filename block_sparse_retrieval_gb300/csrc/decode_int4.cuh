@@ -304,7 +304,7 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
   uint32_t qb[KW][2][2];     // [word][bits 0..7, 8..15 of its halves][codes * 2^-24, * 2^-20]
 #pragma unroll
   for (int i = 0; i < KW; ++i) qb[i][0][0] = qb[i][0][1] = qb[i][1][0] = qb[i][1][1] = 0u;
-  float qs = 0.f;              // factor of the logits (log2 domain)
+  float qs0 = 0.f, qs1 = 0.f;  // factors of the lane's heads' logits (log2 domain)
   float qm0 = 0.f, qm1 = 0.f;  // sum_d q_d of the lane's heads (log2 domain)
 
   // Leaves this warp's state of segment `seg` for the merger (once it is done with the segment
@@ -337,8 +337,8 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
     return true;
   };
 
-  // The unit's query: fp16 with one power of two for all of its heads, the largest magnitude
-  // put into [2^14, 2^15), so that bf16's 8 significant bits stay exact down to 2^-25 of it.
+  // The unit's query: fp16 with a power of two for each head, its largest magnitude put into
+  // [2^14, 2^15), so that bf16's 8 significant bits stay exact down to 2^-25 of it.
   auto load_query = [&](const unsigned char* q) {
     constexpr int QV = D / 32;  // 16-byte loads: elements (D / 4) t .. of the column's head
     const int head = kNarrow ? ln.g & 3 : ln.g;
@@ -359,7 +359,8 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
         sum += bf16_lo(u[e]) + bf16_hi(u[e]);
       }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     qm0 = __shfl_sync(0xffffffffu, sum, 4 * hd) * a.scale_log2;
@@ -367,7 +368,9 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
     int e = (int)(top >> 23) - 127;        // floor(log2 top), -127 for zeros and subnormals
     e = min(max(e, -112), 100);
     const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-    qs = __uint_as_float((uint32_t)(127 + 10 + e) << 23) * a.scale_log2;  // 2^(24 - 14 + e)
+    const float qs = __uint_as_float((uint32_t)(127 + 10 + e) << 23) * a.scale_log2;  // 2^(24 - 14 + e)
+    qs0 = __shfl_sync(0xffffffffu, qs, 4 * hd);
+    qs1 = __shfl_sync(0xffffffffu, qs, 4 * hd + 4);
 #pragma unroll
     for (int i = 0; i < QV; ++i) {
       const uint32_t u[4] = {(uint32_t)w[i].x, (uint32_t)w[i].y, (uint32_t)w[i].z,
@@ -416,9 +419,9 @@ __device__ __forceinline__ void consumer_loop_int4(const DecodeArgs& a, unsigned
           const uint32_t kr = k_rows[32 * w + 4 * j + 2 * x], vr = v_rows[32 * w + 4 * j + 2 * x];
           const float c0 = kNarrow ? (second ? acc[2] : acc[0]) : acc[2 * x];
           const float c1 = kNarrow ? (second ? acc[3] : acc[1]) : acc[2 * x + 1];
-          const float f = int4_scale(kr) * qs, lo = int4_lo(kr);
-          z[w][j][x][0] = fmaf(c0, f, lo * qm0);
-          z[w][j][x][1] = fmaf(c1, f, lo * qm1);
+          const float ks = int4_scale(kr), lo = int4_lo(kr);
+          z[w][j][x][0] = fmaf(c0, ks * qs0, lo * qm0);
+          z[w][j][x][1] = fmaf(c1, ks * qs1, lo * qm1);
           vs[w][j][x] = int4_scale(vr) * (x == 0 ? 1.f : 0.0625f);
           vl[w][j][x] = int4_lo(vr);
         }

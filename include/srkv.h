@@ -396,8 +396,8 @@ srkv_status srkv_retrieval_decode_fp8(const srkv_config* cfg, const void* q, con
 /*
  * srkv_retrieval_decode over a 4-bit cache (srkv_quantize_kv_int4, srkv_append_kv_int4): the attended K and
  * V values are lo + code * scale.  Both products take the codes as fp16 operands with fp32
- * accumulation; the query enters as fp16 times one power of two for the heads of a group (exact down
- * to 2^-25 of the group's largest magnitude), each softmax weight times its row's V scale as fp16 (11 bits
+ * accumulation; the query enters as fp16 times a power of two for each head (exact down
+ * to 2^-25 of the head's largest magnitude), each softmax weight times its row's V scale as fp16 (11 bits
  * down to 2^-20 of the largest such product of the head's tokens that a warp has met, to half a step of
  * 2^-31 of it below), the scales and minima in fp32.
  *   Magnitudes: fp32 holds the logits and their parts (|lo| times the query's sum, scale times the query) and the
