@@ -15,11 +15,11 @@
 // is two fp16 subnormals, code * 2^-24 or code * 2^-20, operands as they are (subnormals are exact
 // there), and one shift per word reaches the other four.  The powers of two are taken out of the query
 // (16 times smaller at the second kind's elements) and of the weights likewise.
-// Measured: dense batch 4 x 131072 (570 MB of slabs) 100 us, 84 % of the copy peak, 12.9 instructions
+// Measured: dense batch 4 x 131072 (570 MB of slabs) 100 us, 84 % of the copy peak, 13.0 instructions
 // a token and kv head; an SM issues on 46 % of its cycles and its warps wait for pages a third of the
-// time.  At top-k 0.2 41.4 us (57 %): the scoring and the
+// time.  At top-k 0.2 41.5 us (57 %): the scoring and the
 // launches around the 23 us of bytes.  The 65536-token layer 13.6 us in one kernel, of which 3.4 are bytes.
-// Groups of 8 heads: dense 110 us (77 %, 14.1 instructions), 42.1 and 14.4.
+// Groups of 8 heads: dense 111 us (76 %, 14.2 instructions), 42.2 and 14.4.
 //
 // A page is 4 groups of 32 tokens, one for each warp of a group of 4; the CTA's groups work on
 // consecutive stages (3 of them, 2 for groups of more than 4 heads), so that 3 warps share a scheduler
