@@ -1,0 +1,241 @@
+// chunk_simt.cu -- attention of a chunk over the paged cache on CUDA cores, in full precision: the fp32 path.
+//
+// A CTA takes a tile of 64 rows and walks its pages 64 tokens at a time: S = Q K^T by 4 x 4 blocks of a thread,
+// a running maximum and sum per row in fp32, O += P V by 4 rows x d / 16 columns of a thread.  Bound by the
+// fp32 rate of the CUDA cores (4 d operations per row and token); shared memory is read 16 bytes at a time with rows
+// padded by one such word, so that neither product waits for it.
+#include "chunk_plan.cuh"
+
+namespace srkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = kChunkTileSimt;
+constexpr int kTok = 64;  // tokens a step
+
+template <int D>
+struct SimtGeom {
+  static constexpr int LD = D + 4;  // padded row of Q, K and V
+  static constexpr int LP = kTok + 4;
+  static constexpr size_t kQ = 0, kK = kQ + sizeof(float) * kRows * LD, kV = kK + sizeof(float) * kTok * LD,
+                          kP = kV + sizeof(float) * kTok * LD, kSmem = kP + sizeof(float) * kRows * LP;
+};
+
+// acc += P V; with kSkip a weight of zero leaves its token out altogether (it may be hidden, and hold a NaN).
+template <int D, bool kSkip>
+__device__ __forceinline__ void add_values(const float* sp, const float* sv, int ty, int tx,
+                                           float (&acc)[4][D / 16]) {
+  using S = SimtGeom<D>;
+  for (int t = 0; t < kTok; t += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * S::LP + t);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(sv + (t + u) * S::LD + c * 64 + tx * 4);
+        const float vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!kSkip || w != 0.f) acc[i][c * 4 + e] = fmaf(w, vv[e], acc[i][c * 4 + e]);
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs a) {
+  using S = SimtGeom<D>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int32_t next;
+  float* sq = reinterpret_cast<float*>(smem + S::kQ);
+  float* sk = reinterpret_cast<float*>(smem + S::kK);
+  float* sv = reinterpret_cast<float*>(smem + S::kV);
+  float* sp = reinterpret_cast<float*>(smem + S::kP);
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  griddep_wait();
+  griddep_launch_dependents();
+  ChunkHead* head = chunk_head(a);
+  const int32_t n_items = head->items;
+  const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.lay.items);
+  uint32_t eflags = 0;
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) next = atomicAdd(&head->next, 1);
+    __syncthreads();
+    if (next >= n_items) break;
+    const ChunkItem it = items[next];
+    const int32_t p_lo = it.p0 + it.row0 / a.G, p_hi = it.p0 + (it.row0 + it.rows - 1) / a.G;
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), c = i % (D / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < it.rows) {
+        const int32_t rho = it.row0 + row;
+        const T* q = static_cast<const T*>(a.q) + (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
+                         (int64_t)(it.head * a.G + rho % a.G) * D;
+        x = load4(q + c * 4);
+      }
+      *reinterpret_cast<float4*>(sq + row * S::LD + c * 4) = x;
+    }
+    int32_t pos[4];
+    float m[4], l[4], acc[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pos[i] = it.p0 + (it.row0 + ty * 4 + i) / a.G;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) acc[i][e] = 0.f;
+    }
+    for (int32_t j = it.j0; j < it.j1; ++j) {
+      const int32_t b = j < it.na ? j : j + it.shift;
+      const int32_t page = a.block_table[(int64_t)it.request * a.max_blocks + b];
+      if (page < 0 || (int64_t)page >= a.num_pages) {
+        eflags |= SRKV_EFLAG_PAGE_RANGE;
+        continue;
+      }
+      const bool masked = chunk_masked(b, p_lo, p_hi, a.init, a.local);
+      const int64_t slab = ((int64_t)page * a.Hkv + it.head) * (int64_t)kBlock * D;
+      for (int t0 = 0; t0 < kBlock; t0 += kTok) {
+        const int32_t tok = b * kBlock + t0;
+        if (tok > p_hi) break;
+        __syncthreads();
+        for (int i = tid; i < kTok * (D / 4); i += kThreads) {
+          const int row = i / (D / 4), c = i % (D / 4);
+          float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+          if (tok + row < it.L) {
+            const int64_t at = slab + (int64_t)(t0 + row) * D + c * 4;
+            k = load4(static_cast<const T*>(a.k_cache) + at);
+            v = load4(static_cast<const T*>(a.v_cache) + at);
+          }
+          *reinterpret_cast<float4*>(sk + row * S::LD + c * 4) = k;
+          *reinterpret_cast<float4*>(sv + row * S::LD + c * 4) = v;
+        }
+        __syncthreads();
+        float s[4][4];  // rows ty * 4 + i, tokens tx + 16 j
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) s[i][jj] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D; c += 4) {
+          float4 q[4], k[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * S::LD + c);
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+            k[jj] = *reinterpret_cast<const float4*>(sk + (tx + 16 * jj) * S::LD + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              s[i][jj] = fmaf(q[i].x, k[jj].x, s[i][jj]);
+              s[i][jj] = fmaf(q[i].y, k[jj].y, s[i][jj]);
+              s[i][jj] = fmaf(q[i].z, k[jj].z, s[i][jj]);
+              s[i][jj] = fmaf(q[i].w, k[jj].w, s[i][jj]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float top = m[i];
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            s[i][jj] *= a.scale_log2;
+            if (masked && !chunk_attends(pos[i], tok + tx + 16 * jj, a.init, a.local)) s[i][jj] = -INFINITY;
+            top = fmaxf(top, s[i][jj]);
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float ref = top == -INFINITY ? 0.f : top;
+          const float w = exp2f(m[i] - ref);
+          float sum = 0.f;
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const float p = exp2f(s[i][jj] - ref);
+            sum += p;
+            sp[(ty * 4 + i) * S::LP + tx + 16 * jj] = p;
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          m[i] = top;
+          l[i] = fmaf(l[i], w, sum);
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) acc[i][e] *= w;
+        }
+        __syncwarp();  // a row's weights come from the 16 lanes that read them
+        if (masked)
+          add_values<D, true>(sp, sv, ty, tx, acc);
+        else
+          add_values<D, false>(sp, sv, ty, tx, acc);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = ty * 4 + i;
+      if (row >= it.rows) continue;
+      if (it.slot >= 0) {
+        const int64_t at = it.slot + row;
+        float* acc_out = reinterpret_cast<float*>(a.ws + a.lay.acc) + at * D;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          *reinterpret_cast<float4*>(acc_out + c * 64 + tx * 4) =
+              make_float4(acc[i][c * 4], acc[i][c * 4 + 1], acc[i][c * 4 + 2], acc[i][c * 4 + 3]);
+        if (tx == 0)
+          *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.ws + a.lay.ml) + 2 * at) =
+              make_float2(m[i], l[i]);
+      } else {
+        const int32_t rho = it.row0 + row;
+        T* out = static_cast<T*>(a.out) +
+                 ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D;
+        const float w = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          store4(out + c * 64 + tx * 4, make_float4(acc[i][c * 4] * w, acc[i][c * 4 + 1] * w,
+                                                    acc[i][c * 4 + 2] * w, acc[i][c * 4 + 3] * w));
+      }
+    }
+  }
+  if (tid == 0) raise_flags(a.error_flags, eflags);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
+  // The shared-memory opt-in is set once per device (not during graph capture).
+  static bool configured[128] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)SimtGeom<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  return launch_pdl(chunk_simt_kernel<T, D>, dim3(a.ctas), dim3(kThreads), SimtGeom<D>::kSmem, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_simt(const ChunkArgs& a, int32_t dtype, cudaStream_t stream) {
+  if (dtype == SRKV_BF16)
+    return a.d == 128 ? launch_d<__nv_bfloat16, 128>(a, stream) : launch_d<__nv_bfloat16, 64>(a, stream);
+  return a.d == 128 ? launch_d<float, 128>(a, stream) : launch_d<float, 64>(a, stream);
+}
+
+}  // namespace srkv

@@ -7,6 +7,7 @@
 
 #include <mutex>
 
+#include "chunk_plan.cuh"
 #include "int4_page.cuh"
 #include "srkv_internal.cuh"
 
@@ -276,6 +277,65 @@ srkv_status retrieval_decode(const srkv_config* cfg, const void* q, const void* 
                         compressed) != cudaSuccess)
     return SRKV_ERR_CUDA;
   return launch_decode(cfg, a, early ? 1 : 0, s);
+}
+
+// Rows of `heads` heads whose tokens lie `stride` elements apart: 16-byte vectors that do not overlap.
+bool strided_ok(const void* p, int64_t stride, const srkv_config& cfg, int32_t heads) {
+  const int64_t per = 16 / (cfg.dtype == SRKV_BF16 ? 2 : 4);
+  return aligned(p, 16) && stride % per == 0 && stride >= (int64_t)heads * cfg.head_dim;
+}
+
+// Both chunk attention calls; `windowed`: the configuration's first tokens and window, else all before.
+srkv_status chunk_attention(const srkv_config* cfg, const void* q, int64_t q_stride,
+                            const void* k_cache, const void* v_cache, int64_t num_pages,
+                            const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* chunk_offsets, int32_t total_tokens,
+                            const int32_t* seq_lens, int32_t batch, void* out, void* workspace,
+                            size_t workspace_bytes, int32_t* error_flags, bool windowed,
+                            cudaStream_t stream) {
+  if (!config_ok(cfg) || batch < 0 || total_tokens < 0 || max_blocks <= 0 ||
+      max_blocks > kMaxBlocks || num_pages < 0)
+    return SRKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_tokens == 0) return SRKV_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !chunk_offsets || !seq_lens || !out ||
+      num_pages == 0)
+    return SRKV_ERR_INVALID_ARG;
+  if (!strided_ok(q, q_stride, *cfg, cfg->num_q_heads) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(out, 16))
+    return SRKV_ERR_INVALID_ARG;
+  ChunkArgs a;
+  const size_t need = chunk_workspace(*cfg, total_tokens, batch, &a.lay);
+  if (need == 0 || num_pages > INT32_MAX || (int64_t)cfg->num_kv_heads * kBlock > INT32_MAX)
+    return SRKV_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SRKV_ERR_WORKSPACE;
+  const int32_t sms = sm_count();
+  if (sms <= 0) return SRKV_ERR_CUDA;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.num_pages = num_pages;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.offsets = chunk_offsets;
+  a.tokens = total_tokens;
+  a.seq_lens = seq_lens;
+  a.batch = batch;
+  a.out = out;
+  a.ws = static_cast<char*>(workspace);
+  a.error_flags = error_flags;
+  a.Hq = cfg->num_q_heads;
+  a.Hkv = cfg->num_kv_heads;
+  a.G = cfg->num_q_heads / cfg->num_kv_heads;
+  a.d = cfg->head_dim;
+  a.init = windowed ? cfg->init_tokens : INT32_MAX;
+  a.local = windowed ? cfg->local_tokens : 0;
+  a.scale_log2 = kLog2e / sqrtf((float)cfg->head_dim);
+  a.tile = chunk_tile(*cfg);
+  a.ctas = 2 * sms;
+  if (launch_chunk_plan(a, stream) != cudaSuccess) return SRKV_ERR_CUDA;
+  if (launch_chunk_simt(a, cfg->dtype, stream) != cudaSuccess) return SRKV_ERR_CUDA;
+  return cuda_status(launch_chunk_merge(a, cfg->dtype, stream));
 }
 
 }  // namespace
@@ -772,6 +832,69 @@ srkv_status srkv_sparse_paged_decode_noalloc(const srkv_config* cfg, const void*
                                         SRKV_NOALLOC_WORKSPACE_BYTES, error_flags, a);
   if (st != SRKV_OK || batch == 0) return st;
   return launch_decode(cfg, a, 0, (cudaStream_t)stream);
+}
+
+srkv_status srkv_append_kv_rope(const srkv_config* cfg, const void* q, int64_t q_stride,
+                                const void* k_new, int64_t k_stride, const void* v_new,
+                                int64_t v_stride, const int32_t* chunk_offsets,
+                                int32_t total_tokens, const double* rope_freqs, int32_t rope_dim,
+                                int32_t interleaved, void* q_out, void* k_cache, void* v_cache,
+                                int64_t num_pages, const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* seq_lens, int32_t batch, float* reps,
+                                int32_t* error_flags, srkv_stream stream) {
+  if (!config_ok(cfg) || batch < 0 || total_tokens < 0 || max_blocks <= 0 ||
+      max_blocks > kMaxBlocks || num_pages < 0 || rope_dim < 0 || rope_dim > cfg->head_dim ||
+      rope_dim % 2)
+    return SRKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_tokens == 0) return SRKV_OK;
+  if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !chunk_offsets || !seq_lens ||
+      !reps || num_pages == 0 || (rope_dim > 0 && !rope_freqs) || !q != !q_out)
+    return SRKV_ERR_INVALID_ARG;
+  if (!strided_ok(k_new, k_stride, *cfg, cfg->num_kv_heads) ||
+      !strided_ok(v_new, v_stride, *cfg, cfg->num_kv_heads) ||
+      (q && !strided_ok(q, q_stride, *cfg, cfg->num_q_heads)) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(reps, 16) ||
+      !aligned(rope_freqs, 8))
+    return SRKV_ERR_INVALID_ARG;
+  if (rope_dim % 16) return SRKV_ERR_UNSUPPORTED;
+  if (((int64_t)total_tokens / kBlock + 2 * (int64_t)batch) * cfg->num_kv_heads + total_tokens >
+      INT32_MAX / 2)
+    return SRKV_ERR_UNSUPPORTED;
+  return cuda_status(launch_append_rope(*cfg, q, q_stride, k_new, k_stride, v_new, v_stride,
+                                        chunk_offsets, total_tokens, rope_freqs, rope_dim,
+                                        interleaved, q_out, k_cache, v_cache, num_pages,
+                                        block_table, max_blocks, seq_lens, batch, reps,
+                                        error_flags, stream));
+}
+
+size_t srkv_chunk_workspace_size(const srkv_config* cfg, int32_t total_tokens, int32_t batch) {
+  if (!config_ok(cfg) || total_tokens < 0 || batch < 0) return 0;
+  return chunk_workspace(*cfg, total_tokens, batch, nullptr);
+}
+
+srkv_status srkv_chunk_attention(const srkv_config* cfg, const void* q, int64_t q_stride,
+                                 const void* k_cache, const void* v_cache, int64_t num_pages,
+                                 const int32_t* block_table, int32_t max_blocks,
+                                 const int32_t* chunk_offsets, int32_t total_tokens,
+                                 const int32_t* seq_lens, int32_t batch, void* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* error_flags,
+                                 srkv_stream stream) {
+  return chunk_attention(cfg, q, q_stride, k_cache, v_cache, num_pages, block_table, max_blocks,
+                         chunk_offsets, total_tokens, seq_lens, batch, out, workspace,
+                         workspace_bytes, error_flags, false, stream);
+}
+
+srkv_status srkv_chunk_attention_window(const srkv_config* cfg, const void* q, int64_t q_stride,
+                                        const void* k_cache, const void* v_cache,
+                                        int64_t num_pages, const int32_t* block_table,
+                                        int32_t max_blocks, const int32_t* chunk_offsets,
+                                        int32_t total_tokens, const int32_t* seq_lens,
+                                        int32_t batch, void* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* error_flags,
+                                        srkv_stream stream) {
+  return chunk_attention(cfg, q, q_stride, k_cache, v_cache, num_pages, block_table, max_blocks,
+                         chunk_offsets, total_tokens, seq_lens, batch, out, workspace,
+                         workspace_bytes, error_flags, true, stream);
 }
 
 }  // extern "C"

@@ -552,6 +552,16 @@ cudaError_t launch_append_kv(const srkv_config& cfg, const void* k_new, const vo
                              const int32_t* seq_lens, int32_t batch, float* reps,
                              int32_t* error_flags, cudaStream_t stream);
 
+// Chunks of new tokens, rotated and appended (append_rope.cu); q may be null.
+cudaError_t launch_append_rope(const srkv_config& cfg, const void* q, int64_t q_stride,
+                               const void* k_new, int64_t k_stride, const void* v_new,
+                               int64_t v_stride, const int32_t* offsets, int32_t tokens,
+                               const double* freqs, int32_t rope_dim, int32_t interleaved,
+                               void* q_out, void* k_cache, void* v_cache, int64_t num_pages,
+                               const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seq_lens, int32_t batch, float* reps,
+                               int32_t* error_flags, cudaStream_t stream);
+
 cudaError_t launch_score_topk(const srkv_config& cfg, const void* q, const float* reps,
                               int64_t num_pages, const int32_t* block_table,
                               int32_t max_blocks, const int32_t* seq_lens,

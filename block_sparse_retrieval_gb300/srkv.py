@@ -23,6 +23,7 @@ CFG_KEYS = ("num_q_heads", "num_kv_heads", "head_dim", "block_size", "init_token
             "local_tokens", "topk_percent", "dense_boundary", "dtype")
 BF16, F32 = 0, 1
 EFLAG_PAGE_RANGE, EFLAG_SEQ_LEN, EFLAG_SELECTION, EFLAG_TIMEOUT, EFLAG_PREFIX = 1, 2, 4, 8, 16
+EFLAG_CHUNK = 32
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
           3: "workspace missing or too small", 4: "CUDA error"}
 EXPORTS = ("srkv_default_config", "srkv_status_string", "srkv_topk_count",
@@ -35,7 +36,8 @@ EXPORTS = ("srkv_default_config", "srkv_status_string", "srkv_topk_count",
            "srkv_prefix_decode_workspace_size", "srkv_sparse_paged_decode_prefix",
            "srkv_retrieval_decode_prefix", "srkv_host_staging_size",
            "srkv_retrieval_decode_host", "srkv_kv_int4_slab_bytes", "srkv_quantize_kv_int4",
-           "srkv_dequantize_kv_int4", "srkv_append_kv_int4", "srkv_retrieval_decode_int4")
+           "srkv_dequantize_kv_int4", "srkv_append_kv_int4", "srkv_retrieval_decode_int4", "srkv_append_kv_rope",
+           "srkv_chunk_workspace_size", "srkv_chunk_attention", "srkv_chunk_attention_window")
 NOALLOC_WORKSPACE_BYTES = 16 << 20
 
 
@@ -124,6 +126,14 @@ def load() -> ctypes.CDLL:
                                         _I32, _P, _P, _P]
     lib.srkv_retrieval_decode_int4.argtypes = [ctypes.POINTER(Config), _P, _P, _P, _I64, _P, _I32,
                                                _P, _P, _I32, _P, _I32, _P, _P, _P, _SZ, _P, _P]
+    lib.srkv_append_kv_rope.argtypes = [ctypes.POINTER(Config), _P, _I64, _P, _I64, _P, _I64, _P,
+                                        _I32, _P, _I32, _I32, _P, _P, _P, _I64, _P, _I32, _P, _I32,
+                                        _P, _P, _P]
+    lib.srkv_chunk_workspace_size.argtypes = [ctypes.POINTER(Config), _I32, _I32]
+    lib.srkv_chunk_workspace_size.restype = _SZ
+    for name in ("srkv_chunk_attention", "srkv_chunk_attention_window"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(Config), _P, _I64, _P, _P, _I64, _P, _I32, _P,
+                                       _I32, _P, _I32, _P, _P, _SZ, _P, _P]
     lib.srkv_selftest_wait_timeout.argtypes = [_P, _P]
     lib.srkv_selftest_wait_timeout.restype = ctypes.c_int
     for name in ("srkv_build_block_reps", "srkv_score_topk", "srkv_sparse_paged_decode",
@@ -132,7 +142,8 @@ def load() -> ctypes.CDLL:
                  "srkv_retrieval_decode_fp8", "srkv_sparse_paged_decode_prefix",
                  "srkv_retrieval_decode_prefix", "srkv_retrieval_decode_host",
                  "srkv_append_kv", "srkv_quantize_kv_int4", "srkv_dequantize_kv_int4",
-                 "srkv_append_kv_int4", "srkv_retrieval_decode_int4"):
+                 "srkv_append_kv_int4", "srkv_retrieval_decode_int4", "srkv_append_kv_rope",
+                 "srkv_chunk_attention", "srkv_chunk_attention_window"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -321,6 +332,141 @@ def append_kv(cfg: Mapping, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: t
         _dev(seq_lens, "seq_lens", torch.int32), seq_lens.numel(),
         _dev(reps, "reps", torch.float32), _dev(error_flags, "error_flags", torch.int32),
         _stream(stream)), "srkv_append_kv")
+
+
+def _token_rows(t: torch.Tensor | None, name: str, dtype: torch.dtype, device: torch.device):
+    """A packed [tokens][heads][d] tensor whose heads lie side by side, tokens any stride apart: its
+    pointer and that stride in elements."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    n, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), s0 if n > 1 else heads * d
+
+
+def _chunk_device(first: torch.Tensor, **others) -> torch.device:
+    """The one device of a chunk call's tensors: the current one, whose stream the call goes to."""
+    if not first.is_cuda:
+        raise ValueError("q, k_new and the caches must be CUDA tensors")
+    dev = first.device
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor,
+                   rope_freqs: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_table: torch.Tensor, chunk_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                   reps: torch.Tensor, q_out: torch.Tensor | None = None,
+                   error_flags: torch.Tensor | None = None, stream=None, *,
+                   interleaved: bool = False) -> None:
+    """Rotates a ragged chunk of new tokens to their positions, writes keys and values to the pages and
+    refreshes the vectors of the pages written; the rotated queries go to q_out.
+
+    Request r brings rows [chunk_offsets[r], chunk_offsets[r + 1]) of q [T][Hq][d], k_new and v_new
+    [T][Hkv][d] (views of a fused projection will do: a token's heads are contiguous, tokens any stride
+    apart), at positions seq_lens[r] on; the caller then adds the chunk's tokens to seq_lens.
+    rope_freqs: float64 [rope_dim / 2], radians per token (None: no rotation); interleaved: pairs
+    (2j, 2j + 1) instead of (j, j + rope_dim / 2).  q None: no queries."""
+    Hq, Hkv, S, d = _cache_dims(cfg)
+    _shape(block_table, "block_table", None, None)
+    B = block_table.shape[0]
+    _shape(k_new, "k_new", None, Hkv, d)
+    T = k_new.shape[0]
+    _shape(q, "q", T, Hq, d)
+    _shape(q_out, "q_out", T, Hq, d)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    _shape(v_new, "v_new", T, Hkv, d)
+    _shape(rope_freqs, "rope_freqs", None)
+    _shape(k_cache, "k_cache", None, Hkv, S, d)
+    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
+    _shape(chunk_offsets, "chunk_offsets", B + 1)
+    _shape(seq_lens, "seq_lens", B)
+    _shape(reps, "reps", None, Hkv, d)
+    _rows(reps, "reps", k_cache.shape[0])
+    _shape(error_flags, "error_flags", 1)
+    dev = _chunk_device(k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
+                        chunk_offsets=chunk_offsets, rope_freqs=rope_freqs, reps=reps, q_out=q_out,
+                        error_flags=error_flags)
+    c = config(cfg)
+    st = _store_dtype(cfg)
+    qp, qs = _token_rows(q, "q", st, dev)
+    kp, ks = _token_rows(k_new, "k_new", st, dev)
+    vp, vs = _token_rows(v_new, "v_new", st, dev)
+    _check(load().srkv_append_kv_rope(
+        ctypes.byref(c), qp, qs, kp, ks, vp, vs, _dev(chunk_offsets, "chunk_offsets", torch.int32), T,
+        _dev(rope_freqs, "rope_freqs", torch.float64),
+        0 if rope_freqs is None else 2 * rope_freqs.numel(), int(interleaved),
+        _dev(q_out, "q_out", st), _dev(k_cache, "k_cache", st), _dev(v_cache, "v_cache", st),
+        k_cache.shape[0], _dev(block_table, "block_table", torch.int32), block_table.shape[1],
+        _dev(seq_lens, "seq_lens", torch.int32), B, _dev(reps, "reps", torch.float32),
+        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), "srkv_append_kv_rope")
+
+
+def chunk_workspace_size(cfg: Mapping, total_tokens: int, batch: int) -> int:
+    """Workspace bytes of the chunk attention calls for `total_tokens` rows of `batch` requests."""
+    c = config(cfg)
+    return int(load().srkv_chunk_workspace_size(ctypes.byref(c), total_tokens, batch))
+
+
+def _chunk_attention(name: str, cfg: Mapping, q, k_cache, v_cache, block_table, chunk_offsets,
+                     seq_lens, out, workspace, error_flags, stream) -> None:
+    Hq, Hkv, S, d = _cache_dims(cfg)
+    _shape(block_table, "block_table", None, None)
+    B = block_table.shape[0]
+    _shape(q, "q", None, Hq, d)
+    _shape(k_cache, "k_cache", None, Hkv, S, d)
+    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
+    _shape(chunk_offsets, "chunk_offsets", B + 1)
+    _shape(seq_lens, "seq_lens", B)
+    _shape(out, "out", q.shape[0], Hq, d)
+    _shape(error_flags, "error_flags", 1)
+    dev = _chunk_device(k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
+                        chunk_offsets=chunk_offsets, out=out, workspace=workspace,
+                        error_flags=error_flags)
+    c = config(cfg)
+    st = _store_dtype(cfg)
+    qp, qs = _token_rows(q, "q", st, dev)
+    _check(getattr(load(), name)(
+        ctypes.byref(c), qp, qs, _dev(k_cache, "k_cache", st), _dev(v_cache, "v_cache", st),
+        k_cache.shape[0], _dev(block_table, "block_table", torch.int32), block_table.shape[1],
+        _dev(chunk_offsets, "chunk_offsets", torch.int32), q.shape[0],
+        _dev(seq_lens, "seq_lens", torch.int32), B, _dev(out, "out", st),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), name)
+
+
+def chunk_attention(cfg: Mapping, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, chunk_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                    out: torch.Tensor, workspace: torch.Tensor,
+                    error_flags: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of a ragged chunk of new tokens over the paged cache that holds them: rows
+    [chunk_offsets[r], chunk_offsets[r + 1]) of q [T][Hq][d] are the last tokens of request r's
+    seq_lens[r].  workspace: chunk_workspace_size(cfg, T, B) bytes."""
+    _chunk_attention("srkv_chunk_attention", cfg, q, k_cache, v_cache, block_table, chunk_offsets,
+                     seq_lens, out, workspace, error_flags, stream)
+
+
+def chunk_attention_window(cfg: Mapping, q: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, block_table: torch.Tensor,
+                           chunk_offsets: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
+                           workspace: torch.Tensor, error_flags: torch.Tensor | None = None,
+                           stream=None) -> None:
+    """chunk_attention over the configuration's first tokens (init_tokens) and each position's window
+    (local_tokens) alone."""
+    _chunk_attention("srkv_chunk_attention_window", cfg, q, k_cache, v_cache, block_table,
+                     chunk_offsets, seq_lens, out, workspace, error_flags, stream)
 
 
 def score_topk(cfg: Mapping, q: torch.Tensor, reps: torch.Tensor, block_table: torch.Tensor,

@@ -84,6 +84,8 @@ typedef enum { SRKV_BF16 = 0, SRKV_F32 = 1 } srkv_dtype;
 #define SRKV_EFLAG_PREFIX 16u    /* a request maps a block of the declared shared prefix to
                                     another page than the batch's other requests (the
                                     shared-prefix calls read one page for all of them) */
+#define SRKV_EFLAG_CHUNK 32u     /* chunk_offsets go down or leave [0, total_tokens], or a chunk
+                                    is longer than its sequence (chunk calls) */
 
 /* Configuration: the method's knobs ("Configuration Parameters") and the head layout. */
 typedef struct {
@@ -150,6 +152,46 @@ srkv_status srkv_append_kv(const srkv_config* cfg, const void* k_new, const void
                            const int32_t* block_table, int32_t max_blocks,
                            const int32_t* seq_lens, int32_t batch, float* reps,
                            int32_t* error_flags, srkv_stream stream);
+
+/*
+ * A ragged chunk of new tokens appended to the cache, rotated to their positions on the way: a
+ * prompt or a piece of one, one token of each request at decode, or both in one batch (the page
+ * vectors of openGauss's "Feature Description" stay current, as with srkv_append_kv; the pages name no
+ * rotation, whose place in a serving step is between the projections and the cache).  Request r
+ * brings rows [chunk_offsets[r], chunk_offsets[r + 1]) of the packed inputs, n_r of them; row i of
+ * them stands at position p = seq_lens[r] + i.
+ *   rotation: for j < rope_dim / 2, with a = p * rope_freqs[j] (radians), the pair (x, y) of elements
+ *     (j, j + rope_dim / 2), or (2j, 2j + 1) if `interleaved`, becomes (x cos a - y sin a,
+ *     y cos a + x sin a); elements from rope_dim on stay.  The angle is reduced to a turn without
+ *     rounding whatever the position, sine, cosine and products are fp32, and the result is rounded
+ *     once to the cache dtype.
+ *   q_out[row][j][:] = rotated q[row][j]           (q and q_out both NULL: no queries)
+ *   K row p % S of page block_table[r][p / S]      = rotated k_new[row][h]
+ *   V row of the same place                        = v_new[row][h]
+ *   reps of every page written = mean of its keys, as held, over its rows up to the chunk's last one:
+ *     the value that srkv_build_block_reps gives for that many valid tokens.
+ *   q: [total_tokens][Hq][d], k_new, v_new: [total_tokens][Hkv][d] in the cache dtype, tokens q_stride,
+ *   k_stride, v_stride elements apart (the parts of one fused projection, for instance; multiples of 16
+ *   bytes, at least one token's heads); q_out: [total_tokens][Hq][d], may be q itself where q_stride =
+ *   Hq d; all 16-byte aligned.  rope_freqs: device double [rope_dim / 2]; rope_dim: even, 0 to d, 0 leaves
+ *   out the rotation; a multiple of 16, else SRKV_ERR_UNSUPPORTED.  chunk_offsets: device int32
+ *   [batch + 1], from 0 or more up to total_tokens or less, not decreasing; n_r = 0 is allowed, and rows
+ *   of the packed tensors outside every request are left alone.  seq_lens: the lengths before the
+ *   chunk, read only: the caller advances them (seq_lens[r] += n_r), and gives every request pages of its own
+ *   for the tokens written.
+ *   A request whose offsets are wrong (SRKV_EFLAG_CHUNK) or whose tokens do not all fit in
+ *   [0, max_blocks * S) (SRKV_EFLAG_SEQ_LEN) is skipped, a page id outside [0, num_pages) skips that page
+ *   (SRKV_EFLAG_PAGE_RANGE; queries are rotated all the same); both are flagged.
+ * Asynchronous on `stream`; one kernel.
+ */
+srkv_status srkv_append_kv_rope(const srkv_config* cfg, const void* q, int64_t q_stride,
+                                const void* k_new, int64_t k_stride, const void* v_new,
+                                int64_t v_stride, const int32_t* chunk_offsets,
+                                int32_t total_tokens, const double* rope_freqs, int32_t rope_dim,
+                                int32_t interleaved, void* q_out, void* k_cache, void* v_cache,
+                                int64_t num_pages, const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* seq_lens, int32_t batch, float* reps,
+                                int32_t* error_flags, srkv_stream stream);
 
 /*
  * Compressed pages (KV-cache survey "大模型推理百倍加速之KV cache篇": quantising the cache is
@@ -461,6 +503,52 @@ srkv_status srkv_retrieval_decode_prefix(const srkv_config* cfg, const void* q,
                                          int32_t kmax, int32_t* nsel, void* out, void* workspace,
                                          size_t workspace_bytes, int32_t* error_flags,
                                          srkv_stream stream);
+
+/*
+ * Attention of a ragged chunk of new tokens over the paged cache that already holds them (what comes
+ * between srkv_append_kv_rope and the first decode step: a prompt, a later piece of one, or, with one
+ * token a request, a decode step that leaves no block out).  Request r brings the query rows
+ * [chunk_offsets[r], chunk_offsets[r + 1]), n_r of them; with L = seq_lens[r], the new tokens counted,
+ * row i stands at position p = L - n_r + i, and
+ *   srkv_chunk_attention:         attends the tokens t <= p;
+ *   srkv_chunk_attention_window:  those of them with t < init_tokens or t > p - local_tokens: the first
+ *     tokens and the window of the position (StreamingLLM's attention, survey "大模型推理百倍加速之KV
+ *     cache篇": sinks and a sliding window), as the decode calls see them without a kept block.
+ * out[row][j][:] = softmax over those tokens of q[row][j].K_t / sqrt(d), times V_t; a row that attends
+ * nothing gives 0.  A row depends on no token that it does not attend, whatever that token's key and value
+ * hold (NaN and infinities too), nor on anything behind L.  Logits, maxima, sums and outputs are held in
+ * fp32.  With bf16 the softmax weights are rounded to bf16 for the product with V (relative 2^-9 each); with
+ * fp32 nothing is rounded below fp32.
+ *   q: [total_tokens][Hq][d], tokens q_stride elements apart (a multiple of 16 bytes, at least Hq d);
+ *   out: [total_tokens][Hq][d]; both 16-byte aligned.  Rows outside every request are left as they were.
+ *   chunk_offsets: as for srkv_append_kv_rope.  Any group size Hq / Hkv.
+ *   workspace: >= srkv_chunk_workspace_size(cfg, total_tokens, batch) bytes, 256-byte aligned; its
+ *   contents on entry do not matter; it is scratch of this call until the stream reaches its end.
+ *   A request whose offsets are wrong is skipped; of a chunk longer than its sequence the first rows
+ *   attend nothing; both flag SRKV_EFLAG_CHUNK.  A length outside [0, max_blocks * S] is clamped into it
+ *   (SRKV_EFLAG_SEQ_LEN).  The tokens of a page whose id is outside [0, num_pages) are left out
+ *   (SRKV_EFLAG_PAGE_RANGE).
+ *   The output is a function of the inputs alone: bitwise the same on every call.
+ * Asynchronous on `stream`; three kernels.
+ */
+size_t srkv_chunk_workspace_size(const srkv_config* cfg, int32_t total_tokens, int32_t batch);
+
+srkv_status srkv_chunk_attention(const srkv_config* cfg, const void* q, int64_t q_stride,
+                                 const void* k_cache, const void* v_cache, int64_t num_pages,
+                                 const int32_t* block_table, int32_t max_blocks,
+                                 const int32_t* chunk_offsets, int32_t total_tokens,
+                                 const int32_t* seq_lens, int32_t batch, void* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* error_flags,
+                                 srkv_stream stream);
+
+srkv_status srkv_chunk_attention_window(const srkv_config* cfg, const void* q, int64_t q_stride,
+                                        const void* k_cache, const void* v_cache,
+                                        int64_t num_pages, const int32_t* block_table,
+                                        int32_t max_blocks, const int32_t* chunk_offsets,
+                                        int32_t total_tokens, const int32_t* seq_lens,
+                                        int32_t batch, void* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* error_flags,
+                                        srkv_stream stream);
 
 /*
  * Number of kernels one srkv_retrieval_decode call with these arguments launches on the
