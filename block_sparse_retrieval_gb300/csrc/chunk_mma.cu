@@ -1,0 +1,580 @@
+// chunk_mma.cu -- attention of a chunk over the paged cache on the tensor cores (bf16).
+//
+// A CTA takes an item: up to 256 rows (two tiles of 128) of one (request, kv head) over a list of pages.  Per
+// page and tile:  S = Q K^T (128 x 128, fp32, in tensor memory);  the tile's warpgroup, one thread a row, reads its
+// row, updates the row's maximum and sum, and writes P = 2^(c S - c m) as bf16 over S;  O += P V (O in tensor memory).
+// The products of one tile run while the other tile's warpgroup is at its exponentials.
+//
+//   warps 0-3, 4-7   softmax and output of tile 0, 1
+//   warp 8           issues the products
+//   warp 9           takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
+//   warps 10, 11     copy the queries of the next item once the last product with the present ones is done
+//
+// The reference m that the exponentials subtract follows the maximum only when that has grown by more than 2^8:
+// O is then scaled by hand.  Sums and outputs stay exact for any reference; fp32 holds the larger weights.
+//
+// Hidden tokens.  A weight of zero does not hide a value that is not finite, so the pages of an item that some
+// row sees in part are looked through before their product: rows behind the sequence are cleared, and elements
+// that are not finite are replaced by zero and their token noted; the rows that do attend such a token get
+// the element back at the end.
+#include "chunk_plan.cuh"
+#include "tcgen05.cuh"
+
+namespace srkv {
+
+bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_pages, int32_t Hkv, int32_t d,
+                      bool e4m3);
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSlots = 2;      // items known at a time
+constexpr int kPageInfo = 16;  // pages between their copy and their softmax, at most
+constexpr int kOdd = 8;        // pages that an item's rows see in part, at most: 3 at each end of a window of 256 rows, 1 at the first tokens
+constexpr float kGrow = 8.f;   // log2 of the growth of a maximum that the reference lets pass
+
+template <int D>
+struct Geo {
+  static constexpr int kTileBytes = 128 * D * 2;       // a tile of Q, a page of K or V
+  static constexpr int kBlockBytes = 128 * 128;        // its blocks of 64 columns
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t kS = 0, kO = 256;          // columns of tensor memory: S0 S1 O0 O1
+  static constexpr size_t kOffQ = 0, kOffStage = 2 * kTileBytes,
+                          kOffBar = kOffStage + (size_t)kStages * kTileBytes;
+};
+
+struct OddPage {
+  uint32_t tokens[4];  // those with an element that is not finite
+  int32_t block;
+};
+
+struct Shared {
+  uint64_t full[10], empty[10];
+  uint64_t item_full[kSlots], item_empty[kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  ChunkItem item[kSlots];
+  int32_t page_ok[kPageInfo];
+  OddPage odd[kSlots][kOdd];
+  int32_t n_odd[kSlots];
+  uint32_t tmem;
+};
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+__device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Counts uses of a ring of N barriers: index, and the parity to wait for (the consumer's; the producer
+// waits for the other one, which a fresh barrier passes).
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ int32_t page_of(const ChunkItem& it, int32_t j) {
+  return j < it.na ? j : j + it.shift;
+}
+
+__device__ __forceinline__ void item_span(const ChunkItem& it, int32_t G, int32_t& p_lo, int32_t& p_hi) {
+  p_lo = it.p0 + it.row0 / G;
+  p_hi = it.p0 + (it.row0 + it.rows - 1) / G;
+}
+
+// A page of V that some row sees in part, in shared memory: rows from `valid` on are cleared, elements that are
+// not finite replaced by zero.  Returns (in every lane) the rows that had one.
+template <int D>
+__device__ __noinline__ uint4 clean_values(unsigned char* stage, int32_t valid, int lane) {
+  uint32_t bad[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int row = g * 32 + lane;
+    for (int c = 0; c < D / 8; ++c) {
+      // 16-byte chunks, lanes at different ones (the swizzle permutes them within a row only)
+      const int chunk = (c + lane) % (D / 8);
+      uint4* p = reinterpret_cast<uint4*>(stage + (chunk / 8) * (128 * 128) + row * 128 + (chunk % 8) * 16);
+      if (row >= valid) {
+        *p = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      uint4 x = *p;
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      bool hit = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, hit = true;
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, hit = true;
+      }
+      if (hit) {
+        *p = make_uint4(w[0], w[1], w[2], w[3]);
+        bad[g] = 1;
+      }
+    }
+    bad[g] = __ballot_sync(0xffffffffu, bad[g]);
+  }
+  return make_uint4(bad[0], bad[1], bad[2], bad[3]);
+}
+
+// Adds what clean_values took out of the values that this row attends to its output element `col`.
+__device__ __noinline__ float odd_value(const ChunkArgs& a, const ChunkItem& it, const OddPage* odd, int n,
+                                        int32_t pos, int col) {
+  float x = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const int32_t page = a.block_table[(int64_t)it.request * a.max_blocks + odd[i].block];
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) +
+                             ((int64_t)page * a.Hkv + it.head) * (int64_t)kBlock * a.d + col;
+    for (int g = 0; g < 4; ++g)
+      for (uint32_t m = odd[i].tokens[g]; m; m &= m - 1) {
+        const int row = g * 32 + __ffs(m) - 1;
+        if (!chunk_attends(pos, odd[i].block * kBlock + row, a.init, a.local)) continue;
+        const float f = __bfloat162float(v[(int64_t)row * a.d]);
+        if (!(fabsf(f) < INFINITY)) x += f;
+      }
+  }
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ Maps maps) {
+  using G = Geo<D>;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Shared& sh = *reinterpret_cast<Shared*>(smem + G::kOffBar);
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      mbar_init(&sh.item_empty[i], 11);  // every warp but the one that takes items
+    }
+    mbar_init(&sh.q_full, 2);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 2);  // the products, and the notes of clean_values
+    }
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&sh.tmem, 512);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = sh.tmem;
+  griddep_wait();
+  griddep_launch_dependents();
+  uint32_t eflags = 0;
+  bool ok = true;  // no wait has run out
+  Ring<kSlots> slot;
+  // Next item for a consumer warp: false at the end.
+  auto take = [&](ChunkItem& it) {
+    ok = ok && mbar_wait(&sh.item_full[slot.at], slot.phase);
+    if (!ok) return false;
+    it = sh.item[slot.at];
+    return it.request >= 0;
+  };
+  auto done = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.item_empty[slot.at]);
+    slot.next();
+  };
+
+  if (warp == 9) {
+    // ---------------------------------------------------------------- items and pages
+    ChunkHead* head = chunk_head(a);
+    const int32_t n_items = head->items;
+    const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.lay.items);
+    Ring<G::kStages> st;
+    int64_t issued = 0;
+    uint32_t info = 0;
+    int32_t next = blockIdx.x;
+    for (;;) {
+      ok = ok && mbar_wait(&sh.item_empty[slot.at], slot.phase ^ 1);
+      if (!ok) break;
+      ChunkItem it;
+      it.request = -1;
+      if (next < n_items) it = items[next];
+      if (lane == 0) {
+        sh.item[slot.at] = it;
+        sh.n_odd[slot.at] = 0;
+        mbar_arrive(&sh.item_full[slot.at]);
+      }
+      slot.next();
+      if (next >= n_items) break;
+      for (int32_t j0 = it.j0; j0 < it.j1 && ok; j0 += 32) {
+        int32_t page = 0;
+        bool good = true;
+        if (j0 + lane < it.j1) {
+          page = a.block_table[(int64_t)it.request * a.max_blocks + page_of(it, j0 + lane)];
+          good = page >= 0 && (int64_t)page < a.num_pages;
+          if (!good) {
+            eflags |= SRKV_EFLAG_PAGE_RANGE;
+            page = (int32_t)a.num_pages;  // behind the cache: the copy fills with zeros
+          }
+        }
+        const int n = min(32, it.j1 - j0);
+        for (int i = 0; i < n && ok; ++i) {
+          const int32_t z = __shfl_sync(0xffffffffu, page, i);
+          const int32_t fine = __shfl_sync(0xffffffffu, (int32_t)good, i);
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = mbar_wait(&sh.empty[st.at], st.phase ^ 1);
+            if (!ok) break;
+            if (lane == 0) {
+              if (kv == 0) sh.page_ok[info % kPageInfo] = fine;
+              unsigned char* dst = smem + G::kOffStage + (size_t)st.at * G::kTileBytes;
+              mbar_arrive_expect_tx(&sh.full[st.at], G::kTileBytes);
+#pragma unroll
+              for (int b = 0; b < D / 64; ++b)
+                tma_page(dst + b * G::kBlockBytes, kv ? &maps.v : &maps.k, 64 * b, it.head * kBlock, z,
+                         &sh.full[st.at]);
+            }
+            __syncwarp();
+            st.next();
+            ++issued;
+          }
+          ++info;
+        }
+      }
+      if (lane == 0) next = atomicAdd(&head->next, 1) + (int32_t)gridDim.x;
+      next = __shfl_sync(0xffffffffu, next, 0);
+    }
+    // every copy lands before the CTA ends: the last use of each stage
+    for (int i = 0; i < G::kStages && i < issued; ++i) {
+      if (st.at == 0) {
+        st.at = G::kStages;
+        st.phase ^= 1;
+      }
+      --st.at;
+      ok = mbar_wait(&sh.full[st.at], st.phase) && ok;
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
+    const uint32_t q0 = smem_u32(smem + G::kOffQ), stage0 = smem_u32(smem + G::kOffStage);
+    Ring<G::kStages> st;
+    Ring<1> qr, pr[2];
+    auto qk = [&](int i, int s) {  // S_i = Q_i K^T
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k / 4) * G::kBlockBytes + (k % 4) * 32;
+        mma_ss(tmem + G::kS + 128 * i, smem_desc(q0 + i * G::kTileBytes + off, 0),
+               smem_desc(stage0 + s * G::kTileBytes + off, 0), kQK, k > 0);
+      }
+      mma_commit(&sh.s_full[i]);
+    };
+    auto pv = [&](int i, int s, bool first) {  // O_i (+)= P_i V
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 8 * k,
+               smem_desc(stage0 + s * G::kTileBytes + k * 2048, G::kBlockBytes), kPV, !first || k > 0);
+    };
+    ChunkItem it;
+    while (take(it)) {
+      const int tiles = it.rows > 128 ? 2 : 1;
+      const int32_t n = it.j1 - it.j0;
+      int32_t p_lo, p_hi;
+      item_span(it, a.G, p_lo, p_hi);
+      if (n > 0) {
+        ok = ok && mbar_wait(&sh.q_full, qr.phase) && mbar_wait(&sh.full[st.at], st.phase);
+        if (!ok) break;
+        qr.next();
+        tcgen05_fence_after();
+        if (lane == 0) {
+          for (int i = 0; i < tiles; ++i) qk(i, st.at);
+          mma_commit(&sh.empty[st.at]);
+          if (n == 1) mma_commit(&sh.q_empty);
+        }
+        __syncwarp();
+        st.next();
+      }
+      for (int32_t j = 0; j < n && ok; ++j) {
+        const Ring<G::kStages> v = st;
+        st.next();
+        const Ring<G::kStages> k = st;
+        if (j + 1 < n) st.next();
+        ok = mbar_wait(&sh.full[v.at], v.phase);
+        if (!ok) break;
+        const int32_t b = page_of(it, it.j0 + j);
+        if (chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
+          const uint4 bad =
+              clean_values<D>(smem + G::kOffStage + (size_t)v.at * G::kTileBytes, it.L - b * kBlock, lane);
+          const int32_t at = sh.n_odd[slot.at];
+          __syncwarp();
+          if (lane == 0 && (bad.x | bad.y | bad.z | bad.w) && at < kOdd) {
+            OddPage& o = sh.odd[slot.at][at];
+            o.tokens[0] = bad.x;
+            o.tokens[1] = bad.y;
+            o.tokens[2] = bad.z;
+            o.tokens[3] = bad.w;
+            o.block = b;
+            sh.n_odd[slot.at] = at + 1;
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+        for (int i = 0; i < tiles; ++i) {
+          ok = ok && mbar_wait(&sh.p_full[i], pr[i].phase);
+          if (!ok) break;
+          pr[i].next();
+          if (i == 0 && j + 1 < n) ok = mbar_wait(&sh.full[k.at], k.phase);
+          if (!ok) break;
+          tcgen05_fence_after();
+          if (lane == 0) {
+            pv(i, v.at, j == 0);
+            if (i == tiles - 1) mma_commit(&sh.empty[v.at]);
+            if (j + 1 < n) {
+              qk(i, k.at);
+              if (i == tiles - 1) {
+                mma_commit(&sh.empty[k.at]);
+                if (j + 2 == n) mma_commit(&sh.q_empty);
+              }
+            } else {
+              mma_commit(&sh.o_full[i]);
+              mbar_arrive(&sh.o_full[i]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      done();
+    }
+    if (!ok) {  // a wait ran out: products in flight still end before the tensor memory is freed
+      if (lane == 0) mma_commit(&sh.drain);
+      __syncwarp();
+      mbar_wait(&sh.drain, 0);
+    }
+  } else if (warp >= 10) {
+    // ---------------------------------------------------------------- queries
+    ChunkItem it;
+    Ring<1> qr;
+    while (take(it)) {
+      if (it.j1 > it.j0) {
+        ok = ok && mbar_wait(&sh.q_empty, qr.phase ^ 1);
+        if (!ok) break;
+        qr.next();
+        constexpr int C = D / 8;  // 16-byte chunks of a row
+        const int t = (warp - 10) * 32 + lane, chunk = t % C;
+        for (int row = t / C; row < it.rows; row += 64 / C) {
+          const int32_t rho = it.row0 + row;
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                     (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
+                                     (int64_t)(it.head * a.G + rho % a.G) * D + chunk * 8;
+          const uint32_t dst = smem_u32(smem + G::kOffQ) + (row / 128) * G::kTileBytes +
+                               (chunk / 8) * G::kBlockBytes + (row % 128) * 128 +
+                               ((chunk ^ row) % 8) * 16;
+          cp_async_16(dst, src);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+      }
+      done();
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax and output
+    const int tile = warp / 4, row = 128 * tile + 32 * (warp % 4) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
+    const uint32_t ts = tmem + G::kS + 128 * tile + lanes, to = tmem + G::kO + D * tile + lanes;
+    const float scale = a.scale_log2;
+    Ring<1> sr, orr;
+    uint32_t info = 0;
+    ChunkItem it;
+    while (take(it)) {
+      const int32_t n = it.j1 - it.j0;
+      const bool here = 128 * tile < it.rows;                       // the tile is in use
+      const bool work = 128 * tile + 32 * (warp % 4) < it.rows;     // some row of this warp is
+      const bool mine = row < it.rows;                              // this lane's row is
+      int32_t p_lo, p_hi;
+      item_span(it, a.G, p_lo, p_hi);
+      const int32_t pos = it.p0 + (it.row0 + row) / a.G;
+      float m = -INFINITY, l = 0.f;
+      for (int32_t j = 0; here && j < n && ok; ++j, ++info) {
+        ok = mbar_wait(&sh.s_full[tile], sr.phase);
+        if (!ok) break;
+        sr.next();
+        tcgen05_fence_after();
+        if (work) {
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_use32(s + 32 * c);
+          const int32_t b = page_of(it, it.j0 + j);
+          const bool fine = sh.page_ok[info % kPageInfo] != 0;
+          if (!fine || chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
+            const int32_t t0 = b * kBlock;
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (!fine || !chunk_attends(pos, t0 + e, a.init, a.local)) s[e] = 0xff800000u;
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 128; ++e) top[e % 4] = fmaxf(top[e % 4], __uint_as_float(s[e]));
+          const float now = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          if (j == 0) {
+            m = now;
+          } else {
+            const bool grow = mine && (now - m) * scale > kGrow;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float w = grow ? fast_exp2((m - now) * scale) : 1.f;
+              if (grow) m = now;
+              l *= w;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * c, o);
+                tmem_wait_ld();
+                tmem_use32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+                tmem_st32(to + 32 * c, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : -m * scale;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) {
+            const float x = fast_exp2(fmaf(__uint_as_float(s[e]), scale, ref));
+            const float y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), scale, ref));
+            sum[(e / 2) % 4] += x + y;
+            s[e / 2] = pack_bf16(x, y);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st32(ts, s);
+          tmem_st32(ts + 32, s + 32);
+          tmem_wait_st();
+        }
+        tcgen05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[tile]);
+      }
+      if (!here) info += n;
+      if (!ok) break;
+      if (here) {
+        if (n > 0) {
+          ok = mbar_wait(&sh.o_full[tile], orr.phase);
+          if (!ok) break;
+          orr.next();
+          tcgen05_fence_after();
+        }
+        const int n_odd = n > 0 ? sh.n_odd[slot.at] : 0;
+        const int32_t rho = it.row0 + row;
+        const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                             ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D;
+        float* acc = reinterpret_cast<float*>(a.ws + a.lay.acc) + (int64_t)(it.slot + row) * D;
+        if (work) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_ld32(to + 32 * c, o);
+              tmem_wait_ld();
+              tmem_use32(o);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = n > 0 ? __float_as_uint(__uint_as_float(o[e]) * w) : 0u;
+            if (l == 0.f) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+            if (n_odd > 0 && mine) {
+#pragma unroll 1
+              for (int e = 0; e < 32; ++e) {
+                const float x = odd_value(a, it, sh.odd[slot.at], n_odd, pos, 32 * c + e);
+#pragma unroll
+                for (int f = 0; f < 32; ++f)
+                  if (f == e) o[f] = __float_as_uint(__uint_as_float(o[f]) + x);
+              }
+            }
+            if (mine) {
+              if (it.slot >= 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<uint4*>(acc + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  uint4 v;
+                  v.x = pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                  v.y = pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                  v.z = pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+                  v.w = pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+                  *reinterpret_cast<uint4*>(out + 32 * c + e) = v;
+                }
+              }
+            }
+          }
+          if (mine && it.slot >= 0)
+            *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.ws + a.lay.ml) + 2 * (int64_t)(it.slot + row)) =
+                make_float2(m == -INFINITY ? m : m * scale, l);
+        }
+        tcgen05_fence_before();
+      }
+      done();
+    }
+  }
+  if (!ok) eflags |= SRKV_EFLAG_TIMEOUT;
+  eflags = __reduce_or_sync(0xffffffffu, eflags);
+  if (lane == 0) raise_flags(a.error_flags, eflags);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
+  using G = Geo<D>;
+  constexpr size_t smem = G::kOffBar + sizeof(Shared) + 1024;
+  static_assert(smem <= 232448, "shared memory opt-in limit");
+  static_assert(G::kStages <= 10, "barriers");
+  // The shared-memory opt-in is set once per device (not during graph capture).
+  static bool configured[128] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(chunk_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  Maps maps;
+  if (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, false) ||
+      !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, false))
+    return cudaErrorInvalidValue;
+  return launch_pdl(chunk_mma_kernel<D>, dim3(a.ctas), dim3(kThreads), smem, stream, a, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_mma(const ChunkArgs& a, cudaStream_t stream) {
+  return a.d == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
+}
+
+}  // namespace srkv

@@ -321,7 +321,9 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a) {
 
 }  // namespace
 
-int32_t chunk_tile(const srkv_config&) { return kChunkTileSimt; }
+int32_t chunk_tile(const srkv_config& cfg) {
+  return cfg.dtype == SRKV_BF16 ? kChunkTile : kChunkTileSimt;
+}
 
 size_t chunk_workspace(const srkv_config& cfg, int32_t tokens, int32_t batch, ChunkLayout* out) {
   ChunkLayout w;

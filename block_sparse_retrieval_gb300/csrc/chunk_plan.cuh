@@ -119,7 +119,7 @@ int32_t chunk_tile(const srkv_config& cfg);
 size_t chunk_workspace(const srkv_config& cfg, int32_t tokens, int32_t batch, ChunkLayout* lay);
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t dtype, cudaStream_t stream);
-cudaError_t launch_chunk_simt(const ChunkArgs& a, int32_t dtype, cudaStream_t stream);
+cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t stream);
 cudaError_t launch_chunk_mma(const ChunkArgs& a, cudaStream_t stream);
 
 }  // namespace srkv

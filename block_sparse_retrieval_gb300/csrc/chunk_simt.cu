@@ -49,16 +49,8 @@ __device__ __forceinline__ void add_values(const float* sp, const float* sv, int
 }
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs a) {
   using S = SimtGeom<D>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -86,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < it.rows) {
         const int32_t rho = it.row0 + row;
-        const T* q = static_cast<const T*>(a.q) + (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
+        const float* q = static_cast<const float*>(a.q) + (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
                          (int64_t)(it.head * a.G + rho % a.G) * D;
         x = load4(q + c * 4);
       }
@@ -120,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
           float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
           if (tok + row < it.L) {
             const int64_t at = slab + (int64_t)(t0 + row) * D + c * 4;
-            k = load4(static_cast<const T*>(a.k_cache) + at);
-            v = load4(static_cast<const T*>(a.v_cache) + at);
+            k = load4(static_cast<const float*>(a.k_cache) + at);
+            v = load4(static_cast<const float*>(a.v_cache) + at);
           }
           *reinterpret_cast<float4*>(sk + row * S::LD + c * 4) = k;
           *reinterpret_cast<float4*>(sv + row * S::LD + c * 4) = v;
@@ -200,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
               make_float2(m[i], l[i]);
       } else {
         const int32_t rho = it.row0 + row;
-        T* out = static_cast<T*>(a.out) +
+        float* out = static_cast<float*>(a.out) +
                  ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D;
         const float w = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
@@ -213,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
   if (tid == 0) raise_flags(a.error_flags, eflags);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
   // The shared-memory opt-in is set once per device (not during graph capture).
   static bool configured[128] = {false};
@@ -222,20 +214,18 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(chunk_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)SimtGeom<D>::kSmem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  return launch_pdl(chunk_simt_kernel<T, D>, dim3(a.ctas), dim3(kThreads), SimtGeom<D>::kSmem, stream, a);
+  return launch_pdl(chunk_simt_kernel<D>, dim3(a.ctas), dim3(kThreads), SimtGeom<D>::kSmem, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_simt(const ChunkArgs& a, int32_t dtype, cudaStream_t stream) {
-  if (dtype == SRKV_BF16)
-    return a.d == 128 ? launch_d<__nv_bfloat16, 128>(a, stream) : launch_d<__nv_bfloat16, 64>(a, stream);
-  return a.d == 128 ? launch_d<float, 128>(a, stream) : launch_d<float, 64>(a, stream);
+cudaError_t launch_chunk_simt(const ChunkArgs& a, cudaStream_t stream) {
+  return a.d == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
 }
 
 }  // namespace srkv

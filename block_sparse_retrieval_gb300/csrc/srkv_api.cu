@@ -332,9 +332,11 @@ srkv_status chunk_attention(const srkv_config* cfg, const void* q, int64_t q_str
   a.local = windowed ? cfg->local_tokens : 0;
   a.scale_log2 = kLog2e / sqrtf((float)cfg->head_dim);
   a.tile = chunk_tile(*cfg);
-  a.ctas = 2 * sms;
+  const bool mma = cfg->dtype == SRKV_BF16;
+  a.ctas = mma ? sms : 2 * sms;
   if (launch_chunk_plan(a, stream) != cudaSuccess) return SRKV_ERR_CUDA;
-  if (launch_chunk_simt(a, cfg->dtype, stream) != cudaSuccess) return SRKV_ERR_CUDA;
+  if ((mma ? launch_chunk_mma(a, stream) : launch_chunk_simt(a, stream)) != cudaSuccess)
+    return SRKV_ERR_CUDA;
   return cuda_status(launch_chunk_merge(a, cfg->dtype, stream));
 }
 
