@@ -31,6 +31,8 @@ constexpr int kThreads = 384;
 constexpr int kSlots = 2;      // items known at a time
 constexpr int kPageInfo = 16;  // pages between their copy and their softmax, at most
 constexpr int kOdd = 8;        // pages that an item's rows see in part, at most: 3 at each end of a window of 256 rows, 1 at the first tokens
+// Registers: the softmax threads hold a row of 128 logits; 256 x 208 + 128 x 88 = 384 x 168, what the block is launched with.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kGrow = 8.f;   // log2 of the growth of a maximum that the reference lets pass
 
 template <int D>
@@ -52,7 +54,7 @@ struct Shared {
   uint64_t full[10], empty[10];
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // P in two halves of its tokens
   uint64_t drain;
   ChunkItem item[kSlots];
   int32_t page_ok[kPageInfo];
@@ -100,11 +102,12 @@ __device__ __forceinline__ void item_span(const ChunkItem& it, int32_t G, int32_
 // A page of V that some row sees in part, in shared memory: rows from `valid` on are cleared, elements that are
 // not finite replaced by zero.  Returns (in every lane) the rows that had one.
 template <int D>
-__device__ __noinline__ uint4 clean_values(unsigned char* stage, int32_t valid, int lane) {
+__device__ __forceinline__ uint4 clean_values(unsigned char* stage, int32_t valid, int lane) {
   uint32_t bad[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const int row = g * 32 + lane;
+#pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
       // 16-byte chunks, lanes at different ones (the swizzle permutes them within a row only)
       const int chunk = (c + lane) % (D / 8);
@@ -131,14 +134,14 @@ __device__ __noinline__ uint4 clean_values(unsigned char* stage, int32_t valid, 
   return make_uint4(bad[0], bad[1], bad[2], bad[3]);
 }
 
-// Adds what clean_values took out of the values that this row attends to its output element `col`.
-__device__ __noinline__ float odd_value(const ChunkArgs& a, const ChunkItem& it, const OddPage* odd, int n,
-                                        int32_t pos, int col) {
+// What clean_values took out of element `col` of the values that a row at `pos` attends.
+__device__ __forceinline__ float odd_value(const ChunkArgs& a, int32_t request, int32_t head, const OddPage* odd,
+                                           int n, int32_t pos, int col) {
   float x = 0.f;
   for (int i = 0; i < n; ++i) {
-    const int32_t page = a.block_table[(int64_t)it.request * a.max_blocks + odd[i].block];
+    const int32_t page = a.block_table[(int64_t)request * a.max_blocks + odd[i].block];
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) +
-                             ((int64_t)page * a.Hkv + it.head) * (int64_t)kBlock * a.d + col;
+                             ((int64_t)page * a.Hkv + head) * (int64_t)kBlock * a.d + col;
     for (int g = 0; g < 4; ++g)
       for (uint32_t m = odd[i].tokens[g]; m; m &= m - 1) {
         const int row = g * 32 + __ffs(m) - 1;
@@ -148,6 +151,32 @@ __device__ __noinline__ float odd_value(const ChunkArgs& a, const ChunkItem& it,
       }
   }
   return x;
+}
+
+// Bits e < n of a word.
+__device__ __forceinline__ uint32_t bits_below(int32_t n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Which of the tokens t0 .. t0 + 31 a row at `pos` attends.
+__device__ __forceinline__ uint32_t attended_bits(int32_t pos, int32_t t0, int32_t init, int32_t local) {
+  const int32_t from = local > pos ? 0 : pos - local + 1;  // its window's first token
+  return bits_below(pos - t0 + 1) & (bits_below(init - t0) | ~bits_below(from - t0));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int D>
@@ -172,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i][0], 4);
+      mbar_init(&sh.p_full[i][1], 4);
       mbar_init(&sh.o_full[i], 2);  // the products, and the notes of clean_values
     }
     fence_mbar_init();
@@ -200,199 +230,206 @@ __global__ void __launch_bounds__(kThreads, 1)
     slot.next();
   };
 
-  if (warp == 9) {
-    // ---------------------------------------------------------------- items and pages
-    ChunkHead* head = chunk_head(a);
-    const int32_t n_items = head->items;
-    const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.lay.items);
-    Ring<G::kStages> st;
-    int64_t issued = 0;
-    uint32_t info = 0;
-    int32_t next = blockIdx.x;
-    for (;;) {
-      ok = ok && mbar_wait(&sh.item_empty[slot.at], slot.phase ^ 1);
-      if (!ok) break;
-      ChunkItem it;
-      it.request = -1;
-      if (next < n_items) it = items[next];
-      if (lane == 0) {
-        sh.item[slot.at] = it;
-        sh.n_odd[slot.at] = 0;
-        mbar_arrive(&sh.item_full[slot.at]);
-      }
-      slot.next();
-      if (next >= n_items) break;
-      for (int32_t j0 = it.j0; j0 < it.j1 && ok; j0 += 32) {
-        int32_t page = 0;
-        bool good = true;
-        if (j0 + lane < it.j1) {
-          page = a.block_table[(int64_t)it.request * a.max_blocks + page_of(it, j0 + lane)];
-          good = page >= 0 && (int64_t)page < a.num_pages;
-          if (!good) {
-            eflags |= SRKV_EFLAG_PAGE_RANGE;
-            page = (int32_t)a.num_pages;  // behind the cache: the copy fills with zeros
-          }
-        }
-        const int n = min(32, it.j1 - j0);
-        for (int i = 0; i < n && ok; ++i) {
-          const int32_t z = __shfl_sync(0xffffffffu, page, i);
-          const int32_t fine = __shfl_sync(0xffffffffu, (int32_t)good, i);
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            ok = mbar_wait(&sh.empty[st.at], st.phase ^ 1);
-            if (!ok) break;
-            if (lane == 0) {
-              if (kv == 0) sh.page_ok[info % kPageInfo] = fine;
-              unsigned char* dst = smem + G::kOffStage + (size_t)st.at * G::kTileBytes;
-              mbar_arrive_expect_tx(&sh.full[st.at], G::kTileBytes);
-#pragma unroll
-              for (int b = 0; b < D / 64; ++b)
-                tma_page(dst + b * G::kBlockBytes, kv ? &maps.v : &maps.k, 64 * b, it.head * kBlock, z,
-                         &sh.full[st.at]);
-            }
-            __syncwarp();
-            st.next();
-            ++issued;
-          }
-          ++info;
-        }
-      }
-      if (lane == 0) next = atomicAdd(&head->next, 1) + (int32_t)gridDim.x;
-      next = __shfl_sync(0xffffffffu, next, 0);
-    }
-    // every copy lands before the CTA ends: the last use of each stage
-    for (int i = 0; i < G::kStages && i < issued; ++i) {
-      if (st.at == 0) {
-        st.at = G::kStages;
-        st.phase ^= 1;
-      }
-      --st.at;
-      ok = mbar_wait(&sh.full[st.at], st.phase) && ok;
-    }
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- products
-    constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
-    const uint32_t q0 = smem_u32(smem + G::kOffQ), stage0 = smem_u32(smem + G::kOffStage);
-    Ring<G::kStages> st;
-    Ring<1> qr, pr[2];
-    auto qk = [&](int i, int s) {  // S_i = Q_i K^T
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k / 4) * G::kBlockBytes + (k % 4) * 32;
-        mma_ss(tmem + G::kS + 128 * i, smem_desc(q0 + i * G::kTileBytes + off, 0),
-               smem_desc(stage0 + s * G::kTileBytes + off, 0), kQK, k > 0);
-      }
-      mma_commit(&sh.s_full[i]);
-    };
-    auto pv = [&](int i, int s, bool first) {  // O_i (+)= P_i V
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 8 * k,
-               smem_desc(stage0 + s * G::kTileBytes + k * 2048, G::kBlockBytes), kPV, !first || k > 0);
-    };
-    ChunkItem it;
-    while (take(it)) {
-      const int tiles = it.rows > 128 ? 2 : 1;
-      const int32_t n = it.j1 - it.j0;
-      int32_t p_lo, p_hi;
-      item_span(it, a.G, p_lo, p_hi);
-      if (n > 0) {
-        ok = ok && mbar_wait(&sh.q_full, qr.phase) && mbar_wait(&sh.full[st.at], st.phase);
+  if (warp >= 8) {
+    fewer_registers<kOtherRegs>();
+    if (warp == 9) {
+      // ---------------------------------------------------------------- items and pages
+      ChunkHead* head = chunk_head(a);
+      const int32_t n_items = head->items;
+      const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.lay.items);
+      Ring<G::kStages> st;
+      int64_t issued = 0;
+      uint32_t info = 0;
+      int32_t next = blockIdx.x;
+      for (;;) {
+        ok = ok && mbar_wait(&sh.item_empty[slot.at], slot.phase ^ 1);
         if (!ok) break;
-        qr.next();
-        tcgen05_fence_after();
+        ChunkItem it;
+        it.request = -1;
+        if (next < n_items) it = items[next];
         if (lane == 0) {
-          for (int i = 0; i < tiles; ++i) qk(i, st.at);
-          mma_commit(&sh.empty[st.at]);
-          if (n == 1) mma_commit(&sh.q_empty);
+          sh.item[slot.at] = it;
+          sh.n_odd[slot.at] = 0;
+          mbar_arrive(&sh.item_full[slot.at]);
         }
-        __syncwarp();
-        st.next();
-      }
-      for (int32_t j = 0; j < n && ok; ++j) {
-        const Ring<G::kStages> v = st;
-        st.next();
-        const Ring<G::kStages> k = st;
-        if (j + 1 < n) st.next();
-        ok = mbar_wait(&sh.full[v.at], v.phase);
-        if (!ok) break;
-        const int32_t b = page_of(it, it.j0 + j);
-        if (chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
-          const uint4 bad =
-              clean_values<D>(smem + G::kOffStage + (size_t)v.at * G::kTileBytes, it.L - b * kBlock, lane);
-          const int32_t at = sh.n_odd[slot.at];
-          __syncwarp();
-          if (lane == 0 && (bad.x | bad.y | bad.z | bad.w) && at < kOdd) {
-            OddPage& o = sh.odd[slot.at][at];
-            o.tokens[0] = bad.x;
-            o.tokens[1] = bad.y;
-            o.tokens[2] = bad.z;
-            o.tokens[3] = bad.w;
-            o.block = b;
-            sh.n_odd[slot.at] = at + 1;
+        slot.next();
+        if (next >= n_items) break;
+        for (int32_t j0 = it.j0; j0 < it.j1 && ok; j0 += 32) {
+          int32_t page = 0;
+          bool good = true;
+          if (j0 + lane < it.j1) {
+            page = a.block_table[(int64_t)it.request * a.max_blocks + page_of(it, j0 + lane)];
+            good = page >= 0 && (int64_t)page < a.num_pages;
+            if (!good) {
+              eflags |= SRKV_EFLAG_PAGE_RANGE;
+              page = (int32_t)a.num_pages;  // behind the cache: the copy fills with zeros
+            }
           }
-          fence_async_smem();
-          __syncwarp();
+          const int n = min(32, it.j1 - j0);
+          for (int i = 0; i < n && ok; ++i) {
+            const int32_t z = __shfl_sync(0xffffffffu, page, i);
+            const int32_t fine = __shfl_sync(0xffffffffu, (int32_t)good, i);
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+              ok = mbar_wait(&sh.empty[st.at], st.phase ^ 1);
+              if (!ok) break;
+              if (lane == 0) {
+                if (kv == 0) sh.page_ok[info % kPageInfo] = fine;
+                unsigned char* dst = smem + G::kOffStage + (size_t)st.at * G::kTileBytes;
+                mbar_arrive_expect_tx(&sh.full[st.at], G::kTileBytes);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b)
+                  tma_page(dst + b * G::kBlockBytes, kv ? &maps.v : &maps.k, 64 * b, it.head * kBlock, z,
+                           &sh.full[st.at]);
+              }
+              __syncwarp();
+              st.next();
+              ++issued;
+            }
+            ++info;
+          }
         }
-        for (int i = 0; i < tiles; ++i) {
-          ok = ok && mbar_wait(&sh.p_full[i], pr[i].phase);
+        if (lane == 0) next = atomicAdd(&head->next, 1) + (int32_t)gridDim.x;
+        next = __shfl_sync(0xffffffffu, next, 0);
+      }
+      // every copy lands before the CTA ends: the last use of each stage
+      for (int i = 0; i < G::kStages && i < issued; ++i) {
+        if (st.at == 0) {
+          st.at = G::kStages;
+          st.phase ^= 1;
+        }
+        --st.at;
+        ok = mbar_wait(&sh.full[st.at], st.phase) && ok;
+      }
+    } else if (warp == 8) {
+      // ---------------------------------------------------------------- products
+      constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
+      const uint32_t q0 = smem_u32(smem + G::kOffQ), stage0 = smem_u32(smem + G::kOffStage);
+      Ring<G::kStages> st;
+      Ring<1> qr, pr[2];
+      auto qk = [&](int i, int s) {  // S_i = Q_i K^T
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * G::kBlockBytes + (k % 4) * 32;
+          mma_ss(tmem + G::kS + 128 * i, smem_desc(q0 + i * G::kTileBytes + off, 0),
+                 smem_desc(stage0 + s * G::kTileBytes + off, 0), kQK, k > 0);
+        }
+        mma_commit(&sh.s_full[i]);
+      };
+      auto pv = [&](int i, int s, int half, bool first) {  // O_i (+)= P_i V over a half of the tokens
+#pragma unroll
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
+          mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 8 * k,
+                 smem_desc(stage0 + s * G::kTileBytes + k * 2048, G::kBlockBytes), kPV, !first || k > 0);
+      };
+      ChunkItem it;
+      while (take(it)) {
+        const int tiles = it.rows > 128 ? 2 : 1;
+        const int32_t n = it.j1 - it.j0;
+        int32_t p_lo, p_hi;
+        item_span(it, a.G, p_lo, p_hi);
+        if (n > 0) {
+          ok = ok && mbar_wait(&sh.q_full, qr.phase) && mbar_wait(&sh.full[st.at], st.phase);
           if (!ok) break;
-          pr[i].next();
-          if (i == 0 && j + 1 < n) ok = mbar_wait(&sh.full[k.at], k.phase);
-          if (!ok) break;
+          qr.next();
           tcgen05_fence_after();
           if (lane == 0) {
-            pv(i, v.at, j == 0);
-            if (i == tiles - 1) mma_commit(&sh.empty[v.at]);
-            if (j + 1 < n) {
-              qk(i, k.at);
-              if (i == tiles - 1) {
-                mma_commit(&sh.empty[k.at]);
-                if (j + 2 == n) mma_commit(&sh.q_empty);
-              }
-            } else {
-              mma_commit(&sh.o_full[i]);
-              mbar_arrive(&sh.o_full[i]);
-            }
+            for (int i = 0; i < tiles; ++i) qk(i, st.at);
+            mma_commit(&sh.empty[st.at]);
+            if (n == 1) mma_commit(&sh.q_empty);
           }
           __syncwarp();
+          st.next();
         }
+        for (int32_t j = 0; j < n && ok; ++j) {
+          const Ring<G::kStages> v = st;
+          st.next();
+          const Ring<G::kStages> k = st;
+          if (j + 1 < n) st.next();
+          ok = mbar_wait(&sh.full[v.at], v.phase);
+          if (!ok) break;
+          const int32_t b = page_of(it, it.j0 + j);
+          if (chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
+            const uint4 bad =
+                clean_values<D>(smem + G::kOffStage + (size_t)v.at * G::kTileBytes, it.L - b * kBlock, lane);
+            const int32_t at = sh.n_odd[slot.at];
+            __syncwarp();
+            if (lane == 0 && (bad.x | bad.y | bad.z | bad.w) && at < kOdd) {
+              OddPage& o = sh.odd[slot.at][at];
+              o.tokens[0] = bad.x;
+              o.tokens[1] = bad.y;
+              o.tokens[2] = bad.z;
+              o.tokens[3] = bad.w;
+              o.block = b;
+              sh.n_odd[slot.at] = at + 1;
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+          for (int i = 0; i < tiles; ++i) {
+            for (int half = 0; half < 2 && ok; ++half) {
+              ok = mbar_wait(&sh.p_full[i][half], pr[i].phase);
+              if (!ok) break;
+              tcgen05_fence_after();
+              if (lane == 0) pv(i, v.at, half, j == 0);
+              __syncwarp();
+            }
+            pr[i].next();
+            if (i == 0 && j + 1 < n) ok = ok && mbar_wait(&sh.full[k.at], k.phase);
+            if (!ok) break;
+            if (lane == 0) {
+              if (i == tiles - 1) mma_commit(&sh.empty[v.at]);
+              if (j + 1 < n) {
+                qk(i, k.at);
+                if (i == tiles - 1) {
+                  mma_commit(&sh.empty[k.at]);
+                  if (j + 2 == n) mma_commit(&sh.q_empty);
+                }
+              } else {
+                mma_commit(&sh.o_full[i]);
+                mbar_arrive(&sh.o_full[i]);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        done();
       }
-      done();
-    }
-    if (!ok) {  // a wait ran out: products in flight still end before the tensor memory is freed
-      if (lane == 0) mma_commit(&sh.drain);
-      __syncwarp();
-      mbar_wait(&sh.drain, 0);
-    }
-  } else if (warp >= 10) {
-    // ---------------------------------------------------------------- queries
-    ChunkItem it;
-    Ring<1> qr;
-    while (take(it)) {
-      if (it.j1 > it.j0) {
-        ok = ok && mbar_wait(&sh.q_empty, qr.phase ^ 1);
-        if (!ok) break;
-        qr.next();
-        constexpr int C = D / 8;  // 16-byte chunks of a row
-        const int t = (warp - 10) * 32 + lane, chunk = t % C;
-        for (int row = t / C; row < it.rows; row += 64 / C) {
-          const int32_t rho = it.row0 + row;
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                     (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
-                                     (int64_t)(it.head * a.G + rho % a.G) * D + chunk * 8;
-          const uint32_t dst = smem_u32(smem + G::kOffQ) + (row / 128) * G::kTileBytes +
-                               (chunk / 8) * G::kBlockBytes + (row % 128) * 128 +
-                               ((chunk ^ row) % 8) * 16;
-          cp_async_16(dst, src);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_smem();
+      if (!ok) {  // a wait ran out: products in flight still end before the tensor memory is freed
+        if (lane == 0) mma_commit(&sh.drain);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full);
+        mbar_wait(&sh.drain, 0);
       }
-      done();
+    } else {
+      // ---------------------------------------------------------------- queries
+      ChunkItem it;
+      Ring<1> qr;
+      while (take(it)) {
+        if (it.j1 > it.j0) {
+          ok = ok && mbar_wait(&sh.q_empty, qr.phase ^ 1);
+          if (!ok) break;
+          qr.next();
+          constexpr int C = D / 8;  // 16-byte chunks of a row
+          const int t = (warp - 10) * 32 + lane, chunk = t % C;
+          for (int row = t / C; row < it.rows; row += 64 / C) {
+            const int32_t rho = it.row0 + row;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                       (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
+                                       (int64_t)(it.head * a.G + rho % a.G) * D + chunk * 8;
+            const uint32_t dst = smem_u32(smem + G::kOffQ) + (row / 128) * G::kTileBytes +
+                                 (chunk / 8) * G::kBlockBytes + (row % 128) * 128 +
+                                 ((chunk ^ row) % 8) * 16;
+            cp_async_16(dst, src);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full);
+        }
+        done();
+      }
     }
   } else {
+    more_registers<kSoftmaxRegs>();
     // ---------------------------------------------------------------- softmax and output
     const int tile = warp / 4, row = 128 * tile + 32 * (warp % 4) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
@@ -409,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t p_lo, p_hi;
       item_span(it, a.G, p_lo, p_hi);
       const int32_t pos = it.p0 + (it.row0 + row) / a.G;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY;
+      float2 sum = make_float2(0.f, 0.f);
       for (int32_t j = 0; here && j < n && ok; ++j, ++info) {
         ok = mbar_wait(&sh.s_full[tile], sr.phase);
         if (!ok) break;
@@ -425,15 +463,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t b = page_of(it, it.j0 + j);
           const bool fine = sh.page_ok[info % kPageInfo] != 0;
           if (!fine || chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
-            const int32_t t0 = b * kBlock;
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (!fine || !chunk_attends(pos, t0 + e, a.init, a.local)) s[e] = 0xff800000u;
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t on = fine ? attended_bits(pos, b * kBlock + 32 * c, a.init, a.local) : 0u;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(on >> e & 1u)) s[32 * c + e] = 0xff800000u;
+            }
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float top[4];
 #pragma unroll
-          for (int e = 0; e < 128; ++e) top[e % 4] = fmaxf(top[e % 4], __uint_as_float(s[e]));
-          const float now = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          for (int i = 0; i < 4; ++i) top[i] = max3(i ? -INFINITY : m, __uint_as_float(s[i]), __uint_as_float(s[i + 4]));
+#pragma unroll
+          for (int e = 8; e < 128; e += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top[i] = max3(top[i], __uint_as_float(s[e + i]), __uint_as_float(s[e + i + 4]));
+          const float now = max3(fmaxf(top[0], top[1]), top[2], top[3]);
           if (j == 0) {
             m = now;
           } else {
@@ -441,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, grow)) {
               const float w = grow ? fast_exp2((m - now) * scale) : 1.f;
               if (grow) m = now;
-              l *= w;
+              sum.x *= w;
+              sum.y *= w;
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -455,22 +502,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : -m * scale;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int e = 0; e < 128; e += 2) {
-            const float x = fast_exp2(fmaf(__uint_as_float(s[e]), scale, ref));
-            const float y = fast_exp2(fmaf(__uint_as_float(s[e + 1]), scale, ref));
-            sum[(e / 2) % 4] += x + y;
-            s[e / 2] = pack_bf16(x, y);
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int e = 64 * half; e < 64 * half + 64; e += 2) {
+              float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, ref2);
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              part[(e / 2) % 2] = __fadd2_rn(part[(e / 2) % 2], x);
+              s[e / 2] = pack_bf16(x.x, x.y);
+            }
+            tmem_st32(ts + 32 * half, s + 32 * half);
+            tmem_wait_st();
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[tile][half]);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st32(ts, s);
-          tmem_st32(ts + 32, s + 32);
-          tmem_wait_st();
+          sum = __fadd2_rn(sum, __fadd2_rn(part[0], part[1]));
+        } else {
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.p_full[tile][0]);
+            mbar_arrive(&sh.p_full[tile][1]);
+          }
         }
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[tile]);
       }
       if (!here) info += n;
       if (!ok) break;
@@ -483,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int n_odd = n > 0 ? sh.n_odd[slot.at] : 0;
         const int32_t rho = it.row0 + row;
+        const float l = sum.x + sum.y;
         const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                              ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D;
@@ -505,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n_odd > 0 && mine) {
 #pragma unroll 1
               for (int e = 0; e < 32; ++e) {
-                const float x = odd_value(a, it, sh.odd[slot.at], n_odd, pos, 32 * c + e);
+                const float x = odd_value(a, it.request, it.head, sh.odd[slot.at], n_odd, pos, 32 * c + e);
 #pragma unroll
                 for (int f = 0; f < 32; ++f)
                   if (f == e) o[f] = __float_as_uint(__uint_as_float(o[f]) + x);

@@ -334,141 +334,6 @@ def append_kv(cfg: Mapping, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: t
         _stream(stream)), "srkv_append_kv")
 
 
-def _token_rows(t: torch.Tensor | None, name: str, dtype: torch.dtype, device: torch.device):
-    """A packed [tokens][heads][d] tensor whose heads lie side by side, tokens any stride apart: its
-    pointer and that stride in elements."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    n, heads, d = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != d):
-        raise ValueError(f"{name}: each token's heads must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), s0 if n > 1 else heads * d
-
-
-def _chunk_device(first: torch.Tensor, **others) -> torch.device:
-    """The one device of a chunk call's tensors: the current one, whose stream the call goes to."""
-    if not first.is_cuda:
-        raise ValueError("q, k_new and the caches must be CUDA tensors")
-    dev = first.device
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor,
-                   rope_freqs: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                   block_table: torch.Tensor, chunk_offsets: torch.Tensor, seq_lens: torch.Tensor,
-                   reps: torch.Tensor, q_out: torch.Tensor | None = None,
-                   error_flags: torch.Tensor | None = None, stream=None, *,
-                   interleaved: bool = False) -> None:
-    """Rotates a ragged chunk of new tokens to their positions, writes keys and values to the pages and
-    refreshes the vectors of the pages written; the rotated queries go to q_out.
-
-    Request r brings rows [chunk_offsets[r], chunk_offsets[r + 1]) of q [T][Hq][d], k_new and v_new
-    [T][Hkv][d] (views of a fused projection will do: a token's heads are contiguous, tokens any stride
-    apart), at positions seq_lens[r] on; the caller then adds the chunk's tokens to seq_lens.
-    rope_freqs: float64 [rope_dim / 2], radians per token (None: no rotation); interleaved: pairs
-    (2j, 2j + 1) instead of (j, j + rope_dim / 2).  q None: no queries."""
-    Hq, Hkv, S, d = _cache_dims(cfg)
-    _shape(block_table, "block_table", None, None)
-    B = block_table.shape[0]
-    _shape(k_new, "k_new", None, Hkv, d)
-    T = k_new.shape[0]
-    _shape(q, "q", T, Hq, d)
-    _shape(q_out, "q_out", T, Hq, d)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    _shape(v_new, "v_new", T, Hkv, d)
-    _shape(rope_freqs, "rope_freqs", None)
-    _shape(k_cache, "k_cache", None, Hkv, S, d)
-    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
-    _shape(chunk_offsets, "chunk_offsets", B + 1)
-    _shape(seq_lens, "seq_lens", B)
-    _shape(reps, "reps", None, Hkv, d)
-    _rows(reps, "reps", k_cache.shape[0])
-    _shape(error_flags, "error_flags", 1)
-    dev = _chunk_device(k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
-                        chunk_offsets=chunk_offsets, rope_freqs=rope_freqs, reps=reps, q_out=q_out,
-                        error_flags=error_flags)
-    c = config(cfg)
-    st = _store_dtype(cfg)
-    qp, qs = _token_rows(q, "q", st, dev)
-    kp, ks = _token_rows(k_new, "k_new", st, dev)
-    vp, vs = _token_rows(v_new, "v_new", st, dev)
-    _check(load().srkv_append_kv_rope(
-        ctypes.byref(c), qp, qs, kp, ks, vp, vs, _dev(chunk_offsets, "chunk_offsets", torch.int32), T,
-        _dev(rope_freqs, "rope_freqs", torch.float64),
-        0 if rope_freqs is None else 2 * rope_freqs.numel(), int(interleaved),
-        _dev(q_out, "q_out", st), _dev(k_cache, "k_cache", st), _dev(v_cache, "v_cache", st),
-        k_cache.shape[0], _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-        _dev(seq_lens, "seq_lens", torch.int32), B, _dev(reps, "reps", torch.float32),
-        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), "srkv_append_kv_rope")
-
-
-def chunk_workspace_size(cfg: Mapping, total_tokens: int, batch: int) -> int:
-    """Workspace bytes of the chunk attention calls for `total_tokens` rows of `batch` requests."""
-    c = config(cfg)
-    return int(load().srkv_chunk_workspace_size(ctypes.byref(c), total_tokens, batch))
-
-
-def _chunk_attention(name: str, cfg: Mapping, q, k_cache, v_cache, block_table, chunk_offsets,
-                     seq_lens, out, workspace, error_flags, stream) -> None:
-    Hq, Hkv, S, d = _cache_dims(cfg)
-    _shape(block_table, "block_table", None, None)
-    B = block_table.shape[0]
-    _shape(q, "q", None, Hq, d)
-    _shape(k_cache, "k_cache", None, Hkv, S, d)
-    _shape(v_cache, "v_cache", k_cache.shape[0], Hkv, S, d)
-    _shape(chunk_offsets, "chunk_offsets", B + 1)
-    _shape(seq_lens, "seq_lens", B)
-    _shape(out, "out", q.shape[0], Hq, d)
-    _shape(error_flags, "error_flags", 1)
-    dev = _chunk_device(k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
-                        chunk_offsets=chunk_offsets, out=out, workspace=workspace,
-                        error_flags=error_flags)
-    c = config(cfg)
-    st = _store_dtype(cfg)
-    qp, qs = _token_rows(q, "q", st, dev)
-    _check(getattr(load(), name)(
-        ctypes.byref(c), qp, qs, _dev(k_cache, "k_cache", st), _dev(v_cache, "v_cache", st),
-        k_cache.shape[0], _dev(block_table, "block_table", torch.int32), block_table.shape[1],
-        _dev(chunk_offsets, "chunk_offsets", torch.int32), q.shape[0],
-        _dev(seq_lens, "seq_lens", torch.int32), B, _dev(out, "out", st),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _dev(error_flags, "error_flags", torch.int32), _stream(stream)), name)
-
-
-def chunk_attention(cfg: Mapping, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                    block_table: torch.Tensor, chunk_offsets: torch.Tensor, seq_lens: torch.Tensor,
-                    out: torch.Tensor, workspace: torch.Tensor,
-                    error_flags: torch.Tensor | None = None, stream=None) -> None:
-    """Causal attention of a ragged chunk of new tokens over the paged cache that holds them: rows
-    [chunk_offsets[r], chunk_offsets[r + 1]) of q [T][Hq][d] are the last tokens of request r's
-    seq_lens[r].  workspace: chunk_workspace_size(cfg, T, B) bytes."""
-    _chunk_attention("srkv_chunk_attention", cfg, q, k_cache, v_cache, block_table, chunk_offsets,
-                     seq_lens, out, workspace, error_flags, stream)
-
-
-def chunk_attention_window(cfg: Mapping, q: torch.Tensor, k_cache: torch.Tensor,
-                           v_cache: torch.Tensor, block_table: torch.Tensor,
-                           chunk_offsets: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
-                           workspace: torch.Tensor, error_flags: torch.Tensor | None = None,
-                           stream=None) -> None:
-    """chunk_attention over the configuration's first tokens (init_tokens) and each position's window
-    (local_tokens) alone."""
-    _chunk_attention("srkv_chunk_attention_window", cfg, q, k_cache, v_cache, block_table,
-                     chunk_offsets, seq_lens, out, workspace, error_flags, stream)
-
-
 def score_topk(cfg: Mapping, q: torch.Tensor, reps: torch.Tensor, block_table: torch.Tensor,
                seq_lens: torch.Tensor, prompt_lens: torch.Tensor | None, sel: torch.Tensor,
                nsel: torch.Tensor, error_flags: torch.Tensor | None = None,
@@ -847,7 +712,7 @@ def _int4_pages(kv_int4: torch.Tensor, Hkv: int, slab: int) -> int:
     return shape[0]
 
 
-def _bf16_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, want: tuple) -> int:
+def _cache_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, want: tuple) -> int:
     shape = k_cache.shape
     if len(shape) != 4 or shape[1:] != want:
         raise ValueError(f"k_cache must have shape [*, {', '.join(map(str, want))}], got {list(shape)}")
@@ -864,7 +729,7 @@ def quantize_kv_int4(cfg: Mapping, k_cache: torch.Tensor, v_cache: torch.Tensor,
     page_ids[i]) of kv_int4, uint8 [pages][Hkv][kv_int4_slab_bytes(cfg)]."""
     key = _cfg_values(cfg)
     _, Hkv, d, S = key[:4]
-    pages = _bf16_pages(k_cache, v_cache, (Hkv, S, d))
+    pages = _cache_pages(k_cache, v_cache, (Hkv, S, d))
     slabs = _int4_pages(kv_int4, Hkv, S * (d + 8))
     _shape(page_ids, "page_ids", None)
     n = page_ids.shape[0]
@@ -893,7 +758,7 @@ def dequantize_kv_int4(cfg: Mapping, kv_int4: torch.Tensor, int4_page_ids: torch
     int4_page_ids[i]) of the bf16 caches."""
     key = _cfg_values(cfg)
     _, Hkv, d, S = key[:4]
-    pages = _bf16_pages(k_cache, v_cache, (Hkv, S, d))
+    pages = _cache_pages(k_cache, v_cache, (Hkv, S, d))
     slabs = _int4_pages(kv_int4, Hkv, S * (d + 8))
     _shape(int4_page_ids, "int4_page_ids", None)
     n = int4_page_ids.shape[0]
@@ -987,6 +852,145 @@ def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
         nsel.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
         None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)),
         "srkv_retrieval_decode_int4")
+
+
+# Chunks of new tokens: as lean as the 4-bit calls, as one token of one request is a chunk too.
+
+def _packed(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, shape: tuple) -> int:
+    """Checks packed rows [tokens][heads][d] whose tokens may lie any stride apart, a token's heads side by
+    side; returns that stride in elements."""
+    if t.shape != shape:
+        _need(t, name, shape)
+    if t.dtype is not dtype or t.get_device() != dev:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return s0 if shape[0] > 1 else shape[1] * shape[2]
+
+
+def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor,
+                   rope_freqs: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_table: torch.Tensor, chunk_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                   reps: torch.Tensor, q_out: torch.Tensor | None = None,
+                   error_flags: torch.Tensor | None = None, stream=None, *,
+                   interleaved: bool = False) -> None:
+    """Rotates a ragged chunk of new tokens to their positions, writes keys and values to the pages and
+    refreshes the vectors of the pages written; the rotated queries go to q_out.
+
+    Request r brings rows [chunk_offsets[r], chunk_offsets[r + 1]) of q [T][Hq][d], k_new and v_new
+    [T][Hkv][d] (views of a fused projection will do: a token's heads are contiguous, tokens any stride
+    apart), at positions seq_lens[r] on; the caller then adds the chunk's tokens to seq_lens.
+    rope_freqs: float64 [rope_dim / 2], radians per token (None: no rotation); interleaved: pairs
+    (2j, 2j + 1) instead of (j, j + rope_dim / 2).  q and q_out None: no queries."""
+    key = _cfg_values(cfg)
+    Hq, Hkv, d, S = key[:4]
+    dt = torch.float32 if key[8] else torch.bfloat16
+    B, max_blocks = _table(block_table)
+    shape = k_new.shape
+    T = shape[0] if len(shape) == 3 else 0
+    rows = (T, Hkv, d)
+    if shape != rows or v_new.shape != rows:
+        _need(k_new, "k_new", rows)
+        _need(v_new, "v_new", rows)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None and (q.shape != (T, Hq, d) or q_out.shape != (T, Hq, d)):
+        _need(q, "q", (T, Hq, d))
+        _need(q_out, "q_out", (T, Hq, d))
+    if chunk_offsets.shape != (B + 1,) or seq_lens.shape != (B,):
+        _need(chunk_offsets, "chunk_offsets", (B + 1,))
+        _need(seq_lens, "seq_lens", (B,))
+    if rope_freqs is not None and rope_freqs.dim() != 1:
+        raise ValueError(f"rope_freqs must have shape [*], got {list(rope_freqs.shape)}")
+    if error_flags is not None and error_flags.shape != (1,):
+        _need(error_flags, "error_flags", (1,))
+    pages = _cache_pages(k_cache, v_cache, (Hkv, S, d))
+    _vectors(reps, Hkv, d, pages)
+    dev = k_cache.get_device()
+    if not (0 <= dev == _current_device() and _held(dev, dt, k_cache, v_cache)
+            and _held(dev, torch.int32, block_table, chunk_offsets, seq_lens)
+            and _held(dev, torch.float32, reps) and (q_out is None or _held(dev, dt, q_out))
+            and (rope_freqs is None or _held(dev, torch.float64, rope_freqs))
+            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+        _refuse(dev, "k_cache", k_cache=(k_cache, dt), v_cache=(v_cache, dt), block_table=(block_table, torch.int32),
+                chunk_offsets=(chunk_offsets, torch.int32), seq_lens=(seq_lens, torch.int32),
+                reps=(reps, torch.float32), q_out=(q_out, dt), rope_freqs=(rope_freqs, torch.float64),
+                error_flags=(error_flags, torch.int32))
+    qp = qo = None
+    qs = 0
+    if q is not None:
+        qs, qp, qo = _packed(q, "q", dt, dev, (T, Hq, d)), q.data_ptr(), q_out.data_ptr()
+    ks, vs = _packed(k_new, "k_new", dt, dev, rows), _packed(v_new, "v_new", dt, dev, rows)
+    freqs, rope_dim = (None, 0) if rope_freqs is None else (rope_freqs.data_ptr(), 2 * rope_freqs.shape[0])
+    _check((_lib or load()).srkv_append_kv_rope(
+        _cfg_ref(key), qp, qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs, chunk_offsets.data_ptr(), T, freqs,
+        rope_dim, 1 if interleaved else 0, qo, k_cache.data_ptr(), v_cache.data_ptr(), pages,
+        block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B, reps.data_ptr(),
+        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)), "srkv_append_kv_rope")
+
+
+def chunk_workspace_size(cfg: Mapping, total_tokens: int, batch: int) -> int:
+    """Workspace bytes of the chunk attention calls for `total_tokens` rows of `batch` requests."""
+    return int(load().srkv_chunk_workspace_size(_cfg_ref(_cfg_values(cfg)), total_tokens, batch))
+
+
+def _chunk_attention(name: str, cfg: Mapping, q, k_cache, v_cache, block_table, chunk_offsets,
+                     seq_lens, out, workspace, error_flags, stream) -> None:
+    key = _cfg_values(cfg)
+    Hq, Hkv, d, S = key[:4]
+    dt = torch.float32 if key[8] else torch.bfloat16
+    B, max_blocks = _table(block_table)
+    shape = q.shape
+    T = shape[0] if len(shape) == 3 else 0
+    rows = (T, Hq, d)
+    if (shape != rows or out.shape != rows or chunk_offsets.shape != (B + 1,) or seq_lens.shape != (B,)
+            or (error_flags is not None and error_flags.shape != (1,))):
+        _need(q, "q", rows)
+        _need(out, "out", rows)
+        _need(chunk_offsets, "chunk_offsets", (B + 1,))
+        _need(seq_lens, "seq_lens", (B,))
+        if error_flags is not None:
+            _need(error_flags, "error_flags", (1,))
+    pages = _cache_pages(k_cache, v_cache, (Hkv, S, d))
+    dev = k_cache.get_device()
+    if not (0 <= dev == _current_device() and _held(dev, dt, k_cache, v_cache, out)
+            and _held(dev, torch.int32, block_table, chunk_offsets, seq_lens)
+            and _held(dev, workspace.dtype, workspace)
+            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+        _refuse(dev, "k_cache", k_cache=(k_cache, dt), v_cache=(v_cache, dt), out=(out, dt),
+                block_table=(block_table, torch.int32), chunk_offsets=(chunk_offsets, torch.int32),
+                seq_lens=(seq_lens, torch.int32), workspace=(workspace, workspace.dtype),
+                error_flags=(error_flags, torch.int32))
+    qs = _packed(q, "q", dt, dev, rows)
+    _check(getattr(_lib or load(), name)(
+        _cfg_ref(key), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), pages, block_table.data_ptr(),
+        max_blocks, chunk_offsets.data_ptr(), T, seq_lens.data_ptr(), B, out.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)), name)
+
+
+def chunk_attention(cfg: Mapping, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, chunk_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                    out: torch.Tensor, workspace: torch.Tensor,
+                    error_flags: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of a ragged chunk of new tokens over the paged cache that holds them: rows
+    [chunk_offsets[r], chunk_offsets[r + 1]) of q [T][Hq][d] (tokens any stride apart) are the last tokens of
+    request r's seq_lens[r].  workspace: chunk_workspace_size(cfg, T, B) bytes."""
+    _chunk_attention("srkv_chunk_attention", cfg, q, k_cache, v_cache, block_table, chunk_offsets,
+                     seq_lens, out, workspace, error_flags, stream)
+
+
+def chunk_attention_window(cfg: Mapping, q: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, block_table: torch.Tensor,
+                           chunk_offsets: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
+                           workspace: torch.Tensor, error_flags: torch.Tensor | None = None,
+                           stream=None) -> None:
+    """chunk_attention over the configuration's first tokens (init_tokens) and each position's window
+    (local_tokens) alone."""
+    _chunk_attention("srkv_chunk_attention_window", cfg, q, k_cache, v_cache, block_table,
+                     chunk_offsets, seq_lens, out, workspace, error_flags, stream)
 
 
 def selftest_wait_timeout(error_flags: torch.Tensor, stream=None) -> None:
