@@ -38,9 +38,9 @@ struct __align__(16) ChunkMerge {
 };
 
 struct ChunkHead {  // counters of one call, written by the plan
-  int32_t items, merges;
+  int32_t items, merges;  // merges: divided tiles times heads
   int32_t next;       // the next item to hand out
-  int32_t merge_rows;  // rows of the largest merge
+  int32_t merge_rows, merge_parts;  // rows, and parts, of the largest merge
 };
 
 // Workspace (256-byte aligned parts).
