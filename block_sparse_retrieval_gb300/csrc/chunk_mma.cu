@@ -5,10 +5,11 @@
 // row, updates the row's maximum and sum, and writes P = 2^(c S - c m) as bf16 over S;  O += P V (O in tensor memory).
 // The products of one tile run while the other tile's warpgroup is at its exponentials.
 //
-//   warps 0-3, 4-7   softmax and output of tile 0, 1
-//   warp 8           issues the products
-//   warp 9           takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
-//   warps 10, 11     copy the queries of the next item once the last product with the present ones is done
+//   warps 0-7, 8-15  softmax and output of tile 0, 1: two threads a row, 64 of a page's tokens each
+//   warp 16          issues the products
+//   warp 17          takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
+//   warps 18, 19     copy the queries of the next item once the last product with the present ones is done; 19 cleans
+//                    values (below)
 //
 // The reference m that the exponentials subtract follows the maximum only when that has grown by more than 2^8:
 // O is then scaled by hand.  Sums and outputs stay exact for any reference; fp32 holds the larger weights.
@@ -27,19 +28,21 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_pages, int
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kPageWarp = 17, kQueryWarp = 18, kCleanWarp = 19;
 constexpr int kSlots = 2;      // items known at a time
-constexpr int kPageInfo = 16;  // pages between their copy and their softmax, at most
+constexpr int kPageInfo = 8;   // pages between their copy and their softmax, at most
+constexpr int kParts = 4;      // pages seen in part and not yet multiplied, at most: their stages are not refilled
 constexpr int kOdd = 8;        // pages that an item's rows see in part, at most: 3 at each end of a window of 256 rows, 1 at the first tokens
-// Registers: the softmax threads hold a row of 128 logits; 256 x 208 + 128 x 88 = 384 x 168, what the block is launched with.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Registers: 512 x 104 + 128 x 64 = 640 x 96, what the block is launched with.
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr float kGrow = 8.f;   // log2 of the growth of a maximum that the reference lets pass
 
 template <int D>
 struct Geo {
   static constexpr int kTileBytes = 128 * D * 2;       // a tile of Q, a page of K or V
   static constexpr int kBlockBytes = 128 * 128;        // its blocks of 64 columns
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kS = 0, kO = 256;          // columns of tensor memory: S0 S1 O0 O1
   static constexpr size_t kOffQ = 0, kOffStage = 2 * kTileBytes,
                           kOffBar = kOffStage + (size_t)kStages * kTileBytes;
@@ -51,17 +54,23 @@ struct OddPage {
 };
 
 struct Shared {
-  uint64_t full[10], empty[10];
+  uint64_t full[8], empty[8];
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2][2], o_full[2];  // P in two halves of its tokens
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // P in two parts: the first 32 tokens of each half, the others
+  uint64_t pair[2][4];  // the two warps of a tile's 32 rows
+  uint64_t v_part[kParts], v_clean[kParts];
+  int2 part[kParts];  // stage of a page seen in part, and the parity of its copy
   uint64_t drain;
   ChunkItem item[kSlots];
-  int32_t page_ok[kPageInfo];
+  int2 page[kPageInfo];   // block, and how it is seen
+  float note[2][2][128];  // [tile][half][row]: a maximum, or a sum
   OddPage odd[kSlots][kOdd];
   int32_t n_odd[kSlots];
   uint32_t tmem;
 };
+
+enum { kPart = 1, kAbsent = 2 };  // how an item's rows see a page: 0 whole
 
 struct Maps {
   CUtensorMap k, v;
@@ -103,33 +112,43 @@ __device__ __forceinline__ void item_span(const ChunkItem& it, int32_t G, int32_
 // not finite replaced by zero.  Returns (in every lane) the rows that had one.
 template <int D>
 __device__ __forceinline__ uint4 clean_values(unsigned char* stage, int32_t valid, int lane) {
-  uint32_t bad[4] = {0, 0, 0, 0};
+  uint32_t bad[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const int row = g * 32 + lane;
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      // 16-byte chunks, lanes at different ones (the swizzle permutes them within a row only)
+    // 16-byte chunks, the lanes at different ones (the swizzle permutes them within a row only)
+    auto at = [&](int c) {
       const int chunk = (c + lane) % (D / 8);
-      uint4* p = reinterpret_cast<uint4*>(stage + (chunk / 8) * (128 * 128) + row * 128 + (chunk % 8) * 16);
-      if (row >= valid) {
-        *p = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      uint4 x = *p;
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      bool hit = false;
+      return reinterpret_cast<uint4*>(stage + (chunk / 8) * (128 * 128) + row * 128 + (chunk % 8) * 16);
+    };
+    uint32_t odd = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, hit = true;
-        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, hit = true;
-      }
-      if (hit) {
-        *p = make_uint4(w[0], w[1], w[2], w[3]);
-        bad[g] = 1;
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = *at(c);
+      // an exponent of all ones carries into the sign bit's place
+      odd |= ((x.x & 0x7fff7fffu) + 0x00800080u) | ((x.y & 0x7fff7fffu) + 0x00800080u) |
+             ((x.z & 0x7fff7fffu) + 0x00800080u) | ((x.w & 0x7fff7fffu) + 0x00800080u);
+    }
+    if (row >= valid) {
+      odd = 0;
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) *at(c) = make_uint4(0, 0, 0, 0);
+    }
+    odd &= 0x80008000u;
+    if (odd) {
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *at(c);
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+          if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+        }
+        *at(c) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    bad[g] = __ballot_sync(0xffffffffu, bad[g]);
+    bad[g] = __ballot_sync(0xffffffffu, odd != 0);
   }
   return make_uint4(bad[0], bad[1], bad[2], bad[3]);
 }
@@ -164,6 +183,13 @@ __device__ __forceinline__ uint32_t attended_bits(int32_t pos, int32_t t0, int32
   return bits_below(pos - t0 + 1) & (bits_below(init - t0) | ~bits_below(from - t0));
 }
 
+// Logits of hidden tokens to minus infinity.
+__device__ __forceinline__ void hide(uint32_t* s, uint32_t on) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(on >> e & 1u)) s[e] = 0xff800000u;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -183,8 +209,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ Maps maps) {
   using G = Geo<D>;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];  // the swizzle's period
   Shared& sh = *reinterpret_cast<Shared*>(smem + G::kOffBar);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
@@ -194,20 +219,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 11);  // every warp but the one that takes items
+      mbar_init(&sh.item_empty[i], 19);  // every warp but the one that takes items
     }
     mbar_init(&sh.q_full, 2);
     mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&sh.v_part[i], 1);
+      mbar_init(&sh.v_clean[i], 1);
+    }
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i][0], 4);
-      mbar_init(&sh.p_full[i][1], 4);
+      for (int c = 0; c < 2; ++c) mbar_init(&sh.p_full[i][c], 8);
+      for (int w = 0; w < 4; ++w) mbar_init(&sh.pair[i][w], 2);
       mbar_init(&sh.o_full[i], 2);  // the products, and the notes of clean_values
     }
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(&sh.tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
@@ -217,12 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t eflags = 0;
   bool ok = true;  // no wait has run out
   Ring<kSlots> slot;
-  // Next item for a consumer warp: false at the end.
-  auto take = [&](ChunkItem& it) {
+  // Next item for a consumer warp, in sh.item[slot.at] until done(): false at the end.
+  auto take = [&] {
     ok = ok && mbar_wait(&sh.item_full[slot.at], slot.phase);
-    if (!ok) return false;
-    it = sh.item[slot.at];
-    return it.request >= 0;
+    return ok && sh.item[slot.at].request >= 0;
   };
   auto done = [&] {
     __syncwarp();
@@ -230,14 +257,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     slot.next();
   };
 
-  if (warp >= 8) {
+  if (warp >= kMmaWarp) {
     fewer_registers<kOtherRegs>();
-    if (warp == 9) {
+    if (warp == kPageWarp) {
       // ---------------------------------------------------------------- items and pages
       ChunkHead* head = chunk_head(a);
       const int32_t n_items = head->items;
       const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.lay.items);
       Ring<G::kStages> st;
+      Ring<kParts> part;
       int64_t issued = 0;
       uint32_t info = 0;
       int32_t next = blockIdx.x;
@@ -254,34 +282,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         slot.next();
         if (next >= n_items) break;
+        int32_t p_lo, p_hi;
+        item_span(it, a.G, p_lo, p_hi);
         for (int32_t j0 = it.j0; j0 < it.j1 && ok; j0 += 32) {
-          int32_t page = 0;
-          bool good = true;
+          int32_t page = 0, b = 0, seen = 0;
           if (j0 + lane < it.j1) {
-            page = a.block_table[(int64_t)it.request * a.max_blocks + page_of(it, j0 + lane)];
-            good = page >= 0 && (int64_t)page < a.num_pages;
-            if (!good) {
+            b = page_of(it, j0 + lane);
+            page = a.block_table[(int64_t)it.request * a.max_blocks + b];
+            if (chunk_masked(b, p_lo, p_hi, a.init, a.local)) seen = kPart;
+            if (page < 0 || (int64_t)page >= a.num_pages) {
               eflags |= SRKV_EFLAG_PAGE_RANGE;
               page = (int32_t)a.num_pages;  // behind the cache: the copy fills with zeros
+              seen |= kAbsent;
             }
           }
           const int n = min(32, it.j1 - j0);
           for (int i = 0; i < n && ok; ++i) {
             const int32_t z = __shfl_sync(0xffffffffu, page, i);
-            const int32_t fine = __shfl_sync(0xffffffffu, (int32_t)good, i);
+            const int2 note = make_int2(__shfl_sync(0xffffffffu, b, i), __shfl_sync(0xffffffffu, seen, i));
             for (int kv = 0; kv < 2 && ok; ++kv) {
               ok = mbar_wait(&sh.empty[st.at], st.phase ^ 1);
               if (!ok) break;
               if (lane == 0) {
-                if (kv == 0) sh.page_ok[info % kPageInfo] = fine;
+                if (kv == 0) sh.page[info % kPageInfo] = note;
                 unsigned char* dst = smem + G::kOffStage + (size_t)st.at * G::kTileBytes;
                 mbar_arrive_expect_tx(&sh.full[st.at], G::kTileBytes);
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b)
                   tma_page(dst + b * G::kBlockBytes, kv ? &maps.v : &maps.k, 64 * b, it.head * kBlock, z,
                            &sh.full[st.at]);
+                if (kv == 1 && (note.y & kPart)) {
+                  sh.part[part.at] = make_int2(st.at, (int)st.phase);
+                  mbar_arrive(&sh.v_part[part.at]);
+                }
               }
               __syncwarp();
+              if (kv == 1 && (note.y & kPart)) part.next();
               st.next();
               ++issued;
             }
@@ -300,33 +336,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         --st.at;
         ok = mbar_wait(&sh.full[st.at], st.phase) && ok;
       }
-    } else if (warp == 8) {
+    } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- products
       constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
-      const uint32_t q0 = smem_u32(smem + G::kOffQ), stage0 = smem_u32(smem + G::kOffStage);
+      const uint32_t q_desc = smem_desc(smem_u32(smem + G::kOffQ), 0);
+      const uint32_t k_desc = smem_desc(smem_u32(smem + G::kOffStage), 0);
+      const uint32_t v_desc = smem_desc(smem_u32(smem + G::kOffStage), G::kBlockBytes);
       Ring<G::kStages> st;
       Ring<1> qr, pr[2];
+      Ring<kParts> part;
+      uint32_t info = 0;
       auto qk = [&](int i, int s) {  // S_i = Q_i K^T
+        const uint32_t q = q_desc + i * (G::kTileBytes >> 4), k = k_desc + s * (G::kTileBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * G::kBlockBytes + (k % 4) * 32;
-          mma_ss(tmem + G::kS + 128 * i, smem_desc(q0 + i * G::kTileBytes + off, 0),
-                 smem_desc(stage0 + s * G::kTileBytes + off, 0), kQK, k > 0);
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = ((e / 4) * G::kBlockBytes + (e % 4) * 32) >> 4;
+          mma_ss(tmem + G::kS + 128 * i, q + off, k + off, kQK, e > 0);
         }
         mma_commit(&sh.s_full[i]);
       };
-      auto pv = [&](int i, int s, int half, bool first) {  // O_i (+)= P_i V over a half of the tokens
+      // O_i (+)= P_i V over a part of the tokens; each half of P lies at the start of its half of S.
+      auto pv = [&](int i, int s, int part, bool first) {
+        const uint32_t v = v_desc + s * (G::kTileBytes >> 4);
 #pragma unroll
-        for (int k = 4 * half; k < 4 * half + 4; ++k)
-          mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 8 * k,
-                 smem_desc(stage0 + s * G::kTileBytes + k * 2048, G::kBlockBytes), kPV, !first || k > 0);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 2 * part; e < 2 * part + 2; ++e)
+            mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 64 * h + 8 * e, v + (4 * h + e) * (2048 >> 4), kPV,
+                   !first || part + h + e > 0);
       };
-      ChunkItem it;
-      while (take(it)) {
+      while (take()) {
+        const ChunkItem& it = sh.item[slot.at];
         const int tiles = it.rows > 128 ? 2 : 1;
         const int32_t n = it.j1 - it.j0;
-        int32_t p_lo, p_hi;
-        item_span(it, a.G, p_lo, p_hi);
         if (n > 0) {
           ok = ok && mbar_wait(&sh.q_full, qr.phase) && mbar_wait(&sh.full[st.at], st.phase);
           if (!ok) break;
@@ -347,34 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < n) st.next();
           ok = mbar_wait(&sh.full[v.at], v.phase);
           if (!ok) break;
-          const int32_t b = page_of(it, it.j0 + j);
-          if (chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
-            const uint4 bad =
-                clean_values<D>(smem + G::kOffStage + (size_t)v.at * G::kTileBytes, it.L - b * kBlock, lane);
-            const int32_t at = sh.n_odd[slot.at];
-            __syncwarp();
-            if (lane == 0 && (bad.x | bad.y | bad.z | bad.w) && at < kOdd) {
-              OddPage& o = sh.odd[slot.at][at];
-              o.tokens[0] = bad.x;
-              o.tokens[1] = bad.y;
-              o.tokens[2] = bad.z;
-              o.tokens[3] = bad.w;
-              o.block = b;
-              sh.n_odd[slot.at] = at + 1;
-            }
-            fence_async_smem();
-            __syncwarp();
+          if (sh.page[info++ % kPageInfo].y & kPart) {
+            ok = mbar_wait(&sh.v_clean[part.at], part.phase);
+            if (!ok) break;
+            part.next();
           }
           for (int i = 0; i < tiles; ++i) {
-            for (int half = 0; half < 2 && ok; ++half) {
-              ok = mbar_wait(&sh.p_full[i][half], pr[i].phase);
+            for (int part = 0; part < 2 && ok; ++part) {
+              ok = mbar_wait(&sh.p_full[i][part], pr[i].phase);
               if (!ok) break;
               tcgen05_fence_after();
-              if (lane == 0) pv(i, v.at, half, j == 0);
+              if (lane == 0) pv(i, v.at, part, j == 0);
               __syncwarp();
             }
+            if (!ok) break;
             pr[i].next();
-            if (i == 0 && j + 1 < n) ok = ok && mbar_wait(&sh.full[k.at], k.phase);
+            if (i == 0 && j + 1 < n) ok = mbar_wait(&sh.full[k.at], k.phase);
             if (!ok) break;
             if (lane == 0) {
               if (i == tiles - 1) mma_commit(&sh.empty[v.at]);
@@ -400,16 +430,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&sh.drain, 0);
       }
     } else {
-      // ---------------------------------------------------------------- queries
-      ChunkItem it;
+      // ---------------------------------------------------------------- queries, and values to be cleaned
+      Ring<kParts> part;
       Ring<1> qr;
-      while (take(it)) {
+      while (take()) {
+        const ChunkItem& it = sh.item[slot.at];
         if (it.j1 > it.j0) {
           ok = ok && mbar_wait(&sh.q_empty, qr.phase ^ 1);
           if (!ok) break;
           qr.next();
           constexpr int C = D / 8;  // 16-byte chunks of a row
-          const int t = (warp - 10) * 32 + lane, chunk = t % C;
+          const int t = (warp - kQueryWarp) * 32 + lane, chunk = t % C;
           for (int row = t / C; row < it.rows; row += 64 / C) {
             const int32_t rho = it.row0 + row;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
@@ -425,26 +456,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.q_full);
         }
+        if (warp == kCleanWarp) {  // the values of pages seen in part, ahead of their product
+          int32_t p_lo, p_hi;
+          item_span(it, a.G, p_lo, p_hi);
+          for (int32_t j = it.j0; j < it.j1 && ok; ++j) {
+            const int32_t b = page_of(it, j);
+            if (!chunk_masked(b, p_lo, p_hi, a.init, a.local)) continue;
+            ok = mbar_wait(&sh.v_part[part.at], part.phase);
+            if (!ok) break;
+            const int2 where = sh.part[part.at];
+            ok = mbar_wait(&sh.full[where.x], (uint32_t)where.y);
+            if (!ok) break;
+            const uint4 bad =
+                clean_values<D>(smem + G::kOffStage + (size_t)where.x * G::kTileBytes, it.L - b * kBlock, lane);
+            if (lane == 0 && (bad.x | bad.y | bad.z | bad.w) && sh.n_odd[slot.at] < kOdd) {
+              OddPage& o = sh.odd[slot.at][sh.n_odd[slot.at]++];
+              o.tokens[0] = bad.x;
+              o.tokens[1] = bad.y;
+              o.tokens[2] = bad.z;
+              o.tokens[3] = bad.w;
+              o.block = b;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.v_clean[part.at]);
+            part.next();
+          }
+        }
         done();
       }
     }
   } else {
     more_registers<kSoftmaxRegs>();
     // ---------------------------------------------------------------- softmax and output
-    const int tile = warp / 4, row = 128 * tile + 32 * (warp % 4) + lane;
-    const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
-    const uint32_t ts = tmem + G::kS + 128 * tile + lanes, to = tmem + G::kO + D * tile + lanes;
+    const int tile = warp / 8, half = warp / 4 % 2, quad = warp % 4, in_tile = 32 * quad + lane;
+    const int row = 128 * tile + in_tile;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t ts = tmem + G::kS + 128 * tile + 64 * half + lanes;
+    const uint32_t to = tmem + G::kO + D * tile + D / 2 * half + lanes;
     const float scale = a.scale_log2;
-    Ring<1> sr, orr;
+    Ring<1> sr, orr, xr;
+    // Both warps of a row wait for each other's note in shared memory.
+    auto exchange = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pair[tile][quad]);
+      ok = mbar_wait(&sh.pair[tile][quad], xr.phase);
+      xr.next();
+    };
     uint32_t info = 0;
-    ChunkItem it;
-    while (take(it)) {
+    while (take()) {
+      const ChunkItem& it = sh.item[slot.at];
       const int32_t n = it.j1 - it.j0;
-      const bool here = 128 * tile < it.rows;                       // the tile is in use
-      const bool work = 128 * tile + 32 * (warp % 4) < it.rows;     // some row of this warp is
-      const bool mine = row < it.rows;                              // this lane's row is
-      int32_t p_lo, p_hi;
-      item_span(it, a.G, p_lo, p_hi);
+      const bool here = 128 * tile < it.rows;              // the tile is in use
+      const bool work = 128 * tile + 32 * quad < it.rows;  // some row of this warp is
+      const bool mine = row < it.rows;                     // this lane's row is
       const int32_t pos = it.p0 + (it.row0 + row) / a.G;
       float m = -INFINITY;
       float2 sum = make_float2(0.f, 0.f);
@@ -454,32 +519,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         sr.next();
         tcgen05_fence_after();
         if (work) {
-          uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+          uint32_t s[64];
+          tmem_ld32(ts, s);
+          tmem_ld32(ts + 32, s + 32);
+          const int2 page = sh.page[info % kPageInfo];
           tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_use32(s + 32 * c);
-          const int32_t b = page_of(it, it.j0 + j);
-          const bool fine = sh.page_ok[info % kPageInfo] != 0;
-          if (!fine || chunk_masked(b, p_lo, p_hi, a.init, a.local)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t on = fine ? attended_bits(pos, b * kBlock + 32 * c, a.init, a.local) : 0u;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(on >> e & 1u)) s[32 * c + e] = 0xff800000u;
-            }
+          tmem_use32(s);
+          tmem_use32(s + 32);
+          uint32_t late = 0xffffffffu;  // what the row attends of the second 32 tokens
+          if (page.y) {
+            const int32_t t0 = page.x * kBlock + 64 * half;
+            hide(s, !(page.y & kAbsent) ? attended_bits(pos, t0, a.init, a.local) : 0u);
+            late = !(page.y & kAbsent) ? attended_bits(pos, t0 + 32, a.init, a.local) : 0u;
+            hide(s + 32, late);
           }
           float top[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top[i] = max3(i ? -INFINITY : m, __uint_as_float(s[i]), __uint_as_float(s[i + 4]));
+          for (int i = 0; i < 4; ++i) top[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 4]));
 #pragma unroll
-          for (int e = 8; e < 128; e += 8)
+          for (int e = 8; e < 64; e += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               top[i] = max3(top[i], __uint_as_float(s[e + i]), __uint_as_float(s[e + i + 4]));
-          const float now = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+          const float here_top = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+          sh.note[tile][half][in_tile] = here_top;  // read before this page's P is complete, so before the next S
+          exchange();
+          if (!ok) break;
+          const float now = max3(m, here_top, sh.note[tile][half ^ 1][in_tile]);
           if (j == 0) {
             m = now;
           } else {
@@ -491,63 +557,80 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum.y *= w;
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(to + 32 * c, o);
+                uint32_t o[16];
+                tmem_ld16(to + 16 * c, o);
                 tmem_wait_ld();
-                tmem_use32(o);
+                tmem_use16(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
-                tmem_st32(to + 32 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+                tmem_st16(to + 16 * c, o);
               }
             }
           }
           const float ref = m == -INFINITY ? 0.f : -m * scale;
           const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
           float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // the second half of the logits is read again rather than held over all this
+          tmem_ld32(ts + 32, s + 32);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int c = 0; c < 2; ++c) {
+            if (c == 1) {
+              tmem_wait_ld();
+              tmem_use32(s + 32);
+              if (page.y) hide(s + 32, late);
+            }
+            uint32_t p[16];
 #pragma unroll
-            for (int e = 64 * half; e < 64 * half + 64; e += 2) {
-              float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, ref2);
+            for (int e = 0; e < 32; e += 2) {
+              float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(s[32 * c + e]), __uint_as_float(s[32 * c + e + 1])), scale2, ref2);
               x.x = fast_exp2(x.x);
               x.y = fast_exp2(x.y);
               part[(e / 2) % 2] = __fadd2_rn(part[(e / 2) % 2], x);
-              s[e / 2] = pack_bf16(x.x, x.y);
+              p[e / 2] = pack_bf16(x.x, x.y);
             }
-            tmem_st32(ts + 32 * half, s + 32 * half);
+            tmem_st16(ts + 16 * c, p);
             tmem_wait_st();
             tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[tile][half]);
+            if (lane == 0) mbar_arrive(&sh.p_full[tile][c]);
           }
           sum = __fadd2_rn(sum, __fadd2_rn(part[0], part[1]));
-        } else {
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh.p_full[tile][0]);
-            mbar_arrive(&sh.p_full[tile][1]);
-          }
+        } else if (lane == 0) {
+          mbar_arrive(&sh.p_full[tile][0]);
+          mbar_arrive(&sh.p_full[tile][1]);
         }
       }
       if (!here) info += n;
       if (!ok) break;
       if (here) {
+        float l = 0.f;
         if (n > 0) {
           ok = mbar_wait(&sh.o_full[tile], orr.phase);
           if (!ok) break;
           orr.next();
           tcgen05_fence_after();
+          if (work) {
+            l = sum.x + sum.y;
+            sh.note[tile][half][in_tile] = l;
+            exchange();
+            if (!ok) break;
+            const float other = sh.note[tile][half ^ 1][in_tile];
+            l = half ? other + l : l + other;
+            exchange();  // before the next item's notes
+            if (!ok) break;
+          }
         }
-        const int n_odd = n > 0 ? sh.n_odd[slot.at] : 0;
-        const int32_t rho = it.row0 + row;
-        const float l = sum.x + sum.y;
-        const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                             ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D;
-        float* acc = reinterpret_cast<float*>(a.ws + a.lay.acc) + (int64_t)(it.slot + row) * D;
         if (work) {
+          const int n_odd = n > 0 ? sh.n_odd[slot.at] : 0;
+          const int32_t rho = it.row0 + row;
+          const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
+          const int col = D / 2 * half;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                               ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D + col;
+          float* acc = reinterpret_cast<float*>(a.ws + a.lay.acc) + (int64_t)(it.slot + row) * D + col;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 64; ++c) {
             uint32_t o[32];
             if (n > 0) {
               tmem_ld32(to + 32 * c, o);
@@ -555,15 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_use32(o);
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = n > 0 ? __float_as_uint(__uint_as_float(o[e]) * w) : 0u;
-            if (l == 0.f) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0u;
-            }
+            for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * w);
             if (n_odd > 0 && mine) {
 #pragma unroll 1
               for (int e = 0; e < 32; ++e) {
-                const float x = odd_value(a, it.request, it.head, sh.odd[slot.at], n_odd, pos, 32 * c + e);
+                const float x =
+                    odd_value(a, it.request, it.head, sh.odd[slot.at], n_odd, pos, col + 32 * c + e);
 #pragma unroll
                 for (int f = 0; f < 32; ++f)
                   if (f == e) o[f] = __float_as_uint(__uint_as_float(o[f]) + x);
@@ -587,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (mine && it.slot >= 0)
+          if (mine && half == 0 && it.slot >= 0)
             *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.ws + a.lay.ml) + 2 * (int64_t)(it.slot + row)) =
                 make_float2(m == -INFINITY ? m : m * scale, l);
         }
@@ -602,15 +682,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
 template <int D>
 cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
   using G = Geo<D>;
-  constexpr size_t smem = G::kOffBar + sizeof(Shared) + 1024;
+  constexpr size_t smem = G::kOffBar + sizeof(Shared);
   static_assert(smem <= 232448, "shared memory opt-in limit");
-  static_assert(G::kStages <= 10, "barriers");
+  static_assert(G::kStages <= 2 * kParts && G::kStages <= 8, "rings");
   // The shared-memory opt-in is set once per device (not during graph capture).
   static bool configured[128] = {false};
   int dev = 0;

@@ -1,18 +1,18 @@
 // chunk_plan.cu -- the plan of a chunk's attention, and the merge of divided tiles.
 //
 // Lengths live on the device, so the work is divided there: one CTA lists the items, longest first, and the
-// attention kernel's CTAs take them one by one.  With many tiles no list is divided; with few, lists are divided
-// so that every SM has work: some lengths of an item are tried, and the one whose estimate (the longest of: the average load, and
-// for every size the rounds that the items of at least that size need) is least is taken.
+// attention kernel's CTAs take them one by one.  With many tiles no list is divided; with few, some ways of cutting
+// the lists are tried, and the one with the least estimate is taken: the average load of a CTA, or, for the items of at
+// least some size, the rounds that these need, whichever is most.
 #include "chunk_plan.cuh"
 
 namespace srkv {
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBuckets = 192;  // sizes 0 .. 7, then eight per octave
-constexpr int kTrials = kPlanWarps;
+constexpr int kTrials = 8;
 constexpr float kItemCost = 1.5f;  // what starting and ending an item costs, in pages
 constexpr float kPartCost = 1.f;   // what a partial result adds
 
@@ -25,13 +25,32 @@ __device__ __forceinline__ int32_t size_of(int b) {  // the least size of a buck
   return b < 8 ? b : (8 + (b & 7)) << (b / 8 - 1);
 }
 
-// Length of an item under trial k, for an average load of `avg` pages a CTA; trial 0 divides nothing.
-__device__ __forceinline__ int32_t trial_pages(int k, float avg) {
-  constexpr float f[kTrials] = {0.f, 4.f,  2.f, 1.5f, 1.25f, 1.12f, 1.05f, 1.f,
-                                .9f, .75f, .6f, .52f, .5f,   .36f,  .34f,  .25f};
-  if (k == 0) return INT32_MAX;
-  const float n = ceilf(avg * f[k]);
-  return n < 1.f ? 1 : n > 1e9f ? 1000000000 : (int32_t)n;
+// How trial k divides the page lists: those of the first `whole` tiles not at all, the others, one behind the
+// other (tile by tile, head by head), at every `grid` pages.  Trial 0 divides nothing.  Where lists are fewer than
+// CTAs, the others divide all of them, into some fraction of an SM's load; else the first ones do, and the last ones
+// divide what is left after full rounds of whole tiles.
+struct Cuts {
+  int32_t whole, grid;
+};
+__device__ __forceinline__ Cuts trial_cuts(int k, int32_t tiles, int32_t round_tiles, float avg, float rest_avg) {
+  constexpr float few[kTrials] = {0.f, 1.5f, 1.2f, 1.f, .75f, .5f, .34f, .25f};
+  constexpr float many[kTrials] = {0.f, 1.f, .5f, .25f, 1.f, .67f, .5f, .34f};
+  if (k == 0) return {tiles, INT32_MAX};
+  const bool rounds = round_tiles > 0 && k >= 4;
+  const float n = ceilf((rounds ? rest_avg : avg) * (round_tiles > 0 ? many[k] : few[k]));
+  return {rounds ? round_tiles : 0, n < 2.f ? 2 : n > 1e9f ? 1000000000 : (int32_t)n};
+}
+
+// The pieces of a list of n pages that starts at page `from` of the row of lists: the first one's end, and how
+// many there are.
+struct Pieces {
+  int32_t first, count;
+};
+__device__ __forceinline__ Pieces pieces_of(long long from, int32_t n, int32_t grid) {
+  const uint32_t into = from >> 32 ? (uint32_t)(from % grid) : (uint32_t)from % (uint32_t)grid;
+  const int32_t to_cut = grid - (int32_t)into;
+  if (n <= to_cut) return {n, 1};
+  return {to_cut, 1 + (n - to_cut + grid - 1) / grid};
 }
 
 // The requests as the plan sees them: on chip while they are few, else in the workspace and the call's arrays.
@@ -42,7 +61,7 @@ struct Requests {
   const int32_t* len;
   int32_t count;
 };
-constexpr int kHeld = kPlanThreads;  // requests, and tiles, that are held on chip
+constexpr int kHeld = 512;  // requests, and tiles, that are held on chip
 
 struct Tile {
   int32_t request, row0, rows, tok0, p0, L;
@@ -70,6 +89,23 @@ __device__ __forceinline__ Tile load_tile(const ChunkArgs& a, const Requests& q,
   return t;
 }
 
+__device__ __forceinline__ ChunkItem make_item(const Tile& t, int32_t h, int32_t j0, int32_t j1, int32_t slot) {
+  ChunkItem it;
+  it.request = t.request;
+  it.head = h;
+  it.row0 = t.row0;
+  it.rows = t.rows;
+  it.j0 = j0;
+  it.j1 = j1;
+  it.na = t.g.na;
+  it.shift = t.g.shift;
+  it.slot = slot;
+  it.tok0 = t.tok0;
+  it.p0 = t.p0;
+  it.L = t.L;
+  return it;
+}
+
 template <typename I>
 __device__ __forceinline__ I warp_scan(I v, int lane) {
 #pragma unroll
@@ -83,8 +119,10 @@ __device__ __forceinline__ I warp_scan(I v, int lane) {
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a) {
   __shared__ int32_t hist[kTrials][kBuckets];
   __shared__ int32_t cursor[kBuckets];
-  __shared__ int32_t held[4][kHeld], pages[kHeld], rows[kHeld];
-  __shared__ unsigned long long part_rows[kTrials], pages_sum;
+  __shared__ int32_t held[4][kHeld];
+  __shared__ Tile tile[kHeld];
+  __shared__ long long before[kHeld];  // pages of the tiles before, for one head
+  __shared__ unsigned long long part_rows[kTrials];
   __shared__ long long warp_sum[kPlanWarps];
   __shared__ int32_t split_items[kTrials], n_merges, n_rows, max_rows, max_parts;
   __shared__ float estimate[kTrials];
@@ -96,7 +134,6 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     split_items[tid] = 0;
   }
   if (tid == 0) {
-    pages_sum = 0;
     n_merges = 0;
     n_rows = 0;
     max_rows = 0;
@@ -131,17 +168,17 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     const long long x = warp_scan(tiles, lane);
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    long long before = base, all = base;
+    long long first_tile = base, all = base;
 #pragma unroll
     for (int w = 0; w < kPlanWarps; ++w) {
       const long long y = warp_sum[w];
-      if (w < warp) before += y;
+      if (w < warp) first_tile += y;
       all += y;
     }
     if (r < a.batch) {
       // offsets that go back and forth could ask for more tiles than the workspace holds
-      if (before + x > cap) eflags |= SRKV_EFLAG_CHUNK;
-      const int32_t first = (int32_t)min(before + x - tiles, (long long)cap);
+      if (first_tile + x > cap) eflags |= SRKV_EFLAG_CHUNK;
+      const int32_t first = (int32_t)min(first_tile + x - tiles, (long long)cap);
       if (few) {
         held[0][tid] = first;
         held[1][tid] = n;
@@ -159,47 +196,58 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   const Requests q = {few ? held[0] : req, few ? held[1] : req + a.batch + 1, few ? held[2] : a.offsets,
                       few ? held[3] : a.seq_lens, a.batch};
 
-  // ---- the load
-  unsigned long long sum = 0;
-  for (int32_t t = tid; t < tiles; t += kPlanThreads) {
-    const Tile tl = load_tile(a, q, t);
-    sum += (unsigned long long)tl.g.n;
-    if (t < kHeld) {
-      pages[t] = tl.g.n;
-      rows[t] = tl.rows;
+  // ---- the load: pages of the lists, and of those before each tile
+  long long sum = 0;
+  for (int32_t t0 = 0; t0 < tiles; t0 += kPlanThreads) {
+    const int32_t t = t0 + tid;
+    int32_t n = 0;
+    if (t < tiles) {
+      const Tile tl = load_tile(a, q, t);
+      n = tl.g.n;
+      if (t < kHeld) tile[t] = tl;
     }
-  }
+    const long long x = warp_scan((long long)n, lane);
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long at = sum;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0 && sum) atomicAdd(&pages_sum, sum * (unsigned long long)a.Hkv);
-  __syncthreads();
+    for (int w = 0; w < kPlanWarps; ++w) {
+      if (w < warp) at += warp_sum[w];
+      sum += warp_sum[w];
+    }
+    if (t < kHeld) before[t] = at + x - n;
+    __syncthreads();
+  }
+  const float avg = (float)(sum * a.Hkv) / (float)a.ctas;
+  // Lists are divided only where tiles are few: many balance by themselves.
+  const int trials = tiles <= kHeld && tiles * (int64_t)a.Hkv < 16 * (int64_t)a.ctas ? kTrials : 1;
+  const int32_t round_tiles = (int32_t)((int64_t)tiles * a.Hkv / a.ctas * a.ctas / a.Hkv);
+  const float rest_avg = trials == 1 || round_tiles == tiles
+                             ? 0.f
+                             : (float)((sum - before[round_tiles]) * a.Hkv) / (float)a.ctas;
 
-  // ---- the sizes that each trial gives: a thread per (tile, trial)
-  const float avg = (float)pages_sum / (float)a.ctas;
-  const int trials = tiles * (int64_t)a.Hkv >= 8 * (int64_t)a.ctas ? 1 : kTrials;
-  {
-    const int k = trials == 1 ? 0 : tid % kTrials;
-    const int32_t step = trials == 1 ? kPlanThreads : kPlanThreads / kTrials;
-    const int32_t c = trial_pages(k, avg);
+  // ---- the sizes that each trial gives: a thread per (list, trial)
+  if (trials == 1) {
+    for (int32_t t = tid; t < tiles; t += kPlanThreads)
+      atomicAdd(&hist[0][bucket_of(t < kHeld ? tile[t].g.n : load_tile(a, q, t).g.n)], a.Hkv);
+  } else {
+    const int k = tid % kTrials;
+    const Cuts cut = trial_cuts(k, tiles, round_tiles, avg, rest_avg);
     int32_t split = 0;
     unsigned long long all_rows = 0;
-    for (int32_t t = trials == 1 ? tid : tid / kTrials; t < tiles; t += step) {
-      int32_t n, m;
-      if (t < kHeld) {
-        n = pages[t];
-        m = rows[t];
-      } else {
-        const Tile tl = load_tile(a, q, t);
-        n = tl.g.n;
-        m = tl.rows;
+    for (int32_t u = tid / kTrials; u < tiles * a.Hkv; u += kPlanThreads / kTrials) {
+      const int32_t t = u / a.Hkv, h = u - t * a.Hkv, n = tile[t].g.n;
+      if (t < cut.whole) {
+        atomicAdd(&hist[k][bucket_of(n)], 1);
+        continue;
       }
-      const int32_t s = n > c ? (int32_t)(((uint32_t)n + c - 1) / (uint32_t)c) : 1;
-      const int32_t each = s == 1 ? n : n / s, rest = n - each * s;  // `rest` items are one page longer
-      atomicAdd(&hist[k][bucket_of(each)], (s - rest) * a.Hkv);
-      if (rest) atomicAdd(&hist[k][bucket_of(each + 1)], rest * a.Hkv);
-      if (s > 1) {
-        all_rows += (unsigned long long)s * m * a.Hkv;
-        split += s * a.Hkv;
+      const Pieces p = pieces_of(before[t] * a.Hkv + (long long)h * n, n, cut.grid);
+      atomicAdd(&hist[k][bucket_of(p.first)], 1);
+      if (p.count > 1) {
+        atomicAdd(&hist[k][bucket_of(n - p.first - (p.count - 2) * cut.grid)], 1);
+        if (p.count > 2) atomicAdd(&hist[k][bucket_of(cut.grid)], p.count - 2);
+        all_rows += (unsigned long long)p.count * tile[t].rows;
+        split += p.count;
       }
     }
     if (split) {
@@ -266,58 +314,45 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   }
   __syncthreads();
 
-  // ---- the items: a warp per tile, or every thread where tiles are few
-  const int32_t c = trial_pages(chosen, avg);
+  // ---- the items: of undivided lists a thread each, of divided ones a group of threads
+  const Cuts cut = trial_cuts(chosen, tiles, round_tiles, avg, rest_avg);
   ChunkItem* items = reinterpret_cast<ChunkItem*>(a.ws + a.lay.items);
   ChunkMerge* merges = reinterpret_cast<ChunkMerge*>(a.ws + a.lay.merges);
-  const bool wide = tiles < kPlanWarps / 2;
-  __shared__ int32_t shared_slot[kPlanWarps][2];
-  for (int32_t t = wide ? 0 : warp; t < tiles; t += wide ? 1 : kPlanWarps) {
-    const Tile tl = load_tile(a, q, t);
-    const int32_t s = tl.g.n > c ? (int32_t)(((uint32_t)tl.g.n + c - 1) / (uint32_t)c) : 1;
-    const int32_t each = s == 1 ? tl.g.n : tl.g.n / s, rest = tl.g.n - each * s;
-    int32_t slot = 0, merge = 0;
-    if (s > 1) {
-      if (wide ? tid == 0 : lane == 0) {
-        shared_slot[t % kPlanWarps][0] = atomicAdd(&n_rows, s * tl.rows * a.Hkv);
-        shared_slot[t % kPlanWarps][1] = atomicAdd(&n_merges, a.Hkv);
+  const int64_t whole = (int64_t)min(cut.whole, tiles) * a.Hkv;
+  for (int64_t u = tid; u < whole; u += kPlanThreads) {
+    const int32_t t = (int32_t)(u / a.Hkv), h = (int32_t)(u - (int64_t)t * a.Hkv);
+    const Tile tl = t < kHeld ? tile[t] : load_tile(a, q, t);
+    items[atomicAdd(&cursor[bucket_of(tl.g.n)], 1)] = make_item(tl, h, 0, tl.g.n, -1);
+  }
+  if (cut.whole < tiles) {
+    const int32_t lists = (tiles - cut.whole) * a.Hkv;
+    const int size = lists > 256 ? 4 : lists > 64 ? 8 : 32, sub = lane % size;  // threads a list
+    for (int32_t u0 = 0; u0 < lists; u0 += kPlanThreads / size) {
+      const int32_t u = u0 + tid / size;
+      const bool on = u < lists;
+      const int32_t t = cut.whole + (on ? u / a.Hkv : 0), h = on ? u % a.Hkv : 0;
+      const Tile& tl = tile[t];
+      const Pieces p = pieces_of(before[t] * a.Hkv + (long long)h * tl.g.n, tl.g.n, cut.grid);
+      int32_t slot = -1;
+      if (on && p.count > 1 && sub == 0) {
+        slot = atomicAdd(&n_rows, p.count * tl.rows);
         atomicMax(&max_rows, tl.rows);
-        atomicMax(&max_parts, s);
-      }
-      if (wide)
-        __syncthreads();
-      else
-        __syncwarp();
-      slot = shared_slot[t % kPlanWarps][0];
-      merge = shared_slot[t % kPlanWarps][1];
-      __syncwarp();
-    }
-    for (int32_t i = wide ? tid : lane; i < s * a.Hkv; i += wide ? kPlanThreads : 32) {
-      const int32_t part = i / a.Hkv, h = i - part * a.Hkv;
-      ChunkItem it;
-      it.request = tl.request;
-      it.head = h;
-      it.row0 = tl.row0;
-      it.rows = tl.rows;
-      it.j0 = part * each + min(part, rest);
-      it.j1 = it.j0 + each + (part < rest ? 1 : 0);
-      it.na = tl.g.na;
-      it.shift = tl.g.shift;
-      it.slot = s > 1 ? slot + (h * s + part) * tl.rows : -1;
-      it.tok0 = tl.tok0;
-      it.p0 = tl.p0;
-      it.L = tl.L;
-      const int32_t at = atomicAdd(&cursor[bucket_of(it.j1 - it.j0)], 1);
-      items[at] = it;
-      if (part == 0 && s > 1) {
+        atomicMax(&max_parts, p.count);
         ChunkMerge m;
         m.head = h;
         m.row0 = tl.row0;
         m.rows = tl.rows;
         m.tok0 = tl.tok0;
-        m.slot = slot + h * s * tl.rows;
-        m.parts = s;
-        merges[merge + h] = m;
+        m.slot = slot;
+        m.parts = p.count;
+        merges[atomicAdd(&n_merges, 1)] = m;
+      }
+      slot = __shfl_sync(0xffffffffu, slot, lane - sub);
+      for (int32_t i = sub; on && i < p.count; i += size) {
+        const int32_t j0 = i == 0 ? 0 : p.first + (i - 1) * cut.grid;
+        const int32_t j1 = i == 0 ? p.first : min(tl.g.n, j0 + cut.grid);
+        items[atomicAdd(&cursor[bucket_of(j1 - j0)], 1)] =
+            make_item(tl, h, j0, j1, slot < 0 ? -1 : slot + i * tl.rows);
       }
     }
   }
@@ -331,13 +366,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   raise_flags(a.error_flags, eflags);
 }
 
-// out = sum of 2^(m_i - m) acc_i over the parts of a row, divided by the same sum of l_i.  A row with many parts is
-// shared by up to 8 warps, each taking every so-manyth part, so that all loads are in flight at once; parts and
+// out = sum of 2^(m_i - m) acc_i over the parts of a row, divided by the same sum of l_i.  A warp loads up to
+// kAtOnce parts at once; a row with more is shared by up to 8 warps, each taking every so-manyth part.  Parts and
 // warps are added in order, so the result is the same on every call.
+constexpr int kAtOnce = 4;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a) {
   constexpr int E = D / 32;
-  __shared__ float part_o[8][D], part_l[8];
+  __shared__ float part_o[8][D], part_l[8], part_top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // The attention kernel starts its CTAs' dependents once it has the plan, which is therefore readable already.
   const ChunkHead h = *chunk_head(a);
@@ -346,60 +383,84 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a) {
     griddep_wait();
     return;
   }
-  const int share = h.merge_parts > 12 ? 8 : h.merge_parts > 6 ? 4 : h.merge_parts > 3 ? 2 : 1;  // warps a row
+  const int share = h.merge_parts > 4 * kAtOnce   ? 8
+                    : h.merge_parts > 2 * kAtOnce ? 4
+                    : h.merge_parts > kAtOnce     ? 2
+                                                  : 1;  // warps a row
   const int group = warp / share, which = warp % share, groups = 8 / share;
-  const int64_t n = (int64_t)h.merges * h.merge_rows;
+  const int32_t n = h.merges * h.merge_rows;
   const ChunkMerge* merges = reinterpret_cast<const ChunkMerge*>(a.ws + a.lay.merges);
   const float* ml = reinterpret_cast<const float*>(a.ws + a.lay.ml);
   const float* acc = reinterpret_cast<const float*>(a.ws + a.lay.acc);
   bool waited = false;
-  for (int64_t u0 = (int64_t)blockIdx.x * groups; u0 < n; u0 += (int64_t)gridDim.x * groups) {
-    const int64_t u = u0 + group;
-    const ChunkMerge m = merges[min(u, n - 1) / h.merge_rows];
-    const int32_t row = (int32_t)(min(u, n - 1) % h.merge_rows);
-    const bool on = u < n && row < m.rows;
+  for (int32_t u0 = blockIdx.x * groups; u0 < n; u0 += gridDim.x * groups) {
+    const int32_t u = min(u0 + group, n - 1);
+    const ChunkMerge m = merges[u / h.merge_rows];
+    const int32_t row = u % h.merge_rows;
+    const bool on = u0 + group < n && row < m.rows;
     if (!waited) griddep_wait();
     waited = true;
     float top = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (on) {
-      for (int32_t p = lane; p < m.parts; p += 32) {
-        const float x = ml[2 * (int64_t)(m.slot + p * m.rows + row)];
-        top = x > top ? x : top;
-      }
+    for (int32_t p0 = which; on && p0 < m.parts; p0 += share * kAtOnce) {
+      float2 x[kAtOnce];
+      float f[kAtOnce][E];
 #pragma unroll
-      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-      if (top == -INFINITY) top = 0.f;
-#pragma unroll 4
-      for (int32_t p = which; p < m.parts; p += share) {
-        const int64_t at = m.slot + p * m.rows + row;
-        const float2 x = *reinterpret_cast<const float2*>(ml + 2 * at);
-        const float w = fast_exp2(x.x - top);
-        l = fmaf(x.y, w, l);
-        const float* v = acc + at * D + lane * E;
-        float f[E];
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(v);
-          f[0] = y.x, f[1] = y.y, f[2] = y.z, f[3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(v);
-          f[0] = y.x, f[1] = y.y;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int32_t p = p0 + i * share;
+        x[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[i][e] = 0.f;
+        if (p < m.parts) {
+          const int64_t at = m.slot + (int64_t)p * m.rows + row;
+          x[i] = *reinterpret_cast<const float2*>(ml + 2 * at);
+          const float* v = acc + at * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(v);
+            f[i][0] = y.x, f[i][1] = y.y, f[i][2] = y.z, f[i][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(v);
+            f[i][0] = y.x, f[i][1] = y.y;
+          }
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(f[e], w, o[e]);
       }
+      float now = top;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) now = fmaxf(now, x[i].x);
+      const float ref = now == -INFINITY ? 0.f : now, w0 = fast_exp2(top - ref);
+      l *= w0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= w0;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const float w = fast_exp2(x[i].x - ref);
+        l = fmaf(x[i].y, w, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f[i][e], w, o[e]);
+      }
+      top = now;
     }
     if (share > 1) {
 #pragma unroll
       for (int e = 0; e < E; ++e) part_o[warp][lane * E + e] = o[e];
-      if (lane == 0) part_l[warp] = l;
+      if (lane == 0) {
+        part_l[warp] = l;
+        part_top[warp] = top;
+      }
       __syncthreads();
       if (which == 0) {
-        for (int w = 1; w < share; ++w) {
-          l += part_l[warp + w];
+        float now = top;
+        for (int w = 1; w < share; ++w) now = fmaxf(now, part_top[warp + w]);
+        const float ref = now == -INFINITY ? 0.f : now;
+        l = 0.f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += part_o[warp + w][lane * E + e];
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int w = 0; w < share; ++w) {
+          const float x = fast_exp2(part_top[warp + w] - ref);
+          l = fmaf(part_l[warp + w], x, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(part_o[warp + w][lane * E + e], x, o[e]);
         }
       }
       __syncthreads();
@@ -461,7 +522,7 @@ cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t dtype, cudaStream_t stream) {
-  const dim3 g((unsigned)(2 * a.ctas)), b(256);
+  const dim3 g((unsigned)(4 * a.ctas)), b(256);
   if (dtype == SRKV_BF16)
     return a.d == 128 ? launch_pdl(chunk_merge_kernel<__nv_bfloat16, 128>, g, b, 0, stream, a)
                       : launch_pdl(chunk_merge_kernel<__nv_bfloat16, 64>, g, b, 0, stream, a);

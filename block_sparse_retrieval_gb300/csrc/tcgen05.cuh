@@ -46,6 +46,29 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 #undef SRKV_IN
 }
+#define SRKV_R16(f) SRKV_R8(f, 0), SRKV_R8(f, 8)
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+#define SRKV_OUT(i) "=r"(r[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : SRKV_R16(SRKV_OUT)
+      : "r"(addr));
+#undef SRKV_OUT
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+#define SRKV_IN(i) "r"(r[i])
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+          SRKV_R16(SRKV_IN),
+      "r"(addr)
+      : "memory");
+#undef SRKV_IN
+}
+__device__ __forceinline__ void tmem_use16(uint32_t* r) {
+#define SRKV_IO(i) "+r"(r[i])
+  asm volatile("" : SRKV_R16(SRKV_IO));
+#undef SRKV_IO
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Keeps uses of loaded registers behind the wait in front of it.
@@ -57,12 +80,12 @@ __device__ __forceinline__ void tmem_use32(uint32_t* r) {
 
 // ---- shared-memory operands: rows of 128 bytes with the 128-byte swizzle, groups of eight rows 1024 bytes apart.
 
-// `block`: bytes between one block of 64 columns and the next, for an operand whose columns are its M or N
-// extent; unused (0) where they are its K extent.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t block) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)((block ? block >> 4 : 1) & 0x3fff) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// A descriptor's low word: address, and bytes between one block of 64 columns and the next for an operand whose
+// columns are its M or N extent (unused, 0, where they are its K extent).  Steps along the operand add to it.
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t block) {
+  return addr >> 4 | (block ? block >> 4 : 1u) << 16;
 }
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // its high word: eight rows, version, swizzle
 
 // bf16 x bf16 -> fp32, M x N; `b_rows_are_k`: B's rows run along K (its columns along N).
 constexpr uint32_t mma_desc(int m, int n, bool b_rows_are_k) {
@@ -71,18 +94,20 @@ constexpr uint32_t mma_desc(int m, int n, bool b_rows_are_k) {
 }
 
 // One K step of 16: D (+)= A B with A in shared memory, and with A in tensor memory.  One thread issues.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kDescHigh)
       : "memory");
 }
 // The mbarrier gets one arrival once every product that this thread issued so far is done.
