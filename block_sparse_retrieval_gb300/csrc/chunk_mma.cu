@@ -8,7 +8,7 @@
 //   warps 0-7, 8-15  softmax and output of tile 0, 1: two threads a row, 64 of a page's tokens each
 //   warp 16          issues the products
 //   warp 17          takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
-//   warps 18, 19     copy the queries of the next item once the last product with the present ones is done; 19 cleans
+//   warps 18, 19     copy the queries of the next item once the last product with the present ones is done, and clean
 //                    values (below)
 //
 // The reference m that the exponentials subtract follows the maximum only when that has grown by more than 2^8:
@@ -29,11 +29,12 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_pages, int
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kPageWarp = 17, kQueryWarp = 18, kCleanWarp = 19;
+constexpr int kMmaWarp = 16, kPageWarp = 17, kHelperWarp = 18;
 constexpr int kSlots = 2;      // items known at a time
 constexpr int kPageInfo = 8;   // pages between their copy and their softmax, at most
 constexpr int kParts = 4;      // pages seen in part and not yet multiplied, at most: their stages are not refilled
-constexpr int kOdd = 8;        // pages that an item's rows see in part, at most: 3 at each end of a window of 256 rows, 1 at the first tokens
+constexpr int kOdd = 14;       // half pages that an item's rows see in part, at most: of 3 pages at each end of a window of 256
+                               // rows, and of 1 at the first tokens
 // Registers: 512 x 104 + 128 x 64 = 640 x 96, what the block is launched with.
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr float kGrow = 8.f;   // log2 of the growth of a maximum that the reference lets pass
@@ -49,8 +50,8 @@ struct Geo {
 };
 
 struct OddPage {
-  uint32_t tokens[4];  // those with an element that is not finite
-  int32_t block;
+  uint32_t tokens[2];  // of 64 tokens, those with an element that is not finite
+  int32_t token0;      // the first of the 64
 };
 
 struct Shared {
@@ -108,49 +109,53 @@ __device__ __forceinline__ void item_span(const ChunkItem& it, int32_t G, int32_
   p_hi = it.p0 + (it.row0 + it.rows - 1) / G;
 }
 
-// A page of V that some row sees in part, in shared memory: rows from `valid` on are cleared, elements that are
-// not finite replaced by zero.  Returns (in every lane) the rows that had one.
+// Half a page of V that some row sees in part, in shared memory (64 rows from `half` on): rows from `valid` on
+// are cleared, elements that are not finite replaced by zero.  Returns (in every lane) the rows that had one.
 template <int D>
-__device__ __forceinline__ uint4 clean_values(unsigned char* stage, int32_t valid, int lane) {
-  uint32_t bad[4];
+__device__ __forceinline__ uint2 clean_values(unsigned char* half, int32_t valid, int lane) {
+  uint32_t bad[2];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int row = g * 32 + lane;
-    // 16-byte chunks, the lanes at different ones (the swizzle permutes them within a row only)
-    auto at = [&](int c) {
-      const int chunk = (c + lane) % (D / 8);
-      return reinterpret_cast<uint4*>(stage + (chunk / 8) * (128 * 128) + row * 128 + (chunk % 8) * 16);
-    };
+  for (int g = 0; g < 2; ++g) {
+    // a lane's row is 128 bytes of each block of 64 columns; the lanes start at different 16-byte chunks
+    const uint32_t row = smem_u32(half) + (32 * g + lane) * 128 + (lane & 7) * 16;
     uint32_t odd = 0;
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 x = *at(c);
-      // an exponent of all ones carries into the sign bit's place
-      odd |= ((x.x & 0x7fff7fffu) + 0x00800080u) | ((x.y & 0x7fff7fffu) + 0x00800080u) |
-             ((x.z & 0x7fff7fffu) + 0x00800080u) | ((x.w & 0x7fff7fffu) + 0x00800080u);
-    }
-    if (row >= valid) {
+    for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"((row ^ (c * 16)) + b * (128 * 128)));
+        // an exponent of all ones carries into the sign bit's place
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7fff7fffu) + 0x00800080u;
+      }
+    odd &= 0x80008000u;
+    uint4* at = reinterpret_cast<uint4*>(half + (32 * g + lane) * 128);
+    if (32 * g + lane >= valid) {
       odd = 0;
 #pragma unroll 1
-      for (int c = 0; c < D / 8; ++c) *at(c) = make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) at[b * (128 * 128 / 16) + (c ^ (lane & 7))] = make_uint4(0, 0, 0, 0);
     }
-    odd &= 0x80008000u;
     if (odd) {
 #pragma unroll 1
       for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = *at(c);
+        uint4& x = at[(c / 8) * (128 * 128 / 16) + c % 8];
         uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
           if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
         }
-        *at(c) = make_uint4(w[0], w[1], w[2], w[3]);
+        x = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     bad[g] = __ballot_sync(0xffffffffu, odd != 0);
   }
-  return make_uint4(bad[0], bad[1], bad[2], bad[3]);
+  return make_uint2(bad[0], bad[1]);
 }
 
 // What clean_values took out of element `col` of the values that a row at `pos` attends.
@@ -158,13 +163,14 @@ __device__ __forceinline__ float odd_value(const ChunkArgs& a, int32_t request, 
                                            int n, int32_t pos, int col) {
   float x = 0.f;
   for (int i = 0; i < n; ++i) {
-    const int32_t page = a.block_table[(int64_t)request * a.max_blocks + odd[i].block];
+    const int32_t t0 = odd[i].token0;
+    const int32_t page = a.block_table[(int64_t)request * a.max_blocks + t0 / kBlock];
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) +
-                             ((int64_t)page * a.Hkv + head) * (int64_t)kBlock * a.d + col;
-    for (int g = 0; g < 4; ++g)
+                             (((int64_t)page * a.Hkv + head) * kBlock + t0 % kBlock) * a.d + col;
+    for (int g = 0; g < 2; ++g)
       for (uint32_t m = odd[i].tokens[g]; m; m &= m - 1) {
         const int row = g * 32 + __ffs(m) - 1;
-        if (!chunk_attends(pos, odd[i].block * kBlock + row, a.init, a.local)) continue;
+        if (!chunk_attends(pos, t0 + row, a.init, a.local)) continue;
         const float f = __bfloat162float(v[(int64_t)row * a.d]);
         if (!(fabsf(f) < INFINITY)) x += f;
       }
@@ -196,6 +202,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Every lane holds N 16-byte pieces of its own row; after it, lane l holds piece l % N of rows N (l / N) + 0 .. N - 1
+// of the warp, so that N lanes together hold a row's run of bytes.
+template <int N>
+__device__ __forceinline__ void transpose(uint32_t* v, int lane) {
+#pragma unroll
+  for (int b = 1; b < N; b <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (k & b) continue;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t &lo = v[4 * k + w], &hi = v[4 * (k | b) + w];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & b ? lo : hi, b);
+        if (lane & b)
+          lo = got;
+        else
+          hi = got;
+      }
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -225,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&sh.v_part[i], 1);
-      mbar_init(&sh.v_clean[i], 1);
+      mbar_init(&sh.v_clean[i], 2);
     }
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 2; ++i) {
@@ -431,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------------------------------------------------------- queries, and values to be cleaned
+      const int helper = warp - kHelperWarp;
       Ring<kParts> part;
       Ring<1> qr;
       while (take()) {
@@ -439,49 +467,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && mbar_wait(&sh.q_empty, qr.phase ^ 1);
           if (!ok) break;
           qr.next();
-          constexpr int C = D / 8;  // 16-byte chunks of a row
-          const int t = (warp - kQueryWarp) * 32 + lane, chunk = t % C;
-          for (int row = t / C; row < it.rows; row += 64 / C) {
-            const int32_t rho = it.row0 + row;
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                       (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
-                                       (int64_t)(it.head * a.G + rho % a.G) * D + chunk * 8;
+          constexpr int C = D / 8, kStep = 64 / C;  // 16-byte chunks of a row, rows a pass
+          const int t = helper * 32 + lane, chunk = t % C;
+          const int32_t rho = it.row0 + t / C, head0 = it.head * a.G;
+          int32_t token = rho / a.G, g = rho - token * a.G;
+          const int32_t dt = kStep / a.G, dg = kStep - dt * a.G;
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)it.tok0 * a.q_stride + chunk * 8;
+          const int32_t rows = it.rows;
+#pragma unroll 4
+          for (int row = t / C; row < rows; row += kStep) {
             const uint32_t dst = smem_u32(smem + G::kOffQ) + (row / 128) * G::kTileBytes +
-                                 (chunk / 8) * G::kBlockBytes + (row % 128) * 128 +
-                                 ((chunk ^ row) % 8) * 16;
-            cp_async_16(dst, src);
+                                 (chunk / 8) * G::kBlockBytes + (row % 128) * 128 + ((chunk ^ row) % 8) * 16;
+            cp_async_16(dst, q + (int64_t)token * a.q_stride + (head0 + g) * D);
+            token += dt;
+            g += dg;
+            if (g >= a.G) {
+              g -= a.G;
+              ++token;
+            }
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.q_full);
         }
-        if (warp == kCleanWarp) {  // the values of pages seen in part, ahead of their product
-          int32_t p_lo, p_hi;
-          item_span(it, a.G, p_lo, p_hi);
-          for (int32_t j = it.j0; j < it.j1 && ok; ++j) {
-            const int32_t b = page_of(it, j);
-            if (!chunk_masked(b, p_lo, p_hi, a.init, a.local)) continue;
-            ok = mbar_wait(&sh.v_part[part.at], part.phase);
-            if (!ok) break;
-            const int2 where = sh.part[part.at];
-            ok = mbar_wait(&sh.full[where.x], (uint32_t)where.y);
-            if (!ok) break;
-            const uint4 bad =
-                clean_values<D>(smem + G::kOffStage + (size_t)where.x * G::kTileBytes, it.L - b * kBlock, lane);
-            if (lane == 0 && (bad.x | bad.y | bad.z | bad.w) && sh.n_odd[slot.at] < kOdd) {
-              OddPage& o = sh.odd[slot.at][sh.n_odd[slot.at]++];
-              o.tokens[0] = bad.x;
-              o.tokens[1] = bad.y;
-              o.tokens[2] = bad.z;
-              o.tokens[3] = bad.w;
-              o.block = b;
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.v_clean[part.at]);
-            part.next();
+        // the values of pages seen in part, ahead of their product: half a page each
+        int32_t p_lo, p_hi;
+        item_span(it, a.G, p_lo, p_hi);
+        for (int32_t j = it.j0; j < it.j1 && ok; ++j) {
+          const int32_t b = page_of(it, j);
+          if (!chunk_masked(b, p_lo, p_hi, a.init, a.local)) continue;
+          ok = mbar_wait(&sh.v_part[part.at], part.phase);
+          if (!ok) break;
+          const int2 where = sh.part[part.at];
+          ok = mbar_wait(&sh.full[where.x], (uint32_t)where.y);
+          if (!ok) break;
+          const int row0 = 64 * helper, t0 = b * kBlock + row0;
+          const uint2 bad = clean_values<D>(
+              smem + G::kOffStage + (size_t)where.x * G::kTileBytes + row0 * 128, it.L - t0, lane);
+          if (lane == 0 && (bad.x | bad.y)) {
+            const int at = atomicAdd(&sh.n_odd[slot.at], 1);
+            if (at < kOdd) sh.odd[slot.at][at] = {{bad.x, bad.y}, t0};
           }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_clean[part.at]);
+          part.next();
         }
         done();
       }
@@ -626,9 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t rho = it.row0 + row;
           const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
           const int col = D / 2 * half;
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                               ((int64_t)(it.tok0 + rho / a.G) * a.Hq + it.head * a.G + rho % a.G) * D + col;
-          float* acc = reinterpret_cast<float*>(a.ws + a.lay.acc) + (int64_t)(it.slot + row) * D + col;
+          // rows of the output that this warp's lanes stand for, -1: none
+          const int32_t token = rho / a.G;
+          const int32_t at = !mine ? -1
+                             : it.slot >= 0 ? it.slot + row
+                                            : (it.tok0 + token) * a.Hq + it.head * a.G + (rho - token * a.G);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             uint32_t o[32];
@@ -649,21 +682,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (f == e) o[f] = __float_as_uint(__uint_as_float(o[f]) + x);
               }
             }
-            if (mine) {
-              if (it.slot >= 0) {
+            if (it.slot >= 0) {
+              transpose<8>(o, lane);
+              float* acc = reinterpret_cast<float*>(a.ws + a.lay.acc) + col + 32 * c + 4 * (lane % 8);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<uint4*>(acc + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              } else {
+              for (int k = 0; k < 8; ++k) {
+                const int32_t r = __shfl_sync(0xffffffffu, at, (lane & ~7) + k);
+                if (r >= 0)
+                  *reinterpret_cast<uint4*>(acc + (int64_t)r * D) =
+                      make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              }
+            } else {
+              uint32_t v[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 v;
-                  v.x = pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-                  v.y = pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                  v.z = pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-                  v.w = pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-                  *reinterpret_cast<uint4*>(out + 32 * c + e) = v;
-                }
+              for (int e = 0; e < 32; e += 2)
+                v[e / 2] = pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+              transpose<4>(v, lane);
+              __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + col + 32 * c + 8 * (lane % 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int32_t r = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
+                if (r >= 0)
+                  *reinterpret_cast<uint4*>(out + (int64_t)r * D) =
+                      make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
               }
             }
           }
