@@ -25,6 +25,8 @@ namespace srkv {
 
 bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_pages, int32_t Hkv, int32_t d,
                       bool e4m3);
+bool encode_rows_map(CUtensorMap* map, const void* q, int64_t tokens, int64_t stride, int32_t heads, int32_t d,
+                     int32_t box_heads, int32_t box_tokens);
 
 namespace {
 
@@ -75,6 +77,8 @@ enum { kPart = 1, kAbsent = 2 };  // how an item's rows see a page: 0 whole
 
 struct Maps {
   CUtensorMap k, v;
+  CUtensorMap q;       // valid where q_box > 0
+  int32_t q_box;       // tokens of a tile of 128 rows, where the group divides 128; else 0
 };
 
 __device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -467,29 +471,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && mbar_wait(&sh.q_empty, qr.phase ^ 1);
           if (!ok) break;
           qr.next();
-          constexpr int C = D / 8, kStep = 64 / C;  // 16-byte chunks of a row, rows a pass
-          const int t = helper * 32 + lane, chunk = t % C;
-          const int32_t rho = it.row0 + t / C, head0 = it.head * a.G;
-          int32_t token = rho / a.G, g = rho - token * a.G;
-          const int32_t dt = kStep / a.G, dg = kStep - dt * a.G;
-          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)it.tok0 * a.q_stride + chunk * 8;
-          const int32_t rows = it.rows;
-#pragma unroll 4
-          for (int row = t / C; row < rows; row += kStep) {
-            const uint32_t dst = smem_u32(smem + G::kOffQ) + (row / 128) * G::kTileBytes +
-                                 (chunk / 8) * G::kBlockBytes + (row % 128) * 128 + ((chunk ^ row) % 8) * 16;
-            cp_async_16(dst, q + (int64_t)token * a.q_stride + (head0 + g) * D);
-            token += dt;
-            g += dg;
-            if (g >= a.G) {
-              g -= a.G;
-              ++token;
+          if (maps.q_box > 0) {  // a tile's tokens and heads are a box, its rows in their order
+            if (helper == 0 && lane == 0) {
+              const int tiles = it.rows > 128 ? 2 : 1;
+              mbar_arrive_expect_tx(&sh.q_full, tiles * G::kTileBytes);
+              for (int i = 0; i < tiles; ++i)
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b)
+                  tma_page(smem + G::kOffQ + i * G::kTileBytes + b * G::kBlockBytes, &maps.q, 64 * b,
+                           it.head * a.G, it.tok0 + it.row0 / a.G + i * maps.q_box, &sh.q_full);
             }
+          } else {
+            constexpr int C = D / 8, kStep = 64 / C;  // 16-byte chunks of a row, rows a pass
+            const int t = helper * 32 + lane, chunk = t % C;
+            const int32_t rho = it.row0 + t / C, head0 = it.head * a.G;
+            int32_t token = rho / a.G, g = rho - token * a.G;
+            const int32_t dt = kStep / a.G, dg = kStep - dt * a.G;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)it.tok0 * a.q_stride + chunk * 8;
+            const int32_t rows = it.rows;
+#pragma unroll 4
+            for (int row = t / C; row < rows; row += kStep) {
+              const uint32_t dst = smem_u32(smem + G::kOffQ) + (row / 128) * G::kTileBytes +
+                                   (chunk / 8) * G::kBlockBytes + (row % 128) * 128 + ((chunk ^ row) % 8) * 16;
+              cp_async_16(dst, q + (int64_t)token * a.q_stride + (head0 + g) * D);
+              token += dt;
+              g += dg;
+              if (g >= a.G) {
+                g -= a.G;
+                ++token;
+              }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full);
+          if (lane == 0 && (maps.q_box == 0 || helper)) mbar_arrive(&sh.q_full);
         }
         // the values of pages seen in part, ahead of their product: half a page each
         int32_t p_lo, p_hi;
@@ -509,13 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int at = atomicAdd(&sh.n_odd[slot.at], 1);
             if (at < kOdd) sh.odd[slot.at][at] = {{bad.x, bad.y}, t0};
           }
-          fence_async_smem();
+          if (bad.x | bad.y || it.L - t0 < 64) fence_async_smem();  // something was written
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.v_clean[part.at]);
           part.next();
         }
         done();
       }
+      if (!ok) mbar_wait(&sh.q_full, qr.phase ^ 1);  // a wait ran out: a copy in flight lands before the CTA ends
     }
   } else {
     more_registers<kSoftmaxRegs>();
@@ -746,6 +763,10 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
   Maps maps;
   if (!encode_cache_map(&maps.k, a.k_cache, a.num_pages, a.Hkv, D, false) ||
       !encode_cache_map(&maps.v, a.v_cache, a.num_pages, a.Hkv, D, false))
+    return cudaErrorInvalidValue;
+  maps.q_box = a.G <= 128 && 128 % a.G == 0 ? 128 / a.G : 0;
+  if (maps.q_box > 0 &&
+      !encode_rows_map(&maps.q, a.q, a.tokens, a.q_stride, a.Hq, D, a.G, maps.q_box))
     return cudaErrorInvalidValue;
   return launch_pdl(chunk_mma_kernel<D>, dim3(a.ctas), dim3(kThreads), smem, stream, a, maps);
 }

@@ -1,57 +1,35 @@
-// chunk_plan.cu -- the plan of a chunk's attention, and the merge of divided tiles.
+// chunk_plan.cu -- the plan of a chunk's attention, and the merge of divided lists.
 //
 // Lengths live on the device, so the work is divided there: one CTA lists the items, longest first, and the
-// attention kernel's CTAs take them one by one.  With many tiles no list is divided; with few, some ways of cutting
-// the lists are tried, and the one with the least estimate is taken: the average load of a CTA, or, for the items of at
-// least some size, the rounds that these need, whichever is most.
+// attention kernel's CTAs take them one by one.  Lists are kept whole where they balance by themselves; else they are
+// cut: where they are fewer than CTAs all of them, else those that remain after full rounds of whole ones.
+//
+// This kernel's time is the fetch of its own instructions (a launch finds none of them on its SM: some 300 cycles
+// for every 8), not its arithmetic.  So loops are kept rolled, divisions by the head counts are multiplications, and
+// what is done twice is a function: 16.4 us with the loops unrolled, 7.9 so (one request).
 #include "chunk_plan.cuh"
 
 namespace srkv {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kBuckets = 192;  // sizes 0 .. 7, then eight per octave
-constexpr int kTrials = 8;
-constexpr float kItemCost = 1.5f;  // what starting and ending an item costs, in pages
-constexpr float kPartCost = 1.f;   // what a partial result adds
+constexpr int kBuckets = 64;   // sizes 0 .. 3, then two per octave
+constexpr int kHeld = 512;     // requests, and tiles, that are held on chip
+constexpr float kItemCost = 2.f;  // what starting and ending an item costs, in pages
+constexpr float kMergeCost = 2.f, kRowCost = 1.f / 8192;  // what the merge adds, and each row of a partial result
 
 __device__ __forceinline__ int bucket_of(int32_t n) {
-  if (n < 8) return n;
+  if (n < 4) return n;
   const int e = 31 - __clz(n);
-  return 8 * (e - 2) + ((n >> (e - 3)) & 7);
-}
-__device__ __forceinline__ int32_t size_of(int b) {  // the least size of a bucket
-  return b < 8 ? b : (8 + (b & 7)) << (b / 8 - 1);
+  return 2 * e + ((n >> (e - 1)) & 1);
 }
 
-// How trial k divides the page lists: those of the first `whole` tiles not at all, the others, one behind the
-// other (tile by tile, head by head), at every `grid` pages.  Trial 0 divides nothing.  Where lists are fewer than
-// CTAs, the others divide all of them, into some fraction of an SM's load; else the first ones do, and the last ones
-// divide what is left after full rounds of whole tiles.
+// How lists are cut: those of the first `whole` tiles not at all; the others, one behind the other (tile by tile,
+// head by head), at every `grid` pages, or, if `parts` > 0, each into that many equal parts.
 struct Cuts {
-  int32_t whole, grid;
+  int32_t whole, grid, parts;
 };
-__device__ __forceinline__ Cuts trial_cuts(int k, int32_t tiles, int32_t round_tiles, float avg, float rest_avg) {
-  constexpr float few[kTrials] = {0.f, 1.5f, 1.2f, 1.f, .75f, .5f, .34f, .25f};
-  constexpr float many[kTrials] = {0.f, 1.f, .5f, .25f, 1.f, .67f, .5f, .34f};
-  if (k == 0) return {tiles, INT32_MAX};
-  const bool rounds = round_tiles > 0 && k >= 4;
-  const float n = ceilf((rounds ? rest_avg : avg) * (round_tiles > 0 ? many[k] : few[k]));
-  return {rounds ? round_tiles : 0, n < 2.f ? 2 : n > 1e9f ? 1000000000 : (int32_t)n};
-}
-
-// The pieces of a list of n pages that starts at page `from` of the row of lists: the first one's end, and how
-// many there are.
-struct Pieces {
-  int32_t first, count;
-};
-__device__ __forceinline__ Pieces pieces_of(long long from, int32_t n, int32_t grid) {
-  const uint32_t into = from >> 32 ? (uint32_t)(from % grid) : (uint32_t)from % (uint32_t)grid;
-  const int32_t to_cut = grid - (int32_t)into;
-  if (n <= to_cut) return {n, 1};
-  return {to_cut, 1 + (n - to_cut + grid - 1) / grid};
-}
 
 // The requests as the plan sees them: on chip while they are few, else in the workspace and the call's arrays.
 struct Requests {
@@ -61,16 +39,16 @@ struct Requests {
   const int32_t* len;
   int32_t count;
 };
-constexpr int kHeld = 512;  // requests, and tiles, that are held on chip
 
 struct Tile {
   int32_t request, row0, rows, tok0, p0, L;
   ChunkPages g;
 };
 
-__device__ __forceinline__ Tile load_tile(const ChunkArgs& a, const Requests& q, int32_t tau) {
+__device__ __noinline__ Tile load_tile(const ChunkArgs& a, const Requests& q, int32_t tau) {
   Tile t;
   int32_t lo = 0, hi = q.count;  // the last request whose first tile is at or before tau
+#pragma unroll 1
   while (hi - lo > 1) {
     const int32_t mid = lo + (hi - lo) / 2;
     if (q.first[mid] <= tau)
@@ -80,35 +58,41 @@ __device__ __forceinline__ Tile load_tile(const ChunkArgs& a, const Requests& q,
   }
   t.request = lo;
   const int32_t n = q.n[lo];
-  t.row0 = (tau - q.first[lo]) * a.tile;
-  t.rows = min(a.tile, n * a.G - t.row0);
+  t.row0 = (tau - q.first[lo]) << a.tile_log2;
+  t.rows = min(1 << a.tile_log2, n * a.G - t.row0);
   t.tok0 = q.offset[lo];
   t.L = (int32_t)min((int64_t)max(q.len[lo], 0), (int64_t)a.max_blocks * kBlock);
   t.p0 = t.L - n;
-  t.g = chunk_pages(t.p0 + t.row0 / a.G, t.p0 + (t.row0 + t.rows - 1) / a.G, a.init, a.local);
+  t.g = chunk_pages(t.p0 + (int32_t)a.by_group.div(t.row0), t.p0 + (int32_t)a.by_group.div(t.row0 + t.rows - 1),
+                    a.init, a.local);
   return t;
 }
 
-__device__ __forceinline__ ChunkItem make_item(const Tile& t, int32_t h, int32_t j0, int32_t j1, int32_t slot) {
-  ChunkItem it;
-  it.request = t.request;
-  it.head = h;
-  it.row0 = t.row0;
-  it.rows = t.rows;
-  it.j0 = j0;
-  it.j1 = j1;
-  it.na = t.g.na;
-  it.shift = t.g.shift;
-  it.slot = slot;
-  it.tok0 = t.tok0;
-  it.p0 = t.p0;
-  it.L = t.L;
-  return it;
+// The pieces of list h of a tile: the first one's end, the length of the next ones, and how many there are.
+struct Pieces {
+  int32_t first, each, count;
+};
+__device__ __noinline__ Pieces pieces_of(const Cuts& cut, int32_t t, int32_t h, int32_t n, long long before,
+                                         int32_t heads) {
+  Pieces p = {n, 1, 1};
+  if (t >= cut.whole) {
+    p.each = cut.grid;
+    if (cut.parts > 0) {
+      p.each = max(1, (n + cut.parts - 1) / cut.parts);
+      p.first = min(n, p.each);
+    } else {
+      // the row of lists is cut where its position, modulo the grid, is zero (modulo 2^32 first: the cuts of very
+      // long rows are as good anywhere)
+      p.first = min(n, cut.grid - (int32_t)((uint32_t)(before * heads + (long long)h * n) % (uint32_t)cut.grid));
+    }
+    p.count = 1 + (n - p.first + p.each - 1) / p.each;
+  }
+  return p;
 }
 
 template <typename I>
 __device__ __forceinline__ I warp_scan(I v, int lane) {
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const I y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
@@ -116,28 +100,33 @@ __device__ __forceinline__ I warp_scan(I v, int lane) {
   return v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a) {
-  __shared__ int32_t hist[kTrials][kBuckets];
-  __shared__ int32_t cursor[kBuckets];
+// Inclusive sum over the CTA's threads; *all is the whole sum.  `sums`: a word for each warp.
+__device__ __noinline__ long long block_scan(long long v, long long* sums, long long* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v, lane);
+  __syncthreads();
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  const long long w = warp_scan(lane < kPlanWarps ? sums[lane] : 0ll, lane);
+  *all = __shfl_sync(0xffffffffu, w, kPlanWarps - 1);
+  if (warp > 0) v += __shfl_sync(0xffffffffu, w, warp - 1);
+  return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ int32_t hist[kBuckets];
   __shared__ int32_t held[4][kHeld];
   __shared__ Tile tile[kHeld];
   __shared__ long long before[kHeld];  // pages of the tiles before, for one head
-  __shared__ unsigned long long part_rows[kTrials];
-  __shared__ long long warp_sum[kPlanWarps];
-  __shared__ int32_t split_items[kTrials], n_merges, n_rows, max_rows, max_parts;
-  __shared__ float estimate[kTrials];
-  __shared__ int32_t chosen;
+  __shared__ long long sums[kPlanWarps];
+  __shared__ int32_t n_merges, n_rows, max_rows, max_parts, longest, shortest, most_rows;
+  __shared__ Cuts cut;
+  __shared__ bool again;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kTrials * kBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
-  if (tid < kTrials) {
-    part_rows[tid] = 0;
-    split_items[tid] = 0;
-  }
+  if (tid < kBuckets) hist[tid] = 0;
   if (tid == 0) {
-    n_merges = 0;
-    n_rows = 0;
-    max_rows = 0;
-    max_parts = 0;
+    n_merges = n_rows = max_rows = max_parts = longest = most_rows = 0;
+    shortest = INT32_MAX;
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -146,8 +135,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   const bool few = a.batch <= kHeld;
   int32_t* req = reinterpret_cast<int32_t*>(a.ws + a.lay.req);
   uint32_t eflags = 0;
-  int32_t base = 0;
   const int32_t cap = a.lay.items_cap / a.Hkv - (kChunkSplitItems + a.Hkv - 1) / a.Hkv;  // tiles that good offsets make at most
+  long long base = 0;
+#pragma unroll 1
   for (int32_t r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
     const int32_t r = r0 + tid;
     int32_t n = 0, s = 0, len = 0;
@@ -164,21 +154,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         if (n > len) eflags |= SRKV_EFLAG_CHUNK;
       }
     }
-    const long long tiles = ((int64_t)n * a.G + a.tile - 1) / a.tile;
-    const long long x = warp_scan(tiles, lane);
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long first_tile = base, all = base;
-#pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const long long y = warp_sum[w];
-      if (w < warp) first_tile += y;
-      all += y;
-    }
+    const long long mine = ((int64_t)n * a.G + (1 << a.tile_log2) - 1) >> a.tile_log2;
+    long long all;
+    const long long upto = base + block_scan(mine, sums, &all);
     if (r < a.batch) {
       // offsets that go back and forth could ask for more tiles than the workspace holds
-      if (first_tile + x > cap) eflags |= SRKV_EFLAG_CHUNK;
-      const int32_t first = (int32_t)min(first_tile + x - tiles, (long long)cap);
+      if (upto > cap) eflags |= SRKV_EFLAG_CHUNK;
+      const int32_t first = (int32_t)min(upto - mine, (long long)cap);
       if (few) {
         held[0][tid] = first;
         held[1][tid] = n;
@@ -189,171 +171,138 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         req[a.batch + 1 + r] = n;
       }
     }
-    base = (int32_t)min(all, (long long)cap);
-    __syncthreads();
+    base = min(base + all, (long long)cap);
   }
-  const int32_t tiles = base;
+  __syncthreads();
+  const int32_t tiles = (int32_t)base;
   const Requests q = {few ? held[0] : req, few ? held[1] : req + a.batch + 1, few ? held[2] : a.offsets,
                       few ? held[3] : a.seq_lens, a.batch};
 
-  // ---- the load: pages of the lists, and of those before each tile
-  long long sum = 0;
+  // ---- their page lists, and the pages before each
+  long long pages = 0;
+#pragma unroll 1
   for (int32_t t0 = 0; t0 < tiles; t0 += kPlanThreads) {
     const int32_t t = t0 + tid;
     int32_t n = 0;
     if (t < tiles) {
       const Tile tl = load_tile(a, q, t);
       n = tl.g.n;
+      atomicMax(&longest, n);
+      atomicMin(&shortest, n);
+      atomicMax(&most_rows, tl.rows);
       if (t < kHeld) tile[t] = tl;
     }
-    const long long x = warp_scan((long long)n, lane);
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long at = sum;
-#pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w) {
-      if (w < warp) at += warp_sum[w];
-      sum += warp_sum[w];
-    }
-    if (t < kHeld) before[t] = at + x - n;
-    __syncthreads();
+    long long all;
+    const long long upto = pages + block_scan(n, sums, &all);
+    if (t < kHeld) before[t] = upto - n;
+    pages += all;
   }
-  const float avg = (float)(sum * a.Hkv) / (float)a.ctas;
-  // Lists are divided only where tiles are few: many balance by themselves.
-  const int trials = tiles <= kHeld && tiles * (int64_t)a.Hkv < 16 * (int64_t)a.ctas ? kTrials : 1;
-  const int32_t round_tiles = (int32_t)((int64_t)tiles * a.Hkv / a.ctas * a.ctas / a.Hkv);
-  const float rest_avg = trials == 1 || round_tiles == tiles
-                             ? 0.f
-                             : (float)((sum - before[round_tiles]) * a.Hkv) / (float)a.ctas;
+  __syncthreads();
 
-  // ---- the sizes that each trial gives: a thread per (list, trial)
-  if (trials == 1) {
-    for (int32_t t = tid; t < tiles; t += kPlanThreads)
-      atomicAdd(&hist[0][bucket_of(t < kHeld ? tile[t].g.n : load_tile(a, q, t).g.n)], a.Hkv);
-  } else {
-    const int k = tid % kTrials;
-    const Cuts cut = trial_cuts(k, tiles, round_tiles, avg, rest_avg);
-    int32_t split = 0;
-    unsigned long long all_rows = 0;
-    for (int32_t u = tid / kTrials; u < tiles * a.Hkv; u += kPlanThreads / kTrials) {
-      const int32_t t = u / a.Hkv, h = u - t * a.Hkv, n = tile[t].g.n;
-      if (t < cut.whole) {
-        atomicAdd(&hist[k][bucket_of(n)], 1);
-        continue;
-      }
-      const Pieces p = pieces_of(before[t] * a.Hkv + (long long)h * n, n, cut.grid);
-      atomicAdd(&hist[k][bucket_of(p.first)], 1);
+  // ---- the sizes of whole lists; then, where cutting is better, those of the pieces
+  const int64_t lists = (int64_t)tiles * a.Hkv;
+  if (tid == 0) {
+    cut = {tiles, 1, 0};
+    again = false;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+#pragma unroll 1
+    for (int64_t u = tid; u < lists; u += kPlanThreads) {
+      const int32_t t = (int32_t)a.by_heads.div((uint32_t)u), h = (int32_t)u - t * a.Hkv;
+      const int32_t n = t < kHeld ? tile[t].g.n : load_tile(a, q, t).g.n;
+      const Pieces p = pieces_of(cut, t, h, n, t < kHeld ? before[t] : 0, a.Hkv);
+      atomicAdd(&hist[bucket_of(p.first)], 1);
       if (p.count > 1) {
-        atomicAdd(&hist[k][bucket_of(n - p.first - (p.count - 2) * cut.grid)], 1);
-        if (p.count > 2) atomicAdd(&hist[k][bucket_of(cut.grid)], p.count - 2);
-        all_rows += (unsigned long long)p.count * tile[t].rows;
-        split += p.count;
+        atomicAdd(&hist[bucket_of(n - p.first - (p.count - 2) * p.each)], 1);
+        if (p.count > 2) atomicAdd(&hist[bucket_of(p.each)], p.count - 2);
       }
     }
-    if (split) {
-      atomicAdd(&part_rows[k], all_rows);
-      atomicAdd(&split_items[k], split);
-    }
-  }
-  __syncthreads();
-
-  // ---- each warp estimates one trial
-  if (warp < trials) {
-    float worst = 0.f, total = 0.f;
-    int32_t seen = 0;
-#pragma unroll
-    for (int b0 = kBuckets - 32; b0 >= 0; b0 -= 32) {
-      const int b = b0 + 31 - lane;  // the larger sizes first
-      const int32_t n = hist[warp][b];
-      if (!__any_sync(0xffffffffu, n != 0)) continue;
-      const int32_t upto = seen + warp_scan(n, lane);
-      const float cost = (float)size_of(b) + kItemCost;
-      if (n > 0) worst = fmaxf(worst, (float)((upto + a.ctas - 1) / a.ctas) * cost);
-      total += (float)n * cost;
-      seen = __shfl_sync(0xffffffffu, upto, 31);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      worst = fmaxf(worst, __shfl_xor_sync(0xffffffffu, worst, o));
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    if (lane == 0) {
-      const bool fits = part_rows[warp] <= (unsigned long long)a.lay.rows_cap &&
-                        split_items[warp] <= kChunkSplitItems;
-      const float est = fmaxf(worst, total / a.ctas) + (split_items[warp] > 0 ? kPartCost : 0.f);
-      estimate[warp] = fits || warp == 0 ? est : 3e38f;
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float e = lane < trials ? estimate[lane] : INFINITY;
-    int best = lane;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float f = __shfl_xor_sync(0xffffffffu, e, o);
-      const int other = __shfl_xor_sync(0xffffffffu, best, o);
-      if (f < e || (f == e && other < best)) {
-        e = f;
-        best = other;
+    __syncthreads();
+    if (warp == 0) {
+      // the longest items come first: their places
+      int32_t at = 0;
+#pragma unroll 1
+      for (int b = kBuckets - 1 - lane; b >= 0; b -= 32) {
+        const int32_t n = hist[b], upto = at + warp_scan(n, lane);
+        hist[b] = upto - n;
+        at = __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (lane == 0) {
+        ChunkHead* head = chunk_head(a);
+        head->items = at;
+        head->next = 0;
+        again = false;
+        if (pass == 0 && tiles <= kHeld && lists < 16 * (int64_t)a.ctas) {
+          const float whole_lists = (float)lists, total = (float)pages * (float)a.Hkv;
+          const float load = total * a.per_cta;
+          // whole lists: the average load; or the longest one; or, with some CTAs idle while the last lists run, the
+          // load and those CTAs' share of a shortest list
+          const float items = whole_lists * a.per_cta, idle = ceilf(items) - items;
+          const float worst = fmaxf((float)longest, load + idle * (float)shortest) + kItemCost * ceilf(items);
+          Cuts c = {0, 1, 0};
+          float cost;
+          if (lists < a.ctas) {
+            c.grid = max(2, (int32_t)ceilf(fminf(load, 1e9f)));
+            cost = load + 2.f * kItemCost + kMergeCost;
+            if (longest == shortest) {  // equal lists: into as many equal parts as make one round
+              const int32_t parts = a.ctas / (int32_t)lists;
+              const float each = ceilf((float)longest / (float)parts) + kItemCost + kMergeCost;
+              if (parts > 1 && each <= cost) {
+                cost = each;
+                c.parts = parts;
+              }
+            }
+          } else {  // full rounds of whole lists, the rest into halves of what remains for a CTA
+            c.whole = (int32_t)a.by_heads.div((uint32_t)(lists - lists % a.ctas));
+            const long long rest = c.whole < tiles ? pages - before[c.whole] : 0;
+            c.grid = max(2, (int32_t)ceilf(fminf(.5f * (float)rest * (float)a.Hkv * a.per_cta, 1e9f)));
+            cost = load + kItemCost * (items + 2.f) + kMergeCost;
+          }
+          // a cut list has at most one piece more than the cuts in it, and there are at most two cuts a CTA
+          const int64_t pieces = lists - (int64_t)c.whole * a.Hkv + 2 * (int64_t)a.ctas;
+          cost += (float)pieces * (float)most_rows * kRowCost;
+          if (cost < worst && c.whole < tiles && pieces <= kChunkSplitItems &&
+              pieces * most_rows <= a.lay.rows_cap) {
+            cut = c;
+            again = true;
+          }
+        }
       }
     }
-    int32_t at = 0;
-#pragma unroll
-    for (int b0 = kBuckets - 32; b0 >= 0; b0 -= 32) {  // the longest items come first
-      const int b = b0 + 31 - lane;
-      const int32_t n = hist[best][b], upto = at + warp_scan(n, lane);
-      cursor[b] = upto - n;
-      at = __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) {
-      chosen = best;
-      ChunkHead* head = chunk_head(a);
-      head->items = at;
-      head->next = 0;
-    }
+    __syncthreads();
+    if (!again) break;
+    if (tid < kBuckets) hist[tid] = 0;
+    __syncthreads();
   }
-  __syncthreads();
 
-  // ---- the items: of undivided lists a thread each, of divided ones a group of threads
-  const Cuts cut = trial_cuts(chosen, tiles, round_tiles, avg, rest_avg);
+  // ---- the items: of whole lists a thread each, else a group of threads
   ChunkItem* items = reinterpret_cast<ChunkItem*>(a.ws + a.lay.items);
   ChunkMerge* merges = reinterpret_cast<ChunkMerge*>(a.ws + a.lay.merges);
-  const int64_t whole = (int64_t)min(cut.whole, tiles) * a.Hkv;
-  for (int64_t u = tid; u < whole; u += kPlanThreads) {
-    const int32_t t = (int32_t)(u / a.Hkv), h = (int32_t)(u - (int64_t)t * a.Hkv);
+  const int size = cut.whole == tiles || lists > 256 ? 1 : lists > 64 ? 4 : 32, sub = lane % size;  // threads a list
+#pragma unroll 1
+  for (int64_t u0 = 0; u0 < lists; u0 += kPlanThreads / size) {
+    const int64_t u = u0 + tid / size;
+    const bool on = u < lists;
+    const int32_t t = on ? (int32_t)a.by_heads.div((uint32_t)u) : 0, h = on ? (int32_t)u - t * a.Hkv : 0;
     const Tile tl = t < kHeld ? tile[t] : load_tile(a, q, t);
-    items[atomicAdd(&cursor[bucket_of(tl.g.n)], 1)] = make_item(tl, h, 0, tl.g.n, -1);
-  }
-  if (cut.whole < tiles) {
-    const int32_t lists = (tiles - cut.whole) * a.Hkv;
-    const int size = lists > 256 ? 4 : lists > 64 ? 8 : 32, sub = lane % size;  // threads a list
-    for (int32_t u0 = 0; u0 < lists; u0 += kPlanThreads / size) {
-      const int32_t u = u0 + tid / size;
-      const bool on = u < lists;
-      const int32_t t = cut.whole + (on ? u / a.Hkv : 0), h = on ? u % a.Hkv : 0;
-      const Tile& tl = tile[t];
-      const Pieces p = pieces_of(before[t] * a.Hkv + (long long)h * tl.g.n, tl.g.n, cut.grid);
-      int32_t slot = -1;
-      if (on && p.count > 1 && sub == 0) {
-        slot = atomicAdd(&n_rows, p.count * tl.rows);
-        atomicMax(&max_rows, tl.rows);
-        atomicMax(&max_parts, p.count);
-        ChunkMerge m;
-        m.head = h;
-        m.row0 = tl.row0;
-        m.rows = tl.rows;
-        m.tok0 = tl.tok0;
-        m.slot = slot;
-        m.parts = p.count;
-        merges[atomicAdd(&n_merges, 1)] = m;
-      }
-      slot = __shfl_sync(0xffffffffu, slot, lane - sub);
-      for (int32_t i = sub; on && i < p.count; i += size) {
-        const int32_t j0 = i == 0 ? 0 : p.first + (i - 1) * cut.grid;
-        const int32_t j1 = i == 0 ? p.first : min(tl.g.n, j0 + cut.grid);
-        items[atomicAdd(&cursor[bucket_of(j1 - j0)], 1)] =
-            make_item(tl, h, j0, j1, slot < 0 ? -1 : slot + i * tl.rows);
-      }
+    const Pieces p = pieces_of(cut, t, h, tl.g.n, t < kHeld ? before[t] : 0, a.Hkv);
+    int32_t slot = -1;
+    if (on && p.count > 1 && sub == 0) {
+      slot = atomicAdd(&n_rows, p.count * tl.rows);
+      atomicMax(&max_rows, tl.rows);
+      atomicMax(&max_parts, p.count);
+      merges[atomicAdd(&n_merges, 1)] = {h, tl.row0, tl.rows, tl.tok0, slot, p.count};
+    }
+    slot = __shfl_sync(0xffffffffu, slot, lane - sub);
+#pragma unroll 1
+    for (int32_t i = sub; on && i < p.count; i += size) {
+      const int32_t j0 = i == 0 ? 0 : p.first + (i - 1) * p.each;
+      const int32_t j1 = i == 0 ? p.first : min(tl.g.n, j0 + p.each);
+      items[atomicAdd(&hist[bucket_of(j1 - j0)], 1)] = {tl.request, h,      tl.row0, tl.rows,
+                                                        j0,         j1,     tl.g.na, tl.g.shift,
+                                                        slot < 0 ? -1 : slot + i * tl.rows, tl.tok0, tl.p0, tl.L};
     }
   }
   __syncthreads();

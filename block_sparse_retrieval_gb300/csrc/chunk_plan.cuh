@@ -37,6 +37,21 @@ struct __align__(16) ChunkMerge {
   int32_t slot, parts;
 };
 
+// Division of any 32-bit number by one known on the host, as a multiplication (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication", 1994, figure 4.1).
+struct DivideBy {
+  uint32_t m, s1, s2;
+  static DivideBy of(uint32_t d) {
+    uint32_t l = 0;
+    while (l < 32 && (1ull << l) < d) ++l;
+    return {(uint32_t)((((1ull << l) - d) << 32) / d + 1), l < 1 ? l : 1, l > 0 ? l - 1 : 0};
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    const uint32_t t = __umulhi(m, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+};
+
 struct ChunkHead {  // counters of one call, written by the plan
   int32_t items, merges;  // merges: divided tiles times heads
   int32_t next;       // the next item to hand out
@@ -73,8 +88,10 @@ struct ChunkArgs {
   int32_t Hq, Hkv, G, d;
   int32_t init, local;  // without a window: init = INT32_MAX, local = 0
   float scale_log2;     // log2(e) / sqrt(d)
-  int32_t tile;         // rows of a tile
+  int32_t tile_log2;    // rows of a tile
   int32_t ctas;         // CTAs that take items
+  float per_cta;        // 1 / ctas
+  DivideBy by_group, by_heads;  // by G and Hkv
 };
 
 __host__ __device__ __forceinline__ ChunkHead* chunk_head(const ChunkArgs& a) {

@@ -346,6 +346,21 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_pages, int
   return true;
 }
 
+// [tokens][heads][d] of bf16 whose tokens lie `stride` elements apart: boxes of 64 columns, box_heads heads and
+// box_tokens tokens, 128-byte swizzle.
+bool encode_rows_map(CUtensorMap* map, const void* q, int64_t tokens, int64_t stride, int32_t heads,
+                     int32_t d, int32_t box_heads, int32_t box_tokens) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int Fmt>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t stream) {
   // The shared-memory opt-in is set once per device (not during graph capture).

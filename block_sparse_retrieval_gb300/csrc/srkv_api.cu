@@ -331,9 +331,13 @@ srkv_status chunk_attention(const srkv_config* cfg, const void* q, int64_t q_str
   a.init = windowed ? cfg->init_tokens : INT32_MAX;
   a.local = windowed ? cfg->local_tokens : 0;
   a.scale_log2 = kLog2e / sqrtf((float)cfg->head_dim);
-  a.tile = chunk_tile(*cfg);
+  a.tile_log2 = 0;
+  while ((1 << a.tile_log2) < chunk_tile(*cfg)) ++a.tile_log2;
+  a.by_group = DivideBy::of((uint32_t)a.G);
+  a.by_heads = DivideBy::of((uint32_t)a.Hkv);
   const bool mma = cfg->dtype == SRKV_BF16;
   a.ctas = mma ? sms : 2 * sms;
+  a.per_cta = 1.f / (float)a.ctas;
   if (launch_chunk_plan(a, stream) != cudaSuccess) return SRKV_ERR_CUDA;
   if ((mma ? launch_chunk_mma(a, stream) : launch_chunk_simt(a, stream)) != cudaSuccess)
     return SRKV_ERR_CUDA;
