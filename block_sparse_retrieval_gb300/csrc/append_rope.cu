@@ -10,8 +10,8 @@
 // and cosine on +-pi/4 in fp32 (terms up to x^9 and x^10: the next ones are below 2^-28 and 2^-31).  A 64-bit
 // floating product would do the same at 1/64 of the fp32 rate: some 30 us for 8192 tokens of 8 heads.
 //
-// Work.  One CTA per (page touched, kv head): its 8 warps hold the page's 128 rows in registers, 16 each, the
-// rows already there as read and the new ones as rotated, so that the vector needs no second read.  Other CTAs
+// Work.  One CTA per (page touched, kv head): its 8 warps go through the page's 128 rows, 16 each, the rows
+// already there as read and the new ones as rotated, and sum them on the way, so that the vector needs no second read.  Other CTAs
 // rotate the queries, a warp per token (or eight warps per token where tokens are few), with the token's
 // angles computed once for all its heads.
 #include "rep_sums.cuh"
@@ -49,9 +49,11 @@ __device__ __forceinline__ int32_t page_base(int32_t offset, int32_t r) {
   return offset / kBlock + 2 * r;
 }
 
-// The last request whose first item is at or before x: 32 requests a round.
+// The last request whose first item is at or before x: 32 requests a round.  With one token a request, token x is
+// request x's: looked at first, as each round waits for the one before.
 __device__ __forceinline__ int32_t find_request(const RopeArgs& a, int32_t x, bool pages, int lane) {
   int32_t lo = 0, n = a.batch;
+  if (!pages && x < n && a.offsets[x] == x && a.offsets[x + 1] == x + 1) return x;
   while (n > 1) {
     const int32_t step = (n + 31) / 32, i = lane * step;
     bool at = false;
@@ -195,8 +197,10 @@ struct Rotor {
   }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRepThreads) append_rope_kernel(const RopeArgs a) {
+// kDeep: all the old rows of a page are in flight at once (few tokens a request, where every wait shows);
+// else two rows, in registers for four CTAs an SM (8192 tokens: 45.7 us with all rows, 38.5 with four, 35.4).
+template <typename T, int D, bool kDeep>
+__global__ void __launch_bounds__(kRepThreads, 4) append_rope_kernel(const RopeArgs a) {
   using R = RepGeom<T, D>;
   __shared__ float part[kRepWarps * D];
   __shared__ uint64_t table[D / 2];
@@ -279,34 +283,77 @@ __global__ void __launch_bounds__(kRepThreads) append_rope_kernel(const RopeArgs
   Rotor<T, D> rot;
   rot.init(table, a.rope_dim, a.interleaved != 0, lane);
   const int row0 = warp * R::RPW + sub;
-  int4 raw[R::IPW];
+  float acc[R::EPV];
 #pragma unroll
-  for (int i = 0; i < R::IPW; ++i) {
-    const int row = row0 + i * R::RPI;
-    raw[i] = make_int4(0, 0, 0, 0);
-    if (row < lo)
-      raw[i] = reinterpret_cast<const int4*>(kc + row * D)[chunk];
-    else if (row < hi)
-      raw[i] = reinterpret_cast<const int4*>(kn + (int64_t)(rq.begin + row - first) * a.k_stride)[chunk];
-  }
-#pragma unroll
-  for (int i = 0; i < R::IPW; ++i) {
-    const int row = row0 + i * R::RPI;
-    const bool here = row >= lo && row < hi;
-    if (!__any_sync(0xffffffffu, here)) continue;
-    int4 v = make_int4(0, 0, 0, 0);
-    if (here)
-      v = reinterpret_cast<const int4*>(vn + (int64_t)(rq.begin + row - first) * a.v_stride)[chunk];
+  for (int e = 0; e < R::EPV; ++e) acc[e] = 0.f;
+  // Row `row` rotated and written, with its value; what the cache holds of it.
+  auto write = [&](int row, bool here, const int4& k, const int4& v) {
     rot.angles(block * kBlock + row);
-    const int4 y = rot.turn(raw[i]);
+    const int4 y = rot.turn(k);
     if (here) {
-      raw[i] = y;
       reinterpret_cast<int4*>(kc + row * D)[chunk] = y;
       reinterpret_cast<int4*>(vc + row * D)[chunk] = v;
     }
+    return y;
+  };
+  auto load_new = [&](int row, int4& k, int4& v) {
+    const int64_t token = rq.begin + row - first;
+    k = reinterpret_cast<const int4*>(kn + token * a.k_stride)[chunk];
+    v = reinterpret_cast<const int4*>(vn + token * a.v_stride)[chunk];
+  };
+  if constexpr (kDeep) {
+    // through shared memory, each lane its own pieces
+    extern __shared__ int4 slab[];
+    int4* own = slab + row0 * R::LPR + chunk;
+#pragma unroll
+    for (int i = 0; i < R::IPW; ++i) {
+      const int row = row0 + i * R::RPI;
+      if (row < lo)
+        cp_async_16(smem_u32(own + i * R::RPI * R::LPR), reinterpret_cast<const int4*>(kc + row * D) + chunk);
+      else if (row >= hi)
+        own[i * R::RPI * R::LPR] = make_int4(0, 0, 0, 0);
+    }
+    const int warp0 = warp * R::RPW;
+#pragma unroll 1
+    for (int i = max(lo - warp0, 0) / R::RPI; i < R::IPW && warp0 + i * R::RPI < hi; ++i) {
+      const int row = row0 + i * R::RPI;
+      const bool here = row >= lo && row < hi;
+      int4 k = make_int4(0, 0, 0, 0), v = k;
+      if (here) load_new(row, k, v);
+      const int4 y = write(row, here, k, v);
+      if (here) own[i * R::RPI * R::LPR] = y;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < R::IPW; ++i) add_row<T, D>(own[i * R::RPI * R::LPR], acc);
+  } else {
+    constexpr int kBatch = 2;
+#pragma unroll 1
+    for (int i0 = 0; i0 < R::IPW; i0 += kBatch) {
+      if (row0 - sub + i0 * R::RPI >= hi) break;  // (for the whole warp)
+      int4 raw[kBatch], v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int row = row0 + (i0 + i) * R::RPI;
+        raw[i] = v[i] = make_int4(0, 0, 0, 0);
+        if (row < lo)
+          raw[i] = reinterpret_cast<const int4*>(kc + row * D)[chunk];
+        else if (row < hi)
+          load_new(row, raw[i], v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int row = row0 + (i0 + i) * R::RPI;
+        const bool here = row >= lo && row < hi;
+        if (__any_sync(0xffffffffu, here)) {
+          const int4 y = write(row, here, raw[i], v[i]);
+          if (here) raw[i] = y;
+        }
+        add_row<T, D>(raw[i], acc);
+      }
+    }
   }
-  float acc[R::EPV];
-  warp_sum_rows<T, D>(raw, acc);
+  across_rows<T, D>(acc);
   store_column_sums<T, D>(part, warp, lane, acc);
   __syncthreads();
   finish_columns<T, D>(part, warp, lane, hi, a.reps + ((int64_t)page * a.Hkv + h) * D);
@@ -354,12 +401,32 @@ cudaError_t launch_append_rope(const srkv_config& cfg, const void* q, int64_t q_
   const int64_t grid = (int64_t)a.kv_items * a.Hkv + (q_units + kRepWarps - 1) / kRepWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 g((unsigned)grid), b(kRepThreads);
-  if (cfg.dtype == SRKV_BF16)
-    return cfg.head_dim == 128
-               ? launch_pdl(append_rope_kernel<__nv_bfloat16, 128>, g, b, 0, stream, a)
-               : launch_pdl(append_rope_kernel<__nv_bfloat16, 64>, g, b, 0, stream, a);
-  return cfg.head_dim == 128 ? launch_pdl(append_rope_kernel<float, 128>, g, b, 0, stream, a)
-                             : launch_pdl(append_rope_kernel<float, 64>, g, b, 0, stream, a);
+  const bool deep = a.by_token;
+  const size_t slab = deep ? (size_t)kBlock * cfg.head_dim * (cfg.dtype == SRKV_BF16 ? 2 : 4) : 0;
+  auto launch = [&](auto kernel) { return launch_pdl(kernel, g, b, slab, stream, a); };
+  if (cfg.dtype == SRKV_BF16) {
+    if (cfg.head_dim == 128)
+      return deep ? launch(append_rope_kernel<__nv_bfloat16, 128, true>)
+                  : launch(append_rope_kernel<__nv_bfloat16, 128, false>);
+    return deep ? launch(append_rope_kernel<__nv_bfloat16, 64, true>)
+                : launch(append_rope_kernel<__nv_bfloat16, 64, false>);
+  }
+  if (cfg.head_dim == 128) {
+    // 64 KB of shared memory: the opt-in is set once per device (not during graph capture)
+    static bool configured[128] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    if (deep && !configured[dev]) {
+      e = cudaFuncSetAttribute(append_rope_kernel<float, 128, true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)slab);
+      if (e != cudaSuccess) return e;
+      configured[dev] = true;
+    }
+    return deep ? launch(append_rope_kernel<float, 128, true>) : launch(append_rope_kernel<float, 128, false>);
+  }
+  return deep ? launch(append_rope_kernel<float, 64, true>) : launch(append_rope_kernel<float, 64, false>);
 }
 
 }  // namespace srkv

@@ -58,21 +58,19 @@ struct RepGeom {
   static_assert(kSmemAlloc <= 232448, "shared memory opt-in limit");
 };
 
-// Sums raw[i], row i of the lane's rows, over the warp: lanes [0, LPR) get the sums of columns
+// Adds a lane's 16 bytes of a row to its sums, one row after the other ...
+template <typename T, int D>
+__device__ __forceinline__ void add_row(const int4& raw, float (&acc)[RepGeom<T, D>::EPV]) {
+  float f[RepGeom<T, D>::EPV];
+  Vec16<T>::widen(raw, f);
+#pragma unroll
+  for (int e = 0; e < RepGeom<T, D>::EPV; ++e) acc[e] += f[e];
+}
+// ... and the lanes' sums of the same columns: lanes [0, LPR) get the sums of columns
 // [lane * EPV, lane * EPV + EPV) (the other lanes hold copies).
 template <typename T, int D>
-__device__ __forceinline__ void warp_sum_rows(const int4 (&raw)[RepGeom<T, D>::IPW],
-                                              float (&acc)[RepGeom<T, D>::EPV]) {
+__device__ __forceinline__ void across_rows(float (&acc)[RepGeom<T, D>::EPV]) {
   using R = RepGeom<T, D>;
-#pragma unroll
-  for (int e = 0; e < R::EPV; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < R::IPW; ++i) {
-    float f[R::EPV];
-    Vec16<T>::widen(raw[i], f);
-#pragma unroll
-    for (int e = 0; e < R::EPV; ++e) acc[e] += f[e];
-  }
 #pragma unroll
   for (int o = R::LPR; o < 32; o <<= 1)
 #pragma unroll
@@ -93,7 +91,11 @@ __device__ __forceinline__ void warp_column_sums(Load&& load, int warp, int lane
     const int row = warp * R::RPW + sub + i * R::RPI;
     raw[i] = row < v ? load(row, chunk) : make_int4(0, 0, 0, 0);
   }
-  warp_sum_rows<T, D>(raw, acc);
+#pragma unroll
+  for (int e = 0; e < R::EPV; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < R::IPW; ++i) add_row<T, D>(raw[i], acc);
+  across_rows<T, D>(acc);
 }
 
 // part[w][c] = warp w's column sums; lanes [0, CPW) of warp `warp` finish columns

@@ -856,19 +856,26 @@ def retrieval_decode_int4(cfg: Mapping, q: torch.Tensor, kv_int4: torch.Tensor,
 
 # Chunks of new tokens: as lean as the 4-bit calls, as one token of one request is a chunk too.
 
-def _packed(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, shape: tuple) -> int:
-    """Checks packed rows [tokens][heads][d] whose tokens may lie any stride apart, a token's heads side by
-    side; returns that stride in elements."""
-    if t.shape != shape:
-        _need(t, name, shape)
+def _held_as(dev: int, *pairs) -> bool:
+    """_held for (tensor, dtype) pairs; a tensor of None is skipped."""
+    for t, dtype in pairs:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _stride(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
+    """Elements between the tokens of packed rows [tokens][heads][d], whatever they are; a token's heads lie
+    side by side."""
     if t.dtype is not dtype or t.get_device() != dev:
         if t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
+    n, heads, d = t.shape
+    if s2 != 1 or (s1 != d and heads > 1):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    return s0 if shape[0] > 1 else shape[1] * shape[2]
+    return s0 if n > 1 else heads * d
 
 
 def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -889,12 +896,12 @@ def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_
     Hq, Hkv, d, S = key[:4]
     dt = torch.float32 if key[8] else torch.bfloat16
     B, max_blocks = _table(block_table)
-    shape = k_new.shape
-    T = shape[0] if len(shape) == 3 else 0
-    rows = (T, Hkv, d)
-    if shape != rows or v_new.shape != rows:
+    rows = k_new.shape
+    if len(rows) != 3 or rows[1] != Hkv or rows[2] != d or v_new.shape != rows:
+        rows = (rows[0] if len(rows) == 3 else 0, Hkv, d)
         _need(k_new, "k_new", rows)
         _need(v_new, "v_new", rows)
+    T = rows[0]
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None and (q.shape != (T, Hq, d) or q_out.shape != (T, Hq, d)):
@@ -910,11 +917,10 @@ def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_
     pages = _cache_pages(k_cache, v_cache, (Hkv, S, d))
     _vectors(reps, Hkv, d, pages)
     dev = k_cache.get_device()
-    if not (0 <= dev == _current_device() and _held(dev, dt, k_cache, v_cache)
-            and _held(dev, torch.int32, block_table, chunk_offsets, seq_lens)
-            and _held(dev, torch.float32, reps) and (q_out is None or _held(dev, dt, q_out))
-            and (rope_freqs is None or _held(dev, torch.float64, rope_freqs))
-            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+    i32 = torch.int32
+    if not (0 <= dev == _current_device()
+            and _held_as(dev, (k_cache, dt), (v_cache, dt), (q_out, dt), (block_table, i32), (chunk_offsets, i32),
+                         (seq_lens, i32), (reps, torch.float32), (rope_freqs, torch.float64), (error_flags, i32))):
         _refuse(dev, "k_cache", k_cache=(k_cache, dt), v_cache=(v_cache, dt), block_table=(block_table, torch.int32),
                 chunk_offsets=(chunk_offsets, torch.int32), seq_lens=(seq_lens, torch.int32),
                 reps=(reps, torch.float32), q_out=(q_out, dt), rope_freqs=(rope_freqs, torch.float64),
@@ -922,14 +928,16 @@ def append_kv_rope(cfg: Mapping, q: torch.Tensor | None, k_new: torch.Tensor, v_
     qp = qo = None
     qs = 0
     if q is not None:
-        qs, qp, qo = _packed(q, "q", dt, dev, (T, Hq, d)), q.data_ptr(), q_out.data_ptr()
-    ks, vs = _packed(k_new, "k_new", dt, dev, rows), _packed(v_new, "v_new", dt, dev, rows)
+        qs, qp, qo = _stride(q, "q", dt, dev), q.data_ptr(), q_out.data_ptr()
+    ks, vs = _stride(k_new, "k_new", dt, dev), _stride(v_new, "v_new", dt, dev)
     freqs, rope_dim = (None, 0) if rope_freqs is None else (rope_freqs.data_ptr(), 2 * rope_freqs.shape[0])
-    _check((_lib or load()).srkv_append_kv_rope(
+    status = (_lib or load()).srkv_append_kv_rope(
         _cfg_ref(key), qp, qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs, chunk_offsets.data_ptr(), T, freqs,
         rope_dim, 1 if interleaved else 0, qo, k_cache.data_ptr(), v_cache.data_ptr(), pages,
         block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B, reps.data_ptr(),
-        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev)), "srkv_append_kv_rope")
+        None if error_flags is None else error_flags.data_ptr(), _stream_of(stream, dev))
+    if status:
+        _check(status, "srkv_append_kv_rope")
 
 
 def chunk_workspace_size(cfg: Mapping, total_tokens: int, batch: int) -> int:
@@ -956,15 +964,15 @@ def _chunk_attention(name: str, cfg: Mapping, q, k_cache, v_cache, block_table, 
             _need(error_flags, "error_flags", (1,))
     pages = _cache_pages(k_cache, v_cache, (Hkv, S, d))
     dev = k_cache.get_device()
-    if not (0 <= dev == _current_device() and _held(dev, dt, k_cache, v_cache, out)
-            and _held(dev, torch.int32, block_table, chunk_offsets, seq_lens)
-            and _held(dev, workspace.dtype, workspace)
-            and (error_flags is None or _held(dev, torch.int32, error_flags))):
+    i32 = torch.int32
+    if not (0 <= dev == _current_device()
+            and _held_as(dev, (k_cache, dt), (v_cache, dt), (out, dt), (block_table, i32), (chunk_offsets, i32),
+                         (seq_lens, i32), (workspace, workspace.dtype), (error_flags, i32))):
         _refuse(dev, "k_cache", k_cache=(k_cache, dt), v_cache=(v_cache, dt), out=(out, dt),
                 block_table=(block_table, torch.int32), chunk_offsets=(chunk_offsets, torch.int32),
                 seq_lens=(seq_lens, torch.int32), workspace=(workspace, workspace.dtype),
                 error_flags=(error_flags, torch.int32))
-    qs = _packed(q, "q", dt, dev, rows)
+    qs = _stride(q, "q", dt, dev)
     _check(getattr(_lib or load(), name)(
         _cfg_ref(key), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), pages, block_table.data_ptr(),
         max_blocks, chunk_offsets.data_ptr(), T, seq_lens.data_ptr(), B, out.data_ptr(), workspace.data_ptr(),
