@@ -6,10 +6,10 @@
 // The products of one tile run while the other tile's warpgroup is at its exponentials.
 //
 //   warps 0-7, 8-15  softmax and output of tile 0, 1: two threads a row, 64 of a page's tokens each
-//   warp 16          issues the products
-//   warp 17          takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
-//   warps 18, 19     copy the queries of the next item once the last product with the present ones is done, and clean
-//                    values (below)
+//   warps 16, 17     issue the products of tile 0, 1: while one waits or is held up by the full queue, the other fills it
+//   warp 18          takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
+//   warp 19          copies the queries of the next item once the last product with the present ones is done, and
+//                    cleans values (below)
 //
 // The reference m that the exponentials subtract follows the maximum only when that has grown by more than 2^8:
 // O is then scaled by hand.  Sums and outputs stay exact for any reference; fp32 holds the larger weights.
@@ -31,7 +31,7 @@ bool encode_rows_map(CUtensorMap* map, const void* q, int64_t tokens, int64_t st
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kPageWarp = 17, kHelperWarp = 18;
+constexpr int kMmaWarp = 16, kPageWarp = 18;  // and the helper, the last one
 constexpr int kSlots = 2;      // items known at a time
 constexpr int kPageInfo = 8;   // pages between their copy and their softmax, at most
 constexpr int kParts = 4;      // pages seen in part and not yet multiplied, at most: their stages are not refilled
@@ -64,7 +64,8 @@ struct Shared {
   uint64_t pair[2][4];  // the two warps of a tile's 32 rows
   uint64_t v_part[kParts], v_clean[kParts];
   int2 part[kParts];  // stage of a page seen in part, and the parity of its copy
-  uint64_t drain;
+  uint64_t turn[2];  // whose block of products comes next
+  uint64_t drain[2];
   ChunkItem item[kSlots];
   int2 page[kPageInfo];   // block, and how it is seen
   float note[2][2][128];  // [tile][half][row]: a maximum, or a sum
@@ -101,6 +102,19 @@ struct Ring {
       at = 0;
       phase ^= 1;
     }
+  }
+  __device__ __forceinline__ Ring plus(int n) const {  // n < N
+    Ring r = {at + n, phase};
+    if (r.at >= N) {
+      r.at -= N;
+      r.phase ^= 1;
+    }
+    return r;
+  }
+  __device__ __forceinline__ void skip(int32_t n) {
+    const int32_t to = at + n;
+    phase ^= (uint32_t)(to / N) & 1;
+    at = to % N;
   }
 };
 
@@ -246,19 +260,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);  // the products of both tiles
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.item_full[i], 1);
       mbar_init(&sh.item_empty[i], 19);  // every warp but the one that takes items
     }
-    mbar_init(&sh.q_full, 2);
-    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 2);
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&sh.v_part[i], 1);
-      mbar_init(&sh.v_clean[i], 2);
+      mbar_init(&sh.v_clean[i], 1);
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.turn[0], 1);
+    mbar_init(&sh.turn[1], 1);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       for (int c = 0; c < 2; ++c) mbar_init(&sh.p_full[i][c], 8);
@@ -266,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.o_full[i], 2);  // the products, and the notes of clean_values
     }
     fence_mbar_init();
+    mbar_arrive(&sh.turn[0]);
   }
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
   tcgen05_fence_before();
@@ -367,17 +385,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         --st.at;
         ok = mbar_wait(&sh.full[st.at], st.phase) && ok;
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kPageWarp) {
       // ---------------------------------------------------------------- products
       constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
       const uint32_t q_desc = smem_desc(smem_u32(smem + G::kOffQ), 0);
       const uint32_t k_desc = smem_desc(smem_u32(smem + G::kOffStage), 0);
       const uint32_t v_desc = smem_desc(smem_u32(smem + G::kOffStage), G::kBlockBytes);
       Ring<G::kStages> st;
-      Ring<1> qr, pr[2];
+      const int i = warp - kMmaWarp;  // the tile
+      Ring<1> qr, pr, tr;
       Ring<kParts> part;
       uint32_t info = 0;
-      auto qk = [&](int i, int s) {  // S_i = Q_i K^T
+      auto qk = [&](int s) {  // S_i = Q_i K^T
         const uint32_t q = q_desc + i * (G::kTileBytes >> 4), k = k_desc + s * (G::kTileBytes >> 4);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
@@ -387,82 +406,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&sh.s_full[i]);
       };
       // O_i (+)= P_i V over a part of the tokens; each half of P lies at the start of its half of S.
-      auto pv = [&](int i, int s, int part, bool first) {
+      auto pv = [&](int s, int c, bool first) {
         const uint32_t v = v_desc + s * (G::kTileBytes >> 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 2 * part; e < 2 * part + 2; ++e)
-            mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 64 * h + 8 * e, v + (4 * h + e) * (2048 >> 4), kPV,
-                   !first || part + h + e > 0);
+          for (int e = 0; e < 2; ++e)
+            mma_ts(tmem + G::kO + D * i, tmem + G::kS + 128 * i + 64 * h + 8 * (2 * c + e),
+                   v + (4 * h + 2 * c + e) * (2048 >> 4), kPV, !first || c + h + e > 0);
       };
       while (take()) {
         const ChunkItem& it = sh.item[slot.at];
-        const int tiles = it.rows > 128 ? 2 : 1;
         const int32_t n = it.j1 - it.j0;
+        const bool alone = it.rows <= 128;  // tile 1 is not in use: tile 0's warp lets go of the stages for both
         if (n > 0) {
-          ok = ok && mbar_wait(&sh.q_full, qr.phase) && mbar_wait(&sh.full[st.at], st.phase);
+          ok = ok && mbar_wait(&sh.q_full, qr.phase);
           if (!ok) break;
           qr.next();
+        }
+        if (alone && i == 1) {
+          if (n > 0 && lane == 0) mbar_arrive(&sh.q_empty);
+          int32_t p_lo, p_hi;
+          item_span(it, a.G, p_lo, p_hi);
+          for (int32_t j0 = it.j0; j0 < it.j1; j0 += 32)
+            part.skip(__popc(__ballot_sync(
+                0xffffffffu, j0 + lane < it.j1 &&
+                                 chunk_masked(page_of(it, j0 + lane), p_lo, p_hi, a.init, a.local))));
+          st.skip(2 * n);
+          info += n;
+          done();
+          continue;
+        }
+        auto release = [&](uint64_t* bar) {
+          mma_commit(bar);
+          if (alone) mma_commit(bar);
+        };
+        // The tiles' blocks of products alternate: in step, one's run while the other is at its exponentials.
+        auto my_turn = [&] {
+          if (!alone) {
+            ok = ok && mbar_wait(&sh.turn[i], tr.phase);
+            tr.next();
+          }
+          return ok;
+        };
+        auto hand_over = [&] {  // one lane
+          if (!alone) mbar_arrive(&sh.turn[i ^ 1]);
+        };
+        if (n > 0) {
+          ok = mbar_wait(&sh.full[st.at], st.phase);
+          if (!ok || !my_turn()) break;
           tcgen05_fence_after();
           if (lane == 0) {
-            for (int i = 0; i < tiles; ++i) qk(i, st.at);
-            mma_commit(&sh.empty[st.at]);
+            qk(st.at);
+            hand_over();
+            release(&sh.empty[st.at]);
             if (n == 1) mma_commit(&sh.q_empty);
           }
           __syncwarp();
-          st.next();
         }
-        for (int32_t j = 0; j < n && ok; ++j) {
-          const Ring<G::kStages> v = st;
-          st.next();
-          const Ring<G::kStages> k = st;
-          if (j + 1 < n) st.next();
-          ok = mbar_wait(&sh.full[v.at], v.phase);
+        for (int32_t j = 0; j < n && ok; ++j, st = st.plus(2)) {
+          const Ring<G::kStages> v = st.plus(1), k = st.plus(2);
+          const bool more = j + 1 < n;
+          ok = mbar_wait(&sh.full[v.at], v.phase) && (!more || mbar_wait(&sh.full[k.at], k.phase));
           if (!ok) break;
           if (sh.page[info++ % kPageInfo].y & kPart) {
             ok = mbar_wait(&sh.v_clean[part.at], part.phase);
             if (!ok) break;
             part.next();
           }
-          for (int i = 0; i < tiles; ++i) {
-            for (int part = 0; part < 2 && ok; ++part) {
-              ok = mbar_wait(&sh.p_full[i][part], pr[i].phase);
-              if (!ok) break;
-              tcgen05_fence_after();
-              if (lane == 0) pv(i, v.at, part, j == 0);
-              __syncwarp();
-            }
-            if (!ok) break;
-            pr[i].next();
-            if (i == 0 && j + 1 < n) ok = mbar_wait(&sh.full[k.at], k.phase);
-            if (!ok) break;
-            if (lane == 0) {
-              if (i == tiles - 1) mma_commit(&sh.empty[v.at]);
-              if (j + 1 < n) {
-                qk(i, k.at);
-                if (i == tiles - 1) {
-                  mma_commit(&sh.empty[k.at]);
-                  if (j + 2 == n) mma_commit(&sh.q_empty);
-                }
-              } else {
-                mma_commit(&sh.o_full[i]);
-                mbar_arrive(&sh.o_full[i]);
-              }
-            }
+          for (int c = 0; c < 2 && ok; ++c) {
+            ok = mbar_wait(&sh.p_full[i][c], pr.phase);
+            if (!ok || (c == 0 && !my_turn())) break;
+            tcgen05_fence_after();
+            if (lane == 0) pv(v.at, c, j == 0);
             __syncwarp();
           }
+          if (!ok) break;
+          pr.next();
+          if (lane == 0) {
+            if (more) {
+              qk(k.at);
+              hand_over();
+              release(&sh.empty[v.at]);
+              release(&sh.empty[k.at]);
+              if (j + 2 == n) mma_commit(&sh.q_empty);
+            } else {
+              mma_commit(&sh.o_full[i]);
+              hand_over();
+              mbar_arrive(&sh.o_full[i]);
+              release(&sh.empty[v.at]);
+            }
+          }
+          __syncwarp();
         }
+        if (!ok) break;
         done();
       }
       if (!ok) {  // a wait ran out: products in flight still end before the tensor memory is freed
-        if (lane == 0) mma_commit(&sh.drain);
+        if (lane == 0) mma_commit(&sh.drain[i]);
         __syncwarp();
-        mbar_wait(&sh.drain, 0);
+        mbar_wait(&sh.drain[i], 0);
       }
     } else {
       // ---------------------------------------------------------------- queries, and values to be cleaned
-      const int helper = warp - kHelperWarp;
       Ring<kParts> part;
       Ring<1> qr;
       while (take()) {
@@ -472,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           qr.next();
           if (maps.q_box > 0) {  // a tile's tokens and heads are a box, its rows in their order
-            if (helper == 0 && lane == 0) {
+            if (lane == 0) {
               const int tiles = it.rows > 128 ? 2 : 1;
               mbar_arrive_expect_tx(&sh.q_full, tiles * G::kTileBytes);
               for (int i = 0; i < tiles; ++i)
@@ -482,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            it.head * a.G, it.tok0 + it.row0 / a.G + i * maps.q_box, &sh.q_full);
             }
           } else {
-            constexpr int C = D / 8, kStep = 64 / C;  // 16-byte chunks of a row, rows a pass
-            const int t = helper * 32 + lane, chunk = t % C;
+            constexpr int C = D / 8, kStep = 32 / C;  // 16-byte chunks of a row, rows a pass
+            const int t = lane, chunk = t % C;
             const int32_t rho = it.row0 + t / C, head0 = it.head * a.G;
             int32_t token = rho / a.G, g = rho - token * a.G;
             const int32_t dt = kStep / a.G, dg = kStep - dt * a.G;
@@ -505,9 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async_smem();
           }
           __syncwarp();
-          if (lane == 0 && (maps.q_box == 0 || helper)) mbar_arrive(&sh.q_full);
+          if (lane == 0 && maps.q_box == 0) mbar_arrive(&sh.q_full);
         }
-        // the values of pages seen in part, ahead of their product: half a page each
+        // the values of pages seen in part, ahead of their product
         int32_t p_lo, p_hi;
         item_span(it, a.G, p_lo, p_hi);
         for (int32_t j = it.j0; j < it.j1 && ok; ++j) {
@@ -518,14 +564,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int2 where = sh.part[part.at];
           ok = mbar_wait(&sh.full[where.x], (uint32_t)where.y);
           if (!ok) break;
-          const int row0 = 64 * helper, t0 = b * kBlock + row0;
-          const uint2 bad = clean_values<D>(
-              smem + G::kOffStage + (size_t)where.x * G::kTileBytes + row0 * 128, it.L - t0, lane);
-          if (lane == 0 && (bad.x | bad.y)) {
-            const int at = atomicAdd(&sh.n_odd[slot.at], 1);
-            if (at < kOdd) sh.odd[slot.at][at] = {{bad.x, bad.y}, t0};
+          bool wrote = false;
+#pragma unroll 1
+          for (int row0 = 0; row0 < kBlock; row0 += 64) {
+            const int t0 = b * kBlock + row0;
+            const uint2 bad = clean_values<D>(
+                smem + G::kOffStage + (size_t)where.x * G::kTileBytes + row0 * 128, it.L - t0, lane);
+            wrote |= (bad.x | bad.y) || it.L - t0 < 64;
+            if (lane == 0 && (bad.x | bad.y) && sh.n_odd[slot.at] < kOdd)
+              sh.odd[slot.at][sh.n_odd[slot.at]++] = {{bad.x, bad.y}, t0};
           }
-          if (bad.x | bad.y || it.L - t0 < 64) fence_async_smem();  // something was written
+          if (wrote) fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.v_clean[part.at]);
           part.next();
