@@ -16,8 +16,9 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBuckets = 64;   // sizes 0 .. 3, then two per octave
 constexpr int kHeld = 512;     // requests, and tiles, that are held on chip
-constexpr float kItemCost = 2.f;  // what starting and ending an item costs, in pages
-constexpr float kMergeCost = 2.f, kRowCost = 1.f / 8192;  // what the merge adds, and each row of a partial result
+// What starting and ending an item costs, what the merge adds, and each row of a partial result, in pages on tensor
+// cores (1.6 us); a page on CUDA cores takes ten times that.
+constexpr float kItemCost = 2.f, kMergeCost = 2.f, kRowCost = 1.f / 8192;
 
 __device__ __forceinline__ int bucket_of(int32_t n) {
   if (n < 4) return n;
@@ -240,31 +241,30 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
           // whole lists: the average load; or the longest one; or, with some CTAs idle while the last lists run, the
           // load and those CTAs' share of a shortest list
           const float items = whole_lists * a.per_cta, idle = ceilf(items) - items;
-          const float worst = fmaxf((float)longest, load + idle * (float)shortest) + kItemCost * ceilf(items);
+          const float item = kItemCost * a.page_rate, merge = kMergeCost * a.page_rate;
+          const float worst = fmaxf((float)longest, load + idle * (float)shortest) + item * ceilf(items);
           Cuts c = {0, 1, 0};
-          float cost;
-          if (lists < a.ctas) {
-            c.grid = max(2, (int32_t)ceilf(fminf(load, 1e9f)));
-            cost = load + 2.f * kItemCost + kMergeCost;
-            if (longest == shortest) {  // equal lists: into as many equal parts as make one round
-              const int32_t parts = a.ctas / (int32_t)lists;
-              const float each = ceilf((float)longest / (float)parts) + kItemCost + kMergeCost;
-              if (parts > 1 && each <= cost) {
-                cost = each;
-                c.parts = parts;
-              }
+          const bool rounds = lists >= a.ctas;  // full rounds of whole lists, and the rest cut; else all cut
+          if (rounds) c.whole = (int32_t)a.by_heads.div((uint32_t)(lists - lists % a.ctas));
+          const float rest =
+              rounds ? (float)(c.whole < tiles ? pages - before[c.whole] : 0) * (float)a.Hkv * a.per_cta : load;
+          // Pieces for each CTA, as many as the workspace has partial results for: there is at most one more for
+          // each list than there are cuts.
+          const int64_t cut_lists = lists - (int64_t)c.whole * a.Hkv;
+          const int64_t fit = min((int64_t)kChunkSplitItems, (int64_t)(a.lay.rows_cap / max(most_rows, 1))) - cut_lists;
+          const int k = min(rounds ? 2 : 1, (int32_t)(max(fit, (int64_t)0) / a.ctas));
+          c.grid = max(a.page_rate < 1.f ? 1 : 2, (int32_t)ceilf(fminf(rest / (float)max(k, 1), 1e9f)));
+          float cost = load + item * (rounds ? items + 2.f : 2.f) + merge;
+          if (!rounds && longest == shortest && k == 1) {  // equal lists: into as many equal parts as make one round
+            const int32_t parts = a.ctas / max((int32_t)lists, 1);
+            const float each = ceilf((float)longest / (float)parts) + item + merge;
+            if (parts > 1 && each <= cost) {
+              cost = each;
+              c.parts = parts;
             }
-          } else {  // full rounds of whole lists, the rest into halves of what remains for a CTA
-            c.whole = (int32_t)a.by_heads.div((uint32_t)(lists - lists % a.ctas));
-            const long long rest = c.whole < tiles ? pages - before[c.whole] : 0;
-            c.grid = max(2, (int32_t)ceilf(fminf(.5f * (float)rest * (float)a.Hkv * a.per_cta, 1e9f)));
-            cost = load + kItemCost * (items + 2.f) + kMergeCost;
           }
-          // a cut list has at most one piece more than the cuts in it, and there are at most two cuts a CTA
-          const int64_t pieces = lists - (int64_t)c.whole * a.Hkv + 2 * (int64_t)a.ctas;
-          cost += (float)pieces * (float)most_rows * kRowCost;
-          if (cost < worst && c.whole < tiles && pieces <= kChunkSplitItems &&
-              pieces * most_rows <= a.lay.rows_cap) {
+          cost += (float)(cut_lists + (int64_t)k * a.ctas) * (float)most_rows * kRowCost * a.page_rate;
+          if (cost < worst && c.whole < tiles && k > 0) {
             cut = c;
             again = true;
           }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a) {
 }  // namespace
 
 int32_t chunk_tile(const srkv_config& cfg) {
-  return cfg.dtype == SRKV_BF16 ? kChunkTile : kChunkTileSimt;
+  return cfg.dtype == SRKV_BF16 ? kChunkTile : cfg.head_dim == 64 ? kChunkTileSimt64 : kChunkTileSimt128;
 }
 
 size_t chunk_workspace(const srkv_config& cfg, int32_t tokens, int32_t batch, ChunkLayout* out) {

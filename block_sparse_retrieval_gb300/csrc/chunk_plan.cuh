@@ -13,7 +13,7 @@
 namespace srkv {
 
 constexpr int kChunkTile = 256;      // rows of a tile on tensor cores: two accumulators of 128
-constexpr int kChunkTileSimt = 64;   // rows of a tile on CUDA cores
+constexpr int kChunkTileSimt64 = 64, kChunkTileSimt128 = 128;  // rows of a tile on CUDA cores, by head size
 constexpr int32_t kChunkSplitItems = 4096;    // items that divided lists may add
 constexpr int32_t kChunkPartRows = 163840;    // rows of partial results: 640 tiles of 256
 constexpr int32_t kChunkPartsPerRow = 512;    // and no more than this many for every row
@@ -91,6 +91,7 @@ struct ChunkArgs {
   int32_t tile_log2;    // rows of a tile
   int32_t ctas;         // CTAs that take items
   float per_cta;        // 1 / ctas
+  float page_rate;      // how fast a page is, of the tensor cores' rate
   DivideBy by_group, by_heads;  // by G and Hkv
 };
 

@@ -1,58 +1,66 @@
 // chunk_simt.cu -- attention of a chunk over the paged cache on CUDA cores, in full precision: the fp32 path.
 //
-// A CTA takes a tile of 64 rows and walks its pages 64 tokens at a time: S = Q K^T by 4 x 4 blocks of a thread,
-// a running maximum and sum per row in fp32, O += P V by 4 rows x d / 16 columns of a thread.  Bound by the
-// fp32 rate of the CUDA cores (4 d operations per row and token); shared memory is read 16 bytes at a time with rows
-// padded by one such word, so that neither product waits for it.
+// A CTA takes a tile of 64 rows (128 at d 128) and walks its pages 64 tokens at a time: S = Q K^T by 8 rows x 4
+// tokens of a thread, a running maximum and sum per row in fp32, O += P V by 8 rows x d / 16 columns of a thread,
+// both in packed pairs.  Bound by the fp32 rate (4 d operations per row and token) and by the reads of shared memory, of
+// which a warp's products take 16 lines of 128 bytes for 128 operations a lane: 7 ragged requests of up to 300
+// tokens at d 64 take 172 us, 39 % of the fp32 rate (195 with 4 rows x 4 tokens a thread, 24 lines; 214 with tiles of 128
+// rows, which short chunks fill less).  Rows are padded by 16 bytes so that a warp's 16 tokens lie in different
+// banks.  Warps without a row (single tokens) only copy.
 #include "chunk_plan.cuh"
 
 namespace srkv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = kChunkTileSimt;
 constexpr int kTok = 64;  // tokens a step
 
 template <int D>
 struct SimtGeom {
+  static constexpr int kRows = D == 64 ? kChunkTileSimt64 : kChunkTileSimt128;
+  static constexpr int kThreads = 2 * kRows;
   static constexpr int LD = D + 4;  // padded row of Q, K and V
   static constexpr int LP = kTok + 4;
   static constexpr size_t kQ = 0, kK = kQ + sizeof(float) * kRows * LD, kV = kK + sizeof(float) * kTok * LD,
                           kP = kV + sizeof(float) * kTok * LD, kSmem = kP + sizeof(float) * kRows * LP;
 };
 
+constexpr int kPer = 8;  // rows of a thread
+
 // acc += P V; with kSkip a weight of zero leaves its token out altogether (it may be hidden, and hold a NaN).
 template <int D, bool kSkip>
 __device__ __forceinline__ void add_values(const float* sp, const float* sv, int ty, int tx,
-                                           float (&acc)[4][D / 16]) {
+                                           float2 (&acc)[kPer][D / 32]) {
   using S = SimtGeom<D>;
+#pragma unroll 2
   for (int t = 0; t < kTok; t += 4) {
-    float4 p[4];
+    float4 v[4][D / 64];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * S::LP + t);
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+      for (int c = 0; c < D / 64; ++c)
+        v[u][c] = *reinterpret_cast<const float4*>(sv + (t + u) * S::LD + c * 64 + tx * 4);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(sv + (t + u) * S::LD + c * 64 + tx * 4);
-        const float vv[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < kPer; ++i) {
+      const float4 p = *reinterpret_cast<const float4*>(sp + (ty * kPer + i) * S::LP + t);
+      const float w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+      for (int u = 0; u < 4; ++u) {
+        if (kSkip && w[u] == 0.f) continue;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!kSkip || w != 0.f) acc[i][c * 4 + e] = fmaf(w, vv[e], acc[i][c * 4 + e]);
+        for (int c = 0; c < D / 64; ++c) {
+          const float2 ww = make_float2(w[u], w[u]);
+          acc[i][c * 2] = __ffma2_rn(ww, make_float2(v[u][c].x, v[u][c].y), acc[i][c * 2]);
+          acc[i][c * 2 + 1] = __ffma2_rn(ww, make_float2(v[u][c].z, v[u][c].w), acc[i][c * 2 + 1]);
         }
       }
     }
   }
 }
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_simt_kernel(const ChunkArgs a) {
   using S = SimtGeom<D>;
+  constexpr int kThreads = S::kThreads, kRows = S::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int32_t next;
   float* sq = reinterpret_cast<float*>(smem + S::kQ);
@@ -80,19 +88,20 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
         const int32_t rho = it.row0 + row;
         const float* q = static_cast<const float*>(a.q) + (int64_t)(it.tok0 + rho / a.G) * a.q_stride +
                          (int64_t)(it.head * a.G + rho % a.G) * D;
-        x = load4(q + c * 4);
+        x = reinterpret_cast<const float4*>(q)[c];
       }
       *reinterpret_cast<float4*>(sq + row * S::LD + c * 4) = x;
     }
-    int32_t pos[4];
-    float m[4], l[4], acc[4][D / 16];
+    const bool work = (ty & ~1) * kPer < it.rows;  // the warp has a row
+    const int32_t rho0 = it.row0 + ty * kPer;
+    float m[kPer], l[kPer];
+    float2 acc[kPer][D / 32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pos[i] = it.p0 + (it.row0 + ty * 4 + i) / a.G;
+    for (int i = 0; i < kPer; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 16; ++e) acc[i][e] = 0.f;
+      for (int e = 0; e < D / 32; ++e) acc[i][e] = make_float2(0.f, 0.f);
     }
     for (int32_t j = it.j0; j < it.j1; ++j) {
       const int32_t b = j < it.na ? j : j + it.shift;
@@ -112,44 +121,44 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
           float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
           if (tok + row < it.L) {
             const int64_t at = slab + (int64_t)(t0 + row) * D + c * 4;
-            k = load4(static_cast<const float*>(a.k_cache) + at);
-            v = load4(static_cast<const float*>(a.v_cache) + at);
+            k = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + at);
+            v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v_cache) + at);
           }
           *reinterpret_cast<float4*>(sk + row * S::LD + c * 4) = k;
           *reinterpret_cast<float4*>(sv + row * S::LD + c * 4) = v;
         }
         __syncthreads();
-        float s[4][4];  // rows ty * 4 + i, tokens tx + 16 j
+        if (!work) continue;
+        float2 s2[kPer][4];  // rows ty * 8 + i, tokens tx + 16 j: even and odd pairs of columns
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kPer; ++i)
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) s[i][jj] = 0.f;
+          for (int jj = 0; jj < 4; ++jj) s2[i][jj] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
-          float4 q[4], k[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * S::LD + c);
+          float4 k[4];
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj)
             k[jj] = *reinterpret_cast<const float4*>(sk + (tx + 16 * jj) * S::LD + c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < kPer; ++i) {
+            const float4 q = *reinterpret_cast<const float4*>(sq + (ty * kPer + i) * S::LD + c);
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-              s[i][jj] = fmaf(q[i].x, k[jj].x, s[i][jj]);
-              s[i][jj] = fmaf(q[i].y, k[jj].y, s[i][jj]);
-              s[i][jj] = fmaf(q[i].z, k[jj].z, s[i][jj]);
-              s[i][jj] = fmaf(q[i].w, k[jj].w, s[i][jj]);
+              s2[i][jj] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k[jj].x, k[jj].y), s2[i][jj]);
+              s2[i][jj] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k[jj].z, k[jj].w), s2[i][jj]);
             }
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float top = m[i];
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t pos = it.p0 + (int32_t)a.by_group.div(rho0 + i);
+          float top = m[i], s[4];
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj) {
-            s[i][jj] *= a.scale_log2;
-            if (masked && !chunk_attends(pos[i], tok + tx + 16 * jj, a.init, a.local)) s[i][jj] = -INFINITY;
-            top = fmaxf(top, s[i][jj]);
+            s[jj] = (s2[i][jj].x + s2[i][jj].y) * a.scale_log2;
+            if (masked && !chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local)) s[jj] = -INFINITY;
+            top = fmaxf(top, s[jj]);
           }
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -158,16 +167,14 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
           float sum = 0.f;
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj) {
-            const float p = exp2f(s[i][jj] - ref);
+            const float p = exp2f(s[jj] - ref);
             sum += p;
-            sp[(ty * 4 + i) * S::LP + tx + 16 * jj] = p;
+            sp[(ty * kPer + i) * S::LP + tx + 16 * jj] = p;
           }
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           m[i] = top;
-          l[i] = fmaf(l[i], w, sum);
+          l[i] = fmaf(l[i], w, sum);  // of this thread's tokens: added up over the 16 threads at the end
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) acc[i][e] *= w;
+          for (int e = 0; e < D / 32; ++e) acc[i][e] = make_float2(acc[i][e].x * w, acc[i][e].y * w);
         }
         __syncwarp();  // a row's weights come from the 16 lanes that read them
         if (masked)
@@ -176,9 +183,12 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
           add_values<D, false>(sp, sv, ty, tx, acc);
       }
     }
+    if (!work) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = ty * 4 + i;
+    for (int i = 0; i < kPer; ++i) {
+      const int row = ty * kPer + i;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
       if (row >= it.rows) continue;
       if (it.slot >= 0) {
         const int64_t at = it.slot + row;
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           *reinterpret_cast<float4*>(acc_out + c * 64 + tx * 4) =
-              make_float4(acc[i][c * 4], acc[i][c * 4 + 1], acc[i][c * 4 + 2], acc[i][c * 4 + 3]);
+              make_float4(acc[i][c * 2].x, acc[i][c * 2].y, acc[i][c * 2 + 1].x, acc[i][c * 2 + 1].y);
         if (tx == 0)
           *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.ws + a.lay.ml) + 2 * at) =
               make_float2(m[i], l[i]);
@@ -197,8 +207,9 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(const ChunkArgs
         const float w = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          store4(out + c * 64 + tx * 4, make_float4(acc[i][c * 4] * w, acc[i][c * 4 + 1] * w,
-                                                    acc[i][c * 4 + 2] * w, acc[i][c * 4 + 3] * w));
+          *reinterpret_cast<float4*>(out + c * 64 + tx * 4) =
+              make_float4(acc[i][c * 2].x * w, acc[i][c * 2].y * w, acc[i][c * 2 + 1].x * w,
+                          acc[i][c * 2 + 1].y * w);
       }
     }
   }
@@ -219,7 +230,7 @@ cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  return launch_pdl(chunk_simt_kernel<D>, dim3(a.ctas), dim3(kThreads), SimtGeom<D>::kSmem, stream, a);
+  return launch_pdl(chunk_simt_kernel<D>, dim3(a.ctas), dim3(SimtGeom<D>::kThreads), SimtGeom<D>::kSmem, stream, a);
 }
 
 }  // namespace

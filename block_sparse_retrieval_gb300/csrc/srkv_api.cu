@@ -336,8 +336,9 @@ srkv_status chunk_attention(const srkv_config* cfg, const void* q, int64_t q_str
   a.by_group = DivideBy::of((uint32_t)a.G);
   a.by_heads = DivideBy::of((uint32_t)a.Hkv);
   const bool mma = cfg->dtype == SRKV_BF16;
-  a.ctas = mma ? sms : 2 * sms;
+  a.ctas = mma || cfg->head_dim == 128 ? sms : 2 * sms;  // as many as are resident
   a.per_cta = 1.f / (float)a.ctas;
+  a.page_rate = mma ? 1.f : .1f;
   if (launch_chunk_plan(a, stream) != cudaSuccess) return SRKV_ERR_CUDA;
   if ((mma ? launch_chunk_mma(a, stream) : launch_chunk_simt(a, stream)) != cudaSuccess)
     return SRKV_ERR_CUDA;
