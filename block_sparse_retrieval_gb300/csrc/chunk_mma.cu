@@ -35,8 +35,8 @@ constexpr int kMmaWarp = 16, kPageWarp = 18;  // and the helper, the last one
 constexpr int kSlots = 2;      // items known at a time
 constexpr int kPageInfo = 8;   // pages between their copy and their softmax, at most
 constexpr int kParts = 4;      // pages seen in part and not yet multiplied, at most: their stages are not refilled
-constexpr int kOdd = 14;       // half pages that an item's rows see in part, at most: of 3 pages at each end of a window of 256
-                               // rows, and of 1 at the first tokens
+constexpr int kOdd = 7;        // pages that an item's rows see in part, at most: 3 at each end of a window of 256 rows, 1 at
+                               // the first tokens
 // Registers: 512 x 104 + 128 x 64 = 640 x 96, what the block is launched with.
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kTellAhead = 2;  // products of 16 columns before the end of a block at which the other tile's warp is told:
@@ -54,8 +54,8 @@ struct Geo {
 };
 
 struct OddPage {
-  uint32_t tokens[2];  // of 64 tokens, those with an element that is not finite
-  int32_t token0;      // the first of the 64
+  uint32_t tokens[4];  // those with an element that is not finite
+  int32_t block;
 };
 
 struct Shared {
@@ -124,58 +124,59 @@ __device__ __forceinline__ int32_t page_of(const ChunkItem& it, int32_t j) {
   return j < it.na ? j : j + it.shift;
 }
 
-__device__ __forceinline__ void item_span(const ChunkItem& it, int32_t G, int32_t& p_lo, int32_t& p_hi) {
-  p_lo = it.p0 + it.row0 / G;
-  p_hi = it.p0 + (it.row0 + it.rows - 1) / G;
+__device__ __forceinline__ void item_span(const ChunkItem& it, const DivideBy& by_group, int32_t& p_lo,
+                                          int32_t& p_hi) {
+  p_lo = it.p0 + (int32_t)by_group.div(it.row0);
+  p_hi = it.p0 + (int32_t)by_group.div(it.row0 + it.rows - 1);
 }
 
-// Half a page of V that some row sees in part, in shared memory (64 rows from `half` on): rows from `valid` on
-// are cleared, elements that are not finite replaced by zero.  Returns (in every lane) the rows that had one.
+// 32 rows of V in shared memory, of a page that some row sees in part; `behind`: the lane's row is behind the
+// sequence and is cleared; `scan`: it is hidden from some row and not from all, and its elements that are not finite
+// are replaced by zero.  Returns (in every lane) the rows that had one.
 template <int D>
-__device__ __forceinline__ uint2 clean_values(unsigned char* half, int32_t valid, int lane) {
-  uint32_t bad[2];
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    // a lane's row is 128 bytes of each block of 64 columns; the lanes start at different 16-byte chunks
-    const uint32_t row = smem_u32(half) + (32 * g + lane) * 128 + (lane & 7) * 16;
-    uint32_t odd = 0;
-#pragma unroll
+__device__ __forceinline__ uint32_t clean_values(unsigned char* rows, bool behind, bool scan, int lane) {
+  // a lane's row is 128 bytes of each block of 64 columns; the lanes start at different 16-byte chunks
+  const uint32_t row = smem_u32(rows) + lane * 128 + (lane & 7) * 16;
+  if (behind) {
+#pragma unroll 1
     for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"((row ^ (c * 16)) + b * (128 * 128)));
-        // an exponent of all ones carries into the sign bit's place
-#pragma unroll
-        for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7fff7fffu) + 0x00800080u;
-      }
-    odd &= 0x80008000u;
-    uint4* at = reinterpret_cast<uint4*>(half + (32 * g + lane) * 128);
-    if (32 * g + lane >= valid) {
-      odd = 0;
-#pragma unroll 1
-      for (int b = 0; b < D / 64; ++b)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) at[b * (128 * 128 / 16) + (c ^ (lane & 7))] = make_uint4(0, 0, 0, 0);
-    }
-    if (odd) {
-#pragma unroll 1
-      for (int c = 0; c < D / 8; ++c) {
-        uint4& x = at[(c / 8) * (128 * 128 / 16) + c % 8];
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-          if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
-        }
-        x = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    bad[g] = __ballot_sync(0xffffffffu, odd != 0);
+      for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"((row ^ (c * 16)) + b * (128 * 128)), "r"(0)
+                     : "memory");
   }
-  return make_uint2(bad[0], bad[1]);
+  if (!__any_sync(0xffffffffu, scan)) return 0;
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int b = 0; b < D / 64; ++b) {
+    uint32_t w[8][4];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
+                   : "r"((row ^ (c * 16)) + b * (128 * 128)));
+    // an exponent of all ones carries into the sign bit's place
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) odd |= (w[c][i] & 0x7fff7fffu) + 0x00800080u;
+  }
+  odd = scan ? odd & 0x80008000u : 0u;
+  if (odd) {
+    uint4* at = reinterpret_cast<uint4*>(rows + lane * 128);
+#pragma unroll 1
+    for (int c = 0; c < D / 8; ++c) {
+      uint4& x = at[(c / 8) * (128 * 128 / 16) + c % 8];
+      uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+        if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0xffffu;
+      }
+      x = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  return __ballot_sync(0xffffffffu, odd != 0);
 }
 
 // What clean_values took out of element `col` of the values that a row at `pos` attends.
@@ -183,14 +184,13 @@ __device__ __forceinline__ float odd_value(const ChunkArgs& a, int32_t request, 
                                            int n, int32_t pos, int col) {
   float x = 0.f;
   for (int i = 0; i < n; ++i) {
-    const int32_t t0 = odd[i].token0;
-    const int32_t page = a.block_table[(int64_t)request * a.max_blocks + t0 / kBlock];
+    const int32_t page = a.block_table[(int64_t)request * a.max_blocks + odd[i].block];
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) +
-                             (((int64_t)page * a.Hkv + head) * kBlock + t0 % kBlock) * a.d + col;
-    for (int g = 0; g < 2; ++g)
+                             ((int64_t)page * a.Hkv + head) * (int64_t)kBlock * a.d + col;
+    for (int g = 0; g < 4; ++g)
       for (uint32_t m = odd[i].tokens[g]; m; m &= m - 1) {
         const int row = g * 32 + __ffs(m) - 1;
-        if (!chunk_attends(pos, t0 + row, a.init, a.local)) continue;
+        if (!chunk_attends(pos, odd[i].block * kBlock + row, a.init, a.local)) continue;
         const float f = __bfloat162float(v[(int64_t)row * a.d]);
         if (!(fabsf(f) < INFINITY)) x += f;
       }
@@ -211,6 +211,7 @@ __device__ __forceinline__ uint32_t attended_bits(int32_t pos, int32_t t0, int32
 
 // Logits of hidden tokens to minus infinity.
 __device__ __forceinline__ void hide(uint32_t* s, uint32_t on) {
+  if (__all_sync(0xffffffffu, on == 0xffffffffu)) return;
 #pragma unroll
   for (int e = 0; e < 32; ++e)
     if (!(on >> e & 1u)) s[e] = 0xff800000u;
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot.next();
         if (next >= n_items) break;
         int32_t p_lo, p_hi;
-        item_span(it, a.G, p_lo, p_hi);
+        item_span(it, a.by_group, p_lo, p_hi);
         for (int32_t j0 = it.j0; j0 < it.j1 && ok; j0 += 32) {
           int32_t page = 0, b = 0, seen = 0;
           if (j0 + lane < it.j1) {
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (alone && i == 1) {
           if (n > 0 && lane == 0) mbar_arrive(&sh.q_empty);
           int32_t p_lo, p_hi;
-          item_span(it, a.G, p_lo, p_hi);
+          item_span(it, a.by_group, p_lo, p_hi);
           for (int32_t j0 = it.j0; j0 < it.j1; j0 += 32)
             part.skip(__popc(__ballot_sync(
                 0xffffffffu, j0 + lane < it.j1 &&
@@ -525,14 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b)
                   tma_page(smem + G::kOffQ + i * G::kTileBytes + b * G::kBlockBytes, &maps.q, 64 * b,
-                           it.head * a.G, it.tok0 + it.row0 / a.G + i * maps.q_box, &sh.q_full);
+                           it.head * a.G, it.tok0 + (int32_t)a.by_group.div(it.row0) + i * maps.q_box, &sh.q_full);
             }
           } else {
             constexpr int C = D / 8, kStep = 32 / C;  // 16-byte chunks of a row, rows a pass
             const int t = lane, chunk = t % C;
             const int32_t rho = it.row0 + t / C, head0 = it.head * a.G;
-            int32_t token = rho / a.G, g = rho - token * a.G;
-            const int32_t dt = kStep / a.G, dg = kStep - dt * a.G;
+            int32_t token = (int32_t)a.by_group.div(rho), g = rho - token * a.G;
+            const int32_t dt = (int32_t)a.by_group.div(kStep), dg = kStep - dt * a.G;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)it.tok0 * a.q_stride + chunk * 8;
             const int32_t rows = it.rows;
 #pragma unroll 4
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the values of pages seen in part, ahead of their product
         int32_t p_lo, p_hi;
-        item_span(it, a.G, p_lo, p_hi);
+        item_span(it, a.by_group, p_lo, p_hi);
         for (int32_t j = it.j0; j < it.j1 && ok; ++j) {
           const int32_t b = page_of(it, j);
           if (!chunk_masked(b, p_lo, p_hi, a.init, a.local)) continue;
@@ -565,14 +566,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(&sh.full[where.x], (uint32_t)where.y);
           if (!ok) break;
           bool wrote = false;
+          const int n_odd = sh.n_odd[slot.at];
+          uint32_t any = 0;
 #pragma unroll 1
-          for (int row0 = 0; row0 < kBlock; row0 += 64) {
-            const int t0 = b * kBlock + row0;
-            const uint2 bad = clean_values<D>(
-                smem + G::kOffStage + (size_t)where.x * G::kTileBytes + row0 * 128, it.L - t0, lane);
-            wrote |= (bad.x | bad.y) || it.L - t0 < 64;
-            if (lane == 0 && (bad.x | bad.y) && sh.n_odd[slot.at] < kOdd)
-              sh.odd[slot.at][sh.n_odd[slot.at]++] = {{bad.x, bad.y}, t0};
+          for (int g = 0; g < 4; ++g) {
+            const int32_t t = b * kBlock + 32 * g + lane;
+            const bool behind = t >= it.L;
+            // a token that the first row and the last one see is seen by all between; by neither, by none
+            const bool scan = !behind && !(chunk_attends(p_lo, t, a.init, a.local) &&
+                                           chunk_attends(p_hi, t, a.init, a.local));
+            const uint32_t bad = clean_values<D>(
+                smem + G::kOffStage + (size_t)where.x * G::kTileBytes + g * (32 * 128), behind, scan, lane);
+            wrote |= bad || __any_sync(0xffffffffu, behind);
+            any |= bad;
+            if (lane == 0 && n_odd < kOdd) sh.odd[slot.at][n_odd].tokens[g] = bad;
+          }
+          if (lane == 0 && any && n_odd < kOdd) {
+            sh.odd[slot.at][n_odd].block = b;
+            sh.n_odd[slot.at] = n_odd + 1;
           }
           if (wrote) fence_async_smem();
           __syncwarp();
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool here = 128 * tile < it.rows;              // the tile is in use
       const bool work = 128 * tile + 32 * quad < it.rows;  // some row of this warp is
       const bool mine = row < it.rows;                     // this lane's row is
-      const int32_t pos = it.p0 + (it.row0 + row) / a.G;
+      const int32_t pos = it.p0 + (int32_t)a.by_group.div(it.row0 + row);
       float m = -INFINITY;
       float2 sum = make_float2(0.f, 0.f);
       for (int32_t j = 0; here && j < n && ok; ++j, ++info) {
@@ -724,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
           const int col = D / 2 * half;
           // rows of the output that this warp's lanes stand for, -1: none
-          const int32_t token = rho / a.G;
+          const int32_t token = (int32_t)a.by_group.div(rho);
           const int32_t at = !mine ? -1
                              : it.slot >= 0 ? it.slot + row
                                             : (it.tok0 + token) * a.Hq + it.head * a.G + (rho - token * a.G);
