@@ -120,13 +120,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   __shared__ Tile tile[kHeld];
   __shared__ long long before[kHeld];  // pages of the tiles before, for one head
   __shared__ long long sums[kPlanWarps];
-  __shared__ int32_t n_merges, n_rows, max_rows, max_parts, longest, shortest, most_rows;
+  __shared__ int32_t n_items, n_placed, n_merges, n_rows, max_parts, longest, shortest, most_rows;
   __shared__ Cuts cut;
-  __shared__ bool again;
+  __shared__ bool equal;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < kBuckets) hist[tid] = 0;
   if (tid == 0) {
-    n_merges = n_rows = max_rows = max_parts = longest = most_rows = 0;
+    n_items = n_placed = n_merges = n_rows = max_parts = longest = most_rows = 0;
     shortest = INT32_MAX;
   }
   griddep_wait();
@@ -200,18 +200,48 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   }
   __syncthreads();
 
-  // ---- the sizes of whole lists; then, where cutting is better, those of the pieces
-  const int64_t lists = (int64_t)tiles * a.Hkv;
+  // ---- whole lists, or cut ones
+  const int32_t lists = tiles * a.Hkv;
   if (tid == 0) {
-    cut = {tiles, 1, 0};
-    again = false;
+    Cuts c = {tiles, 1, 0};
+    if (tiles <= kHeld && lists < 16 * a.ctas) {
+      // whole lists: the average load; or the longest one; or, with some CTAs idle while the last lists run, the
+      // load and those CTAs' share of a shortest list
+      const float load = (float)pages * (float)a.Hkv * a.per_cta;
+      const float items = (float)lists * a.per_cta, idle = ceilf(items) - items;
+      const float item = kItemCost * a.page_rate, merge = kMergeCost * a.page_rate;
+      const float whole = fmaxf((float)longest, load + idle * (float)shortest) + item * ceilf(items);
+      const bool rounds = lists >= a.ctas;  // full rounds of whole lists, and the rest cut; else all cut
+      c.whole = rounds ? (int32_t)a.by_heads.div((int32_t)items * a.ctas) : 0;
+      const float rest =
+          rounds ? (float)(c.whole < tiles ? pages - before[c.whole] : 0) * (float)a.Hkv * a.per_cta : load;
+      // One piece or two for each CTA, if the workspace has partial results for them: there is at most one more for
+      // each list than there are cuts.
+      const int32_t cut_lists = lists - c.whole * a.Hkv, k = rounds ? 2 : 1, pieces = cut_lists + k * a.ctas;
+      c.grid = max(a.page_rate < 1.f ? 1 : 2, (int32_t)ceilf(fminf(rest / (float)k, 1e9f)));
+      float cost = load + item * (rounds ? items + 2.f : 2.f) + merge;
+      if (!rounds && longest == shortest) {  // equal lists: into as many equal parts as make one round
+        const int32_t parts = (int32_t)((float)a.ctas / (float)max(lists, 1));
+        const float each = ceilf((float)longest / (float)parts) + item + merge;
+        if (parts > 1 && each <= cost) {
+          cost = each;
+          c.parts = parts;
+        }
+      }
+      cost += (float)pieces * (float)most_rows * kRowCost * a.page_rate;
+      if (cost >= whole || pieces > kChunkSplitItems || (int64_t)pieces * most_rows > a.lay.rows_cap)
+        c = {tiles, 1, 0};
+    }
+    cut = c;
+    equal = longest == shortest && (c.whole == tiles || c.parts > 0);
   }
   __syncthreads();
+
+  // ---- the longest items come first, unless all are as good as equal: the sizes, and from them the places
+  if (!equal) {
 #pragma unroll 1
-  for (int pass = 0;; ++pass) {
-#pragma unroll 1
-    for (int64_t u = tid; u < lists; u += kPlanThreads) {
-      const int32_t t = (int32_t)a.by_heads.div((uint32_t)u), h = (int32_t)u - t * a.Hkv;
+    for (int32_t u = tid; u < lists; u += kPlanThreads) {
+      const int32_t t = (int32_t)a.by_heads.div(u), h = u - t * a.Hkv;
       const int32_t n = t < kHeld ? tile[t].g.n : load_tile(a, q, t).g.n;
       const Pieces p = pieces_of(cut, t, h, n, t < kHeld ? before[t] : 0, a.Hkv);
       atomicAdd(&hist[bucket_of(p.first)], 1);
@@ -222,7 +252,6 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     }
     __syncthreads();
     if (warp == 0) {
-      // the longest items come first: their places
       int32_t at = 0;
 #pragma unroll 1
       for (int b = kBuckets - 1 - lane; b >= 0; b -= 32) {
@@ -230,50 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         hist[b] = upto - n;
         at = __shfl_sync(0xffffffffu, upto, 31);
       }
-      if (lane == 0) {
-        ChunkHead* head = chunk_head(a);
-        head->items = at;
-        head->next = 0;
-        again = false;
-        if (pass == 0 && tiles <= kHeld && lists < 16 * (int64_t)a.ctas) {
-          const float whole_lists = (float)lists, total = (float)pages * (float)a.Hkv;
-          const float load = total * a.per_cta;
-          // whole lists: the average load; or the longest one; or, with some CTAs idle while the last lists run, the
-          // load and those CTAs' share of a shortest list
-          const float items = whole_lists * a.per_cta, idle = ceilf(items) - items;
-          const float item = kItemCost * a.page_rate, merge = kMergeCost * a.page_rate;
-          const float worst = fmaxf((float)longest, load + idle * (float)shortest) + item * ceilf(items);
-          Cuts c = {0, 1, 0};
-          const bool rounds = lists >= a.ctas;  // full rounds of whole lists, and the rest cut; else all cut
-          if (rounds) c.whole = (int32_t)a.by_heads.div((uint32_t)(lists - lists % a.ctas));
-          const float rest =
-              rounds ? (float)(c.whole < tiles ? pages - before[c.whole] : 0) * (float)a.Hkv * a.per_cta : load;
-          // Pieces for each CTA, as many as the workspace has partial results for: there is at most one more for
-          // each list than there are cuts.
-          const int64_t cut_lists = lists - (int64_t)c.whole * a.Hkv;
-          const int64_t fit = min((int64_t)kChunkSplitItems, (int64_t)(a.lay.rows_cap / max(most_rows, 1))) - cut_lists;
-          const int k = min(rounds ? 2 : 1, (int32_t)(max(fit, (int64_t)0) / a.ctas));
-          c.grid = max(a.page_rate < 1.f ? 1 : 2, (int32_t)ceilf(fminf(rest / (float)max(k, 1), 1e9f)));
-          float cost = load + item * (rounds ? items + 2.f : 2.f) + merge;
-          if (!rounds && longest == shortest && k == 1) {  // equal lists: into as many equal parts as make one round
-            const int32_t parts = a.ctas / max((int32_t)lists, 1);
-            const float each = ceilf((float)longest / (float)parts) + item + merge;
-            if (parts > 1 && each <= cost) {
-              cost = each;
-              c.parts = parts;
-            }
-          }
-          cost += (float)(cut_lists + (int64_t)k * a.ctas) * (float)most_rows * kRowCost * a.page_rate;
-          if (cost < worst && c.whole < tiles && k > 0) {
-            cut = c;
-            again = true;
-          }
-        }
-      }
     }
-    __syncthreads();
-    if (!again) break;
-    if (tid < kBuckets) hist[tid] = 0;
     __syncthreads();
   }
 
@@ -282,35 +268,34 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   ChunkMerge* merges = reinterpret_cast<ChunkMerge*>(a.ws + a.lay.merges);
   const int size = cut.whole == tiles || lists > 256 ? 1 : lists > 64 ? 4 : 32, sub = lane % size;  // threads a list
 #pragma unroll 1
-  for (int64_t u0 = 0; u0 < lists; u0 += kPlanThreads / size) {
-    const int64_t u = u0 + tid / size;
+  for (int32_t u0 = 0; u0 < lists; u0 += kPlanThreads / size) {
+    const int32_t u = u0 + tid / size;
     const bool on = u < lists;
-    const int32_t t = on ? (int32_t)a.by_heads.div((uint32_t)u) : 0, h = on ? (int32_t)u - t * a.Hkv : 0;
+    const int32_t t = on ? (int32_t)a.by_heads.div(u) : 0, h = on ? u - t * a.Hkv : 0;
     const Tile tl = t < kHeld ? tile[t] : load_tile(a, q, t);
     const Pieces p = pieces_of(cut, t, h, tl.g.n, t < kHeld ? before[t] : 0, a.Hkv);
     int32_t slot = -1;
-    if (on && p.count > 1 && sub == 0) {
-      slot = atomicAdd(&n_rows, p.count * tl.rows);
-      atomicMax(&max_rows, tl.rows);
-      atomicMax(&max_parts, p.count);
-      merges[atomicAdd(&n_merges, 1)] = {h, tl.row0, tl.rows, tl.tok0, slot, p.count};
+    if (on && sub == 0) {
+      atomicAdd(&n_items, p.count);
+      if (p.count > 1) {
+        slot = atomicAdd(&n_rows, p.count * tl.rows);
+        atomicMax(&max_parts, p.count);
+        merges[atomicAdd(&n_merges, 1)] = {h, tl.row0, tl.rows, tl.tok0, slot, p.count};
+      }
     }
     slot = __shfl_sync(0xffffffffu, slot, lane - sub);
 #pragma unroll 1
     for (int32_t i = sub; on && i < p.count; i += size) {
       const int32_t j0 = i == 0 ? 0 : p.first + (i - 1) * p.each;
       const int32_t j1 = i == 0 ? p.first : min(tl.g.n, j0 + p.each);
-      items[atomicAdd(&hist[bucket_of(j1 - j0)], 1)] = {tl.request, h,      tl.row0, tl.rows,
-                                                        j0,         j1,     tl.g.na, tl.g.shift,
-                                                        slot < 0 ? -1 : slot + i * tl.rows, tl.tok0, tl.p0, tl.L};
+      const int32_t at = atomicAdd(equal ? &n_placed : &hist[bucket_of(j1 - j0)], 1);
+      items[at] = {tl.request, h,       tl.row0, tl.rows, j0,   j1, tl.g.na, tl.g.shift, slot < 0 ? -1 : slot + i * tl.rows,
+                   tl.tok0,    tl.p0, tl.L};
     }
   }
   __syncthreads();
   if (tid == 0) {
-    ChunkHead* head = chunk_head(a);
-    head->merges = n_merges;
-    head->merge_rows = max_rows;
-    head->merge_parts = max_parts;
+    *chunk_head(a) = {n_items, n_merges, 0, most_rows, max_parts};
   }
   raise_flags(a.error_flags, eflags);
 }
