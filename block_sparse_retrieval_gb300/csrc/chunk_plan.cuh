@@ -122,7 +122,7 @@ __host__ __device__ __forceinline__ ChunkPages chunk_pages(int32_t p_lo, int32_t
 
 // Does a row at position p attend token t?
 __device__ __forceinline__ bool chunk_attends(int32_t p, int32_t t, int32_t init, int32_t local) {
-  return t <= p && (t < init || t > p - local);
+  return t <= p && (t < init || p - t < local);
 }
 
 // Is some token of page b hidden from some row at positions p_lo .. p_hi?

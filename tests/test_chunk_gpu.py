@@ -262,6 +262,37 @@ def test_pages_past_32_bits():
     assert torch.equal(attend(small), want)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("reqs", [[(1, 13 * i % 400) for i in range(700)], [(i % 90, 3 * i) for i in range(600)],
+                                  [(8000, 0)]], ids=["700 tokens", "600 chunks", "8000 rows"])
+def test_more_requests_or_tiles_than_are_held_on_chip(reqs, dtype):
+    Hq, Hkv = (33, 1) if len(reqs) == 1 else (4, 2)  # 264000 rows of one head: a thousand tiles
+    case = ref.Case(reqs, Hq=Hq, Hkv=Hkv, d=64, dtype=dtype, seed=18, init=20, local=100)
+    if len(reqs) > 1:
+        check(case)
+    check(case, window=True)
+
+
+def test_positions_near_the_largest():
+    """A sequence of 2^31 - 128 tokens, windowed (only the pages in sight exist)."""
+    L = (1 << 31) - 128
+    for dtype in (BF, F32):
+        case = ref.Case([(5, 395)], Hq=4, Hkv=1, d=64, dtype=dtype, seed=19, init=0, local=300)
+        want = attend(case, window=True)
+        blocks = L // 128
+        table = torch.full((1, blocks), -1, dtype=torch.int32, device=DEV)
+        # 400 tokens end 112 before a page's end; as many tokens before the far end
+        far = L - 112
+        table[0, far // 128 - 3:far // 128 + 1] = case.table[0, :4]
+        case.table, case.lens = table, torch.tensor([far], dtype=torch.int32, device=DEV)
+        got = attend(case, window=True)
+        assert int(case.flags) == 0 and torch.equal(got, want)
+        case.cfg["local_tokens"] = (1 << 31) - 1  # everything, hidden pages among it
+        case.lens = torch.tensor([400], dtype=torch.int32, device=DEV)
+        case.table = ref.Case([(5, 395)], Hq=4, Hkv=1, d=64, dtype=dtype, seed=19).table
+        assert torch.equal(attend(case, window=True), attend(case))
+
+
 def test_no_rows_is_no_work():
     case = ref.Case([(0, 100), (0, 0)], seed=17)
     attend(case)
