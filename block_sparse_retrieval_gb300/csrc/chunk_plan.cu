@@ -6,7 +6,7 @@
 //
 // This kernel's time is the fetch of its own instructions (a launch finds none of them on its SM: some 300 cycles
 // for every 8), not its arithmetic.  So loops are kept rolled, divisions by the head counts are multiplications, and
-// what is done twice is a function: 16.4 us with the loops unrolled, 7.9 so (one request).
+// what is done twice is a function: 16.4 us with the loops unrolled, some 6 so (one request).
 #include "chunk_plan.cuh"
 
 namespace srkv {
@@ -82,8 +82,7 @@ __device__ __noinline__ Pieces pieces_of(const Cuts& cut, int32_t t, int32_t h, 
       p.each = max(1, (n + cut.parts - 1) / cut.parts);
       p.first = min(n, p.each);
     } else {
-      // the row of lists is cut where its position, modulo the grid, is zero (modulo 2^32 first: the cuts of very
-      // long rows are as good anywhere)
+      // the row of lists is cut where its position is a multiple of the grid (rows of 2^32 pages are not cut)
       p.first = min(n, cut.grid - (int32_t)((uint32_t)(before * heads + (long long)h * n) % (uint32_t)cut.grid));
     }
     p.count = 1 + (n - p.first + p.each - 1) / p.each;
@@ -136,7 +135,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   const bool few = a.batch <= kHeld;
   int32_t* req = reinterpret_cast<int32_t*>(a.ws + a.lay.req);
   uint32_t eflags = 0;
-  const int32_t cap = a.lay.items_cap / a.Hkv - (kChunkSplitItems + a.Hkv - 1) / a.Hkv;  // tiles that good offsets make at most
+  // tiles that good offsets make at most
+  const int32_t cap = a.lay.items_cap / a.Hkv - (kChunkSplitItems + a.Hkv - 1) / a.Hkv;
   long long base = 0;
 #pragma unroll 1
   for (int32_t r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         }
       }
       cost += (float)pieces * (float)most_rows * kRowCost * a.page_rate;
-      if (cost >= whole || pieces > kChunkSplitItems || (int64_t)pieces * most_rows > a.lay.rows_cap)
+      if (cost >= whole || pieces > kChunkSplitItems || (int64_t)pieces * most_rows > a.lay.rows_cap ||
+          pages * a.Hkv > (long long)UINT32_MAX)
         c = {tiles, 1, 0};
     }
     cut = c;
@@ -289,8 +290,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       const int32_t j0 = i == 0 ? 0 : p.first + (i - 1) * p.each;
       const int32_t j1 = i == 0 ? p.first : min(tl.g.n, j0 + p.each);
       const int32_t at = atomicAdd(equal ? &n_placed : &hist[bucket_of(j1 - j0)], 1);
-      items[at] = {tl.request, h,       tl.row0, tl.rows, j0,   j1, tl.g.na, tl.g.shift, slot < 0 ? -1 : slot + i * tl.rows,
-                   tl.tok0,    tl.p0, tl.L};
+      items[at] = {tl.request, h,          tl.row0, tl.rows,
+                   j0,         j1,         tl.g.na, tl.g.shift,
+                   slot < 0 ? -1 : slot + i * tl.rows, tl.tok0, tl.p0, tl.L};
     }
   }
   __syncthreads();
