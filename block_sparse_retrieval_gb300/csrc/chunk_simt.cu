@@ -1,27 +1,30 @@
 // chunk_simt.cu -- attention of a chunk over the paged cache on CUDA cores, in full precision: the fp32 path.
 //
-// A CTA takes a tile of 64 rows (128 at d 128) and walks its pages 64 tokens at a time: S = Q K^T by 8 rows x 4
-// tokens of a thread, a running maximum and sum per row in fp32, O += P V by 8 rows x d / 16 columns of a thread,
-// both in packed pairs.  Bound by the fp32 rate (4 d operations per row and token) and by the reads of shared memory, of
-// which a warp's products take 16 lines of 128 bytes for 128 operations a lane: 7 ragged requests of up to 300
-// tokens at d 64 take 172 us, 39 % of the fp32 rate (195 with 4 rows x 4 tokens a thread, 24 lines; 214 with tiles of 128
-// rows, which short chunks fill less).  Rows are padded by 16 bytes so that a warp's 16 tokens lie in different
-// banks.  Warps without a row (single tokens) only copy.
+// A CTA takes a tile of 64 rows (128 at d 128) and walks its pages 64 tokens (32) at a time, the next ones on
+// their way meanwhile: S = Q K^T by 8 rows x 4 tokens (2) of a thread, a running maximum and sum per row in fp32,
+// O += P V by 8 rows x d / 16 columns of a thread, both in packed pairs of fp32.  Bound by the fp32 rate (4 d
+// operations per row and token) and, as 8 warps an SM leave little to fall back on, by the latency of its own
+// chains: 7 ragged requests of up to 300 tokens at d 64 take 175 us, 38 % of that rate (195 with 4 rows x 4 tokens a
+// thread, whose reads of shared memory took 24 lines for 128 operations a lane instead of 16; 214 with tiles of
+// 128 rows, which short chunks fill less; 178 without the copies ahead).  Rows are padded by 16 bytes so that a
+// warp's tokens lie in different banks.  Warps without a row (single tokens) only copy.
 #include "chunk_plan.cuh"
 
 namespace srkv {
 namespace {
 
-constexpr int kTok = 64;  // tokens a step
 
 template <int D>
 struct SimtGeom {
   static constexpr int kRows = D == 64 ? kChunkTileSimt64 : kChunkTileSimt128;
   static constexpr int kThreads = 2 * kRows;
-  static constexpr int LD = D + 4;  // padded row of Q, K and V
+  static constexpr int kTok = D == 64 ? 64 : 32;  // tokens a step
+  static constexpr int kCols = kTok / 16;         // of them a thread's
+  static constexpr int LD = D + 4;                // padded row of Q, K and V
   static constexpr int LP = kTok + 4;
-  static constexpr size_t kQ = 0, kK = kQ + sizeof(float) * kRows * LD, kV = kK + sizeof(float) * kTok * LD,
-                          kP = kV + sizeof(float) * kTok * LD, kSmem = kP + sizeof(float) * kRows * LP;
+  static constexpr size_t kTile = sizeof(float) * kTok * LD;  // K and V: two of each, one in use and one on its way
+  static constexpr size_t kQ = 0, kK = kQ + sizeof(float) * kRows * LD, kV = kK + 2 * kTile, kP = kV + 2 * kTile,
+                          kSmem = kP + sizeof(float) * kRows * LP;
 };
 
 constexpr int kPer = 8;  // rows of a thread
@@ -32,7 +35,7 @@ __device__ __forceinline__ void add_values(const float* sp, const float* sv, int
                                            float2 (&acc)[kPer][D / 32]) {
   using S = SimtGeom<D>;
 #pragma unroll 2
-  for (int t = 0; t < kTok; t += 4) {
+  for (int t = 0; t < S::kTok; t += 4) {
     float4 v[4][D / 64];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -60,12 +63,10 @@ __device__ __forceinline__ void add_values(const float* sp, const float* sv, int
 template <int D>
 __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_simt_kernel(const ChunkArgs a) {
   using S = SimtGeom<D>;
-  constexpr int kThreads = S::kThreads, kRows = S::kRows;
+  constexpr int kThreads = S::kThreads, kRows = S::kRows, kTok = S::kTok, kCols = S::kCols;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int32_t next;
   float* sq = reinterpret_cast<float*>(smem + S::kQ);
-  float* sk = reinterpret_cast<float*>(smem + S::kK);
-  float* sv = reinterpret_cast<float*>(smem + S::kV);
   float* sp = reinterpret_cast<float*>(smem + S::kP);
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   griddep_wait();
@@ -103,48 +104,71 @@ __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) acc[i][e] = make_float2(0.f, 0.f);
     }
-    for (int32_t j = it.j0; j < it.j1; ++j) {
-      const int32_t b = j < it.na ? j : j + it.shift;
-      const int32_t page = a.block_table[(int64_t)it.request * a.max_blocks + b];
-      if (page < 0 || (int64_t)page >= a.num_pages) {
+    // The next step to copy: tokens [t0, t0 + kTok) of position j of the list, whose page is `page`.
+    auto page_at = [&](int32_t j) {
+      return j < it.j1 ? a.block_table[(int64_t)it.request * a.max_blocks + (j < it.na ? j : j + it.shift)] : 0;
+    };
+    int32_t j = it.j0, t0 = 0, page = page_at(j), ahead = page_at(j + 1);
+    auto turn_page = [&] {
+      ++j;
+      t0 = 0;
+      page = ahead;
+      ahead = page_at(j + 1);
+    };
+    auto seek = [&] {  // past pages that are not there
+      while (j < it.j1 && (page < 0 || (int64_t)page >= a.num_pages)) {
         eflags |= SRKV_EFLAG_PAGE_RANGE;
-        continue;
+        turn_page();
       }
+      return j < it.j1;
+    };
+    auto copy = [&](int buffer) {
+      const int32_t tok = (j < it.na ? j : j + it.shift) * kBlock + t0;
+      const int64_t at = (((int64_t)page * a.Hkv + it.head) * kBlock + t0) * D;
+      const float* k = static_cast<const float*>(a.k_cache) + at;
+      const float* v = static_cast<const float*>(a.v_cache) + at;
+      const uint32_t dk = smem_u32(smem + S::kK + buffer * S::kTile), dv = smem_u32(smem + S::kV + buffer * S::kTile);
+#pragma unroll 4
+      for (int i = tid; i < kTok * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), c = i % (D / 4);
+        const uint32_t off = (row * S::LD + c * 4) * sizeof(float);
+        const int n = tok + row < it.L ? 16 : 0;  // behind the sequence: zeros
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dk + off), "l"(k + row * D + c * 4), "r"(n)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dv + off), "l"(v + row * D + c * 4), "r"(n)
+                     : "memory");
+      }
+    };
+    bool more = seek();
+    if (more) copy(0);
+    for (int buffer = 0; more; buffer ^= 1) {
+      const int32_t b = j < it.na ? j : j + it.shift, tok = b * kBlock + t0;
       const bool masked = chunk_masked(b, p_lo, p_hi, a.init, a.local);
-      const int64_t slab = ((int64_t)page * a.Hkv + it.head) * (int64_t)kBlock * D;
-      for (int t0 = 0; t0 < kBlock; t0 += kTok) {
-        const int32_t tok = b * kBlock + t0;
-        if (tok > p_hi) break;
-        __syncthreads();
-        for (int i = tid; i < kTok * (D / 4); i += kThreads) {
-          const int row = i / (D / 4), c = i % (D / 4);
-          float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-          if (tok + row < it.L) {
-            const int64_t at = slab + (int64_t)(t0 + row) * D + c * 4;
-            k = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + at);
-            v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v_cache) + at);
-          }
-          *reinterpret_cast<float4*>(sk + row * S::LD + c * 4) = k;
-          *reinterpret_cast<float4*>(sv + row * S::LD + c * 4) = v;
-        }
-        __syncthreads();
-        if (!work) continue;
-        float2 s2[kPer][4];  // rows ty * 8 + i, tokens tx + 16 j: even and odd pairs of columns
+      const float* sk = reinterpret_cast<const float*>(smem + S::kK + buffer * S::kTile);
+      const float* sv = reinterpret_cast<const float*>(smem + S::kV + buffer * S::kTile);
+      t0 += kTok;
+      if (t0 >= kBlock || tok + kTok > p_hi) turn_page();
+      more = seek();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();  // this step's tokens are there, and the last step's buffer is free
+      if (more) copy(buffer ^ 1);
+      if (work) {
+        float2 s2[kPer][kCols];  // rows ty * 8 + i, tokens tx + 16 j: even and odd pairs of columns
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) s2[i][jj] = make_float2(0.f, 0.f);
+          for (int jj = 0; jj < kCols; ++jj) s2[i][jj] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
-          float4 k[4];
+          float4 k[kCols];
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj)
+          for (int jj = 0; jj < kCols; ++jj)
             k[jj] = *reinterpret_cast<const float4*>(sk + (tx + 16 * jj) * S::LD + c);
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const float4 q = *reinterpret_cast<const float4*>(sq + (ty * kPer + i) * S::LD + c);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
+            for (int jj = 0; jj < kCols; ++jj) {
               s2[i][jj] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k[jj].x, k[jj].y), s2[i][jj]);
               s2[i][jj] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k[jj].z, k[jj].w), s2[i][jj]);
             }
@@ -153,9 +177,9 @@ __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int32_t pos = it.p0 + (int32_t)a.by_group.div(rho0 + i);
-          float top = m[i], s[4];
+          float top = m[i], s[kCols];
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
+          for (int jj = 0; jj < kCols; ++jj) {
             s[jj] = (s2[i][jj].x + s2[i][jj].y) * a.scale_log2;
             if (masked && !chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local)) s[jj] = -INFINITY;
             top = fmaxf(top, s[jj]);
@@ -166,7 +190,7 @@ __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_
           const float w = exp2f(m[i] - ref);
           float sum = 0.f;
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
+          for (int jj = 0; jj < kCols; ++jj) {
             const float p = exp2f(s[jj] - ref);
             sum += p;
             sp[(ty * kPer + i) * S::LP + tx + 16 * jj] = p;
