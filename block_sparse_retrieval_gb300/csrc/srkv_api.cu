@@ -285,6 +285,15 @@ bool strided_ok(const void* p, int64_t stride, const srkv_config& cfg, int32_t h
   return aligned(p, 16) && stride % per == 0 && stride >= (int64_t)heads * cfg.head_dim;
 }
 
+// Do `tokens` rows of `heads` heads, `stride` elements apart, lie wholly before or behind out's packed rows?
+bool apart(const void* in, int64_t stride, int32_t heads, const void* out, int32_t out_heads, int32_t tokens,
+           const srkv_config& cfg) {
+  const uint64_t e = cfg.dtype == SRKV_BF16 ? 2 : 4, d = (uint64_t)cfg.head_dim;
+  const uint64_t i0 = (uint64_t)in, i1 = i0 + ((uint64_t)(tokens - 1) * (uint64_t)stride + heads * d) * e;
+  const uint64_t o0 = (uint64_t)out, o1 = o0 + (uint64_t)tokens * out_heads * d * e;
+  return i1 <= o0 || o1 <= i0;
+}
+
 // Both chunk attention calls; `windowed`: the configuration's first tokens and window, else all before.
 srkv_status chunk_attention(const srkv_config* cfg, const void* q, int64_t q_stride,
                             const void* k_cache, const void* v_cache, int64_t num_pages,
@@ -308,6 +317,8 @@ srkv_status chunk_attention(const srkv_config* cfg, const void* q, int64_t q_str
   if (need == 0 || num_pages > INT32_MAX || (int64_t)cfg->num_kv_heads * kBlock > INT32_MAX)
     return SRKV_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return SRKV_ERR_WORKSPACE;
+  // (a tile's rows are read again for each of its items, when others may be written)
+  if (!apart(q, q_stride, cfg->num_q_heads, out, cfg->num_q_heads, total_tokens, *cfg)) return SRKV_ERR_INVALID_ARG;
   const int32_t sms = sm_count();
   if (sms <= 0) return SRKV_ERR_CUDA;
   a.q = q;
@@ -867,6 +878,12 @@ srkv_status srkv_append_kv_rope(const srkv_config* cfg, const void* q, int64_t q
   if (((int64_t)total_tokens / kBlock + 2 * (int64_t)batch) * cfg->num_kv_heads + total_tokens >
       INT32_MAX / 2)
     return SRKV_ERR_UNSUPPORTED;
+  const int32_t Hq = cfg->num_q_heads, Hkv = cfg->num_kv_heads;
+  const bool in_place = q == q_out && (total_tokens == 1 || q_stride == (int64_t)Hq * cfg->head_dim);
+  if (q && ((!in_place && !apart(q, q_stride, Hq, q_out, Hq, total_tokens, *cfg)) ||
+            !apart(k_new, k_stride, Hkv, q_out, Hq, total_tokens, *cfg) ||
+            !apart(v_new, v_stride, Hkv, q_out, Hq, total_tokens, *cfg)))
+    return SRKV_ERR_INVALID_ARG;
   return cuda_status(launch_append_rope(*cfg, q, q_stride, k_new, k_stride, v_new, v_stride,
                                         chunk_offsets, total_tokens, rope_freqs, rope_dim,
                                         interleaved, q_out, k_cache, v_cache, num_pages,

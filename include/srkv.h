@@ -172,16 +172,18 @@ srkv_status srkv_append_kv(const srkv_config* cfg, const void* k_new, const void
  *     the value that srkv_build_block_reps gives for that many valid tokens.
  *   q: [total_tokens][Hq][d], k_new, v_new: [total_tokens][Hkv][d] in the cache dtype, tokens q_stride,
  *   k_stride, v_stride elements apart (the parts of one fused projection, for instance; multiples of 16
- *   bytes, at least one token's heads); q_out: [total_tokens][Hq][d], may be q itself where q_stride =
- *   Hq d; all 16-byte aligned.  rope_freqs: device double [rope_dim / 2]; rope_dim: even, 0 to d, 0 leaves
- *   out the rotation; a multiple of 16, else SRKV_ERR_UNSUPPORTED.  chunk_offsets: device int32
+ *   bytes, at least one token's heads); q_out: [total_tokens][Hq][d], q itself where q_stride = Hq d, else
+ *   apart from q, k_new and v_new (SRKV_ERR_INVALID_ARG where it lies between their first and last
+ *   element); all 16-byte aligned.  rope_freqs: device double [rope_dim / 2], finite; rope_dim: even, 0 to d,
+ *   0 leaves out the rotation; a multiple of 16, else SRKV_ERR_UNSUPPORTED.  chunk_offsets: device int32
  *   [batch + 1], from 0 or more up to total_tokens or less, not decreasing; n_r = 0 is allowed, and rows
  *   of the packed tensors outside every request are left alone.  seq_lens: the lengths before the
  *   chunk, read only: the caller advances them (seq_lens[r] += n_r), and gives every request pages of its own
  *   for the tokens written.
  *   A request whose offsets are wrong (SRKV_EFLAG_CHUNK) or whose tokens do not all fit in
  *   [0, max_blocks * S) (SRKV_EFLAG_SEQ_LEN) is skipped, a page id outside [0, num_pages) skips that page
- *   (SRKV_EFLAG_PAGE_RANGE; queries are rotated all the same); both are flagged.
+ *   (SRKV_EFLAG_PAGE_RANGE; queries are rotated all the same); all are flagged.  Where offsets go down, rows that
+ *   two requests claim are one's or neither's.
  * Asynchronous on `stream`; one kernel.
  */
 srkv_status srkv_append_kv_rope(const srkv_config* cfg, const void* q, int64_t q_stride,
@@ -515,15 +517,18 @@ srkv_status srkv_retrieval_decode_prefix(const srkv_config* cfg, const void* q,
  *     tokens and the window of the position (StreamingLLM's attention, survey "大模型推理百倍加速之KV
  *     cache篇": sinks and a sliding window), as the decode calls see them without a kept block.
  * out[row][j][:] = softmax over those tokens of q[row][j].K_t / sqrt(d), times V_t; a row that attends
- * nothing gives 0.  A row depends on no token that it does not attend, whatever that token's key and value
- * hold (NaN and infinities too), nor on anything behind L.  Logits, maxima, sums and outputs are held in
- * fp32.  With bf16 the softmax weights are rounded to bf16 for the product with V (relative 2^-9 each); with
- * fp32 nothing is rounded below fp32.
+ * nothing, or whose logits are all -infinity, gives 0.  A row depends on no token that it does not attend,
+ * whatever that token's key and value hold (NaN and infinities too), nor on anything behind L.  Logits,
+ * maxima, sums and outputs are held in fp32.  With bf16 the softmax weights, up to 2^8 each as they are held,
+ * are rounded to bf16 for the product with V (by up to 2^-8 of each), so 2^8 times the sum of the attended
+ * values' magnitudes has to stay in fp32; with fp32 nothing is rounded below fp32.
  *   q: [total_tokens][Hq][d], tokens q_stride elements apart (a multiple of 16 bytes, at least Hq d);
- *   out: [total_tokens][Hq][d]; both 16-byte aligned.  Rows outside every request are left as they were.
+ *   out: [total_tokens][Hq][d], apart from q (SRKV_ERR_INVALID_ARG where it lies between q's first and last
+ *   element); both 16-byte aligned.  Rows outside every request are left as they were.
  *   chunk_offsets: as for srkv_append_kv_rope.  Any group size Hq / Hkv.
  *   workspace: >= srkv_chunk_workspace_size(cfg, total_tokens, batch) bytes, 256-byte aligned; its
- *   contents on entry do not matter; it is scratch of this call until the stream reaches its end.
+ *   contents on entry do not matter; it is scratch of this call until the stream reaches its end, so
+ *   calls that may overlap (streams, captured graphs) take one each.
  *   A request whose offsets are wrong is skipped; of a chunk longer than its sequence the first rows
  *   attend nothing; both flag SRKV_EFLAG_CHUNK.  A length outside [0, max_blocks * S] is clamped into it
  *   (SRKV_EFLAG_SEQ_LEN).  The tokens of a page whose id is outside [0, num_pages) are left out

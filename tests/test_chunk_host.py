@@ -68,6 +68,22 @@ def test_attention_checks_its_arguments(lib, name):
     assert attend(lib, name, ws=ODD, ws_bytes=need) == WORKSPACE
 
 
+def at(byte):
+    return ctypes.c_void_p((1 << 20) + byte)
+
+
+def test_outputs_that_lie_in_their_inputs_are_refused(lib):
+    """5 rows of 8 heads of 128 bf16: 10240 bytes packed, 4 * stride * 2 + 2048 strided."""
+    need = srkv.chunk_workspace_size(CFG, 5, 2)
+    for name in ("srkv_chunk_attention", "srkv_chunk_attention_window"):
+        for o in (dict(), dict(out=at(10240 - 16)), dict(q=at(10240 - 16)), dict(qs=2048, out=at(4 * 4096 + 2048 - 16))):
+            assert attend(lib, name, ws=at(1 << 22), ws_bytes=need, **o) == INVALID, o
+    far = dict(k=at(1 << 21), v=at(1 << 21))
+    for o in (dict(qs=2048), dict(qo=at(16)), dict(q=at(10240 - 16)), dict(k=FAKE), dict(v=FAKE),
+              dict(v=at(10240 - 16)), dict(k=at(1 << 10), ks=1024)):
+        assert append(lib, **{**far, **o}) == INVALID, o
+
+
 def test_workspace_size(lib):
     sizes = [srkv.chunk_workspace_size(CFG, t, b) for t, b in ((1, 1), (64, 64), (8192, 1), (131072, 64))]
     assert all(x % 256 == 0 for x in sizes) and sizes == sorted(sizes) and sizes[0] > 0
