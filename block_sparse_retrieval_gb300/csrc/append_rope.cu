@@ -6,14 +6,18 @@
 // rep_sums.cuh: the value a fresh build gives.
 //
 // Angles.  A frequency is held as the fraction of a turn per token in 64-bit fixed point, so p times it modulo
-// 2^64 is the angle modulo one turn without any rounding: no position is too far.  The top 32 bits, less the nearest quarter turn, go through the Taylor series of sine
-// and cosine on +-pi/4 in fp32 (terms up to x^9 and x^10: the next ones are below 2^-28 and 2^-31).  A 64-bit
-// floating product would do the same at 1/64 of the fp32 rate: some 30 us for 8192 tokens of 8 heads.
+// 2^64 is the angle modulo one turn without any rounding: no position is too far.  The top 32 bits, less the
+// nearest quarter turn, go through the Taylor series of sine and cosine on +-pi/4 in fp32 (terms up to x^9 and x^10:
+// the next ones are below 2^-28 and 2^-31).  A 64-bit floating product would do the same at 1/64 of the fp32
+// rate: some 30 us for 8192 tokens of 8 heads.
 //
 // Work.  One CTA per (page touched, kv head): its 8 warps go through the page's 128 rows, 16 each, the rows
-// already there as read and the new ones as rotated, and sum them on the way, so that the vector needs no second read.  Other CTAs
-// rotate the queries, a warp per token (or eight warps per token where tokens are few), with the token's
-// angles computed once for all its heads.
+// already there as read and the new ones as rotated, and sum them on the way, so that the vector needs no
+// second read.  Other CTAs rotate the queries, a warp per token (or eight warps per token where tokens are
+// few), with the token's angles computed once for all its heads.
+//
+// What bounds it.  8192 tokens of 32 / 8 heads: bytes; 201.6 MB in 35.3 us = 5.7 TB/s, 0.84 of the measured copy rate.
+// 64 tokens: 5.2 us, three dependent reads (lengths, table, rows) and the launch; one token: 3.2 us.
 #include "rep_sums.cuh"
 
 namespace srkv {

@@ -1,23 +1,38 @@
 // chunk_mma.cu -- attention of a chunk over the paged cache on the tensor cores (bf16).
 //
 // A CTA takes an item: up to 256 rows (two tiles of 128) of one (request, kv head) over a list of pages.  Per
-// page and tile:  S = Q K^T (128 x 128, fp32, in tensor memory);  the tile's warpgroup, one thread a row, reads its
-// row, updates the row's maximum and sum, and writes P = 2^(c S - c m) as bf16 over S;  O += P V (O in tensor memory).
-// The products of one tile run while the other tile's warpgroup is at its exponentials.
+// page and tile:  S = Q K^T (128 x 128, fp32, in tensor memory);  the tile's two warpgroups, two threads a row, read it,
+// update the row's maximum and sum, and write P = 2^(c S - R) as bf16 over S;  O += P V (O in tensor memory).
 //
 //   warps 0-7, 8-15  softmax and output of tile 0, 1: two threads a row, 64 of a page's tokens each
-//   warps 16, 17     issue the products of tile 0, 1: while one waits or is held up by the full queue, the other fills it
+//   warps 16, 17     issue the products of tile 0, 1
 //   warp 18          takes items and copies pages (TMA) into a ring of stages: K, V, K, V ...
 //   warp 19          copies the queries of the next item once the last product with the present ones is done, and
 //                    cleans values (below)
 //
-// The reference m that the exponentials subtract follows the maximum only when that has grown by more than 2^8:
-// O is then scaled by hand.  Sums and outputs stay exact for any reference; fp32 holds the larger weights.
+// Why so.  256 rows share a page because the copy of a page (64 KB) then takes half the time of its products
+// (2048 cycles).  S and O of two tiles fill the 512 columns of tensor memory, so P lies on S and the next S waits for O's
+// product: the tiles have to alternate, one's products running while the other is at its exponentials.  Two warps issue
+// them, taking turns (in step, 13.5 ms for 8192 of 131072 tokens): waits and releases of one fall into the other's
+// block (one warp for both: 11.3 ms; two, in turns: 10.7; told two products ahead: 10.3 to 10.5).  P is handed over in
+// two parts, so that its product begins before the last exponential.  One thread a row (128 logits, 208 registers) took
+// 12.4 ms, with 168 registers and spills 19.6.
+//
+// What bounds it.  Long lists: the tensor cores; 2850 cycles a page pair, of which 2048 are products (0.74 of the cycles
+// by the counters), 1589 to 1657 TFLOP/s = 0.82 to 0.86 of the measured burst rate of a library product and
+// 0.92 to 0.96 of the sustained one; what is left is the chain from a product's end over the exponentials to the next
+// turn.  Single tokens: bytes; 64 of them over windows of 8216 take 311 us = 0.98 of the measured copy rate.
+// Short lists: an item's start and end (queries, first page, output), some 3 us that the next item does not hide.
+//
+// Rounding.  P is rounded to bf16 (by up to 2^-8 of each weight: the product's operands share a type with V),
+// its sum taken before that; S, R, sums and O are fp32.  The reference R that the exponentials subtract follows
+// the maximum only when that has grown by more than 2^8 (O is then scaled by hand): sums and outputs are the
+// same for any reference, as long as 2^8 times a sum of values stays in fp32.
 //
 // Hidden tokens.  A weight of zero does not hide a value that is not finite, so the pages of an item that some
-// row sees in part are looked through before their product: rows behind the sequence are cleared, and elements
-// that are not finite are replaced by zero and their token noted; the rows that do attend such a token get
-// the element back at the end.
+// row sees in part are looked through before their product: rows behind the sequence are cleared, and elements of
+// tokens hidden from some row that are not finite are replaced by zero and their token noted; the rows that do attend
+// such a token get the element back at the end.
 #include "chunk_plan.cuh"
 #include "tcgen05.cuh"
 

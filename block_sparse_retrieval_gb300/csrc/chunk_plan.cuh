@@ -2,10 +2,10 @@
 // attention kernels and the merge.
 //
 // The rows of one (request, kv head) are its new tokens' query heads, row = token * G + head of the group, so
-// that one read of a page serves all of them whatever G is.  They are cut into tiles of kChunkTile rows (fewer
-// on the CUDA-core path).  A tile attends a list of pages in ascending order: those below `na`, then, with
-// a window, those from page na + shift on.  A long list may be divided among several items; their partial
-// results are merged (chunk_plan.cu).
+// that one read of a page serves all of them whatever G is.  They are cut into tiles of kChunkTile rows (on
+// CUDA cores of 64 or 128).  A tile attends a list of pages in ascending order: those below `na`, then, with a
+// window, those from page na + shift on.  A long list may be divided among several items; their partial results are
+// merged (chunk_plan.cu).
 #pragma once
 
 #include "srkv_internal.cuh"

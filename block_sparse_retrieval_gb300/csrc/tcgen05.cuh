@@ -37,15 +37,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr));
 #undef SRKV_OUT
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-#define SRKV_IN(i) "r"(r[i])
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SRKV_R32(SRKV_IN),
-      "r"(addr)
-      : "memory");
-#undef SRKV_IN
-}
 #define SRKV_R16(f) SRKV_R8(f, 0), SRKV_R8(f, 8)
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
 #define SRKV_OUT(i) "=r"(r[i])
