@@ -238,8 +238,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Every lane holds N 16-byte pieces of its own row; after it, lane l holds piece l % N of rows N (l / N) + 0 .. N - 1
-// of the warp, so that N lanes together hold a row's run of bytes.
+// Every lane holds N 16-byte pieces of its own row; after it, lane l holds piece l % N of rows N (l / N) + (k ^ l % N),
+// k = 0 .. N - 1, of the warp, so that N lanes together hold a row's run of bytes.
 template <int N>
 __device__ __forceinline__ void transpose(uint32_t* v, int lane) {
 #pragma unroll
@@ -249,12 +249,11 @@ __device__ __forceinline__ void transpose(uint32_t* v, int lane) {
       if (k & b) continue;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t &lo = v[4 * k + w], &hi = v[4 * (k | b) + w];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & b ? lo : hi, b);
-        if (lane & b)
-          lo = got;
-        else
-          hi = got;
+        // piece k for the lane whose bit b is k's: each keeps one of its own and gets the other's like it
+        uint32_t &x = v[4 * k + w], &y = v[4 * (k | b) + w];
+        const uint32_t keep = lane & b ? y : x;
+        y = __shfl_xor_sync(0xffffffffu, lane & b ? x : y, b);
+        x = keep;
       }
     }
 }
@@ -754,16 +753,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t at = !mine ? -1
                              : it.slot >= 0 ? it.slot + row
                                             : (it.tok0 + token) * a.Hq + it.head * a.G + (rho - token * a.G);
-#pragma unroll
+          const float2 w2 = make_float2(w, w);
+#pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
             uint32_t o[32];
             if (n > 0) {
               tmem_ld32(to + 32 * c, o);
               tmem_wait_ld();
               tmem_use32(o);
-            }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * w);
+              for (int e = 0; e < 32; e += 2) {  // (a row without weights: zeros times finite values, so zeros)
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), w2);
+                o[e] = __float_as_uint(x.x);
+                o[e + 1] = __float_as_uint(x.y);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
             if (n_odd > 0 && mine) {
 #pragma unroll 1
               for (int e = 0; e < 32; ++e) {
@@ -779,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float* acc = reinterpret_cast<float*>(a.ws + a.lay.acc) + col + 32 * c + 4 * (lane % 8);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const int32_t r = __shfl_sync(0xffffffffu, at, (lane & ~7) + k);
+                const int32_t r = __shfl_xor_sync(0xffffffffu, at, k);
                 if (r >= 0)
                   *reinterpret_cast<uint4*>(acc + (int64_t)r * D) =
                       make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -793,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + col + 32 * c + 8 * (lane % 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const int32_t r = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
+                const int32_t r = __shfl_xor_sync(0xffffffffu, at, k);
                 if (r >= 0)
                   *reinterpret_cast<uint4*>(out + (int64_t)r * D) =
                       make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
