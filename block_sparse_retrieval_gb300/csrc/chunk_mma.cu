@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kMmaWarp = 16, kPageWarp = 18;  // and the helper, the last one
-constexpr int kSlots = 2;      // items known at a time
+constexpr int kSlots = 3;      // items known at a time
 constexpr int kPageInfo = 8;   // pages between their copy and their softmax, at most
 constexpr int kParts = 4;      // pages seen in part and not yet multiplied, at most: their stages are not refilled
 constexpr int kOdd = 7;        // pages that an item's rows see in part, at most: 3 at each end of a window of 256 rows, 1 at
@@ -73,8 +73,9 @@ struct OddPage {
   int32_t block;
 };
 
+template <int kStages>
 struct Shared {
-  uint64_t full[8], empty[8];
+  uint64_t full[kStages], empty[kStages];
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2][2], o_full[2];  // P in two parts: the first 32 tokens of each half, the others
@@ -84,7 +85,7 @@ struct Shared {
   uint64_t turn[2];  // whose block of products comes next
   uint64_t drain[2];
   ChunkItem item[kSlots];
-  int2 page[kPageInfo];   // block, and how it is seen
+  int32_t page[kPageInfo];  // 4 block + how it is seen
   float note[2][2][128];  // [tile][half][row]: a maximum, or a sum
   OddPage odd[kSlots][kOdd];
   int32_t n_odd[kSlots];
@@ -161,7 +162,8 @@ __device__ __forceinline__ uint32_t clean_values(unsigned char* rows, bool behin
                      : "memory");
   }
   if (!__any_sync(0xffffffffu, scan)) return 0;
-  uint32_t odd = 0;
+  // zero times an element added up: NaN if one is not finite
+  uint32_t odd[4] = {0, 0, 0, 0};
 #pragma unroll 1
   for (int b = 0; b < D / 64; ++b) {
     uint32_t w[8][4];
@@ -170,14 +172,16 @@ __device__ __forceinline__ uint32_t clean_values(unsigned char* rows, bool behin
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
                    : "r"((row ^ (c * 16)) + b * (128 * 128)));
-    // an exponent of all ones carries into the sign bit's place
 #pragma unroll
     for (int c = 0; c < 8; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) odd |= (w[c][i] & 0x7fff7fffu) + 0x00800080u;
+      for (int i = 0; i < 4; ++i) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd[i]) : "r"(w[c][i]), "r"(0));
   }
-  odd = scan ? odd & 0x80008000u : 0u;
-  if (odd) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= (((odd[i] & 0x7fff7fffu) + 0x007f007fu) & 0x80008000u) != 0;
+  any = any && scan;
+  if (any) {
     uint4* at = reinterpret_cast<uint4*>(rows + lane * 128);
 #pragma unroll 1
     for (int c = 0; c < D / 8; ++c) {
@@ -191,7 +195,7 @@ __device__ __forceinline__ uint32_t clean_values(unsigned char* rows, bool behin
       x = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
-  return __ballot_sync(0xffffffffu, odd != 0);
+  return __ballot_sync(0xffffffffu, any);
 }
 
 // What clean_values took out of element `col` of the values that a row at `pos` attends.
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_mma_kernel(const ChunkArgs a, const __grid_constant__ Maps maps) {
   using G = Geo<D>;
   extern __shared__ __align__(1024) unsigned char smem[];  // the swizzle's period
-  Shared& sh = *reinterpret_cast<Shared*>(smem + G::kOffBar);
+  auto& sh = *reinterpret_cast<Shared<G::kStages>*>(smem + G::kOffBar);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n = min(32, it.j1 - j0);
           for (int i = 0; i < n && ok; ++i) {
             const int32_t z = __shfl_sync(0xffffffffu, page, i);
-            const int2 note = make_int2(__shfl_sync(0xffffffffu, b, i), __shfl_sync(0xffffffffu, seen, i));
+            const int32_t note = __shfl_sync(0xffffffffu, 4 * b + seen, i);
             for (int kv = 0; kv < 2 && ok; ++kv) {
               ok = mbar_wait(&sh.empty[st.at], st.phase ^ 1);
               if (!ok) break;
@@ -377,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < D / 64; ++b)
                   tma_page(dst + b * G::kBlockBytes, kv ? &maps.v : &maps.k, 64 * b, it.head * kBlock, z,
                            &sh.full[st.at]);
-                if (kv == 1 && (note.y & kPart)) {
+                if (kv == 1 && (note & kPart)) {
                   sh.part[part.at] = make_int2(st.at, (int)st.phase);
                   mbar_arrive(&sh.v_part[part.at]);
                 }
               }
               __syncwarp();
-              if (kv == 1 && (note.y & kPart)) part.next();
+              if (kv == 1 && (note & kPart)) part.next();
               st.next();
               ++issued;
             }
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = j + 1 < n;
           ok = mbar_wait(&sh.full[v.at], v.phase) && (!more || mbar_wait(&sh.full[k.at], k.phase));
           if (!ok) break;
-          if (sh.page[info++ % kPageInfo].y & kPart) {
+          if (sh.page[info++ % kPageInfo] & kPart) {
             ok = mbar_wait(&sh.v_clean[part.at], part.phase);
             if (!ok) break;
             part.next();
@@ -644,15 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[64];
           tmem_ld32(ts, s);
           tmem_ld32(ts + 32, s + 32);
-          const int2 page = sh.page[info % kPageInfo];
+          const int32_t page = sh.page[info % kPageInfo];
           tmem_wait_ld();
           tmem_use32(s);
           tmem_use32(s + 32);
           uint32_t late = 0xffffffffu;  // what the row attends of the second 32 tokens
-          if (page.y) {
-            const int32_t t0 = page.x * kBlock + 64 * half;
-            hide(s, !(page.y & kAbsent) ? attended_bits(pos, t0, a.init, a.local) : 0u);
-            late = !(page.y & kAbsent) ? attended_bits(pos, t0 + 32, a.init, a.local) : 0u;
+          if (page & 3) {
+            const int32_t t0 = (page >> 2) * kBlock + 64 * half;
+            hide(s, !(page & kAbsent) ? attended_bits(pos, t0, a.init, a.local) : 0u);
+            late = !(page & kAbsent) ? attended_bits(pos, t0 + 32, a.init, a.local) : 0u;
             hide(s + 32, late);
           }
           float top[4];
@@ -699,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c == 1) {
               tmem_wait_ld();
               tmem_use32(s + 32);
-              if (page.y) hide(s + 32, late);
+              if (page & 3) hide(s + 32, late);
             }
             uint32_t p[16];
 #pragma unroll
@@ -828,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch_d(const ChunkArgs& a, cudaStream_t stream) {
   using G = Geo<D>;
-  constexpr size_t smem = G::kOffBar + sizeof(Shared);
+  constexpr size_t smem = G::kOffBar + sizeof(Shared<G::kStages>);
   static_assert(smem <= 232448, "shared memory opt-in limit");
   static_assert(G::kStages <= 2 * kParts && G::kStages <= 8, "rings");
   // The shared-memory opt-in is set once per device (not during graph capture).
