@@ -3,11 +3,12 @@
 // A CTA takes a tile of 64 rows (128 at d 128) and walks its pages 64 tokens (32) at a time, the next ones on
 // their way meanwhile: S = Q K^T by 8 rows x 4 tokens (2) of a thread, a running maximum and sum per row in fp32,
 // O += P V by 8 rows x d / 16 columns of a thread, both in packed pairs of fp32.  Bound by the fp32 rate (4 d
-// operations per row and token) and, as 8 warps an SM leave little to fall back on, by the latency of its own
-// chains: 7 ragged requests of up to 300 tokens at d 64 take 175 us, 38 % of that rate (195 with 4 rows x 4 tokens a
-// thread, whose reads of shared memory took 24 lines for 128 operations a lane instead of 16; 214 with tiles of
-// 128 rows, which short chunks fill less; 178 without the copies ahead).  Rows are padded by 16 bytes so that a
-// warp's tokens lie in different banks.  Warps without a row (single tokens) only copy.
+// operations per row and token): 2048 tokens over 4096 more take 962 us, 42 TFLOP/s, its pipe busy on 58 % of the cycles;
+// 8 warps an SM leave little to fall back on while a sum waits for its last term, so terms of one sum are kept apart
+// (2 % faster).  7 ragged requests of up to 300 tokens at d 64 take 166 us, 30 TFLOP/s, the rest of which is the
+// ends of chunks that fill a tile in part (195 with 4 rows x 4 tokens a thread, whose reads of shared memory took 24
+// lines for 128 operations a lane instead of 16; 214 with tiles of 128 rows).  Rows are padded by 16 bytes so that
+// a warp's tokens lie in different banks.  Warps without a row (single tokens) only copy.
 #include "chunk_plan.cuh"
 
 namespace srkv {
@@ -42,16 +43,21 @@ __device__ __forceinline__ void add_values(const float* sp, const float* sv, int
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
         v[u][c] = *reinterpret_cast<const float4*>(sv + (t + u) * S::LD + c * 64 + tx * 4);
+    float w[kPer][4];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const float4 p = *reinterpret_cast<const float4*>(sp + (ty * kPer + i) * S::LP + t);
-      const float w[4] = {p.x, p.y, p.z, p.w};
+      w[i][0] = p.x, w[i][1] = p.y, w[i][2] = p.z, w[i][3] = p.w;
+    }
+    // a sum's terms as far apart as can be: products wait for those they depend on
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (kSkip && w[u] == 0.f) continue;
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (kSkip && w[i][u] == 0.f) continue;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const float2 ww = make_float2(w[u], w[u]);
+          const float2 ww = make_float2(w[i][u], w[i][u]);
           acc[i][c * 2] = __ffma2_rn(ww, make_float2(v[u][c].x, v[u][c].y), acc[i][c * 2]);
           acc[i][c * 2 + 1] = __ffma2_rn(ww, make_float2(v[u][c].z, v[u][c].w), acc[i][c * 2 + 1]);
         }
@@ -164,15 +170,19 @@ __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_
 #pragma unroll
           for (int jj = 0; jj < kCols; ++jj)
             k[jj] = *reinterpret_cast<const float4*>(sk + (tx + 16 * jj) * S::LD + c);
+          float4 q[kPer];
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(sq + (ty * kPer + i) * S::LD + c);
+          for (int i = 0; i < kPer; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * kPer + i) * S::LD + c);
 #pragma unroll
-            for (int jj = 0; jj < kCols; ++jj) {
-              s2[i][jj] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k[jj].x, k[jj].y), s2[i][jj]);
-              s2[i][jj] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k[jj].z, k[jj].w), s2[i][jj]);
-            }
-          }
+          for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int jj = 0; jj < kCols; ++jj)
+              s2[i][jj] = __ffma2_rn(make_float2(q[i].x, q[i].y), make_float2(k[jj].x, k[jj].y), s2[i][jj]);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int jj = 0; jj < kCols; ++jj)
+              s2[i][jj] = __ffma2_rn(make_float2(q[i].z, q[i].w), make_float2(k[jj].z, k[jj].w), s2[i][jj]);
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
