@@ -316,27 +316,32 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a) {
   constexpr int E = D / 32;
   __shared__ float part_o[8][D], part_l[8], part_top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // The attention kernel starts its CTAs' dependents once it has the plan, which is therefore readable already.
-  const ChunkHead h = *chunk_head(a);
+  // The attention kernel starts its CTAs' dependents once it has the plan, which is therefore readable already, from L2:
+  // this kernel has not waited for it, so nothing says that older lines of it have left an SM's own cache.
+  const int32_t* at = reinterpret_cast<const int32_t*>(chunk_head(a));
+  const int32_t n_merges = __ldcg(at + 1), merge_rows = __ldcg(at + 3), merge_parts = __ldcg(at + 4);
   griddep_launch_dependents();
-  if (h.merges == 0) {
+  if (n_merges == 0) {
     griddep_wait();
     return;
   }
-  const int share = h.merge_parts > 4 * kAtOnce   ? 8
-                    : h.merge_parts > 2 * kAtOnce ? 4
-                    : h.merge_parts > kAtOnce     ? 2
-                                                  : 1;  // warps a row
+  const int share = merge_parts > 4 * kAtOnce   ? 8
+                    : merge_parts > 2 * kAtOnce ? 4
+                    : merge_parts > kAtOnce     ? 2
+                                                : 1;  // warps a row
   const int group = warp / share, which = warp % share, groups = 8 / share;
-  const int32_t n = h.merges * h.merge_rows;
+  const int32_t n = n_merges * merge_rows;
   const ChunkMerge* merges = reinterpret_cast<const ChunkMerge*>(a.ws + a.lay.merges);
   const float* ml = reinterpret_cast<const float*>(a.ws + a.lay.ml);
   const float* acc = reinterpret_cast<const float*>(a.ws + a.lay.acc);
   bool waited = false;
   for (int32_t u0 = blockIdx.x * groups; u0 < n; u0 += gridDim.x * groups) {
     const int32_t u = min(u0 + group, n - 1);
-    const ChunkMerge m = merges[u / h.merge_rows];
-    const int32_t row = u % h.merge_rows;
+    const int4* note = reinterpret_cast<const int4*>(merges + u / merge_rows);
+    const int4 tile = __ldcg(note);
+    const int2 parts = __ldcg(reinterpret_cast<const int2*>(note + 1));
+    const ChunkMerge m = {tile.x, tile.y, tile.z, tile.w, parts.x, parts.y};
+    const int32_t row = u % merge_rows;
     const bool on = u0 + group < n && row < m.rows;
     if (!waited) griddep_wait();
     waited = true;

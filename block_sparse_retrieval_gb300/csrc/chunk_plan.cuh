@@ -36,6 +36,7 @@ struct __align__(16) ChunkMerge {
   int32_t head, row0, rows, tok0;
   int32_t slot, parts;
 };
+static_assert(sizeof(ChunkMerge) == 32, "two loads");
 
 // Division of any 32-bit number by one known on the host, as a multiplication (Granlund and Montgomery, "Division by
 // Invariant Integers using Multiplication", 1994, figure 4.1).
@@ -52,7 +53,7 @@ struct DivideBy {
   }
 };
 
-struct ChunkHead {  // counters of one call, written by the plan
+struct ChunkHead {  // counters of one call, written by the plan (read word by word in the merge)
   int32_t items, merges;  // merges: divided tiles times heads
   int32_t next;       // the next item to hand out
   int32_t merge_rows, merge_parts;  // rows, and parts, of the largest merge
