@@ -18,11 +18,13 @@
 // two parts, so that its product begins before the last exponential.  One thread a row (128 logits, 208 registers) took
 // 12.4 ms, with 168 registers and spills 19.6.
 //
-// What bounds it.  Long lists: the tensor cores; 2850 cycles a page pair, of which 2048 are products (0.74 of the cycles
-// by the counters), 1589 to 1657 TFLOP/s = 0.82 to 0.86 of the measured burst rate of a library product and
-// 0.92 to 0.96 of the sustained one; what is left is the chain from a product's end over the exponentials to the next
-// turn.  Single tokens: bytes; 64 of them over windows of 8216 take 311 us = 0.98 of the measured copy rate.
-// Short lists: an item's start and end (queries, first page, output), some 3 us that the next item does not hide.
+// What bounds it.  Long lists at d 128: the tensor cores; 2740 to 2850 cycles a page pair, of which 2048 are products
+// (77 % of the cycles by the counters), 1510 to 1657 TFLOP/s (by the GPU's power) = 0.78 to 0.86 of the measured burst
+// rate of a library product and 0.88 to 0.96 of the sustained one; what is left is the chain from a product's end
+// over the exponentials to the next turn.  At d 64 the softmax warps: 2510 cycles for 1024 of products.  (There S and P
+// could lie apart and products run ahead; that put both tiles' exponentials in step: 2685.)  Single tokens: bytes; 64
+// of them over windows of 8216 take 304 us, the measured copy rate.  Short lists: an item's start and end
+// (queries, first page, output), some 2 us that the next item does not hide.
 //
 // Rounding.  P is rounded to bf16 (by up to 2^-8 of each weight: the product's operands share a type with V),
 // its sum taken before that; S, R, sums and O are fp32.  The reference R that the exponentials subtract follows
