@@ -325,12 +325,13 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a) {
     griddep_wait();
     return;
   }
-  const int share = merge_parts > 4 * kAtOnce   ? 8
-                    : merge_parts > 2 * kAtOnce ? 4
-                    : merge_parts > kAtOnce     ? 2
-                                                : 1;  // warps a row
-  const int group = warp / share, which = warp % share, groups = 8 / share;
   const int32_t n = n_merges * merge_rows;
+  int share = merge_parts > 4 * kAtOnce   ? 8
+              : merge_parts > 2 * kAtOnce ? 4
+              : merge_parts > kAtOnce     ? 2
+                                          : 1;  // warps a row: no more than there are
+  while (share > 1 && n * (int64_t)share > 8 * gridDim.x) share /= 2;
+  const int group = warp / share, which = warp % share, groups = 8 / share;
   const ChunkMerge* merges = reinterpret_cast<const ChunkMerge*>(a.ws + a.lay.merges);
   const float* ml = reinterpret_cast<const float*>(a.ws + a.lay.ml);
   const float* acc = reinterpret_cast<const float*>(a.ws + a.lay.acc);
