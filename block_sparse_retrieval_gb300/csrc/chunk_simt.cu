@@ -10,10 +10,10 @@
 // lines for 128 operations a lane instead of 16; 214 with tiles of 128 rows).  Rows are padded by 16 bytes so that
 // a warp's tokens lie in different banks.
 //
-// Items of up to 16 rows (single tokens) would leave all warps but one idle; there each warp takes 16 of a step's
-// 64 tokens, with a maximum, a sum and outputs of its own, joined in order at the end, and a thread 4 rows where 8
-// are enough: 64 tokens over 8192 each, 8 heads of 128, 2918 -> 884 us (3.6 TB/s), of 64 835 -> 380 (4.2), bound by
-// the reads of shared memory.
+// Items of fewer rows (single tokens, the ends of chunks) would leave warps idle; there groups of warps share a step's
+// 64 tokens, each with a maximum, a sum and outputs of its own, joined in order at the end; and a thread takes 4
+// rows where 8 in all are enough.  64 single tokens over 8192 each, 8 heads of 128: 2918 -> 875 us (3.7 TB/s), of 64
+// 835 -> 380 (4.2), bound by the reads of shared memory; 6 x 17 rows over up to 3712 tokens 167 -> 109.
 #include "chunk_plan.cuh"
 
 namespace srkv {
@@ -27,23 +27,25 @@ struct SimtGeom {
   static constexpr int LD = D + 4;  // padded row of Q, K and V
 };
 
-// The steps of an item: rows of a thread and in shared memory, tokens a step, and of those a warp's and a thread's.
-// kThin: as few rows as one warp takes, so the warps share a step's tokens instead.
-template <int D, int kPer, bool kThin>
+// The steps of an item: kPer rows of a thread, kRowWarps warps side by side over its rows; where there are more
+// warps, groups of them share a step's tokens.
+template <int D, int kPer, int kRowWarps>
 struct Step {
   using S = SimtGeom<D>;
-  static constexpr int kRows = kThin ? 2 * kPer : S::kRows;
-  static constexpr int kTok = kThin || D == 64 ? 64 : 32;
-  static constexpr int kWarpTok = kThin ? 16 : kTok;
+  static constexpr int kRows = 2 * kPer * kRowWarps;
+  static constexpr int kWarps = S::kThreads / 32;
+  static constexpr int kGroups = kWarps / kRowWarps < 4 ? kWarps / kRowWarps : 4;
+  static constexpr bool kJoined = kGroups > 1;
+  static constexpr int kTok = kJoined || D == 64 ? 64 : 32;  // tokens a step
+  static constexpr int kWarpTok = kTok / kGroups;            // and a warp's, kCols of a thread
   static constexpr int kCols = kWarpTok / 16;
-  static constexpr int kGroups = kTok / kWarpTok;  // warps that share the rows
   static constexpr int LP = kTok + 4;
   static constexpr size_t kTile = sizeof(float) * kTok * S::LD;  // K and V: two of each, one in use and one on its way
   static constexpr size_t kQ = 0, kK = kQ + sizeof(float) * kRows * S::LD, kV = kK + 2 * kTile, kP = kV + 2 * kTile,
                           kSmem = kP + sizeof(float) * kRows * LP;
-  // at a thin item's end, in place of K: each warp's outputs, maxima and sums
+  // at a joined item's end, in place of K: each group's outputs, maxima and sums
   static constexpr size_t kAcc = kK, kMl = kAcc + sizeof(float) * kGroups * kRows * D;
-  static_assert(!kThin || kMl + sizeof(float) * 2 * kGroups * kRows <= kV, "the ends fit K's place");
+  static_assert(!kJoined || kMl + sizeof(float) * 2 * kGroups * kRows <= kV, "the ends fit K's place");
 };
 
 // acc += P V over n tokens; with kSkip a weight of zero leaves its token out altogether (it may be hidden, and hold a
@@ -105,16 +107,16 @@ __device__ __forceinline__ void write_statistics(const ChunkArgs& a, const Chunk
 }
 
 // One item; every thread of the CTA calls it.
-template <int D, int kPer, bool kThin>
+template <int D, int kPer, int kRowWarps>
 __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem& it, unsigned char* smem,
                                          uint32_t& eflags) {
   using S = SimtGeom<D>;
-  using P = Step<D, kPer, kThin>;
+  using P = Step<D, kPer, kRowWarps>;
   constexpr int kThreads = S::kThreads, kTok = P::kTok, kCols = P::kCols;
   float* sq = reinterpret_cast<float*>(smem + P::kQ);
-  const int tid = threadIdx.x, tx = tid % 16, warp = tid / 32;
-  const int ty = kThin ? tid / 16 % 2 : tid / 16;  // of the threads that share the rows
-  const int first = kThin ? warp * P::kWarpTok : 0;  // the warp's first token of a step
+  const int tid = threadIdx.x, tx = tid % 16, group = tid / 32 / kRowWarps;
+  const int ty = tid / 16 % (2 * kRowWarps);  // of the threads over the rows
+  const int first = group * P::kWarpTok;      // the warp's first token of a step
   float* sp = reinterpret_cast<float*>(smem + P::kP) + first;
   const int32_t p_lo = it.p0 + (int32_t)a.by_group.div(it.row0),
                 p_hi = it.p0 + (int32_t)a.by_group.div(it.row0 + it.rows - 1);
@@ -129,7 +131,7 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
     }
     *reinterpret_cast<float4*>(sq + row * S::LD + c * 4) = x;
   }
-  const bool work = kThin ? warp < P::kGroups : (ty & ~1) * kPer < it.rows;  // the warp has a row, and tokens
+  const bool work = group < P::kGroups && (ty & ~1) * kPer < it.rows;  // the warp has tokens, and a row
   const int32_t rho0 = it.row0 + ty * kPer;
   float m[kPer], l[kPer];
   float2 acc[kPer][D / 32];
@@ -247,7 +249,7 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
         add_values<D, kPer, P::kWarpTok, P::LP, false>(sp, sv, ty, tx, acc);
     }
   }
-  if (kThin) __syncthreads();  // K is read
+  if (P::kJoined) __syncthreads();  // K is read
   if (work) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -257,22 +259,22 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         const float4 x = make_float4(acc[i][c * 2].x, acc[i][c * 2].y, acc[i][c * 2 + 1].x, acc[i][c * 2 + 1].y);
-        if (kThin)
-          *reinterpret_cast<float4*>(smem + P::kAcc + sizeof(float) * ((warp * P::kRows + row) * D + c * 64 + tx * 4)) = x;
+        if (P::kJoined)
+          *reinterpret_cast<float4*>(smem + P::kAcc + sizeof(float) * ((group * P::kRows + row) * D + c * 64 + tx * 4)) = x;
         else if (row < it.rows)
           write_row<D>(a, it, row, c * 64 + tx * 4, x, l[i]);
       }
       if (tx == 0) {
-        if (kThin)
-          *reinterpret_cast<float2*>(smem + P::kMl + sizeof(float) * 2 * (warp * P::kRows + row)) =
+        if (P::kJoined)
+          *reinterpret_cast<float2*>(smem + P::kMl + sizeof(float) * 2 * (group * P::kRows + row)) =
               make_float2(m[i], l[i]);
         else if (row < it.rows)
           write_statistics(a, it, row, m[i], l[i]);
       }
     }
   }
-  if (!kThin) return;
-  // the warps' parts of each row, in their order
+  if (!P::kJoined) return;
+  // the groups' parts of each row, in their order
   __syncthreads();
   for (int i = tid; i < it.rows * (D / 4); i += kThreads) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
@@ -294,11 +296,12 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
   }
 }
 
+constexpr size_t larger(size_t x, size_t y) { return x > y ? x : y; }
 template <int D>
-constexpr size_t kSimtSmem = Step<D, 8, false>::kSmem;
-template <int D, int kPer>
-constexpr bool kThinFits = Step<D, kPer, true>::kSmem <= kSimtSmem<D>;
-static_assert(kThinFits<64, 4> && kThinFits<64, 8> && kThinFits<128, 4> && kThinFits<128, 8>, "one size for all items");
+constexpr size_t kSimtSmem = larger(larger(Step<D, 4, 1>::kSmem, Step<D, 8, 1>::kSmem),
+                                    larger(larger(Step<D, 8, 2>::kSmem, Step<D, 8, 4>::kSmem),
+                                           Step<D, 8, SimtGeom<D>::kThreads / 32>::kSmem));
+static_assert(2 * (kSimtSmem<64> + 1024) <= 233472 && kSimtSmem<128> <= 232448, "two CTAs an SM; one");
 
 template <int D>
 __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_simt_kernel(const ChunkArgs a) {
@@ -318,11 +321,15 @@ __global__ void __launch_bounds__(SimtGeom<D>::kThreads, D == 64 ? 2 : 1) chunk_
     if (next >= n_items) break;
     const ChunkItem it = items[next];
     if (it.rows <= 8)
-      attend_item<D, 4, true>(a, it, smem, eflags);
+      attend_item<D, 4, 1>(a, it, smem, eflags);
     else if (it.rows <= 16)
-      attend_item<D, 8, true>(a, it, smem, eflags);
+      attend_item<D, 8, 1>(a, it, smem, eflags);
+    else if (it.rows <= 32)
+      attend_item<D, 8, 2>(a, it, smem, eflags);
+    else if (D == 64 || it.rows <= 64)
+      attend_item<D, 8, 4>(a, it, smem, eflags);
     else
-      attend_item<D, 8, false>(a, it, smem, eflags);
+      attend_item<D, 8, SimtGeom<D>::kThreads / 32>(a, it, smem, eflags);
   }
   if (tid == 0) raise_flags(a.error_flags, eflags);
 }
