@@ -3,9 +3,9 @@
 // A CTA takes a tile of 64 rows (128 at d 128) and walks its pages 64 tokens (32) at a time, the next ones on
 // their way meanwhile: S = Q K^T by 8 rows x 4 tokens (2) of a thread, a running maximum and sum per row in fp32,
 // O += P V by 8 rows x d / 16 columns of a thread, both in packed pairs of fp32.  Bound by the fp32 rate (4 d
-// operations per row and token): 2048 tokens over 4096 more take 962 us, 42 TFLOP/s, its pipe busy on 58 % of the cycles;
+// operations per row and token): 2048 tokens over 4096 more take 980 us, 41 TFLOP/s, its pipe busy on 58 % of the cycles;
 // 8 warps an SM leave little to fall back on while a sum waits for its last term, so terms of one sum are kept apart
-// (2 % faster).  7 ragged requests of up to 300 tokens at d 64 take 166 us, 30 TFLOP/s, the rest of which is the
+// (2 % faster).  7 ragged requests of up to 300 tokens at d 64 take 160 us, 31 TFLOP/s, the rest of which is the
 // ends of chunks that fill a tile in part (195 with 4 rows x 4 tokens a thread, whose reads of shared memory took 24
 // lines for 128 operations a lane instead of 16; 214 with tiles of 128 rows).  Rows are padded by 16 bytes so that
 // a warp's tokens lie in different banks.
