@@ -19,7 +19,6 @@
 namespace srkv {
 namespace {
 
-
 template <int D>
 struct SimtGeom {
   static constexpr int kRows = D == 64 ? kChunkTileSimt64 : kChunkTileSimt128;
