@@ -514,7 +514,7 @@ srkv_status srkv_retrieval_decode_prefix(const srkv_config* cfg, const void* q,
  * row i stands at position p = L - n_r + i, and
  *   srkv_chunk_attention:         attends the tokens t <= p;
  *   srkv_chunk_attention_window:  those of them with t < init_tokens or t > p - local_tokens: the first
- *     tokens and the window of the position (StreamingLLM's attention, survey "大模型推理百倍加速之KV
+ *     tokens and the window of the position (survey "大模型推理百倍加速之KV
  *     cache篇": sinks and a sliding window), as the decode calls see them without a kept block.
  * out[row][j][:] = softmax over those tokens of q[row][j].K_t / sqrt(d), times V_t; a row that attends
  * nothing, or whose logits are all -infinity, gives 0.  A row depends on no token that it does not attend,
