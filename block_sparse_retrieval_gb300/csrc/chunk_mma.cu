@@ -785,7 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (work) {
           const int n_odd = n > 0 ? sh.n_odd[slot.at] : 0;
           const int32_t rho = it.row0 + row;
-          const float w = l == 0.f ? 0.f : it.slot >= 0 ? 1.f : 1.f / l;
+          // A row without a finite logit is zero whatever its values are; a partial result of one keeps what it has, as
+          // another part may have a weight.
+          const bool none = l == 0.f && it.slot < 0;
+          const float w = it.slot >= 0 ? 1.f : 1.f / l;
           const int col = D / 2 * half;
           // rows of the output that this warp's lanes stand for, -1: none
           const int32_t token = (int32_t)a.by_group.div(rho);
@@ -801,16 +804,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld();
               tmem_use32(o);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {  // (a row without weights: zeros times finite values, so zeros)
+              for (int e = 0; e < 32; e += 2) {
                 const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), w2);
-                o[e] = __float_as_uint(x.x);
-                o[e + 1] = __float_as_uint(x.y);
+                o[e] = none ? 0u : __float_as_uint(x.x);
+                o[e + 1] = none ? 0u : __float_as_uint(x.y);
               }
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = 0;
             }
-            if (n_odd > 0 && mine) {
+            if (n_odd > 0 && mine && !none) {
 #pragma unroll 1
               for (int e = 0; e < 32; ++e) {
                 const float x =

@@ -47,8 +47,9 @@ struct Step {
   static_assert(!kJoined || kMl + sizeof(float) * 2 * kGroups * kRows <= kV, "the ends fit K's place");
 };
 
-// acc += P V over n tokens; with kSkip a weight of zero leaves its token out altogether (it may be hidden, and hold a
-// NaN).
+constexpr float kHidden = -1.f;  // in place of a hidden token's weight
+
+// acc += P V over n tokens; with kSkip some may be hidden, which are left out altogether (one may hold a NaN).
 template <int D, int kPer, int kTokens, int LP, bool kSkip>
 __device__ __forceinline__ void add_values(const float* sp, const float* sv, int ty, int tx,
                                            float2 (&acc)[kPer][D / 32]) {
@@ -72,7 +73,7 @@ __device__ __forceinline__ void add_values(const float* sp, const float* sv, int
     for (int u = 0; u < 4; ++u) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (kSkip && w[i][u] == 0.f) continue;
+        if (kSkip && w[i][u] < 0.f) continue;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           const float2 ww = make_float2(w[i][u], w[i][u]);
@@ -96,8 +97,9 @@ __device__ __forceinline__ void write_row(const ChunkArgs& a, const ChunkItem& i
   const int32_t rho = it.row0 + row, token = (int32_t)a.by_group.div(rho);
   float* out = static_cast<float*>(a.out) +
                ((int64_t)(it.tok0 + token) * a.Hq + it.head * a.G + (rho - token * a.G)) * D + col;
-  const float w = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<float4*>(out) = make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
+  const float w = 1.f / l;  // (without a finite logit zeros, whatever the values)
+  *reinterpret_cast<float4*>(out) =
+      l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
 }
 __device__ __forceinline__ void write_statistics(const ChunkArgs& a, const ChunkItem& it, int row, float m, float l) {
   if (it.slot >= 0)
@@ -219,10 +221,12 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
       for (int i = 0; i < kPer; ++i) {
         const int32_t pos = it.p0 + (int32_t)a.by_group.div(rho0 + i);
         float top = m[i], s[kCols];
+        bool hidden[kCols];
 #pragma unroll
         for (int jj = 0; jj < kCols; ++jj) {
           s[jj] = (s2[i][jj].x + s2[i][jj].y) * a.scale_log2;
-          if (masked && !chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local)) s[jj] = -INFINITY;
+          hidden[jj] = masked && !chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local);
+          if (hidden[jj]) s[jj] = -INFINITY;
           top = fmaxf(top, s[jj]);
         }
 #pragma unroll
@@ -234,7 +238,7 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
         for (int jj = 0; jj < kCols; ++jj) {
           const float p = exp2f(s[jj] - ref);
           sum += p;
-          sp[(ty * kPer + i) * P::LP + tx + 16 * jj] = p;
+          sp[(ty * kPer + i) * P::LP + tx + 16 * jj] = hidden[jj] ? kHidden : p;
         }
         m[i] = top;
         l[i] = fmaf(l[i], w, sum);  // of this thread's tokens: added up over the 16 threads at the end

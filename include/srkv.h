@@ -517,7 +517,9 @@ srkv_status srkv_retrieval_decode_prefix(const srkv_config* cfg, const void* q,
  *     tokens and the window of the position (survey "大模型推理百倍加速之KV
  *     cache篇": sinks and a sliding window), as the decode calls see them without a kept block.
  * out[row][j][:] = softmax over those tokens of q[row][j].K_t / sqrt(d), times V_t; a row that attends
- * nothing, or whose logits are all -infinity, gives 0.  A row depends on no token that it does not attend,
+ * nothing, or whose logits are all -infinity, gives 0, whatever its values.  Else an attended value that is not
+ * finite makes its element of the row infinite or NaN, however small its weight (a weight that fp32 does not hold
+ * may turn an infinity into a NaN).  A row depends on no token that it does not attend,
  * whatever that token's key and value hold (NaN and infinities too), nor on anything behind L.  Logits,
  * maxima, sums and outputs are held in fp32.  With bf16 the softmax weights, up to 2^8 each as they are held,
  * are rounded to bf16 for the product with V (by up to 2^-8 of each), so 2^8 times the sum of the attended
