@@ -221,12 +221,10 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
       for (int i = 0; i < kPer; ++i) {
         const int32_t pos = it.p0 + (int32_t)a.by_group.div(rho0 + i);
         float top = m[i], s[kCols];
-        bool hidden[kCols];
 #pragma unroll
         for (int jj = 0; jj < kCols; ++jj) {
           s[jj] = (s2[i][jj].x + s2[i][jj].y) * a.scale_log2;
-          hidden[jj] = masked && !chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local);
-          if (hidden[jj]) s[jj] = -INFINITY;
+          if (masked && !chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local)) s[jj] = -INFINITY;
           top = fmaxf(top, s[jj]);
         }
 #pragma unroll
@@ -238,12 +236,22 @@ __device__ __forceinline__ void attend_item(const ChunkArgs& a, const ChunkItem&
         for (int jj = 0; jj < kCols; ++jj) {
           const float p = exp2f(s[jj] - ref);
           sum += p;
-          sp[(ty * kPer + i) * P::LP + tx + 16 * jj] = hidden[jj] ? kHidden : p;
+          sp[(ty * kPer + i) * P::LP + tx + 16 * jj] = p;
         }
         m[i] = top;
         l[i] = fmaf(l[i], w, sum);  // of this thread's tokens: added up over the 16 threads at the end
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) acc[i][e] = make_float2(acc[i][e].x * w, acc[i][e].y * w);
+      }
+      if (masked) {  // (apart from the weights: marked among them, pages that all rows see paid 3 % for it)
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+          const int32_t pos = it.p0 + (int32_t)a.by_group.div(rho0 + i);
+#pragma unroll
+          for (int jj = 0; jj < kCols; ++jj)
+            if (!chunk_attends(pos, tok + tx + 16 * jj, a.init, a.local))
+              sp[(ty * kPer + i) * P::LP + tx + 16 * jj] = kHidden;
+        }
       }
       __syncwarp();  // a row's weights come from the 16 lanes that read them
       if (masked)
