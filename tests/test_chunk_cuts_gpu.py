@@ -1,0 +1,73 @@
+"""Long page lists among others: that the plan divides them, and that every page of a divided list counts once.  The
+values of the second part are counts (equal logits, a page's values its own), so that a page left out or taken twice
+shows whatever the list's length."""
+import math
+
+import pytest
+import torch
+
+import chunk_ref as ref
+from block_sparse_retrieval_gb300 import srkv
+from test_chunk_gpu import attend
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def planned(case, window=False):
+    """The output, and what the plan left in the workspace: its items, and the lists that it divided."""
+    ws = torch.zeros(srkv.chunk_workspace_size(case.cfg, case.T, len(case.reqs)), dtype=torch.uint8, device=DEV)
+    out = attend(case, window, workspace=ws)
+    torch.cuda.synchronize()
+    assert int(case.flags) == 0
+    return out, *ws[:8].view(torch.int32).tolist()
+
+
+def count(case):
+    """Every logit 0; block b of a request holds 1 + b // d in column b % d."""
+    d = case.cfg["head_dim"]
+    case.q.normal_()
+    for r, (n, p) in enumerate(case.reqs):
+        L = n + p
+        blocks = case.table[r, :-(-L // 128)].long()
+        b = torch.arange(len(blocks), device=DEV)
+        v = torch.zeros(len(blocks), d, device=DEV)
+        v[b, b % d] = (1 + b // d).float()
+        case.k[blocks] = 0
+        case.v[blocks] = v.to(case.dtype)[:, None, None, :]
+        if L % 128:  # behind the sequence
+            case.k[blocks[-1], :, L % 128:] = float("nan")
+            case.v[blocks[-1], :, L % 128:] = float("nan")
+    return case
+
+
+def check_counts(case, out, window=False):
+    d, Hq = case.cfg["head_dim"], case.cfg["num_q_heads"]
+    init, local = (case.cfg["init_tokens"], case.cfg["local_tokens"]) if window else (1 << 30, 0)
+    for r, (n, p) in enumerate(case.reqs):
+        lo, L = int(case.offsets[r]), n + p
+        t = torch.arange(L, device=DEV)
+        one = torch.zeros(L, d, dtype=torch.float64, device=DEV)
+        one[t, t // 128 % d] = (1 + t // 128 // d).double()
+        upto = torch.cat((one.new_zeros(1, d), one.cumsum(0)))
+        del one
+        end = torch.arange(p, L, device=DEV) + 1
+        first = end.clamp(max=init)
+        start = torch.maximum(first, end - local) if local else end
+        total = upto[first] + upto[end] - upto[start]
+        want = total / (first + end - start).clamp(min=1).unsqueeze(1)
+        want = want.unsqueeze(1).expand(n, Hq, d)
+        # weights are 1 and sums are whole numbers below 2^24, so all is exact but the reciprocal, its product
+        # and the rounding to the type
+        tol = (torch.finfo(case.dtype).eps / 2 + 2.0 ** -21) * want
+        bad = ~((out[lo:lo + n].double() - want).abs() <= tol)
+        assert not bad.any(), (r, int(bad.sum()), bad.nonzero()[:3].tolist())
+
+
+def test_a_long_token_beside_a_prompt_is_divided():
+    """As a step of a server that starts a prompt while others decode: 64 full tiles, and lists of 1024 pages."""
+    case = count(ref.Case([(4096, 0), (1, 131071)], Hq=32, Hkv=8, d=128, seed=71))
+    out, items, merges = planned(case)
+    assert merges >= 8 and items >= 65 * 8 + 8 * 6, (items, merges)
+    check_counts(case, out)
