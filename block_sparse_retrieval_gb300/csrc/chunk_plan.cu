@@ -219,8 +219,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
           rounds ? (float)(c.whole < tiles ? pages - before[c.whole] : 0) * (float)a.Hkv * a.per_cta : load;
       // One piece for each CTA, or two (after rounds; on CUDA cores, whose pages take longer than a piece's start and
       // end, from 8 pages on: 7 ragged chunks of 9 pages a CTA 175 -> 169 us, 3 of 3 pages 65 -> 72).
-      const int32_t cut_lists = lists - c.whole * a.Hkv, k = rounds || (a.page_rate < 1.f && rest >= 8.f) ? 2 : 1,
-                    pieces = cut_lists + k * a.ctas;
+      const int32_t cut_lists = lists - c.whole * a.Hkv;
+      // Partial results are those of the lists that are cut: no more of them than there are cuts (one more than planned,
+      // as the average load is rounded), and a piece more than cuts each.
+      auto fits = [&](int32_t cuts) {
+        const int32_t partial = cuts + min(cuts, cut_lists);
+        return partial <= kChunkSplitItems && (int64_t)partial * most_rows <= a.lay.rows_cap;
+      };
+      int32_t k = rounds || (a.page_rate < 1.f && rest >= 8.f) ? 2 : 1;
+      if (!fits(k * a.ctas + 1)) k = 1;  // a tile or two of one head on CUDA cores
+      const int32_t pieces = cut_lists + k * a.ctas;
       c.grid = max(a.page_rate < 1.f ? 1 : 2, (int32_t)ceilf(fminf(rest / (float)k, 1e9f)));
       float cost = load + item * (many ? items + 2.f : 2.f) + merge;
       if (!rounds && longest == shortest) {  // equal lists: into as many equal parts as make one round
@@ -232,11 +240,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         }
       }
       cost += (float)pieces * (float)most_rows * kRowCost * a.page_rate;
-      // Partial results are those of the lists that are cut: no more of them than there are cuts (one more than planned,
-      // as the average load is rounded), and a piece more than cuts each.
-      const int32_t cuts = k * a.ctas + 1, partial = cuts + min(cuts, cut_lists);
-      if (cost >= whole || partial > kChunkSplitItems || (int64_t)partial * most_rows > a.lay.rows_cap ||
-          pages * a.Hkv > (long long)UINT32_MAX)
+      if (cost >= whole || !fits(k * a.ctas + 1) || pages * a.Hkv > (long long)UINT32_MAX)
         c = {tiles, 1, 0};
     }
     cut = c;

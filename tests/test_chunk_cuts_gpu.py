@@ -71,3 +71,13 @@ def test_a_long_token_beside_a_prompt_is_divided():
     out, items, merges = planned(case)
     assert merges >= 8 and items >= 65 * 8 + 8 * 6, (items, merges)
     check_counts(case, out)
+
+
+@pytest.mark.parametrize("n", [1, 16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_one_list_of_one_head_is_divided(dtype, d, n):
+    case = count(ref.Case([(n, 400000)], Hq=1, Hkv=1, d=d, dtype=dtype, seed=72))
+    out, items, merges = planned(case)
+    assert merges == 1 and items >= 100, (items, merges)
+    check_counts(case, out)
