@@ -2,7 +2,9 @@
 //
 // Lengths live on the device, so the work is divided there: one CTA lists the items, longest first, and the
 // attention kernel's CTAs take them one by one.  Lists are kept whole where they balance by themselves; else they are
-// cut: where they are fewer than CTAs all of them, else those that remain after full rounds of whole ones.
+// cut: where they are fewer than CTAs all of them, else those that remain after full rounds of whole ones; where they are
+// many (16 and more a CTA, or of more tiles than are held on chip), those longer than the average load, each by its own
+// length.
 //
 // This kernel's time is the fetch of its own instructions (a launch finds none of them on its SM: some 300 cycles
 // for every 8), not its arithmetic.  So loops are kept rolled, divisions by the head counts are multiplications, and
@@ -27,9 +29,10 @@ __device__ __forceinline__ int bucket_of(int32_t n) {
 }
 
 // How lists are cut: those of the first `whole` tiles not at all; the others, one behind the other (tile by tile,
-// head by head), at every `grid` pages, or, if `parts` > 0, each into that many equal parts.
+// head by head), at every `grid` pages, or, if `parts` > 0, each into that many equal parts, or, if `most` > 0, each
+// into as few equal parts as are no longer than that.
 struct Cuts {
-  int32_t whole, grid, parts;
+  int32_t whole, grid, parts, most;
 };
 
 // The requests as the plan sees them: on chip while they are few, else in the workspace and the call's arrays.
@@ -78,8 +81,9 @@ __device__ __noinline__ Pieces pieces_of(const Cuts& cut, int32_t t, int32_t h, 
   Pieces p = {n, 1, 1};
   if (t >= cut.whole) {
     p.each = cut.grid;
-    if (cut.parts > 0) {
-      p.each = max(1, (n + cut.parts - 1) / cut.parts);
+    if (cut.parts > 0 || cut.most > 0) {
+      const int32_t parts = cut.parts > 0 ? cut.parts : max(1, (n + cut.most - 1) / cut.most);
+      p.each = max(1, (n + parts - 1) / parts);
       p.first = min(n, p.each);
     } else {
       // the row of lists is cut where its position is a multiple of the grid (rows of 2^32 pages are not cut)
@@ -203,14 +207,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   // ---- whole lists, or cut ones
   const int32_t lists = tiles * a.Hkv;
   if (tid == 0) {
-    Cuts c = {tiles, 1, 0};
+    Cuts c = {tiles, 1, 0, 0};
+    // whole lists: the average load; or the longest one; or, with some CTAs idle while the last lists run, the
+    // load and those CTAs' share of a shortest list
+    const float load = (float)pages * (float)a.Hkv * a.per_cta;
+    const float items = (float)lists * a.per_cta, idle = ceilf(items) - items;
+    const float item = kItemCost * a.page_rate, merge = kMergeCost * a.page_rate;
+    const float whole = fmaxf((float)longest, load + idle * (float)shortest) + item * ceilf(items);
     if (tiles <= kHeld && lists < 16 * a.ctas) {
-      // whole lists: the average load; or the longest one; or, with some CTAs idle while the last lists run, the
-      // load and those CTAs' share of a shortest list
-      const float load = (float)pages * (float)a.Hkv * a.per_cta;
-      const float items = (float)lists * a.per_cta, idle = ceilf(items) - items;
-      const float item = kItemCost * a.page_rate, merge = kMergeCost * a.page_rate;
-      const float whole = fmaxf((float)longest, load + idle * (float)shortest) + item * ceilf(items);
       // Full rounds of whole lists, and the rest cut; else all cut, where one list is longer than the average load, too
       // (4 ragged chunks of up to 600 over 32768 tokens 243 -> 136 us).
       const bool many = lists >= a.ctas, rounds = many && (float)longest <= load;
@@ -241,7 +245,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       }
       cost += (float)pieces * (float)most_rows * kRowCost * a.page_rate;
       if (cost >= whole || !fits(k * a.ctas + 1) || pages * a.Hkv > (long long)UINT32_MAX)
-        c = {tiles, 1, 0};
+        c = {tiles, 1, 0, 0};
+    } else if ((float)longest > load) {
+      // A list of n > most pages has fewer than 2 n / most parts, so all have fewer than 2 load / most a CTA, whose
+      // partial results have to fit (and some to spare for the rounding of the load).
+      const float most = ceilf(1.001f * load * fmaxf(1.f, 2.f * (float)a.ctas * (float)most_rows / (float)a.lay.rows_cap));
+      const float cost = load + item * (ceilf(items) + 2.f) + merge +
+                         2.f * (float)a.ctas * (float)most_rows * kRowCost * a.page_rate;
+      if (cost < whole && most < (float)longest) c = {0, 1, 0, (int32_t)most};
     }
     cut = c;
     equal = longest == shortest && (c.whole == tiles || c.parts > 0);

@@ -81,3 +81,17 @@ def test_one_list_of_one_head_is_divided(dtype, d, n):
     out, items, merges = planned(case)
     assert merges == 1 and items >= 100, (items, merges)
     check_counts(case, out)
+
+
+@pytest.mark.parametrize("reqs,Hkv", [([(1, 511)] * 200 + [(1, 131071)] + [(1, 511)] * 120, 8),
+                                      ([(1, 1023)] * 300 + [(1, 131071)] + [(1, 1023)] * 300, 1),
+                                      ([(1, 600)] * 320 + [(300, 65000), (3, 99999)], 8)],
+                         ids=["320 short", "600 short of one head", "two long"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64), (F32, 128)])
+def test_a_long_list_among_many_is_divided(reqs, Hkv, dtype, d):
+    case = count(ref.Case(reqs, Hq=Hkv, Hkv=Hkv, d=d, dtype=dtype, seed=73))
+    out, items, merges = planned(case)
+    lists = sum(-(-n // (256 if dtype == BF else d)) for n, _ in reqs) * Hkv
+    assert merges >= Hkv and items >= lists + 4 * Hkv, (items, lists, merges)
+    check_counts(case, out)
+    assert torch.equal(planned(case)[0], out)
