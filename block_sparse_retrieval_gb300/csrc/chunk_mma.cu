@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t rho = it.row0 + row;
           // A row without a finite logit is zero whatever its values are; a partial result of one keeps what it has, as
           // another part may have a weight.
-          const bool none = l == 0.f && it.slot < 0;
+          const bool none = l == 0.f && it.slot < 0, some = __any_sync(0xffffffffu, none);
           const float w = it.slot >= 0 ? 1.f : 1.f / l;
           const int col = D / 2 * half;
           // rows of the output that this warp's lanes stand for, -1: none
@@ -806,8 +806,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), w2);
-                o[e] = none ? 0u : __float_as_uint(x.x);
-                o[e + 1] = none ? 0u : __float_as_uint(x.y);
+                o[e] = __float_as_uint(x.x);
+                o[e + 1] = __float_as_uint(x.y);
+              }
+              if (some) {  // (a branch that next to no warp takes: 64 selects took 1 % of 1024 single tokens over 512)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = none ? 0u : o[e];
               }
             } else {
 #pragma unroll
