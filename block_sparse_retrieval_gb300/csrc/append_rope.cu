@@ -96,12 +96,14 @@ __device__ __forceinline__ Request load_request(const RopeArgs& a, int32_t r, ui
 }
 
 // freq / (2 pi) modulo 1 in 64-bit fixed point; the product in twice 53 bits, as a fraction of many turns loses
-// its leading bits.
+// its leading bits.  A negative frequency is its opposite's complement: a small negative number's fraction would be
+// next to 1, where 53 bits hold less of it.
 __device__ __forceinline__ uint64_t turns_of(double freq) {
   constexpr double c = 0.15915494309189535, c_lo = -9.839338337591243e-18;  // 1 / (2 pi)
-  const double hi = freq * c, lo = fma(freq, c_lo, fma(freq, c, -hi));
-  return __double2ull_rn((hi - floor(hi)) * 18446744073709551616.0) +
-         (uint64_t)__double2ll_rn(lo * 18446744073709551616.0);
+  const double f = fabs(freq), hi = f * c, lo = fma(f, c_lo, fma(f, c, -hi));
+  const uint64_t turns = __double2ull_rn((hi - floor(hi)) * 18446744073709551616.0) +
+                         (uint64_t)__double2ll_rn(lo * 18446744073709551616.0);
+  return freq < 0. ? 0 - turns : turns;
 }
 
 // Sine and cosine of position p times a frequency (fraction of a turn, 64-bit fixed point).

@@ -174,8 +174,8 @@ srkv_status srkv_append_kv(const srkv_config* cfg, const void* k_new, const void
  *   k_stride, v_stride elements apart (the parts of one fused projection, for instance; multiples of 16
  *   bytes, at least one token's heads); q_out: [total_tokens][Hq][d], q itself where q_stride = Hq d, else
  *   apart from q, k_new and v_new (SRKV_ERR_INVALID_ARG where it lies between their first and last
- *   element); all 16-byte aligned.  rope_freqs: device double [rope_dim / 2], finite; rope_dim: even, 0 to d,
- *   0 leaves out the rotation; a multiple of 16, else SRKV_ERR_UNSUPPORTED.  chunk_offsets: device int32
+ *   element); all 16-byte aligned.  rope_freqs: device double [rope_dim / 2], of magnitudes below 2^32, of any sign;
+ *   rope_dim: even, 0 to d, 0 leaves out the rotation; a multiple of 16, else SRKV_ERR_UNSUPPORTED.  chunk_offsets: device int32
  *   [batch + 1], from 0 or more up to total_tokens or less, not decreasing; n_r = 0 is allowed, and rows
  *   of the packed tensors outside every request are left alone.  seq_lens: the lengths before the
  *   chunk, read only: the caller advances them (seq_lens[r] += n_r), and gives every request pages of its own
