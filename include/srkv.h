@@ -182,8 +182,9 @@ srkv_status srkv_append_kv(const srkv_config* cfg, const void* k_new, const void
  *   for the tokens written.
  *   A request whose offsets are wrong (SRKV_EFLAG_CHUNK) or whose tokens do not all fit in
  *   [0, max_blocks * S) (SRKV_EFLAG_SEQ_LEN) is skipped, a page id outside [0, num_pages) skips that page
- *   (SRKV_EFLAG_PAGE_RANGE; queries are rotated all the same); all are flagged.  Where offsets go down, rows that
- *   two requests claim are one's or neither's.
+ *   (SRKV_EFLAG_PAGE_RANGE; queries are rotated all the same); all are flagged.  Where offsets go down,
+ *   other requests' rows and pages, too, are written as described or left as they were (a row's request is searched for,
+ *   as offsets that do not go down allow).
  * Asynchronous on `stream`; one kernel.
  */
 srkv_status srkv_append_kv_rope(const srkv_config* cfg, const void* q, int64_t q_stride,
@@ -531,8 +532,9 @@ srkv_status srkv_retrieval_decode_prefix(const srkv_config* cfg, const void* q,
  *   workspace: >= srkv_chunk_workspace_size(cfg, total_tokens, batch) bytes, 256-byte aligned; its
  *   contents on entry do not matter; it is scratch of this call until the stream reaches its end, so
  *   calls that may overlap (streams, captured graphs) take one each.
- *   A request whose offsets are wrong is skipped; of a chunk longer than its sequence the first rows
- *   attend nothing; both flag SRKV_EFLAG_CHUNK.  A length outside [0, max_blocks * S] is clamped into it
+ *   A request whose offsets are wrong is skipped (where offsets go down, a row that two requests claim is either's,
+ *   and requests may be skipped that ask for more rows in all than there are); of a chunk longer than its sequence
+ *   the first rows attend nothing; all flag SRKV_EFLAG_CHUNK.  A length outside [0, max_blocks * S] is clamped into it
  *   (SRKV_EFLAG_SEQ_LEN).  The tokens of a page whose id is outside [0, num_pages) are left out
  *   (SRKV_EFLAG_PAGE_RANGE).
  *   The output is a function of the inputs alone: bitwise the same on every call.

@@ -95,3 +95,26 @@ def test_a_long_list_among_many_is_divided(reqs, Hkv, dtype, d):
     assert merges >= Hkv and items >= lists + 4 * Hkv, (items, lists, merges)
     check_counts(case, out)
     assert torch.equal(planned(case)[0], out)
+
+
+@pytest.mark.parametrize("reqs", [[(1, 65535)], [(300, 130772)], [(2, 30000), (257, 66000), (1, 131071)]],
+                         ids=["token", "rows", "mixed"])
+@pytest.mark.parametrize("window", [False, True])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64), (F32, 128)])
+def test_every_page_counts_once(reqs, window, dtype, d):
+    case = count(ref.Case(reqs, Hq=2, Hkv=1, d=d, dtype=dtype, seed=74, init=1000, local=20001))
+    check_counts(case, planned(case, window)[0], window)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_random_values_over_131072_tokens(dtype, d):
+    """Two tiles over a thousand pages against 64 bits, as a whole.  Logits are N(0, 1) and values independent of them, so
+    with weights w the output's mean square is that of w v, summed.  Rounding each weight (by up to 2^-8, evenly: 2^-8 /
+    sqrt 3 in the mean square) and each output (the same) adds sqrt(2 / 3) 2^-8 of that; what fp32 adds (a logit
+    is a sum of d products of up to 12 in all, whose roundings are as good as independent: sqrt(d) 2^-24 12 < 2^-16) the
+    rest.  One page left out is 2^-5."""
+    case = ref.Case([(300, 130772)], Hq=4, Hkv=1, d=d, dtype=dtype, seed=75)
+    out = attend(case)
+    want, _ = ref.attention(case, False)
+    error = float((out.double() - want).square().mean().sqrt() / want.square().mean().sqrt())
+    assert error <= (math.sqrt(2 / 3) * 2.0 ** -8 if dtype == BF else 0.0) + 2.0 ** -16, error
