@@ -19,7 +19,8 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBuckets = 64;   // sizes 0 .. 3, then two per octave
 constexpr int kHeld = 512;     // requests, and tiles, that are held on chip
 // What starting and ending an item costs, what the merge adds, and each row of a partial result, in pages on tensor
-// cores (1.6 us); a page on CUDA cores takes ten times that.
+// cores (1.6 us); a page on CUDA cores takes ten times that.  One figure each for both head sizes and for items of all
+// sizes, whose pages differ by 2 and more: whether and where lists are cut hangs on them, no result's bounds do.
 constexpr float kItemCost = 2.f, kMergeCost = 2.f, kRowCost = 1.f / 8192;
 
 __device__ __forceinline__ int bucket_of(int32_t n) {

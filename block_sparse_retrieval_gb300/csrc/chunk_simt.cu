@@ -3,7 +3,7 @@
 // A CTA takes a tile of 64 rows (128 at d 128) and walks its pages 64 tokens (32) at a time, the next ones on
 // their way meanwhile: S = Q K^T by 8 rows x 4 tokens (2) of a thread, a running maximum and sum per row in fp32,
 // O += P V by 8 rows x d / 16 columns of a thread, both in packed pairs of fp32.  Bound by the fp32 rate (4 d
-// operations per row and token): 2048 tokens over 4096 more take 980 us, 41 TFLOP/s, its pipe busy on 58 % of the cycles;
+// operations per row and token): 2048 tokens over 4096 more take 986 us, 41 TFLOP/s, its pipe busy on 58 % of the cycles;
 // 8 warps an SM leave little to fall back on while a sum waits for its last term, so terms of one sum are kept apart
 // (2 % faster).  7 ragged requests of up to 300 tokens at d 64 take 160 us, 31 TFLOP/s, the rest of which is the
 // ends of chunks that fill a tile in part (195 with 4 rows x 4 tokens a thread, whose reads of shared memory took 24
@@ -12,8 +12,8 @@
 //
 // Items of fewer rows (single tokens, the ends of chunks) would leave warps idle; there groups of warps share a step's
 // 64 tokens, each with a maximum, a sum and outputs of its own, joined in order at the end; and a thread takes 4
-// rows where 8 in all are enough.  64 single tokens over 8192 each, 8 heads of 128: 2918 -> 875 us (3.7 TB/s), of 64
-// 835 -> 380 (4.2), bound by the reads of shared memory; 6 x 17 rows over up to 3712 tokens 167 -> 109.
+// rows where 8 in all are enough.  64 single tokens over 4096 to 8192 each, 8 heads of 128: 2918 -> 880 us (3.7
+// TB/s), of 64 835 -> 380 (4.2), bound by the reads of shared memory; 6 x 17 rows over up to 3712 tokens 167 -> 109.
 #include "chunk_plan.cuh"
 
 namespace srkv {
