@@ -85,6 +85,82 @@ def test_an_append_directly_followed_by_attention(past, steps, dtype, d):
     assert int(c.flags) == 0
 
 
+@pytest.mark.parametrize("past", [[9000], [700, 5000, 90], [400 + 37 * i for i in range(40)]],
+                         ids=["one", "three", "forty"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_an_append_directly_followed_by_a_decode_step(past, dtype, d):
+    """Decode steps over what the rotated append wrote just before, and the chunk attention beside them."""
+    server = Server(past, [[1] * len(past)] * 8, dtype, d)
+    c = server.case
+    bufs = [srkv.DecodeBuffers(c.cfg, len(past), c.max_blocks, c.pages) for _ in server.steps]
+
+    def run(wait):
+        c.k.copy_(server.k0)
+        c.v.copy_(server.v0)
+        server.reps.zero_()
+        for (s, (q, kn, vn), offsets, past_r, lens, outs), b in zip(server.steps, bufs):
+            q_rot = server.q_rot[:len(past)]
+            srkv.append_kv_rope(c.cfg, q, kn, vn, server.f, c.k, c.v, c.table, offsets, past_r, server.reps, q_rot, c.flags)
+            wait()
+            srkv.retrieval_decode(c.cfg, q_rot, c.k, c.v, server.reps, c.table, lens, None, b.sel, b.nsel, b.out,
+                                  b.workspace, b.error_flags)
+            wait()
+            srkv.chunk_attention(c.cfg, q_rot, c.k, c.v, c.table, offsets, lens, outs[0], server.ws, c.flags)
+            wait()
+
+    def take():
+        decoded = []
+        torch.cuda.synchronize()
+        for b in bufs:
+            assert int(b.error_flags) == 0
+            decoded += [b.out.clone(), b.nsel.clone()]
+            b.out.zero_()
+        return server.take() + decoded
+
+    run(torch.cuda.synchronize)
+    want = take()
+    for _ in range(4):
+        run(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(take(), want))
+    assert int(c.flags) == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64), (F32, 128)])
+def test_two_calls_at_once(dtype, d):
+    """On two streams, with a workspace each."""
+    cases = [ref.Case([(300, 900), (1, 9000)], d=d, dtype=dtype, seed=97),
+             ref.Case([(1, 4000), (70, 3000), (5, 60)], d=d, dtype=dtype, seed=98)]
+    want = [attend(c).clone() for c in cases]
+    ws = [torch.zeros(srkv.chunk_workspace_size(c.cfg, c.T, len(c.reqs)), dtype=torch.uint8, device=DEV) for c in cases]
+    outs = [[torch.zeros_like(w) for _ in range(20)] for w in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, w, o, stream in zip(cases, ws, outs, streams):
+            attend(c, out=o[i], workspace=w, stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for w, os in zip(want, outs) for o in os)
+    assert all(int(c.flags) == 0 for c in cases)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(128, 1), (64, 1), (256, 2), (129, 1)])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_large_groups(Hq, Hkv, dtype, d):
+    case = ref.Case([(5, 300), (1, 700)], Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, seed=99)
+    want, tol = ref.attention(case, False)
+    assert ((attend(case).double() - want).abs() <= tol).all() and int(case.flags) == 0
+
+
+def test_one_token_of_a_fused_projection_in_place():
+    run = Run([(1, 300)], seed=100)
+    run.append()
+    want, k = run.q_out.clone(), run.case.k.clone()
+    assert run.q.data_ptr() != run.q_out.data_ptr()
+    run.q_out = run.q  # a single token's heads are contiguous
+    run.append()
+    assert torch.equal(run.q, want) and torch.equal(run.case.k.view(torch.uint8), k.view(torch.uint8))
+
+
 @pytest.mark.parametrize("offsets,good", [([0, 10, 30, 36], [0, 1]), ([-1, 10, 30, 35], [1, 2]),
                                           ([0, 40, 30, 35], [2]), ([0, 10, 1 << 30, 35], [0])])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
